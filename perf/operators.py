@@ -180,12 +180,12 @@ def _prepare_attn(case, gen):
     bf = {"dtype": torch.bfloat16, "device": "cuda"}
     s = {"kind": case["kind"], "hq": hq, "hkv": hkv, "d": d, "scale": d ** -0.5, "batch": len(a["len"]), "qs": a,
          "ks": b, "q": _normal(gen, tq, hq * d, std=1.5), "k": _normal(gen, tk, hkv * d), "v": _normal(gen, tk, hkv * d),
-         "o": torch.empty(tq, hq * d, **bf), "lse": torch.empty(hq, tq, device="cuda")}
+         "o": torch.empty(tq, hq * d, **bf), "lse": torch.empty(hq, tq, device="cuda"),
+         "ws": torch.empty(SCRATCH, dtype=torch.uint8, device="cuda")}
     if case["kind"] == "attn_train":
         s["do"] = _normal(gen, tq, hq * d)
         s["dq"], s["dk"], s["dv"] = (torch.empty(tq, hq * d, **bf), torch.empty(tk, hkv * d, **bf),
                                      torch.empty(tk, hkv * d, **bf))
-        s["ws"] = torch.empty(SCRATCH, dtype=torch.uint8, device="cuda")
     return s
 
 
@@ -366,7 +366,8 @@ def _own(s):
                                 s["draft"], hq, hkv, d, s["scale"], s["o"], ws=s["ws"])
         return {"o": s["o"]}
     cq, ck = s["qs"]["cu"], s["ks"]["cu"]
-    bl.bitlinear_attn_fwd(s["q"], s["k"], s["v"], cq, ck, s["batch"], hq, hkv, d, s["scale"], s["o"], s["lse"])
+    bl.bitlinear_attn_fwd(s["q"], s["k"], s["v"], cq, ck, s["batch"], hq, hkv, d, s["scale"], s["o"], s["lse"],
+                          ws=s["ws"])
     if s["kind"] == "attn":
         return {"o": s["o"], "lse": s["lse"]}
     bl.bitlinear_attn_bwd(s["q"], s["k"], s["v"], s["o"], s["lse"], s["do"], cq, ck, s["batch"], hq, hkv, d, s["scale"],
