@@ -551,6 +551,162 @@ int bitlinear_bwd_relu2_gate(const uint16_t *dY, const int8_t *xq, const float *
  * for bit.  For tests and tuning; returns BL_EINVAL for any other value. */
 int bitlinear_bwd_tiles(int tiles);
 
+/* ---------------------------------------------------------------------
+ * Between the q, k, v BitLinears and the o BitLinear of a block: head norms
+ * and rotary positions, and attention.  The pages describe BitNet as a
+ * transformer around its BitLinears (2B4T article §一, rotary positions) and
+ * give no formulas; those below are the operators' definitions here.
+ *
+ * Shapes: hq query heads, hkv key/value heads (hq a multiple of hkv: query
+ * head h reads key/value head h / (hq/hkv)), head size d 64 or 128.  A row
+ * of Q has hq*d, of K and V hkv*d elements; inputs named with a *_stride
+ * have that many elements between rows (a multiple of 16 bytes, at least the
+ * row), so slices of one fused projection are taken as they are; every
+ * other array is contiguous.  Offsets are formed in 64 bits: only row
+ * counts have to stay below 2^31.  Rows of inputs that belong to no
+ * sequence may hold anything, infinities and NaN included; in rows that do,
+ * values are finite. */
+#define BL_TYPE_F32   0
+#define BL_TYPE_BF16  1
+
+/* Table of the rotation: table[p*(d/2) + i] = (cos a, sin a) with
+ * a = p * base^(-2i/d), formed in binary64 and rounded once to binary32.
+ *   table  device float [max_pos][d/2][2], written.  max_pos >= 1, base > 0
+ * finite.  A caller with scaled positions fills its own table. */
+int bitlinear_rope_table(int64_t max_pos, int64_t d, double base, float *table, void *stream);
+
+/* Head norms of queries and keys with the position rotation, in one pass.
+ * For each row x of a head (q and k), with c, s = table[pos[t]]:
+ *   n = w x / sqrt(mean(x^2) + eps)       (n = x without weights)
+ *   y[i] = n[i] c[i] - n[i + d/2] s[i],  y[i + d/2] = n[i + d/2] c[i] + n[i] s[i]
+ * in binary32, rounded once to bf16; V is copied, rounded to bf16.
+ *   Q, K, V    device, rows as above, binary32 or bf16 (x_type: BL_TYPE_F32,
+ *              the BitLinears' Y, or BL_TYPE_BF16, their bf16 Y).  V and Vr
+ *              may both be NULL.
+ *   q_weight, k_weight  device float [d], both or neither (no norms).
+ *   eps        finite, >= 0.
+ *   pos        device int32 [tokens]; a position outside [0, max_pos) gives
+ *              NaN in that token's q and k rows.
+ *   slots      NULL, or device int64 [tokens]: the row of Kr and Vr that
+ *              token t's k and v go to (rows of a cache); rows that are not
+ *              named stay as they are, slots outside [0, kv_rows) are
+ *              skipped (padding), and the others must be distinct.
+ *   kv_rows    rows of Kr and Vr (without slots: at least tokens).
+ *   Qr         device bf16 [tokens][hq*d]; Kr, Vr  device bf16 [kv_rows][hkv*d].
+ * Outputs must not alias inputs.  tokens == 0 is a no-op. */
+int bitlinear_qk_rope(const void *Q, const void *K, const void *V, int x_type, int64_t q_stride,
+                      int64_t k_stride, int64_t v_stride, int64_t tokens, int64_t hq, int64_t hkv,
+                      int64_t d, const float *q_weight, const float *k_weight, float eps,
+                      const float *table, int64_t max_pos, const int32_t *pos,
+                      const int64_t *slots, int64_t kv_rows, uint16_t *Qr, uint16_t *Kr,
+                      uint16_t *Vr, void *stream);
+
+/* Its backward.  With g = the rotation's transpose applied to dy, n^ =
+ * x / sqrt(mean(x^2) + eps) and a = w g:
+ *   dx = (a - n^ mean(a n^)) / sqrt(mean(x^2) + eps),  dw = sum_t,h g n^
+ * (dx = g without weights; x, x_type and eps are then not read and Q, K may
+ * be NULL).  dx is rounded once to bf16 (the dY of the q and k BitLinears'
+ * bitlinear_bwd); dw is summed in binary32 per wavefront and binary64 over
+ * workgroups, in a fixed order.
+ *   dQr, dKr   device bf16 [tokens][hq*d], [tokens][hkv*d].
+ *   dQ, dK     device bf16, the same shapes, written.
+ *   dq_weight, dk_weight  device float [d], written; NULL without weights.
+ *   ws         bitlinear_qk_rope_bwd_workspace_bytes(d) bytes, 16-byte
+ *              aligned, clobbered; NULL without weights.
+ * tokens == 0 zeroes dq_weight and dk_weight and does nothing else. */
+size_t bitlinear_qk_rope_bwd_workspace_bytes(int64_t d);
+int bitlinear_qk_rope_bwd(const void *Q, const void *K, int x_type, int64_t q_stride,
+                          int64_t k_stride, int64_t tokens, int64_t hq, int64_t hkv, int64_t d,
+                          const float *q_weight, const float *k_weight, float eps,
+                          const float *table, int64_t max_pos, const int32_t *pos,
+                          const uint16_t *dQr, const uint16_t *dKr, uint16_t *dQ, uint16_t *dK,
+                          float *dq_weight, float *dk_weight, void *ws, size_t ws_bytes,
+                          void *stream);
+
+/* Causal attention over packed sequences: sequence b has the query rows
+ * [cu_q[b], cu_q[b+1]) and the key rows [cu_k[b], cu_k[b+1]).  Its query i
+ * (from 0) sees its keys j <= i + k_len - q_len: with equal lengths the
+ * usual mask, with more keys the queries are the last q_len positions (a
+ * prompt's next piece), with fewer the first rows see no key.
+ *   S = scale Q K^T over visible keys,  P = softmax(S),  O = P V,
+ *   lse = ln sum exp S
+ * A row that sees no key has O = 0 and lse = -infinity.  Products are bf16
+ * with binary32 sums, the softmax is binary32, P is rounded to bf16 for the
+ * product with V (relative 2^-9 per key) and O once more.
+ *   Q, K, V    device bf16 rows, strides below 2^22.
+ *   cu_q, cu_k device int32 [batch + 1], not decreasing, within [0, total_q]
+ *              and [0, total_k] (values outside are cut off there); they
+ *              are read by the kernels, so a captured graph may be replayed
+ *              with other lengths within the same totals.
+ *   O          device bf16 [total_q][hq*d]; lse  device float [hq][total_q]
+ *              or NULL.  Rows of no sequence stay as they are.
+ *   ws         bitlinear_attn_fwd_workspace_bytes() bytes, 256-byte
+ *              aligned, clobbered; may be NULL when that is 0.  Calls that
+ *              overlap on one workspace race.
+ * batch 1..65535, scale finite and > 0; total_q == 0 is a no-op. */
+size_t bitlinear_attn_fwd_workspace_bytes(int64_t batch, int64_t total_q, int64_t total_k,
+                                          int64_t hq, int64_t hkv, int64_t d);
+int bitlinear_attn_fwd(const uint16_t *Q, const uint16_t *K, const uint16_t *V, int64_t q_stride,
+                       int64_t k_stride, int64_t v_stride, const int32_t *cu_q,
+                       const int32_t *cu_k, int64_t batch, int64_t total_q, int64_t total_k,
+                       int64_t hq, int64_t hkv, int64_t d, float scale, uint16_t *O, float *lse,
+                       void *ws, size_t ws_bytes, void *stream);
+
+/* Its backward, from the forward's inputs, O and lse:
+ *   delta = rowsum(dO O), dP = dO V^T, dS = P (dP - delta),
+ *   dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO
+ * dK and dV are sums over the query heads of a group.  P, dS and (from
+ * binary32) dO are rounded to bf16 for the products, all sums are binary32,
+ * and the order of every sum is fixed: reruns give the same bits.
+ *   dO   device [total_q][hq*d], bf16 or binary32 (do_type; binary32 is
+ *        what bitlinear_bwd of the o BitLinear writes).
+ *   dQ   device bf16 [total_q][hq*d]; dK, dV  device bf16 [total_k][hkv*d];
+ *        all three written, for the rows of sequences only.
+ *   ws   bitlinear_attn_bwd_workspace_bytes() bytes, 256-byte aligned,
+ *        clobbered. */
+size_t bitlinear_attn_bwd_workspace_bytes(int64_t batch, int64_t total_q, int64_t total_k,
+                                          int64_t hq, int64_t hkv, int64_t d);
+int bitlinear_attn_bwd(const uint16_t *Q, const uint16_t *K, const uint16_t *V, int64_t q_stride,
+                       int64_t k_stride, int64_t v_stride, const uint16_t *O, const float *lse,
+                       const void *dO, int do_type, const int32_t *cu_q, const int32_t *cu_k,
+                       int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv,
+                       int64_t d, float scale, uint16_t *dQ, uint16_t *dK, uint16_t *dV, void *ws,
+                       size_t ws_bytes, void *stream);
+
+/* Attention of each sequence's newest tokens over its cache: one token
+ * (decoding), or a tree of `draft` drafted tokens, whose K and V rows are in
+ * the cache already (bitlinear_qk_rope puts them there).  The cache is pages
+ * of `page` rows; row p of sequence b is row pages[b][p / page] * page +
+ * p % page of K and V.  Of its lens[b] rows the last `draft` are the drafted
+ * tokens'; token i sees every row before those, and drafted token j if bit j
+ * of tree[b][i] is set (tree NULL: j <= i).
+ *   Q        device bf16 [batch * draft] rows of hq*d, q_stride apart.
+ *   K, V     device bf16 [cache_rows][hkv*d] (the pages, one after another;
+ *            rows behind the last whole page are not used).
+ *   pages    device int32 [batch][max_pages]; a page outside the cache holds
+ *            no rows: its positions are seen by no token.  Only the entries
+ *            that lens needs are read.
+ *   lens     device int32 [batch], cut off at [0, max_pages * page].  A
+ *            sequence of 0 rows gives zeros.  With fewer rows than `draft`
+ *            the rows present are those of the last drafted tokens.
+ *   tree     device uint64 [batch][draft] or NULL.
+ *   O        device bf16 [batch * draft][hq*d], written.
+ *   ws       bitlinear_attn_cache_workspace_bytes() bytes, 256-byte
+ *            aligned, clobbered; calls that overlap on it race.
+ * Formulas and roundings as for bitlinear_attn_fwd.  Lengths, pages and tree
+ * are read by the kernels: a captured graph may be replayed with others.
+ * page a multiple of 16, draft 1..64, batch 1..65535, max_pages * page and
+ * cache_rows below 2^31, and batch * ceil(max_pages * page / 32) * hkv *
+ * ceil(draft * (hq/hkv) / 32) below 2^31. */
+size_t bitlinear_attn_cache_workspace_bytes(int64_t batch, int64_t draft, int64_t hq, int64_t hkv,
+                                            int64_t d);
+int bitlinear_attn_cache(const uint16_t *Q, int64_t q_stride, const uint16_t *K,
+                         const uint16_t *V, int64_t cache_rows, const int32_t *pages,
+                         int64_t max_pages, int64_t page, const int32_t *lens,
+                         const uint64_t *tree, int64_t batch, int64_t draft, int64_t hq,
+                         int64_t hkv, int64_t d, float scale, uint16_t *O, void *ws,
+                         size_t ws_bytes, void *stream);
+
 /* Static text for a status code. */
 const char *bitlinear_status_string(int status);
 

@@ -31,6 +31,7 @@ class BitLinearError(RuntimeError):
 
 _lib = None
 _i64, _int, _sz, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+_f32, _f64 = ctypes.c_float, ctypes.c_double
 
 _SIGS = {
     "bitlinear_packed_bytes": (_sz, [_i64, _i64, _int, _int]),
@@ -70,6 +71,20 @@ _SIGS = {
     "bitlinear_latent_update": (_int, [_vp, _vp, _i64, ctypes.c_float, _vp, _vp]),
     "bitlinear_relu2_gate": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
     "bitlinear_relu2_gate_bwd": (_int, [_vp, _vp, _vp, _i64, _vp, _vp, _vp]),
+    "bitlinear_rope_table": (_int, [_i64, _i64, _f64, _vp, _vp]),
+    "bitlinear_qk_rope": (_int, [_vp, _vp, _vp, _int] + [_i64] * 7 + [_vp, _vp, _f32, _vp, _i64, _vp, _vp, _i64,
+                                                                      _vp, _vp, _vp, _vp]),
+    "bitlinear_qk_rope_bwd_workspace_bytes": (_sz, [_i64]),
+    "bitlinear_qk_rope_bwd": (_int, [_vp, _vp, _int] + [_i64] * 6 + [_vp, _vp, _f32, _vp, _i64] + [_vp] * 8 +
+                              [_sz, _vp]),
+    "bitlinear_attn_fwd_workspace_bytes": (_sz, [_i64] * 6),
+    "bitlinear_attn_fwd": (_int, [_vp] * 3 + [_i64] * 3 + [_vp] * 2 + [_i64] * 6 + [_f32] + [_vp] * 3 + [_sz, _vp]),
+    "bitlinear_attn_bwd_workspace_bytes": (_sz, [_i64] * 6),
+    "bitlinear_attn_bwd": (_int, [_vp] * 3 + [_i64] * 3 + [_vp] * 3 + [_int] + [_vp] * 2 + [_i64] * 6 + [_f32] +
+                           [_vp] * 4 + [_sz, _vp]),
+    "bitlinear_attn_cache_workspace_bytes": (_sz, [_i64] * 5),
+    "bitlinear_attn_cache": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _vp, _vp] + [_i64] * 5 + [_f32, _vp, _vp,
+                                                                                                   _sz, _vp]),
     "bitlinear_status_string": (ctypes.c_char_p, [_int]),
     "bitlinear_last_error": (ctypes.c_char_p, []),
 }
@@ -507,3 +522,177 @@ def bitlinear_quant_group(plan, n, m, gamma_over, stream=None):
     st = lib().bitlinear_quant_group(_ptr(plan, (torch.uint8,), None, "plan"), n, m, gamma_over,
                                      _stream(stream))
     _check(st, "bitlinear_quant_group")
+
+
+BL_TYPE_F32, BL_TYPE_BF16 = 0, 1
+
+
+def _rows(t, dtypes, width, name, rows=None):
+    """(pointer, row stride in elements, rows) of rows of `width` elements:
+    [rows, width] or [rows, heads, d], each row contiguous, the rows any
+    distance apart; or a contiguous tensor of any shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    n = t.numel() // width if width > 0 else 0
+    if n * width != t.numel() or (rows is not None and n != rows):
+        raise ValueError(f"{name} has {t.numel()} elements, expected {'rows' if rows is None else rows} x {width}")
+    if t.is_contiguous() or n == 0:
+        return t.data_ptr(), width, n
+    if t.dim() not in (2, 3) or t.shape[0] != n or t.stride(-1) != 1 or (t.dim() == 3 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must have contiguous rows of {width} elements")
+    return t.data_ptr(), t.stride(0) if n > 1 else width, n
+
+
+def _on_current_device(*tensors):
+    d = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != d:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{d}")
+
+
+def _ws(ws, ws_bytes):
+    p = _ptr(ws, (torch.uint8,), None, "ws", optional=True)
+    return p, (ws.numel() if ws is not None else 0) if ws_bytes is None else int(ws_bytes)
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _type_of(name, *tensors):
+    """BL_TYPE_* of tensors that share one of the two input types."""
+    kinds = {t.dtype for t in tensors if t is not None}
+    if len(kinds) != 1 or not kinds <= set(_FLOATS):
+        raise TypeError(f"{name} must all be float32 or all bfloat16 tensors")
+    return BL_TYPE_F32 if torch.float32 in kinds else BL_TYPE_BF16
+
+
+def bitlinear_rope_table(max_pos, d, base, table, stream=None):
+    """Fill table (float32, max_pos * d/2 * 2) with cos and sin of p * base^(-2i/d)."""
+    _on_current_device(table)
+    st = lib().bitlinear_rope_table(int(max_pos), int(d), float(base),
+                                    _ptr(table, (torch.float32,), max_pos * d, "table"), _stream(stream))
+    _check(st, "bitlinear_rope_table")
+
+
+def bitlinear_qk_rope(Q, K, V, tokens, hq, hkv, d, q_weight, k_weight, eps, table, pos, Qr, Kr, Vr, slots=None,
+                      stream=None):
+    """Head norms (with weights) and rotation of Q and K, V copied: bfloat16
+    Qr, Kr, Vr.  Q, K, V: float32 or bfloat16 rows, any row stride; max_pos and
+    kv_rows are taken from the sizes of table and Kr."""
+    _on_current_device(Q, K, V, q_weight, k_weight, table, pos, Qr, Kr, Vr, slots)
+    x_type = _type_of("Q, K and V", Q, K, V)
+    q, qs, _ = _rows(Q, _FLOATS, hq * d, "Q", tokens)
+    k, ks, _ = _rows(K, _FLOATS, hkv * d, "K", tokens)
+    v, vs, _ = _rows(V, _FLOATS, hkv * d, "V", tokens) if V is not None else (None, 0, 0)
+    if Kr is None or Kr.numel() % (hkv * d):
+        raise ValueError(f"Kr must hold rows of {hkv * d} elements")
+    if table.numel() % d:
+        raise ValueError(f"table must hold rows of {d} elements")
+    kv_rows = Kr.numel() // (hkv * d)
+    st = lib().bitlinear_qk_rope(
+        q, k, v, x_type, qs, ks, vs, tokens, hq, hkv, d,
+        _ptr(q_weight, (torch.float32,), d, "q_weight", optional=True),
+        _ptr(k_weight, (torch.float32,), d, "k_weight", optional=True), eps,
+        _ptr(table, (torch.float32,), None, "table"), table.numel() // d, _ptr(pos, (torch.int32,), tokens, "pos"),
+        _ptr(slots, (torch.int64,), tokens, "slots", optional=True), kv_rows,
+        _ptr(Qr, _BF16, tokens * hq * d, "Qr"), _ptr(Kr, _BF16, None, "Kr"),
+        _ptr(Vr, _BF16, kv_rows * hkv * d, "Vr", optional=V is None), _stream(stream))
+    _check(st, "bitlinear_qk_rope")
+
+
+def bitlinear_qk_rope_bwd_workspace_bytes(d):
+    return int(lib().bitlinear_qk_rope_bwd_workspace_bytes(int(d)))
+
+
+def bitlinear_qk_rope_bwd(Q, K, tokens, hq, hkv, d, q_weight, k_weight, eps, table, pos, dQr, dKr, dQ, dK,
+                          dq_weight=None, dk_weight=None, ws=None, ws_bytes=None, stream=None):
+    """Backward of bitlinear_qk_rope for Q and K (which may be None without
+    weights): bfloat16 dQ, dK and, with weights, float32 dq_weight, dk_weight."""
+    _on_current_device(Q, K, q_weight, k_weight, table, pos, dQr, dKr, dQ, dK, dq_weight, dk_weight, ws)
+    x_type, q, qs, k, ks = BL_TYPE_F32, None, 0, None, 0
+    if q_weight is not None:
+        x_type = _type_of("Q and K", Q, K)
+        q, qs, _ = _rows(Q, _FLOATS, hq * d, "Q", tokens)
+        k, ks, _ = _rows(K, _FLOATS, hkv * d, "K", tokens)
+    if table.numel() % d:
+        raise ValueError(f"table must hold rows of {d} elements")
+    w, wn = _ws(ws, ws_bytes)
+    f32 = (torch.float32,)
+    st = lib().bitlinear_qk_rope_bwd(
+        q, k, x_type, qs, ks, tokens, hq, hkv, d, _ptr(q_weight, f32, d, "q_weight", optional=True),
+        _ptr(k_weight, f32, d, "k_weight", optional=True), eps, _ptr(table, f32, None, "table"), table.numel() // d,
+        _ptr(pos, (torch.int32,), tokens, "pos"), _ptr(dQr, _BF16, tokens * hq * d, "dQr"),
+        _ptr(dKr, _BF16, tokens * hkv * d, "dKr"), _ptr(dQ, _BF16, tokens * hq * d, "dQ"),
+        _ptr(dK, _BF16, tokens * hkv * d, "dK"), _ptr(dq_weight, f32, d, "dq_weight", optional=True),
+        _ptr(dk_weight, f32, d, "dk_weight", optional=True), w, wn, _stream(stream))
+    _check(st, "bitlinear_qk_rope_bwd")
+
+
+def bitlinear_attn_fwd_workspace_bytes(batch, total_q, total_k, hq, hkv, d):
+    return int(lib().bitlinear_attn_fwd_workspace_bytes(batch, total_q, total_k, hq, hkv, d))
+
+
+def bitlinear_attn_fwd(Q, K, V, cu_q, cu_k, batch, hq, hkv, d, scale, O, lse=None, ws=None, ws_bytes=None,
+                       stream=None):
+    """Causal attention over packed sequences: bfloat16 O, float32 lse
+    [hq, total_q].  Q, K, V: bfloat16 rows, any row stride."""
+    _on_current_device(Q, K, V, cu_q, cu_k, O, lse, ws)
+    q, qs, tq = _rows(Q, _BF16, hq * d, "Q")
+    k, ks, tk = _rows(K, _BF16, hkv * d, "K")
+    v, vs, _ = _rows(V, _BF16, hkv * d, "V", tk)
+    w, wn = _ws(ws, ws_bytes)
+    st = lib().bitlinear_attn_fwd(
+        q, k, v, qs, ks, vs, _ptr(cu_q, (torch.int32,), batch + 1, "cu_q"), _ptr(cu_k, (torch.int32,), batch + 1, "cu_k"),
+        batch, tq, tk, hq, hkv, d, scale, _ptr(O, _BF16, tq * hq * d, "O"),
+        _ptr(lse, (torch.float32,), hq * tq, "lse", optional=True), w, wn, _stream(stream))
+    _check(st, "bitlinear_attn_fwd")
+
+
+def bitlinear_attn_bwd_workspace_bytes(batch, total_q, total_k, hq, hkv, d):
+    return int(lib().bitlinear_attn_bwd_workspace_bytes(batch, total_q, total_k, hq, hkv, d))
+
+
+def bitlinear_attn_bwd(Q, K, V, O, lse, dO, cu_q, cu_k, batch, hq, hkv, d, scale, dQ, dK, dV, ws=None, ws_bytes=None,
+                       stream=None):
+    """Backward of bitlinear_attn_fwd: bfloat16 dQ, dK, dV.  dO: contiguous
+    bfloat16 or float32."""
+    _on_current_device(Q, K, V, O, lse, dO, cu_q, cu_k, dQ, dK, dV, ws)
+    q, qs, tq = _rows(Q, _BF16, hq * d, "Q")
+    k, ks, tk = _rows(K, _BF16, hkv * d, "K")
+    v, vs, _ = _rows(V, _BF16, hkv * d, "V", tk)
+    w, wn = _ws(ws, ws_bytes)
+    st = lib().bitlinear_attn_bwd(
+        q, k, v, qs, ks, vs, _ptr(O, _BF16, tq * hq * d, "O"), _ptr(lse, (torch.float32,), hq * tq, "lse"),
+        _ptr(dO, _FLOATS, tq * hq * d, "dO"), _type_of("dO", dO), _ptr(cu_q, (torch.int32,), batch + 1, "cu_q"),
+        _ptr(cu_k, (torch.int32,), batch + 1, "cu_k"), batch, tq, tk, hq, hkv, d, scale,
+        _ptr(dQ, _BF16, tq * hq * d, "dQ"), _ptr(dK, _BF16, tk * hkv * d, "dK"), _ptr(dV, _BF16, tk * hkv * d, "dV"),
+        w, wn, _stream(stream))
+    _check(st, "bitlinear_attn_bwd")
+
+
+def bitlinear_attn_cache_workspace_bytes(batch, draft, hq, hkv, d):
+    return int(lib().bitlinear_attn_cache_workspace_bytes(batch, draft, hq, hkv, d))
+
+
+def bitlinear_attn_cache(Q, K, V, pages, page, lens, tree, batch, draft, hq, hkv, d, scale, O, ws=None, ws_bytes=None,
+                         stream=None):
+    """Attention of batch * draft new tokens over a paged cache: bfloat16 O.
+    pages: int32 [batch, max_pages]; tree: int64 or uint64 [batch, draft] bit
+    sets, or None (each drafted token sees those before it)."""
+    _on_current_device(Q, K, V, pages, lens, tree, O, ws)
+    q, qs, _ = _rows(Q, _BF16, hq * d, "Q", batch * draft)
+    if K.numel() % (hkv * d):
+        raise ValueError(f"K must hold rows of {hkv * d} elements")
+    if pages.numel() % max(batch, 1):
+        raise ValueError("pages must hold one row per sequence")
+    w, wn = _ws(ws, ws_bytes)
+    st = lib().bitlinear_attn_cache(
+        q, qs, _ptr(K, _BF16, None, "K"), _ptr(V, _BF16, K.numel(), "V"), K.numel() // (hkv * d),
+        _ptr(pages, (torch.int32,), None, "pages"), pages.numel() // max(batch, 1), page,
+        _ptr(lens, (torch.int32,), batch, "lens"), _ptr(tree, (torch.int64, torch.uint64), batch * draft, "tree", optional=True),
+        batch, draft, hq, hkv, d, scale, _ptr(O, _BF16, batch * draft * hq * d, "O"), w, wn, _stream(stream))
+    _check(st, "bitlinear_attn_cache")

@@ -1057,6 +1057,271 @@ int bitlinear_bwd(const uint16_t* dY, const int8_t* xq, const float* x_scale, co
   return hip_status(e, "backward launch");
 }
 
+// ------------------------------------------------ head norms and rotation
+namespace {
+int check_heads(int64_t hq, int64_t hkv, int64_t d) {
+  if (d != 64 && d != 128) return fail(BL_ESHAPE, "head size must be 64 or 128 (got %lld)", (long long)d);
+  if (hq < 1 || hkv < 1 || hq > 4096 || hq % hkv != 0)
+    return fail(BL_ESHAPE, "hq must be a multiple of hkv, both in 1..4096 (got %lld and %lld)", (long long)hq,
+                (long long)hkv);
+  return BL_OK;
+}
+
+// rows `stride` elements apart, each of `row` elements, 16-byte pieces
+int check_stride(int64_t stride, int64_t row, int64_t piece, int64_t limit, const char* name) {
+  if (stride < row || stride >= limit || stride % piece != 0)
+    return fail(BL_ESHAPE, "%s must be a multiple of %lld in [%lld, %lld) (got %lld)", name, (long long)piece,
+                (long long)row, (long long)limit, (long long)stride);
+  return BL_OK;
+}
+
+int check_type(int type, const char* name) {
+  if (type != BL_TYPE_F32 && type != BL_TYPE_BF16)
+    return fail(BL_EINVAL, "%s must be BL_TYPE_F32 or BL_TYPE_BF16 (got %d)", name, type);
+  return BL_OK;
+}
+
+int check_rope(int64_t tokens, const float* qw, const float* kw, float eps, const float* table, int64_t max_pos,
+               const int32_t* pos, int64_t hq, int64_t hkv, int64_t d) {
+  if (tokens < 0 || tokens >= kLimit) return fail(BL_ESHAPE, "tokens must be in [0, 2^31) (got %lld)", (long long)tokens);
+  // wavefronts of the launch: at least 16 head rows each
+  if (tokens * ((hq + 2 * hkv + 15) / 16) >= 4 * (kLimit - 1))
+    return fail(BL_ESHAPE, "too many head rows for one call (%lld tokens)", (long long)tokens);
+  if (max_pos < 1 || max_pos >= kLimit) return fail(BL_ESHAPE, "max_pos must be in [1, 2^31) (got %lld)", (long long)max_pos);
+  if ((qw == nullptr) != (kw == nullptr)) return fail(BL_EINVAL, "q_weight and k_weight: both or neither");
+  if (tokens == 0) return BL_OK;
+  TRY(check_opt_ptr(qw, 16, "q_weight"));
+  TRY(check_opt_ptr(kw, 16, "k_weight"));
+  if (qw && !(eps >= 0.f && eps <= 3.0e38f)) return fail(BL_EINVAL, "eps must be finite and >= 0");
+  TRY(check_ptr(table, 16, "table"));
+  TRY(check_ptr(pos, 4, "pos"));
+  return BL_OK;
+}
+}  // namespace
+
+int bitlinear_rope_table(int64_t max_pos, int64_t d, double base, float* table, void* stream) {
+  TRY(check_heads(1, 1, d));
+  if (max_pos < 1 || max_pos >= kLimit) return fail(BL_ESHAPE, "max_pos must be in [1, 2^31) (got %lld)", (long long)max_pos);
+  if (!(base > 0.0 && base < 1e300)) return fail(BL_EINVAL, "base must be finite and > 0");
+  TRY(check_ptr(table, 16, "table"));
+  return hip_status(bl::launch_rope_table(table, max_pos, d, base, reinterpret_cast<hipStream_t>(stream)),
+                    "rotation table launch");
+}
+
+int bitlinear_qk_rope(const void* Q, const void* K, const void* V, int x_type, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, int64_t tokens, int64_t hq, int64_t hkv, int64_t d, const float* q_weight,
+                      const float* k_weight, float eps, const float* table, int64_t max_pos, const int32_t* pos,
+                      const int64_t* slots, int64_t kv_rows, uint16_t* Qr, uint16_t* Kr, uint16_t* Vr,
+                      void* stream) {
+  TRY(check_heads(hq, hkv, d));
+  TRY(check_type(x_type, "x_type"));
+  TRY(check_rope(tokens, q_weight, k_weight, eps, table, max_pos, pos, hq, hkv, d));
+  if ((V == nullptr) != (Vr == nullptr) && tokens > 0) return fail(BL_EINVAL, "V and Vr: both or neither");
+  if (kv_rows < 0 || kv_rows >= kLimit || (!slots && kv_rows < tokens))
+    return fail(BL_ESHAPE, "kv_rows must be below 2^31 and, without slots, at least tokens (got %lld)",
+                (long long)kv_rows);
+  if (tokens == 0) return ok();
+  const int64_t piece = x_type == BL_TYPE_F32 ? 4 : 8;
+  TRY(check_stride(q_stride, hq * d, piece, kLimit, "q_stride"));
+  TRY(check_stride(k_stride, hkv * d, piece, kLimit, "k_stride"));
+  if (V) TRY(check_stride(v_stride, hkv * d, piece, kLimit, "v_stride"));
+  TRY(check_ptr(Q, 16, "Q"));
+  TRY(check_ptr(K, 16, "K"));
+  TRY(check_opt_ptr(V, 16, "V"));
+  TRY(check_opt_ptr(slots, 8, "slots"));
+  TRY(check_ptr(Qr, 16, "Qr"));
+  TRY(check_ptr(Kr, 16, "Kr"));
+  TRY(check_opt_ptr(Vr, 16, "Vr"));
+  const bl::RopeArgs a{Q, K, V, q_stride, k_stride, v_stride, tokens, (int)hq, (int)hkv, q_weight, k_weight, eps,
+                       table, max_pos, pos, slots, kv_rows, Qr, Kr, Vr};
+  return hip_status(bl::launch_qk_rope(a, d, x_type == BL_TYPE_F32, reinterpret_cast<hipStream_t>(stream)),
+                    "rotation launch");
+}
+
+size_t bitlinear_qk_rope_bwd_workspace_bytes(int64_t d) {
+  return d == 64 || d == 128 ? bl::rope_bwd_ws_bytes(d) : 0;
+}
+
+int bitlinear_qk_rope_bwd(const void* Q, const void* K, int x_type, int64_t q_stride, int64_t k_stride,
+                          int64_t tokens, int64_t hq, int64_t hkv, int64_t d, const float* q_weight,
+                          const float* k_weight, float eps, const float* table, int64_t max_pos, const int32_t* pos,
+                          const uint16_t* dQr, const uint16_t* dKr, uint16_t* dQ, uint16_t* dK, float* dq_weight,
+                          float* dk_weight, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_heads(hq, hkv, d));
+  const bool norms = q_weight != nullptr;
+  if (norms) TRY(check_type(x_type, "x_type"));
+  TRY(check_rope(tokens, q_weight, k_weight, eps, table, max_pos, pos, hq, hkv, d));
+  if (norms) {
+    TRY(check_ptr(dq_weight, 4, "dq_weight"));
+    TRY(check_ptr(dk_weight, 4, "dk_weight"));
+    const size_t need = bl::rope_bwd_ws_bytes(d);
+    if (!ws || ws_bytes < need)
+      return fail(BL_EWORKSPACE, "rotation backward workspace needs %zu bytes (got %zu)", need,
+                  ws ? ws_bytes : (size_t)0);
+    TRY(check_ptr(ws, 16, "ws"));
+  }
+  if (tokens == 0 && !norms) return ok();
+  if (tokens > 0) {
+    if (norms) {
+      const int64_t piece = x_type == BL_TYPE_F32 ? 4 : 8;
+      TRY(check_stride(q_stride, hq * d, piece, kLimit, "q_stride"));
+      TRY(check_stride(k_stride, hkv * d, piece, kLimit, "k_stride"));
+      TRY(check_ptr(Q, 16, "Q"));
+      TRY(check_ptr(K, 16, "K"));
+    }
+    TRY(check_ptr(dQr, 16, "dQr"));
+    TRY(check_ptr(dKr, 16, "dKr"));
+    TRY(check_ptr(dQ, 16, "dQ"));
+    TRY(check_ptr(dK, 16, "dK"));
+  }
+  const bl::RopeBwdArgs a{Q, K, q_stride, k_stride, tokens, (int)hq, (int)hkv, q_weight, k_weight, eps, table,
+                          max_pos, pos, dQr, dKr, dQ, dK, dq_weight, dk_weight, static_cast<float*>(ws)};
+  return hip_status(bl::launch_qk_rope_bwd(a, d, x_type == BL_TYPE_F32, reinterpret_cast<hipStream_t>(stream)),
+                    "rotation backward launch");
+}
+
+// -------------------------------------------------------------- attention
+namespace {
+constexpr int64_t kStrideLimit = (int64_t)1 << 22;  // a 64-row tile's offsets stay below 2^31 bytes
+
+int check_attn(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d, float scale) {
+  TRY(check_heads(hq, hkv, d));
+  if (batch < 1 || batch > 65535) return fail(BL_ESHAPE, "batch must be in 1..65535 (got %lld)", (long long)batch);
+  if (total_q < 0 || total_k < 0 || total_q >= kLimit || total_k >= kLimit)
+    return fail(BL_ESHAPE, "total_q and total_k must be in [0, 2^31)");
+  // workgroups of a launch (tiles of at least 32 rows, and 16 bytes a thread)
+  if ((total_q / 32 + batch + 8) * hq >= kLimit || total_k / 32 * hkv >= kLimit ||
+      total_q * hq * (d / 8) / 256 >= kLimit - 1)
+    return fail(BL_ESHAPE, "too many rows for one call");
+  if (!(scale > 0.f && scale <= 3.0e38f)) return fail(BL_EINVAL, "scale must be finite and > 0");
+  return BL_OK;
+}
+
+int check_attn_inputs(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, int64_t total_q, int64_t total_k,
+                      int64_t hq, int64_t hkv, int64_t d) {
+  TRY(check_ptr(cu_q, 4, "cu_q"));
+  TRY(check_ptr(cu_k, 4, "cu_k"));
+  TRY(check_stride(q_stride, hq * d, 8, kStrideLimit, "q_stride"));
+  TRY(check_stride(k_stride, hkv * d, 8, kStrideLimit, "k_stride"));
+  TRY(check_stride(v_stride, hkv * d, 8, kStrideLimit, "v_stride"));
+  if (total_q > 0) TRY(check_ptr(Q, 16, "Q"));
+  if (total_k > 0) {
+    TRY(check_ptr(K, 16, "K"));
+    TRY(check_ptr(V, 16, "V"));
+  }
+  return BL_OK;
+}
+
+int check_ws(void* ws, size_t ws_bytes, size_t need) {
+  if (need == 0) return BL_OK;
+  if (!ws || ws_bytes < need)
+    return fail(BL_EWORKSPACE, "attention workspace needs %zu bytes (got %zu)", need, ws ? ws_bytes : (size_t)0);
+  return check_ptr(ws, 256, "ws");
+}
+}  // namespace
+
+size_t bitlinear_attn_fwd_workspace_bytes(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv,
+                                          int64_t d) {
+  if (check_attn(batch, total_q, total_k, hq, hkv, d, 1.f) != BL_OK) return 0;
+  return bl::attn_fwd_ws_bytes(batch, total_q, total_k, hq, hkv, d);
+}
+
+int bitlinear_attn_fwd(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int64_t q_stride, int64_t k_stride,
+                       int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, int64_t batch, int64_t total_q,
+                       int64_t total_k, int64_t hq, int64_t hkv, int64_t d, float scale, uint16_t* O, float* lse,
+                       void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_attn(batch, total_q, total_k, hq, hkv, d, scale));
+  if (total_q == 0) return ok();
+  TRY(check_attn_inputs(Q, K, V, q_stride, k_stride, v_stride, cu_q, cu_k, total_q, total_k, hq, hkv, d));
+  TRY(check_ptr(O, 16, "O"));
+  TRY(check_opt_ptr(lse, 4, "lse"));
+  TRY(check_ws(ws, ws_bytes, bl::attn_fwd_ws_bytes(batch, total_q, total_k, hq, hkv, d)));
+  const bl::AttnArgs a{Q, K, V, q_stride, k_stride, v_stride, cu_q, cu_k, (int)batch, (int)hq, (int)hkv,
+                       total_q, total_k, scale, O, lse};
+  return hip_status(bl::launch_attn_fwd(a, d, ws, reinterpret_cast<hipStream_t>(stream)), "attention launch");
+}
+
+size_t bitlinear_attn_bwd_workspace_bytes(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv,
+                                          int64_t d) {
+  if (check_attn(batch, total_q, total_k, hq, hkv, d, 1.f) != BL_OK) return 0;
+  return bl::attn_bwd_ws_bytes(batch, total_q, total_k, hq, hkv, d);
+}
+
+int bitlinear_attn_bwd(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int64_t q_stride, int64_t k_stride,
+                       int64_t v_stride, const uint16_t* O, const float* lse, const void* dO, int do_type,
+                       const int32_t* cu_q, const int32_t* cu_k, int64_t batch, int64_t total_q, int64_t total_k,
+                       int64_t hq, int64_t hkv, int64_t d, float scale, uint16_t* dQ, uint16_t* dK, uint16_t* dV,
+                       void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_attn(batch, total_q, total_k, hq, hkv, d, scale));
+  TRY(check_type(do_type, "do_type"));
+  if (total_q == 0 && total_k == 0) return ok();
+  TRY(check_attn_inputs(Q, K, V, q_stride, k_stride, v_stride, cu_q, cu_k, total_q, total_k, hq, hkv, d));
+  if (total_q > 0) {
+    TRY(check_ptr(O, 16, "O"));
+    TRY(check_ptr(lse, 4, "lse"));
+    TRY(check_ptr(dO, 16, "dO"));
+    TRY(check_ptr(dQ, 16, "dQ"));
+  }
+  if (total_k > 0) {
+    TRY(check_ptr(dK, 16, "dK"));
+    TRY(check_ptr(dV, 16, "dV"));
+  }
+  TRY(check_ws(ws, ws_bytes, bl::attn_bwd_ws_bytes(batch, total_q, total_k, hq, hkv, d)));
+  const bl::AttnBwdArgs a{Q, K, V, q_stride, k_stride, v_stride, cu_q, cu_k, (int)batch, (int)hq, (int)hkv,
+                          total_q, total_k, scale, O, lse, dO, do_type == BL_TYPE_F32, dQ, dK, dV, ws};
+  return hip_status(bl::launch_attn_bwd(a, d, reinterpret_cast<hipStream_t>(stream)), "attention backward launch");
+}
+
+namespace {
+int check_cache(int64_t batch, int64_t draft, int64_t hq, int64_t hkv, int64_t d) {
+  TRY(check_heads(hq, hkv, d));
+  if (batch < 1 || batch > 65535) return fail(BL_ESHAPE, "batch must be in 1..65535 (got %lld)", (long long)batch);
+  if (draft < 1 || draft > 64) return fail(BL_ESHAPE, "draft must be in 1..64 (got %lld)", (long long)draft);
+  if (batch * draft * hq >= kLimit) return fail(BL_ESHAPE, "batch*draft*hq must stay below 2^31");
+  return BL_OK;
+}
+}  // namespace
+
+size_t bitlinear_attn_cache_workspace_bytes(int64_t batch, int64_t draft, int64_t hq, int64_t hkv, int64_t d) {
+  if (check_cache(batch, draft, hq, hkv, d) != BL_OK) return 0;
+  return bl::attn_cache_ws_bytes(batch, draft, hq, hkv, d);
+}
+
+int bitlinear_attn_cache(const uint16_t* Q, int64_t q_stride, const uint16_t* K, const uint16_t* V,
+                         int64_t cache_rows, const int32_t* pages, int64_t max_pages, int64_t page,
+                         const int32_t* lens, const uint64_t* tree, int64_t batch, int64_t draft, int64_t hq,
+                         int64_t hkv, int64_t d, float scale, uint16_t* O, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_cache(batch, draft, hq, hkv, d));
+  if (page < 16 || page % 16 != 0 || page >= kLimit)
+    return fail(BL_ESHAPE, "page must be a positive multiple of 16 (got %lld)", (long long)page);
+  if (max_pages < 1 || max_pages >= kLimit || max_pages * page >= kLimit)
+    return fail(BL_ESHAPE, "max_pages must be >= 1 and max_pages*page below 2^31 (got %lld)", (long long)max_pages);
+  if (cache_rows < 0 || cache_rows >= kLimit)
+    return fail(BL_ESHAPE, "cache_rows must be in [0, 2^31) (got %lld)", (long long)cache_rows);
+  {  // tiles of the whole call are counted in 32 bits
+    const int64_t tiles = batch * ((max_pages * page + 31) / 32), units = hkv * ((draft * (hq / hkv) + 31) / 32);
+    if (tiles >= kLimit || tiles * units >= kLimit)
+      return fail(BL_ESHAPE, "too many cache tiles for one call (batch %lld, %lld rows each)", (long long)batch,
+                  (long long)(max_pages * page));
+  }
+  if (!(scale > 0.f && scale <= 3.0e38f)) return fail(BL_EINVAL, "scale must be finite and > 0");
+  TRY(check_stride(q_stride, hq * d, 8, kLimit, "q_stride"));
+  TRY(check_ptr(Q, 16, "Q"));
+  if (cache_rows >= page) {
+    TRY(check_ptr(K, 16, "K"));
+    TRY(check_ptr(V, 16, "V"));
+  }
+  TRY(check_ptr(pages, 4, "pages"));
+  TRY(check_ptr(lens, 4, "lens"));
+  TRY(check_opt_ptr(tree, 8, "tree"));
+  TRY(check_ptr(O, 16, "O"));
+  TRY(check_ws(ws, ws_bytes, bl::attn_cache_ws_bytes(batch, draft, hq, hkv, d)));
+  const bl::AttnCacheArgs a{Q, q_stride, K, V, cache_rows / page, pages, max_pages, page, lens, tree,
+                            (int)batch, (int)draft, (int)hq, (int)hkv, scale, O, ws};
+  return hip_status(bl::launch_attn_cache(a, d, reinterpret_cast<hipStream_t>(stream)), "cache attention launch");
+}
+
 const char* bitlinear_status_string(int status) {
   switch (status) {
     case BL_OK: return "ok";

@@ -1,0 +1,254 @@
+// attn.h -- device pieces the attention kernels share: matrix operands of
+// the 32 x 32 x 16 bf16 instruction, LDS tiles filled by DMA, and the order
+// of the work items.
+#pragma once
+
+#include "common.h"
+
+namespace bl {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) void lds_void;
+
+// v_mfma_f32_32x32x16_bf16: lane l holds A[l%32][8(l/32) .. +7] and
+// B[8(l/32) .. +7][l%32]; register i of its result is element
+// [8(i/4) + 4(l/32) + i%4][l%32].
+//
+// All three kernels keep the softmax's row along the lanes: with S^T = K Q^T
+// a lane holds one query's scores (column l%32) and after exp two
+// consecutive groups of four registers are, as they stand, the B operand of
+// the product over keys: its slots 0-3 and 4-7 are then keys 4(l/32) + 0..3
+// and 8 + 4(l/32) + 0..3 of 16, and A is read from LDS in the same order.
+// The probabilities never leave the registers.
+__device__ __forceinline__ v16f mfma32(v8bf a, v8bf b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+// transposing LDS read: of each 16 lanes, lanes 4j..4j+3 address 8 bytes
+// each of row j (16 elements); lane i receives element i of rows 0..3
+__device__ __forceinline__ v4s lds_read_tr(const lds_char* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p));
+}
+__device__ __forceinline__ v8bf lds_read8(const lds_char* p) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) v8bf*>(p);
+}
+__device__ __forceinline__ v8bf join(v4s a, v4s b) {
+  return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+__device__ __forceinline__ uint32_t pk_bf16(float a, float b) {  // nearest, ties to even
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2bf));
+}
+// registers 8s .. 8s+7 of a result as the B operand described above
+__device__ __forceinline__ v8bf operand_of(const v16f& x, int s) {
+  return __builtin_bit_cast(v8bf, u32x4{pk_bf16(x[8 * s], x[8 * s + 1]), pk_bf16(x[8 * s + 2], x[8 * s + 3]),
+                                        pk_bf16(x[8 * s + 4], x[8 * s + 5]), pk_bf16(x[8 * s + 6], x[8 * s + 7])});
+}
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }
+// the other half wavefront's value of the same column, combined with `f`
+template <class F>
+__device__ __forceinline__ float half_join(float v, F f) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+// exchanges a's upper with b's lower half wavefront
+__device__ __forceinline__ void half_swap(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ void lds_load16(__amdgpu_buffer_rsrc_t r, lds_char* dst, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, off, 0, 0, 0);
+}
+__device__ __forceinline__ void lds_load4(__amdgpu_buffer_rsrc_t r, lds_char* dst, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 4, off, 0, 0, 0);
+}
+// wait until at most N of this wavefront's memory operations (LDS DMA
+// included) are in flight, and until its LDS reads have returned
+template <int N>
+__device__ __forceinline__ void wait_dma() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
+}
+// workgroup barrier that leaves LDS DMA in flight (a release would drain it)
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// ---------------------------------------------------------------------
+// A tile of rows of D bf16 in LDS, row after row, the 16-byte pieces of row
+// r permuted: piece c at place c ^ swz(r).  With swz the bit reversal of
+// r % 8, eight consecutive rows' reads of one piece (an A operand by rows)
+// fall into eight different pieces of a 128-byte bank line, and a
+// transposing read's four aligned rows of 64 bytes into both halves of it.
+// ---------------------------------------------------------------------
+__device__ __forceinline__ constexpr int swz(int r) { return ((r & 1) << 2) | (r & 2) | ((r >> 2) & 1); }
+
+template <int D>
+struct Tile {
+  static constexpr int kRowBytes = 2 * D;
+  static constexpr int kPieces = D / 8;            // 16-byte pieces of a row
+  static constexpr int kDmaRows = 64 / kPieces;    // rows of one DMA instruction (4 or 8)
+  static constexpr int kVariants = 8 / kDmaRows;   // row residues mod 8 an instruction can start at
+};
+
+// offset, from the first row of a DMA instruction's rows, that this lane
+// loads; `var`: (first row / kDmaRows) % kVariants
+template <int D>
+__device__ __forceinline__ uint32_t dma_offset(int lane, int var, int64_t stride) {
+  typedef Tile<D> T;
+  const int r = lane / T::kPieces, c = (lane % T::kPieces) ^ swz(r + var * T::kDmaRows);
+  return (uint32_t)(r * (int)stride * 2 + c * 16);
+}
+// address (from the tile's start) of A operand rows 32i + l%32, elements
+// 16s + 8(l/32) .. +7: row_addr + 32i rows, piece_of(s)
+template <int D>
+__device__ __forceinline__ uint32_t a_addr(int lane, int s) {
+  const int r = lane & 31;
+  return (uint32_t)(r * Tile<D>::kRowBytes + (((2 * s + (lane >> 5)) ^ swz(r)) << 4));
+}
+// address of the transposing read that gives lane l column 32t + l%32 of
+// rows 4(l/32) + 0..3 (rows 8 and 16 further on keep the permutation of
+// row r, respectively have that of r + 8: the same, swz looks at r % 8)
+template <int D>
+__device__ __forceinline__ uint32_t tr_addr(int lane, int t) {
+  const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
+  const int c = 4 * t + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  return (uint32_t)(r * Tile<D>::kRowBytes + ((c ^ swz(r)) << 4) + 8 * (lane & 1));
+}
+// A operand [columns 32t..+31][rows r0..r0+15] of a tile, base = tr_addr
+template <int D>
+__device__ __forceinline__ v8bf tr_operand(const lds_char* tile, uint32_t base, int r0) {
+  return join(lds_read_tr(tile + base + r0 * Tile<D>::kRowBytes),
+              lds_read_tr(tile + base + (r0 + 8) * Tile<D>::kRowBytes));
+}
+
+// ---------------------------------------------------------------------
+// Work items are tiles of the sequences, every sequence cut into
+// ceil(len / rows) of them, numbered so that those with the highest level
+// (place in the sequence) come first: under a causal mask the longest work
+// starts first and the short tiles fill up the end.  Every wavefront finds
+// its item by itself: level by bisection over the sequences' tile counts
+// held by the lanes.  Batches beyond kOrdered sequences are walked in order
+// instead (one pass of prefix sums), where a bisection would read the
+// lengths over and over.
+// Lengths come from device memory: rows outside the buffers are cut off
+// here, so wrong offsets cannot lead outside them.
+// ---------------------------------------------------------------------
+constexpr int kOrderedPerLane = 4;
+constexpr int kOrdered = 64 * kOrderedPerLane;
+
+__device__ __forceinline__ int wave_sum_i(int v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+__device__ __forceinline__ int wave_max_i(int v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const int u = __shfl_xor(v, o, 64);
+    v = u > v ? u : v;
+  }
+  return v;
+}
+__device__ __forceinline__ int wave_scan_i(int v, int lane) {  // sum over lanes 0..lane
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o, 64);
+    v += lane >= o ? u : 0;
+  }
+  return v;
+}
+
+// rows [start, start + len) of sequence b
+struct Rows {
+  int start, len;
+};
+__device__ __forceinline__ Rows seq_rows(const int32_t* cu, int b, int64_t total) {
+  int lo = ld_global(cu + b), hi = ld_global(cu + b + 1);
+  lo = lo < 0 ? 0 : lo > total ? (int)total : lo;
+  hi = hi < lo ? lo : hi > total ? (int)total : hi;
+  return Rows{lo, hi - lo};
+}
+
+struct Item {
+  int seq, level;  // seq < 0: none
+};
+__device__ __forceinline__ Item find_item(const int32_t* cu, int batch, int64_t total, int rows, int rank) {
+  const int lane = threadIdx.x & 63;
+  if (batch > kOrdered) {
+    int before = 0;
+    for (int b0 = 0; b0 < batch; b0 += 64) {
+      const int b = b0 + lane;
+      const int n = b < batch ? (seq_rows(cu, b, total).len + rows - 1) / rows : 0;
+      const int incl = before + wave_scan_i(n, lane);
+      const unsigned long long hit = __ballot(incl > rank);
+      if (hit) {
+        const int l = __ffsll(hit) - 1;
+        return Item{b0 + l, rank - (__shfl(incl, l, 64) - __shfl(n, l, 64))};
+      }
+      before = __shfl(incl, 63, 64);
+    }
+    return Item{-1, 0};
+  }
+  int n[kOrderedPerLane], most = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kOrderedPerLane; ++i) {
+    const int b = 64 * i + lane;
+    n[i] = b < batch ? (seq_rows(cu, b, total).len + rows - 1) / rows : 0;
+    most = n[i] > most ? n[i] : most;
+    all += n[i];
+  }
+  if (rank >= wave_sum_i(all)) return Item{-1, 0};
+  // at(L) = items of level L and above; the largest L with at(L) > rank
+  const auto at = [&](int L) {
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kOrderedPerLane; ++i) c += n[i] > L ? n[i] - L : 0;
+    return wave_sum_i(c);
+  };
+  int lo = 0, hi = wave_max_i(most);  // at(lo) > rank >= at(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (at(mid) > rank) lo = mid;
+    else hi = mid;
+  }
+  int skip = rank - at(lo + 1);  // among the sequences with more than lo tiles
+#pragma unroll
+  for (int i = 0; i < kOrderedPerLane; ++i) {
+    const unsigned long long m = __ballot(n[i] > lo);
+    const int c = __popcll(m);
+    if (skip < c) {
+      const bool mine = (m >> lane & 1) && __popcll(m & ((1ull << lane) - 1)) == skip;
+      return Item{64 * i + __ffsll(__ballot(mine)) - 1, lo};
+    }
+    skip -= c;
+  }
+  return Item{-1, 0};
+}
+
+// Workgroup id -> (item rank, head).  Consecutive workgroups go to
+// different XCDs; the heads that share a key/value head take consecutive
+// places on one XCD, so their reads of K and V meet in its L2.
+struct Place {
+  int rank, head;
+};
+__device__ __forceinline__ Place place_of(int id, int hq, int hkv) {
+  const int group = hq / hkv, slot = id >> 3;
+  const int pair = (slot / group) * 8 + (id & 7);
+  return Place{pair / hkv, (pair % hkv) * group + slot % group};
+}
+inline int64_t placed_blocks(int64_t items, int64_t hq, int64_t hkv) {
+  return (items * hkv + 7) / 8 * 8 * (hq / hkv);
+}
+
+}  // namespace bl

@@ -1,0 +1,537 @@
+// attn.hip -- causal attention of packed sequences with grouped heads:
+// forward and backward.
+#include <type_traits>
+
+#include "attn.h"
+#include "launch.h"
+
+namespace bl {
+
+namespace {
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kQRows = 128;  // query rows of a forward / dQ workgroup: 32 per wavefront
+constexpr int kKRows = 64;   // key rows of a tile in LDS
+constexpr int kBRows = 128;  // key rows of a dK / dV workgroup: 32 per wavefront
+constexpr float kInf = __builtin_huge_valf();
+}  // namespace
+
+// One LDS array per stage, the stage a compile-time choice: the compiler
+// then sees that reads of one stage and DMA into the other touch different
+// objects and does not wait for the DMA in flight.
+template <int D>
+struct PairBytes {  // two tiles of 64 rows, then 2 x 64 binary32 row values
+  static constexpr int kTile = kKRows * 2 * D;
+  static constexpr int kAll = 2 * kTile + 512;
+};
+__shared__ __attribute__((aligned(1024))) char g_a128_st0[PairBytes<128>::kAll];
+__shared__ __attribute__((aligned(1024))) char g_a128_st1[PairBytes<128>::kAll];
+__shared__ __attribute__((aligned(1024))) char g_a64_st0[PairBytes<64>::kAll];
+__shared__ __attribute__((aligned(1024))) char g_a64_st1[PairBytes<64>::kAll];
+template <int D, int P>
+__device__ __forceinline__ lds_char* pair_stage() {
+  static_assert(D == 64 || D == 128, "head sizes");
+  if constexpr (D == 128) return (lds_char*)(P == 0 ? g_a128_st0 : g_a128_st1);
+  else return (lds_char*)(P == 0 ? g_a64_st0 : g_a64_st1);
+}
+
+// DMA of 64 rows of two row-major arrays into a stage: wavefront w takes
+// kDma consecutive instructions of each.  Rows past `rows` read zeros (the
+// buffer ends there), so what lies behind a sequence, whatever it holds,
+// never reaches a product.
+template <int D>
+struct PairDma {
+  typedef Tile<D> T;
+  static constexpr int kDma = kKRows / T::kDmaRows / 4;
+  uint32_t off_a[kDma], off_b[kDma];
+  int wave;
+  int64_t stride_a, stride_b;
+  __device__ __forceinline__ PairDma(int lane, int w, int64_t sa, int64_t sb) : wave(w), stride_a(sa), stride_b(sb) {
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) {
+      const int ins = w * kDma + i;
+      off_a[i] = dma_offset<D>(lane, ins % T::kVariants, sa) + (uint32_t)(ins * T::kDmaRows * (int)sa * 2);
+      off_b[i] = dma_offset<D>(lane, ins % T::kVariants, sb) + (uint32_t)(ins * T::kDmaRows * (int)sb * 2);
+    }
+  }
+  // a, b: first row's elements; rows >= 1 of them are the sequence's
+  __device__ __forceinline__ void issue(lds_char* st, const uint16_t* a, const uint16_t* b, int rows) const {
+    const int n = rows < kKRows ? rows : kKRows;
+    const __amdgpu_buffer_rsrc_t ra = rows_rsrc(a, (uint32_t)((n - 1) * (int)stride_a * 2 + 2 * D));
+    const __amdgpu_buffer_rsrc_t rb = rows_rsrc(b, (uint32_t)((n - 1) * (int)stride_b * 2 + 2 * D));
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) lds_load16(ra, st + 1024 * (wave * kDma + i), off_a[i]);
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) lds_load16(rb, st + PairBytes<D>::kTile + 1024 * (wave * kDma + i), off_b[i]);
+  }
+};
+
+// a row's elements as B operands: 16s + 8(l/32) .. +7 for s = 0 .. D/16-1
+template <int D>
+__device__ __forceinline__ void load_row_operand(v8bf* f, const uint16_t* row, int lane, bool in) {
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) {
+    u32x4 v = u32x4{0u, 0u, 0u, 0u};
+    if (in) v = ld_global(reinterpret_cast<const u32x4*>(row + 16 * s + 8 * (lane >> 5)));
+    f[s] = __builtin_bit_cast(v8bf, v);
+  }
+}
+
+// acc^T (column = row of the output, registers = its D elements) times mul,
+// as bf16: after an exchange between the half wavefronts every lane stores
+// 16 bytes of its row at a time
+template <int D>
+__device__ __forceinline__ void store_row(uint16_t* row, const v16f* acc, float mul, int lane, bool in) {
+#pragma unroll
+  for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int e = 8 * u;
+      uint32_t a0 = pk_bf16(acc[t][e] * mul, acc[t][e + 1] * mul);
+      uint32_t a1 = pk_bf16(acc[t][e + 2] * mul, acc[t][e + 3] * mul);
+      uint32_t b0 = pk_bf16(acc[t][e + 4] * mul, acc[t][e + 5] * mul);
+      uint32_t b1 = pk_bf16(acc[t][e + 6] * mul, acc[t][e + 7] * mul);
+      half_swap(a0, b0);
+      half_swap(a1, b1);
+      if (in) st_global(reinterpret_cast<u32x4*>(row + 32 * t + 16 * u + 8 * (lane >> 5)), u32x4{a0, a1, b0, b1});
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void clear(v16f* acc) {
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[t][i] = 0.f;
+}
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// ---------------------------------------------------------------- forward
+// O = softmax(scale Q K^T) V in one pass over the keys: per 64-key tile
+//   S^T = K Q^T,  m' = max(m, max S),  P = 2^((S - m') scale log2 e),
+//   l = l 2^((m - m') ..) + sum P,  O^T = O^T 2^(..) + V^T P^T
+// with m, l, O in binary32; P is rounded to bf16 (half a step, 2^-9
+// relative, averaged over the keys) for the second product, the sum l is of
+// the unrounded P.  m' only moves when a score passes it by 8 in the
+// exponent of 2: P then stays below 2^8 and the 64 accumulators are
+// rescaled a few times per row instead of once per tile.
+template <int D>
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
+  typedef Tile<D> T;
+  constexpr int kTile = PairBytes<D>::kTile;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Place pl = place_of(blockIdx.x, a.hq, a.hkv);
+  const Item it = find_item(a.cu_q, a.batch, a.total_q, kQRows, pl.rank);
+  const int seq = __builtin_amdgcn_readfirstlane(it.seq);
+  if (seq < 0) return;
+  const int head = pl.head, kvh = head / (a.hq / a.hkv);
+  const Rows qr = seq_rows(a.cu_q, seq, a.total_q), kr = seq_rows(a.cu_k, seq, a.total_k);
+  const int q0 = __builtin_amdgcn_readfirstlane(it.level) * kQRows;
+  const int off = kr.len - qr.len;
+  const int w0 = q0 + 32 * wave, r = w0 + (lane & 31);
+  const bool in = r < qr.len;
+  // keys the workgroup's and this wavefront's last rows see
+  const int last = q0 + kQRows < qr.len ? q0 + kQRows : qr.len;
+  const int wlast = w0 + 32 < qr.len ? w0 + 32 : qr.len;
+  const int tiles = (clampi(last + off, 0, kr.len) + kKRows - 1) / kKRows;
+  const int wtiles = w0 < qr.len ? (clampi(wlast + off, 0, kr.len) + kKRows - 1) / kKRows : 0;
+
+  v8bf qf[D / 16];
+  load_row_operand<D>(qf, a.Q + (int64_t)(qr.start + r) * a.q_stride + (int64_t)head * D, lane, in);
+  const PairDma<D> dma(lane, wave, a.k_stride, a.v_stride);
+  const uint16_t* kp = a.K + (int64_t)kr.start * a.k_stride + (int64_t)kvh * D;
+  const uint16_t* vp = a.V + (int64_t)kr.start * a.v_stride + (int64_t)kvh * D;
+  uint32_t ka[D / 16], va[D / 32];
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) ka[s] = a_addr<D>(lane, s);
+#pragma unroll
+  for (int t = 0; t < D / 32; ++t) va[t] = kTile + tr_addr<D>(lane, t);
+
+  const float sl = a.scale * kLog2e;
+  const int seen = r + off - 4 * (lane >> 5);  // last visible key, minus this lane's row offset
+  v16f o[D / 32];
+  clear<D / 32>(o);
+  float m = -kInf, l = 0.f;
+
+  auto step = [&](auto stage, int t) {
+    constexpr int P = decltype(stage)::value;
+    wait_dma<0>();
+    lds_barrier();
+    if (t + 1 < tiles)
+      dma.issue(pair_stage<D, P ^ 1>(), kp + (int64_t)(t + 1) * kKRows * a.k_stride,
+                vp + (int64_t)(t + 1) * kKRows * a.v_stride, kr.len - (t + 1) * kKRows);
+    if (t >= wtiles) return;
+    const lds_char* st = pair_stage<D, P>();
+    v16f s[2];
+    clear<2>(s);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s[i] = mfma32(lds_read8(st + ka[k] + i * 32 * T::kRowBytes), qf[k], s[i]);
+    if (t * kKRows + kKRows > w0 + off + 1) {  // the diagonal
+      const int x = seen - t * kKRows;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[i][j] = 32 * i + 8 * (j >> 2) + (j & 3) <= x ? s[i][j] : -kInf;
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[i][j]);
+    mx = half_join(mx, [](float u, float v) { return fmaxf(u, v); });
+    if (__ballot((mx - m) * sl > 8.f)) {  // (NaN where both are -inf: a row that sees no key yet)
+      const float mn = fmaxf(m, mx);
+      const float f = exp2_hw((m - (mn == -kInf ? 0.f : mn)) * sl);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[d][j] *= f;
+    }
+    const float ms = (m == -kInf ? 0.f : m) * sl;
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        s[i][j] = exp2_hw(fmaf(s[i][j], sl, -ms));
+        sum[i] += s[i][j];
+      }
+    l += sum[0] + sum[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const v8bf p = operand_of(s[i >> 1], i & 1);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) o[d] = mfma32(tr_operand<D>(st, va[d], 16 * i), p, o[d]);
+    }
+  };
+
+  if (tiles > 0) dma.issue(pair_stage<D, 0>(), kp, vp, kr.len);
+  int t = 0;
+  for (; t + 1 < tiles; t += 2) {
+    step(std::integral_constant<int, 0>{}, t);
+    step(std::integral_constant<int, 1>{}, t + 1);
+  }
+  if (t < tiles) step(std::integral_constant<int, 0>{}, t);
+
+  l = half_join(l, [](float u, float v) { return u + v; });
+  // a row that sees no key: zeros, and -inf as the logarithm of its sum
+  store_row<D>(a.O + ((int64_t)(qr.start + r) * a.hq + head) * D, o, l > 0.f ? 1.f / l : 0.f, lane, in);
+  if (a.lse && in && lane < 32)
+    st_global(a.lse + (int64_t)head * a.total_q + qr.start + r, l > 0.f ? fmaf(m, sl, log2_hw(l)) * kLn2 : -kInf);
+}
+
+// --------------------------------------------------------------- backward
+// With P = exp(S - lse) recomputed from the forward's lse:
+//   delta = rowsum(dO O),  dV = P^T dO,  dP = dO V^T,  dS = P (dP - delta),
+//   dQ = scale dS K,  dK = scale dS^T Q
+// in two passes without atomics: one workgroup per 128 query rows walks the
+// keys for dQ, one per 128 keys walks the rows of all query heads of its
+// group for dK and dV.  S and dP are computed in both, 7 products in place
+// of 5; the alternative, dQ added up in memory by the workgroups of all key
+// tiles, writes and reads binary32 dQ once per 128 keys and leaves the order
+// of the sums to chance.  P and dS are rounded to bf16 for the products,
+// every sum is binary32.
+
+// delta and lse * log2 e (+inf where a row sees no key, so P becomes 0), and
+// dO rounded to bf16 where it comes in binary32
+template <int D, bool F32>
+__global__ __launch_bounds__(256) void attn_delta_kernel(const uint16_t* __restrict__ O, const void* __restrict__ dO,
+                                                        const float* __restrict__ lse, int64_t rows, int hq,
+                                                        int64_t total_q, float* __restrict__ delta,
+                                                        float* __restrict__ lse2, uint16_t* __restrict__ dOb) {
+  constexpr int kLanes = D / 8;
+  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;  // (token, head)
+  const int c = threadIdx.x % kLanes;
+  if (row >= rows) return;  // whole groups of kLanes lanes at a time
+  const u32x4 o = ld_global(reinterpret_cast<const u32x4*>(O + row * D) + c);
+  u32x4 g;
+  if constexpr (F32) {
+    const v4f* p = reinterpret_cast<const v4f*>(static_cast<const float*>(dO) + row * D) + 2 * c;
+    const v4f x = ld_global(p), y = ld_global(p + 1);
+    g = u32x4{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(y[0], y[1]), pk_bf16(y[2], y[3])};
+    st_global(reinterpret_cast<u32x4*>(dOb + row * D) + c, g);
+  } else {
+    g = ld_global(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(dO) + row * D) + c);
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s = fmaf(bf16_lo(o[i]), bf16_lo(g[i]), fmaf(bf16_hi(o[i]), bf16_hi(g[i]), s));
+#pragma unroll
+  for (int x = 1; x < kLanes; x <<= 1) s += __shfl_xor(s, x, 64);
+  if (c == 0) {
+    const int64_t t = row / hq, at = (row - t * hq) * total_q + t;
+    const float e = ld_global(lse + at);
+    st_global(delta + at, s);
+    st_global(lse2 + at, e == -kInf ? kInf : e * kLog2e);
+  }
+}
+
+template <int D>
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const uint16_t* __restrict__ dO,
+                                                        const float* __restrict__ delta,
+                                                        const float* __restrict__ lse2) {
+  typedef Tile<D> T;
+  constexpr int kTile = PairBytes<D>::kTile;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Place pl = place_of(blockIdx.x, a.hq, a.hkv);
+  const Item it = find_item(a.cu_q, a.batch, a.total_q, kQRows, pl.rank);
+  const int seq = __builtin_amdgcn_readfirstlane(it.seq);
+  if (seq < 0) return;
+  const int head = pl.head, kvh = head / (a.hq / a.hkv);
+  const Rows qr = seq_rows(a.cu_q, seq, a.total_q), kr = seq_rows(a.cu_k, seq, a.total_k);
+  const int q0 = __builtin_amdgcn_readfirstlane(it.level) * kQRows;
+  const int off = kr.len - qr.len;
+  const int w0 = q0 + 32 * wave, r = w0 + (lane & 31);
+  const bool in = r < qr.len;
+  const int last = q0 + kQRows < qr.len ? q0 + kQRows : qr.len;
+  const int wlast = w0 + 32 < qr.len ? w0 + 32 : qr.len;
+  const int tiles = (clampi(last + off, 0, kr.len) + kKRows - 1) / kKRows;
+  const int wtiles = w0 < qr.len ? (clampi(wlast + off, 0, kr.len) + kKRows - 1) / kKRows : 0;
+
+  const int64_t row = qr.start + r;
+  v8bf qf[D / 16], gf[D / 16];
+  load_row_operand<D>(qf, a.Q + row * a.q_stride + (int64_t)head * D, lane, in);
+  load_row_operand<D>(gf, dO + (row * a.hq + head) * D, lane, in);
+  const float dl = in ? ld_global(delta + (int64_t)head * a.total_q + row) : 0.f;
+  const float le = in ? ld_global(lse2 + (int64_t)head * a.total_q + row) : kInf;
+  const PairDma<D> dma(lane, wave, a.k_stride, a.v_stride);
+  const uint16_t* kp = a.K + (int64_t)kr.start * a.k_stride + (int64_t)kvh * D;
+  const uint16_t* vp = a.V + (int64_t)kr.start * a.v_stride + (int64_t)kvh * D;
+  uint32_t ka[D / 16], kt[D / 32];
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) ka[s] = a_addr<D>(lane, s);
+#pragma unroll
+  for (int t = 0; t < D / 32; ++t) kt[t] = tr_addr<D>(lane, t);
+  const float sl = a.scale * kLog2e;
+  const int seen = r + off - 4 * (lane >> 5);
+  v16f dq[D / 32];
+  clear<D / 32>(dq);
+
+  auto step = [&](auto stage, int t) {
+    constexpr int P = decltype(stage)::value;
+    wait_dma<0>();
+    lds_barrier();
+    if (t + 1 < tiles)
+      dma.issue(pair_stage<D, P ^ 1>(), kp + (int64_t)(t + 1) * kKRows * a.k_stride,
+                vp + (int64_t)(t + 1) * kKRows * a.v_stride, kr.len - (t + 1) * kKRows);
+    if (t >= wtiles) return;
+    const lds_char* st = pair_stage<D, P>();
+    const bool diagonal = t * kKRows + kKRows > w0 + off + 1;
+    const int x = seen - t * kKRows;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v16f s[1], g[1];
+      clear<1>(s);
+      clear<1>(g);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        s[0] = mfma32(lds_read8(st + ka[k] + i * 32 * T::kRowBytes), qf[k], s[0]);
+        g[0] = mfma32(lds_read8(st + kTile + ka[k] + i * 32 * T::kRowBytes), gf[k], g[0]);
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[0][j] = exp2_hw(fmaf(s[0][j], sl, -le));
+      if (diagonal) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[0][j] = 32 * i + 8 * (j >> 2) + (j & 3) <= x ? s[0][j] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[0][j] *= g[0][j] - dl;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const v8bf p = operand_of(s[0], k);
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) dq[d] = mfma32(tr_operand<D>(st, kt[d], 32 * i + 16 * k), p, dq[d]);
+      }
+    }
+  };
+
+  if (tiles > 0) dma.issue(pair_stage<D, 0>(), kp, vp, kr.len);
+  int t = 0;
+  for (; t + 1 < tiles; t += 2) {
+    step(std::integral_constant<int, 0>{}, t);
+    step(std::integral_constant<int, 1>{}, t + 1);
+  }
+  if (t < tiles) step(std::integral_constant<int, 0>{}, t);
+  store_row<D>(a.dQ + (row * a.hq + head) * D, dq, a.scale, lane, in);
+}
+
+// dK and dV of 128 keys.  Lanes run over keys here: S = Q K^T has a key per
+// column, so P and dS are again B operands as they stand, of the products
+// over query rows; K and V stay in registers as operands, Q and dO stream
+// through LDS for all query heads of the group.
+template <int D>
+__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnBwdArgs a, const uint16_t* __restrict__ dO,
+                                                         const float* __restrict__ delta,
+                                                         const float* __restrict__ lse2) {
+  typedef Tile<D> T;
+  constexpr int kTile = PairBytes<D>::kTile;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Place pl = place_of(blockIdx.x, a.hkv, a.hkv);
+  const Item it = find_item(a.cu_k, a.batch, a.total_k, kBRows, pl.rank);
+  const int seq = __builtin_amdgcn_readfirstlane(it.seq);
+  if (seq < 0) return;
+  const int kvh = pl.head, group = a.hq / a.hkv;
+  const Rows qr = seq_rows(a.cu_q, seq, a.total_q), kr = seq_rows(a.cu_k, seq, a.total_k);
+  // the first keys are seen by the most rows: highest level first
+  const int k0 = ((kr.len + kBRows - 1) / kBRows - 1 - __builtin_amdgcn_readfirstlane(it.level)) * kBRows;
+  const int off = kr.len - qr.len;
+  const int w0 = k0 + 32 * wave, j = w0 + (lane & 31);
+  const bool in = j < kr.len;
+  const int first = (k0 - off > 0 ? k0 - off : 0) / kKRows;  // first row tile that sees a key of this workgroup
+  const int n = (qr.len + kKRows - 1) / kKRows - first;      // row tiles per head
+  const int steps = n > 0 ? n * group : 0;
+
+  v8bf kf[D / 16], vf[D / 16];
+  load_row_operand<D>(kf, a.K + (int64_t)(kr.start + j) * a.k_stride + (int64_t)kvh * D, lane, in);
+  load_row_operand<D>(vf, a.V + (int64_t)(kr.start + j) * a.v_stride + (int64_t)kvh * D, lane, in);
+  const int64_t g_stride = (int64_t)a.hq * D;
+  const PairDma<D> dma(lane, wave, a.q_stride, g_stride);
+  uint32_t qa[D / 16], qt[D / 32];
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) qa[s] = a_addr<D>(lane, s);
+#pragma unroll
+  for (int t = 0; t < D / 32; ++t) qt[t] = tr_addr<D>(lane, t);
+  const float sl = a.scale * kLog2e;
+  v16f dk[D / 32], dv[D / 32];
+  clear<D / 32>(dk);
+  clear<D / 32>(dv);
+
+  auto issue = [&](lds_char* st, int h, int t) {
+    const int64_t row = qr.start + t * kKRows;
+    const int rows = qr.len - t * kKRows;
+    const int64_t head = (int64_t)kvh * group + h;
+    dma.issue(st, a.Q + row * a.q_stride + head * D, dO + row * g_stride + head * D, rows);
+    if (wave < 2) {  // the rows' lse (wavefront 0) and delta (wavefront 1); zeros past the sequence
+      const float* p = (wave ? delta : lse2) + head * a.total_q + row;
+      lds_load4(rows_rsrc(p, (uint32_t)((rows < kKRows ? rows : kKRows) * 4)), st + 2 * kTile + 256 * wave,
+                (uint32_t)lane * 4);
+    }
+  };
+  int h = 0, t = first;  // of the step being computed
+  auto step = [&](auto stage, int i) {
+    constexpr int P = decltype(stage)::value;
+    wait_dma<0>();
+    lds_barrier();
+    const int nt = t + 1 < first + n ? t + 1 : first, nh = t + 1 < first + n ? h : h + 1;
+    if (i + 1 < steps) issue(pair_stage<D, P ^ 1>(), nh, nt);
+    const lds_char* st = pair_stage<D, P>();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int r0 = t * kKRows + 32 * q;  // rows r0 .. r0 + 31
+      if (r0 + 31 + off < w0) continue;    // none of them sees a key of this wavefront
+      v16f s[1], g[1];
+      clear<1>(s);
+      clear<1>(g);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        s[0] = mfma32(lds_read8(st + qa[k] + q * 32 * T::kRowBytes), kf[k], s[0]);
+        g[0] = mfma32(lds_read8(st + kTile + qa[k] + q * 32 * T::kRowBytes), vf[k], g[0]);
+      }
+      v4f le[4], dl[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const lds_char* p = st + 2 * kTile + (32 * q + 8 * u + 4 * (lane >> 5)) * 4;
+        le[u] = *reinterpret_cast<const __attribute__((address_space(3))) v4f*>(p);
+        dl[u] = *reinterpret_cast<const __attribute__((address_space(3))) v4f*>(p + 256);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[0][e] = exp2_hw(fmaf(s[0][e], sl, -le[e >> 2][e & 3]));
+      if (r0 + off < w0 + 31) {  // the diagonal
+        const int x = j - off - r0 - 4 * (lane >> 5);  // first row that sees this lane's key
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[0][e] = 8 * (e >> 2) + (e & 3) >= x ? s[0][e] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const v8bf p = operand_of(s[0], k);
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+          dv[d] = mfma32(tr_operand<D>(st + kTile, qt[d], 32 * q + 16 * k), p, dv[d]);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[0][e] *= g[0][e] - dl[e >> 2][e & 3];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const v8bf p = operand_of(s[0], k);
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) dk[d] = mfma32(tr_operand<D>(st, qt[d], 32 * q + 16 * k), p, dk[d]);
+      }
+    }
+    t = nt;
+    h = nh;
+  };
+
+  if (steps > 0) issue(pair_stage<D, 0>(), 0, first);
+  int i = 0;
+  for (; i + 1 < steps; i += 2) {
+    step(std::integral_constant<int, 0>{}, i);
+    step(std::integral_constant<int, 1>{}, i + 1);
+  }
+  if (i < steps) step(std::integral_constant<int, 0>{}, i);
+  const int64_t out = ((int64_t)(kr.start + j) * a.hkv + kvh) * D;
+  store_row<D>(a.dK + out, dk, a.scale, lane, in);
+  store_row<D>(a.dV + out, dv, 1.f, lane, in);
+}
+
+// ------------------------------------------------------------------- host
+namespace {
+int64_t most_tiles(int64_t rows, int64_t batch, int64_t tile) {
+  // every sequence adds at most one partly filled tile
+  return rows / tile + (batch < rows ? batch : rows);
+}
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+size_t bwd_row_bytes(int64_t total_q, int64_t hq) { return align256((size_t)total_q * hq * 4); }
+}  // namespace
+
+size_t attn_fwd_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+
+hipError_t launch_attn_fwd(const AttnArgs& a, int64_t d, void*, hipStream_t s) {
+  const unsigned blocks = (unsigned)placed_blocks(most_tiles(a.total_q, a.batch, kQRows), a.hq, a.hkv);
+  if (d == 128) attn_fwd_kernel<128><<<dim3(blocks), 256, 0, s>>>(a);
+  else attn_fwd_kernel<64><<<dim3(blocks), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// workspace: delta, lse * log2 e ([hq][total_q] each), dO in bf16
+size_t attn_bwd_ws_bytes(int64_t, int64_t total_q, int64_t, int64_t hq, int64_t, int64_t d) {
+  return 2 * bwd_row_bytes(total_q, hq) + align256((size_t)total_q * hq * d * 2);
+}
+
+template <int D>
+static hipError_t bwd_launch(const AttnBwdArgs& a, hipStream_t s) {
+  char* ws = static_cast<char*>(a.ws);
+  float* delta = reinterpret_cast<float*>(ws);
+  float* lse2 = reinterpret_cast<float*>(ws + bwd_row_bytes(a.total_q, a.hq));
+  uint16_t* copy = reinterpret_cast<uint16_t*>(ws + 2 * bwd_row_bytes(a.total_q, a.hq));
+  const uint16_t* dO = a.do_f32 ? copy : static_cast<const uint16_t*>(a.dO);
+  if (a.total_q > 0) {
+    const int64_t rows = a.total_q * a.hq;
+    const dim3 grid((unsigned)((rows * (D / 8) + 255) / 256));
+    if (a.do_f32)
+      attn_delta_kernel<D, true><<<grid, 256, 0, s>>>(a.O, a.dO, a.lse, rows, a.hq, a.total_q, delta, lse2, copy);
+    else
+      attn_delta_kernel<D, false><<<grid, 256, 0, s>>>(a.O, a.dO, a.lse, rows, a.hq, a.total_q, delta, lse2, copy);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    attn_dq_kernel<D><<<dim3((unsigned)placed_blocks(most_tiles(a.total_q, a.batch, kQRows), a.hq, a.hkv)), 256, 0, s>>>(
+        a, dO, delta, lse2);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.total_k > 0)
+    attn_dkv_kernel<D><<<dim3((unsigned)placed_blocks(most_tiles(a.total_k, a.batch, kBRows), a.hkv, a.hkv)), 256, 0, s>>>(
+        a, dO, delta, lse2);
+  return hipGetLastError();
+}
+hipError_t launch_attn_bwd(const AttnBwdArgs& a, int64_t d, hipStream_t s) {
+  return d == 128 ? bwd_launch<128>(a, s) : bwd_launch<64>(a, s);
+}
+
+}  // namespace bl

@@ -367,4 +367,90 @@ hipError_t launch_bwd(const uint16_t* dY, const int8_t* xq, const float* scale, 
 // 2: 256 x 128, 3: 256 x 256); -1 for another value
 int bwd_set_tiles(int tiles);
 
+// ---------------------------------------------------------- rope.hip
+struct RopeArgs {
+  const void *Q, *K, *V;  // rows of hq*d, hkv*d, hkv*d elements (binary32 or bf16); V may be NULL
+  int64_t q_stride, k_stride, v_stride, tokens;
+  int hq, hkv;
+  const float *qw, *kw;  // norm weights [d], both or neither
+  float eps;
+  const float* table;  // [max_pos][d/2][2]
+  int64_t max_pos;
+  const int32_t* pos;
+  const int64_t* slots;  // row of K and V per token, or NULL: the token's own
+  int64_t kv_rows;
+  uint16_t *Qr, *Kr, *Vr;
+};
+struct RopeBwdArgs {
+  const void *Q, *K;
+  int64_t q_stride, k_stride, tokens;
+  int hq, hkv;
+  const float *qw, *kw;
+  float eps;
+  const float* table;
+  int64_t max_pos;
+  const int32_t* pos;
+  const uint16_t *dQr, *dKr;
+  uint16_t *dQ, *dK;
+  float *gqw, *gkw;
+  float* part;  // kRopeDwRows rows of 2d partial sums
+};
+constexpr int kRopeDwRows = 1024;  // workgroups of the backward with norms, at most
+inline size_t rope_bwd_ws_bytes(int64_t d) { return (size_t)kRopeDwRows * 2 * d * 4; }
+hipError_t launch_qk_rope(const RopeArgs& a, int64_t d, bool f32, hipStream_t s);
+hipError_t launch_qk_rope_bwd(const RopeBwdArgs& a, int64_t d, bool f32, hipStream_t s);
+hipError_t launch_rope_table(float* table, int64_t max_pos, int64_t d, double base, hipStream_t s);
+
+// ---------------------------------------------------------- attn.hip
+// Packed sequences: sequence b has query rows [cu_q[b], cu_q[b+1]) and key
+// rows [cu_k[b], cu_k[b+1]); query i sees keys j <= i + k_len - q_len.
+struct AttnArgs {
+  const uint16_t *Q, *K, *V;
+  int64_t q_stride, k_stride, v_stride;  // elements between rows
+  const int32_t *cu_q, *cu_k;
+  int batch, hq, hkv;
+  int64_t total_q, total_k;
+  float scale;
+  uint16_t* O;
+  float* lse;  // [hq][total_q] or NULL
+};
+struct AttnBwdArgs {
+  const uint16_t *Q, *K, *V;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *cu_q, *cu_k;
+  int batch, hq, hkv;
+  int64_t total_q, total_k;
+  float scale;
+  const uint16_t* O;
+  const float* lse;
+  const void* dO;
+  bool do_f32;
+  uint16_t *dQ, *dK, *dV;
+  void* ws;
+};
+size_t attn_fwd_ws_bytes(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d);
+size_t attn_bwd_ws_bytes(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d);
+hipError_t launch_attn_fwd(const AttnArgs& a, int64_t d, void* ws, hipStream_t s);
+hipError_t launch_attn_bwd(const AttnBwdArgs& a, int64_t d, hipStream_t s);
+
+// Paged cache: sequence b's row p is row pages[b][p / page] * page + p % page
+// of K and V ([rows][hkv][d]); lens[b] rows, the last `draft` of them the
+// drafted tokens.
+struct AttnCacheArgs {
+  const uint16_t* Q;
+  int64_t q_stride;
+  const uint16_t *K, *V;
+  int64_t pool;  // pages in K and V
+  const int32_t* pages;
+  int64_t max_pages, page;
+  const int32_t* lens;
+  const uint64_t* tree;  // [batch][draft] or NULL: each token sees those before it
+  int batch, draft, hq, hkv;
+  float scale;
+  uint16_t* O;
+  void* ws;
+};
+size_t attn_cache_ws_bytes(int64_t batch, int64_t draft, int64_t hq, int64_t hkv, int64_t d);
+hipError_t launch_attn_cache(const AttnCacheArgs& a, int64_t d, hipStream_t s);
+
 }  // namespace bl
