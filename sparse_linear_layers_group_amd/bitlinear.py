@@ -114,8 +114,8 @@ def lib():
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle itself: making a Stream object for it takes 2.5 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -525,56 +525,72 @@ def bitlinear_quant_group(plan, n, m, gamma_over, stream=None):
 
 
 BL_TYPE_F32, BL_TYPE_BF16 = 0, 1
+_F32T, _I32T, _U8T, _FLOATS = (torch.float32,), (torch.int32,), (torch.uint8,), (torch.float32, torch.bfloat16)
 
 
-def _rows(t, dtypes, width, name, rows=None):
+# The attention-side calls are short (a few microseconds of GPU work), so
+# their checks are one pass per tensor; _refuse names what was wrong.
+def _refuse(t, dtypes, numel, name, dev):
+    _ptr(t, dtypes, numel, name)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _arg(t, dtypes, numel, name, dev):
+    """Pointer of a contiguous tensor on device `dev`."""
+    try:
+        if t.dtype in dtypes and t.get_device() == dev and t.is_contiguous() and numel in (None, t.numel()):
+            return t.data_ptr()
+    except AttributeError:  # no tensor
+        pass
+    _refuse(t, dtypes, numel, name, dev)
+
+
+def _opt(t, dtypes, numel, name, dev):
+    return None if t is None else _arg(t, dtypes, numel, name, dev)
+
+
+def _rows(t, dtypes, width, name, dev, rows=None):
     """(pointer, row stride in elements, rows) of rows of `width` elements:
     [rows, width] or [rows, heads, d], each row contiguous, the rows any
     distance apart; or a contiguous tensor of any shape."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.get_device() != dev:
+        _ptr(t, dtypes, None, name)
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
     n = t.numel() // width if width > 0 else 0
     if n * width != t.numel() or (rows is not None and n != rows):
         raise ValueError(f"{name} has {t.numel()} elements, expected {'rows' if rows is None else rows} x {width}")
-    if t.is_contiguous() or n == 0:
+    if n == 0 or t.is_contiguous():
         return t.data_ptr(), width, n
     if t.dim() not in (2, 3) or t.shape[0] != n or t.stride(-1) != 1 or (t.dim() == 3 and t.stride(1) != t.shape[2]):
         raise ValueError(f"{name} must have contiguous rows of {width} elements")
     return t.data_ptr(), t.stride(0) if n > 1 else width, n
 
 
-def _on_current_device(*tensors):
-    d = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != d:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{d}")
+def _ws(ws, ws_bytes, dev):
+    if ws is None:
+        return None, 0 if ws_bytes is None else int(ws_bytes)
+    return _arg(ws, _U8T, None, "ws", dev), ws.numel() if ws_bytes is None else int(ws_bytes)
 
 
-def _ws(ws, ws_bytes):
-    p = _ptr(ws, (torch.uint8,), None, "ws", optional=True)
-    return p, (ws.numel() if ws is not None else 0) if ws_bytes is None else int(ws_bytes)
-
-
-_FLOATS = (torch.float32, torch.bfloat16)
-
-
-def _type_of(name, *tensors):
+def _type_of(name, first, *others):
     """BL_TYPE_* of tensors that share one of the two input types."""
-    kinds = {t.dtype for t in tensors if t is not None}
-    if len(kinds) != 1 or not kinds <= set(_FLOATS):
+    kind = getattr(first, "dtype", None)
+    if kind not in _FLOATS or any(t is not None and t.dtype != kind for t in others):
         raise TypeError(f"{name} must all be float32 or all bfloat16 tensors")
-    return BL_TYPE_F32 if torch.float32 in kinds else BL_TYPE_BF16
+    return BL_TYPE_F32 if kind == torch.float32 else BL_TYPE_BF16
+
+
+def _table_rows(table, d, dev):
+    p = _arg(table, _F32T, None, "table", dev)
+    if d < 1 or table.numel() % d:
+        raise ValueError(f"table must hold rows of {d} elements")
+    return p, table.numel() // d
 
 
 def bitlinear_rope_table(max_pos, d, base, table, stream=None):
     """Fill table (float32, max_pos * d/2 * 2) with cos and sin of p * base^(-2i/d)."""
-    _on_current_device(table)
-    st = lib().bitlinear_rope_table(int(max_pos), int(d), float(base),
-                                    _ptr(table, (torch.float32,), max_pos * d, "table"), _stream(stream))
+    dev = torch.cuda.current_device()
+    st = lib().bitlinear_rope_table(max_pos, d, base, _arg(table, _F32T, max_pos * d, "table", dev), _stream(stream))
     _check(st, "bitlinear_rope_table")
 
 
@@ -583,24 +599,21 @@ def bitlinear_qk_rope(Q, K, V, tokens, hq, hkv, d, q_weight, k_weight, eps, tabl
     """Head norms (with weights) and rotation of Q and K, V copied: bfloat16
     Qr, Kr, Vr.  Q, K, V: float32 or bfloat16 rows, any row stride; max_pos and
     kv_rows are taken from the sizes of table and Kr."""
-    _on_current_device(Q, K, V, q_weight, k_weight, table, pos, Qr, Kr, Vr, slots)
+    dev = torch.cuda.current_device()
     x_type = _type_of("Q, K and V", Q, K, V)
-    q, qs, _ = _rows(Q, _FLOATS, hq * d, "Q", tokens)
-    k, ks, _ = _rows(K, _FLOATS, hkv * d, "K", tokens)
-    v, vs, _ = _rows(V, _FLOATS, hkv * d, "V", tokens) if V is not None else (None, 0, 0)
-    if Kr is None or Kr.numel() % (hkv * d):
-        raise ValueError(f"Kr must hold rows of {hkv * d} elements")
-    if table.numel() % d:
-        raise ValueError(f"table must hold rows of {d} elements")
+    q, qs, _ = _rows(Q, _FLOATS, hq * d, "Q", dev, tokens)
+    k, ks, _ = _rows(K, _FLOATS, hkv * d, "K", dev, tokens)
+    v, vs, _ = _rows(V, _FLOATS, hkv * d, "V", dev, tokens) if V is not None else (None, 0, 0)
+    kr = _arg(Kr, _BF16, None, "Kr", dev)
     kv_rows = Kr.numel() // (hkv * d)
+    if kv_rows * hkv * d != Kr.numel():
+        raise ValueError(f"Kr must hold rows of {hkv * d} elements")
+    t, max_pos = _table_rows(table, d, dev)
     st = lib().bitlinear_qk_rope(
-        q, k, v, x_type, qs, ks, vs, tokens, hq, hkv, d,
-        _ptr(q_weight, (torch.float32,), d, "q_weight", optional=True),
-        _ptr(k_weight, (torch.float32,), d, "k_weight", optional=True), eps,
-        _ptr(table, (torch.float32,), None, "table"), table.numel() // d, _ptr(pos, (torch.int32,), tokens, "pos"),
-        _ptr(slots, (torch.int64,), tokens, "slots", optional=True), kv_rows,
-        _ptr(Qr, _BF16, tokens * hq * d, "Qr"), _ptr(Kr, _BF16, None, "Kr"),
-        _ptr(Vr, _BF16, kv_rows * hkv * d, "Vr", optional=V is None), _stream(stream))
+        q, k, v, x_type, qs, ks, vs, tokens, hq, hkv, d, _opt(q_weight, _F32T, d, "q_weight", dev),
+        _opt(k_weight, _F32T, d, "k_weight", dev), eps, t, max_pos, _arg(pos, _I32T, tokens, "pos", dev),
+        _opt(slots, (torch.int64,), tokens, "slots", dev), kv_rows, _arg(Qr, _BF16, tokens * hq * d, "Qr", dev), kr,
+        _opt(Vr, _BF16, Kr.numel(), "Vr", dev), _stream(stream))
     _check(st, "bitlinear_qk_rope")
 
 
@@ -612,23 +625,21 @@ def bitlinear_qk_rope_bwd(Q, K, tokens, hq, hkv, d, q_weight, k_weight, eps, tab
                           dq_weight=None, dk_weight=None, ws=None, ws_bytes=None, stream=None):
     """Backward of bitlinear_qk_rope for Q and K (which may be None without
     weights): bfloat16 dQ, dK and, with weights, float32 dq_weight, dk_weight."""
-    _on_current_device(Q, K, q_weight, k_weight, table, pos, dQr, dKr, dQ, dK, dq_weight, dk_weight, ws)
+    dev = torch.cuda.current_device()
     x_type, q, qs, k, ks = BL_TYPE_F32, None, 0, None, 0
     if q_weight is not None:
         x_type = _type_of("Q and K", Q, K)
-        q, qs, _ = _rows(Q, _FLOATS, hq * d, "Q", tokens)
-        k, ks, _ = _rows(K, _FLOATS, hkv * d, "K", tokens)
-    if table.numel() % d:
-        raise ValueError(f"table must hold rows of {d} elements")
-    w, wn = _ws(ws, ws_bytes)
-    f32 = (torch.float32,)
+        q, qs, _ = _rows(Q, _FLOATS, hq * d, "Q", dev, tokens)
+        k, ks, _ = _rows(K, _FLOATS, hkv * d, "K", dev, tokens)
+    t, max_pos = _table_rows(table, d, dev)
+    w, wn = _ws(ws, ws_bytes, dev)
     st = lib().bitlinear_qk_rope_bwd(
-        q, k, x_type, qs, ks, tokens, hq, hkv, d, _ptr(q_weight, f32, d, "q_weight", optional=True),
-        _ptr(k_weight, f32, d, "k_weight", optional=True), eps, _ptr(table, f32, None, "table"), table.numel() // d,
-        _ptr(pos, (torch.int32,), tokens, "pos"), _ptr(dQr, _BF16, tokens * hq * d, "dQr"),
-        _ptr(dKr, _BF16, tokens * hkv * d, "dKr"), _ptr(dQ, _BF16, tokens * hq * d, "dQ"),
-        _ptr(dK, _BF16, tokens * hkv * d, "dK"), _ptr(dq_weight, f32, d, "dq_weight", optional=True),
-        _ptr(dk_weight, f32, d, "dk_weight", optional=True), w, wn, _stream(stream))
+        q, k, x_type, qs, ks, tokens, hq, hkv, d, _opt(q_weight, _F32T, d, "q_weight", dev),
+        _opt(k_weight, _F32T, d, "k_weight", dev), eps, t, max_pos, _arg(pos, _I32T, tokens, "pos", dev),
+        _arg(dQr, _BF16, tokens * hq * d, "dQr", dev), _arg(dKr, _BF16, tokens * hkv * d, "dKr", dev),
+        _arg(dQ, _BF16, tokens * hq * d, "dQ", dev), _arg(dK, _BF16, tokens * hkv * d, "dK", dev),
+        _opt(dq_weight, _F32T, d, "dq_weight", dev), _opt(dk_weight, _F32T, d, "dk_weight", dev), w, wn,
+        _stream(stream))
     _check(st, "bitlinear_qk_rope_bwd")
 
 
@@ -640,15 +651,15 @@ def bitlinear_attn_fwd(Q, K, V, cu_q, cu_k, batch, hq, hkv, d, scale, O, lse=Non
                        stream=None):
     """Causal attention over packed sequences: bfloat16 O, float32 lse
     [hq, total_q].  Q, K, V: bfloat16 rows, any row stride."""
-    _on_current_device(Q, K, V, cu_q, cu_k, O, lse, ws)
-    q, qs, tq = _rows(Q, _BF16, hq * d, "Q")
-    k, ks, tk = _rows(K, _BF16, hkv * d, "K")
-    v, vs, _ = _rows(V, _BF16, hkv * d, "V", tk)
-    w, wn = _ws(ws, ws_bytes)
+    dev = torch.cuda.current_device()
+    q, qs, tq = _rows(Q, _BF16, hq * d, "Q", dev)
+    k, ks, tk = _rows(K, _BF16, hkv * d, "K", dev)
+    v, vs, _ = _rows(V, _BF16, hkv * d, "V", dev, tk)
+    w, wn = _ws(ws, ws_bytes, dev)
     st = lib().bitlinear_attn_fwd(
-        q, k, v, qs, ks, vs, _ptr(cu_q, (torch.int32,), batch + 1, "cu_q"), _ptr(cu_k, (torch.int32,), batch + 1, "cu_k"),
-        batch, tq, tk, hq, hkv, d, scale, _ptr(O, _BF16, tq * hq * d, "O"),
-        _ptr(lse, (torch.float32,), hq * tq, "lse", optional=True), w, wn, _stream(stream))
+        q, k, v, qs, ks, vs, _arg(cu_q, _I32T, batch + 1, "cu_q", dev), _arg(cu_k, _I32T, batch + 1, "cu_k", dev),
+        batch, tq, tk, hq, hkv, d, scale, _arg(O, _BF16, tq * hq * d, "O", dev), _opt(lse, _F32T, hq * tq, "lse", dev),
+        w, wn, _stream(stream))
     _check(st, "bitlinear_attn_fwd")
 
 
@@ -660,17 +671,17 @@ def bitlinear_attn_bwd(Q, K, V, O, lse, dO, cu_q, cu_k, batch, hq, hkv, d, scale
                        stream=None):
     """Backward of bitlinear_attn_fwd: bfloat16 dQ, dK, dV.  dO: contiguous
     bfloat16 or float32."""
-    _on_current_device(Q, K, V, O, lse, dO, cu_q, cu_k, dQ, dK, dV, ws)
-    q, qs, tq = _rows(Q, _BF16, hq * d, "Q")
-    k, ks, tk = _rows(K, _BF16, hkv * d, "K")
-    v, vs, _ = _rows(V, _BF16, hkv * d, "V", tk)
-    w, wn = _ws(ws, ws_bytes)
+    dev = torch.cuda.current_device()
+    q, qs, tq = _rows(Q, _BF16, hq * d, "Q", dev)
+    k, ks, tk = _rows(K, _BF16, hkv * d, "K", dev)
+    v, vs, _ = _rows(V, _BF16, hkv * d, "V", dev, tk)
+    w, wn = _ws(ws, ws_bytes, dev)
+    n = tq * hq * d
     st = lib().bitlinear_attn_bwd(
-        q, k, v, qs, ks, vs, _ptr(O, _BF16, tq * hq * d, "O"), _ptr(lse, (torch.float32,), hq * tq, "lse"),
-        _ptr(dO, _FLOATS, tq * hq * d, "dO"), _type_of("dO", dO), _ptr(cu_q, (torch.int32,), batch + 1, "cu_q"),
-        _ptr(cu_k, (torch.int32,), batch + 1, "cu_k"), batch, tq, tk, hq, hkv, d, scale,
-        _ptr(dQ, _BF16, tq * hq * d, "dQ"), _ptr(dK, _BF16, tk * hkv * d, "dK"), _ptr(dV, _BF16, tk * hkv * d, "dV"),
-        w, wn, _stream(stream))
+        q, k, v, qs, ks, vs, _arg(O, _BF16, n, "O", dev), _arg(lse, _F32T, hq * tq, "lse", dev),
+        _arg(dO, _FLOATS, n, "dO", dev), _type_of("dO", dO), _arg(cu_q, _I32T, batch + 1, "cu_q", dev),
+        _arg(cu_k, _I32T, batch + 1, "cu_k", dev), batch, tq, tk, hq, hkv, d, scale, _arg(dQ, _BF16, n, "dQ", dev),
+        _arg(dK, _BF16, tk * hkv * d, "dK", dev), _arg(dV, _BF16, tk * hkv * d, "dV", dev), w, wn, _stream(stream))
     _check(st, "bitlinear_attn_bwd")
 
 
@@ -683,16 +694,17 @@ def bitlinear_attn_cache(Q, K, V, pages, page, lens, tree, batch, draft, hq, hkv
     """Attention of batch * draft new tokens over a paged cache: bfloat16 O.
     pages: int32 [batch, max_pages]; tree: int64 or uint64 [batch, draft] bit
     sets, or None (each drafted token sees those before it)."""
-    _on_current_device(Q, K, V, pages, lens, tree, O, ws)
-    q, qs, _ = _rows(Q, _BF16, hq * d, "Q", batch * draft)
-    if K.numel() % (hkv * d):
+    dev = torch.cuda.current_device()
+    q, qs, _ = _rows(Q, _BF16, hq * d, "Q", dev, batch * draft)
+    k = _arg(K, _BF16, None, "K", dev)
+    rows, width = K.numel() // (hkv * d), pages.numel() // batch
+    if rows * hkv * d != K.numel():
         raise ValueError(f"K must hold rows of {hkv * d} elements")
-    if pages.numel() % max(batch, 1):
+    if width * batch != pages.numel():
         raise ValueError("pages must hold one row per sequence")
-    w, wn = _ws(ws, ws_bytes)
+    w, wn = _ws(ws, ws_bytes, dev)
     st = lib().bitlinear_attn_cache(
-        q, qs, _ptr(K, _BF16, None, "K"), _ptr(V, _BF16, K.numel(), "V"), K.numel() // (hkv * d),
-        _ptr(pages, (torch.int32,), None, "pages"), pages.numel() // max(batch, 1), page,
-        _ptr(lens, (torch.int32,), batch, "lens"), _ptr(tree, (torch.int64, torch.uint64), batch * draft, "tree", optional=True),
-        batch, draft, hq, hkv, d, scale, _ptr(O, _BF16, batch * draft * hq * d, "O"), w, wn, _stream(stream))
+        q, qs, k, _arg(V, _BF16, K.numel(), "V", dev), rows, _arg(pages, _I32T, None, "pages", dev), width, page,
+        _arg(lens, _I32T, batch, "lens", dev), _opt(tree, (torch.int64, torch.uint64), batch * draft, "tree", dev),
+        batch, draft, hq, hkv, d, scale, _arg(O, _BF16, batch * draft * hq * d, "O", dev), w, wn, _stream(stream))
     _check(st, "bitlinear_attn_cache")

@@ -11,6 +11,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kQRows = 128;  // query rows of a forward / dQ workgroup: 32 per wavefront
 constexpr int kKRows = 64;   // key rows of a tile in LDS
+constexpr int kExactTiles = 4;  // dQ workgroups with at most this many key tiles form delta from P dP
 constexpr int kBRows = 128;  // key rows of a dK / dV workgroup: 32 per wavefront
 constexpr float kInf = __builtin_huge_valf();
 }  // namespace
@@ -236,6 +237,14 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
 // tiles, writes and reads binary32 dQ once per 128 keys and leaves the order
 // of the sums to chance.  P and dS are rounded to bf16 for the products,
 // every sum is binary32.
+//
+// delta from the bf16 O carries O's rounding into every dS of its row.  Over
+// many keys that is small against the rounding of dS itself, but rows that
+// see few keys make up most of the gradients' norm: there it raised the
+// relative error of dQ and dK from 2.4e-3 to 2.7e-3 (bf16 outputs alone:
+// 1.7e-3).  Workgroups of at most kExactTiles key tiles therefore form
+// delta = sum P dP in binary32 in a sweep of their own and leave it in
+// memory for the dK / dV pass.
 
 // delta and lse * log2 e (+inf where a row sees no key, so P becomes 0), and
 // dO rounded to bf16 where it comes in binary32
@@ -273,7 +282,7 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(const uint16_t* __restr
 
 template <int D>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const uint16_t* __restrict__ dO,
-                                                        const float* __restrict__ delta,
+                                                        float* __restrict__ delta,
                                                         const float* __restrict__ lse2) {
   typedef Tile<D> T;
   constexpr int kTile = PairBytes<D>::kTile;
@@ -298,7 +307,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const ui
   v8bf qf[D / 16], gf[D / 16];
   load_row_operand<D>(qf, a.Q + row * a.q_stride + (int64_t)head * D, lane, in);
   load_row_operand<D>(gf, dO + (row * a.hq + head) * D, lane, in);
-  const float dl = in ? ld_global(delta + (int64_t)head * a.total_q + row) : 0.f;
+  float dl = in ? ld_global(delta + (int64_t)head * a.total_q + row) : 0.f;
   const float le = in ? ld_global(lse2 + (int64_t)head * a.total_q + row) : kInf;
   const PairDma<D> dma(lane, wave, a.k_stride, a.v_stride);
   const uint16_t* kp = a.K + (int64_t)kr.start * a.k_stride + (int64_t)kvh * D;
@@ -312,8 +321,9 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const ui
   const int seen = r + off - 4 * (lane >> 5);
   v16f dq[D / 32];
   clear<D / 32>(dq);
+  float exact = 0.f;  // this lane's share of sum P dP
 
-  auto step = [&](auto stage, int t) {
+  auto step = [&](auto stage, auto sums, int t) {
     constexpr int P = decltype(stage)::value;
     wait_dma<0>();
     lds_barrier();
@@ -340,24 +350,39 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const ui
 #pragma unroll
         for (int j = 0; j < 16; ++j) s[0][j] = 32 * i + 8 * (j >> 2) + (j & 3) <= x ? s[0][j] : 0.f;
       }
+      if constexpr (decltype(sums)::value) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s[0][j] *= g[0][j] - dl;
+        for (int j = 0; j < 16; ++j) exact = fmaf(s[0][j], g[0][j], exact);
+      } else {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const v8bf p = operand_of(s[0], k);
+        for (int j = 0; j < 16; ++j) s[0][j] *= g[0][j] - dl;
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) dq[d] = mfma32(tr_operand<D>(st, kt[d], 32 * i + 16 * k), p, dq[d]);
+        for (int k = 0; k < 2; ++k) {
+          const v8bf p = operand_of(s[0], k);
+#pragma unroll
+          for (int d = 0; d < D / 32; ++d) dq[d] = mfma32(tr_operand<D>(st, kt[d], 32 * i + 16 * k), p, dq[d]);
+        }
       }
     }
   };
-
-  if (tiles > 0) dma.issue(pair_stage<D, 0>(), kp, vp, kr.len);
-  int t = 0;
-  for (; t + 1 < tiles; t += 2) {
-    step(std::integral_constant<int, 0>{}, t);
-    step(std::integral_constant<int, 1>{}, t + 1);
+  auto sweep = [&](auto sums) {
+    typedef std::integral_constant<int, 0> S0;
+    typedef std::integral_constant<int, 1> S1;
+    if (tiles > 0) dma.issue(pair_stage<D, 0>(), kp, vp, kr.len);
+    int t = 0;
+    for (; t + 1 < tiles; t += 2) {
+      step(S0{}, sums, t);
+      step(S1{}, sums, t + 1);
+    }
+    if (t < tiles) step(S0{}, sums, t);
+  };
+  if (tiles <= kExactTiles) {
+    sweep(std::true_type{});
+    dl = half_join(exact, [](float u, float v) { return u + v; });
+    if (in && lane < 32) st_global(delta + (int64_t)head * a.total_q + row, dl);
+    lds_barrier();  // both stages are free for the second sweep
   }
-  if (t < tiles) step(std::integral_constant<int, 0>{}, t);
+  sweep(std::false_type{});
   store_row<D>(a.dQ + (row * a.hq + head) * D, dq, a.scale, lane, in);
 }
 
