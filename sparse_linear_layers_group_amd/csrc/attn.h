@@ -86,19 +86,24 @@ __device__ __forceinline__ void lds_barrier() {
 
 // ---------------------------------------------------------------------
 // A tile of rows of D bf16 in LDS, row after row, the 16-byte pieces of row
-// r permuted: piece c at place c ^ swz(r).  With swz the bit reversal of
-// r % 8, eight consecutive rows' reads of one piece (an A operand by rows)
-// fall into eight different pieces of a 128-byte bank line, and a
-// transposing read's four aligned rows of 64 bytes into both halves of it.
+// r permuted: piece c at place c ^ swz(r).  LDS serves 256 bytes a clock to
+// these reads, a 16-byte read 16 lanes at a time, an 8-byte transposing read
+// 32 lanes at a time.  The permutation spreads both over all of a 256-byte
+// bank line: 16 consecutive rows' reads of one piece (an A operand by rows),
+// and a transposing read's four aligned rows of 64 bytes.  (A permutation by
+// r % 8 within 128 bytes left both at half that rate: 128 of the 265 LDS
+// clocks of a 64-key tile of the forward were bank conflicts.)
 // ---------------------------------------------------------------------
-__device__ __forceinline__ constexpr int swz(int r) { return ((r & 1) << 2) | (r & 2) | ((r >> 2) & 1); }
-
 template <int D>
 struct Tile {
   static constexpr int kRowBytes = 2 * D;
   static constexpr int kPieces = D / 8;            // 16-byte pieces of a row
   static constexpr int kDmaRows = 64 / kPieces;    // rows of one DMA instruction (4 or 8)
-  static constexpr int kVariants = 8 / kDmaRows;   // row residues mod 8 an instruction can start at
+  static constexpr int kVariants = 16 / kDmaRows;  // row residues mod 16 an instruction can start at
+  static constexpr uint32_t kFar = D == 128 ? 32 : 16;  // address bits that differ between rows r and r + 8
+  __device__ static __forceinline__ constexpr int swz(int r) {
+    return D == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : ((r & 2) << 1) | ((r >> 1) & 2) | ((r >> 3) & 1);
+  }
 };
 
 // offset, from the first row of a DMA instruction's rows, that this lane
@@ -106,30 +111,37 @@ struct Tile {
 template <int D>
 __device__ __forceinline__ uint32_t dma_offset(int lane, int var, int64_t stride) {
   typedef Tile<D> T;
-  const int r = lane / T::kPieces, c = (lane % T::kPieces) ^ swz(r + var * T::kDmaRows);
+  const int r = lane / T::kPieces, c = (lane % T::kPieces) ^ T::swz(r + var * T::kDmaRows);
   return (uint32_t)(r * (int)stride * 2 + c * 16);
 }
-// address (from the tile's start) of A operand rows 32i + l%32, elements
-// 16s + 8(l/32) .. +7: row_addr + 32i rows, piece_of(s)
+// address (from the tile's start) of the operand of rows l%32, elements
+// 16s + 8(l/32) .. +7; 32 rows further on the permutation is the same
 template <int D>
 __device__ __forceinline__ uint32_t a_addr(int lane, int s) {
   const int r = lane & 31;
-  return (uint32_t)(r * Tile<D>::kRowBytes + (((2 * s + (lane >> 5)) ^ swz(r)) << 4));
+  return (uint32_t)(r * Tile<D>::kRowBytes + (((2 * s + (lane >> 5)) ^ Tile<D>::swz(r)) << 4));
 }
 // address of the transposing read that gives lane l column 32t + l%32 of
-// rows 4(l/32) + 0..3 (rows 8 and 16 further on keep the permutation of
-// row r, respectively have that of r + 8: the same, swz looks at r % 8)
+// rows 4(l/32) + 0..3; 16 rows further on the permutation is the same
 template <int D>
 __device__ __forceinline__ uint32_t tr_addr(int lane, int t) {
   const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
   const int c = 4 * t + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-  return (uint32_t)(r * Tile<D>::kRowBytes + ((c ^ swz(r)) << 4) + 8 * (lane & 1));
+  return (uint32_t)(r * Tile<D>::kRowBytes + ((c ^ Tile<D>::swz(r)) << 4) + 8 * (lane & 1));
 }
-// A operand [columns 32t..+31][rows r0..r0+15] of a tile, base = tr_addr
+// the two addresses of an A operand [columns 32t..+31][16 rows]: rows
+// 4(l/32) + 0..3 and the same 8 rows further on
+struct TrAddr {
+  uint32_t near, far;
+};
 template <int D>
-__device__ __forceinline__ v8bf tr_operand(const lds_char* tile, uint32_t base, int r0) {
-  return join(lds_read_tr(tile + base + r0 * Tile<D>::kRowBytes),
-              lds_read_tr(tile + base + (r0 + 8) * Tile<D>::kRowBytes));
+__device__ __forceinline__ TrAddr tr_addrs(int lane, int t, uint32_t base) {
+  const uint32_t a = tr_addr<D>(lane, t);
+  return TrAddr{base + a, base + (a ^ Tile<D>::kFar) + 8 * Tile<D>::kRowBytes};
+}
+template <int D>
+__device__ __forceinline__ v8bf tr_operand(const lds_char* tile, TrAddr a, int r0) {
+  return join(lds_read_tr(tile + a.near + r0 * Tile<D>::kRowBytes), lds_read_tr(tile + a.far + r0 * Tile<D>::kRowBytes));
 }
 
 // ---------------------------------------------------------------------
@@ -236,19 +248,25 @@ __device__ __forceinline__ Item find_item(const int32_t* cu, int batch, int64_t 
   return Item{-1, 0};
 }
 
-// Workgroup id -> (item rank, head).  Consecutive workgroups go to
-// different XCDs; the heads that share a key/value head take consecutive
-// places on one XCD, so their reads of K and V meet in its L2.
+// Workgroup id -> (item rank, head) for `pairs` key/value heads and `per`
+// workgroups of each.  Consecutive workgroups go to different XCDs, whose L2
+// caches are separate.  Eight ranks at a time are dealt so that an XCD's
+// workgroups have the fewest possible key/value heads among them (8 * pairs
+// (head, rank) pairs in that order, `pairs` to each XCD): they read the same
+// rows at about the same time, and those reads meet in its L2.  Odd blocks
+// of ranks run backwards, so no XCD always has the longer items.
 struct Place {
-  int rank, head;
+  int rank, pair, part;
 };
-__device__ __forceinline__ Place place_of(int id, int hq, int hkv) {
-  const int group = hq / hkv, slot = id >> 3;
-  const int pair = (slot / group) * 8 + (id & 7);
-  return Place{pair / hkv, (pair % hkv) * group + slot % group};
+__device__ __forceinline__ Place place_of(int id, int pairs, int per) {
+  const int xcd = id & 7, slot = id >> 3;
+  const int s = slot / per, block = s / pairs;
+  const int at = xcd * pairs + (s - block * pairs);
+  const int r = at & 7;
+  return Place{block * 8 + (block & 1 ? 7 - r : r), at >> 3, slot - s * per};
 }
-inline int64_t placed_blocks(int64_t items, int64_t hq, int64_t hkv) {
-  return (items * hkv + 7) / 8 * 8 * (hq / hkv);
+inline int64_t placed_blocks(int64_t items, int64_t pairs, int64_t per) {
+  return (items + 7) / 8 * 8 * pairs * per;
 }
 
 }  // namespace bl

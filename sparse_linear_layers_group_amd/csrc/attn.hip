@@ -12,7 +12,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kQRows = 128;  // query rows of a forward / dQ workgroup: 32 per wavefront
 constexpr int kKRows = 64;   // key rows of a tile in LDS
 constexpr int kExactTiles = 4;  // dQ workgroups with at most this many key tiles form delta from P dP
-constexpr int kBRows = 128;  // key rows of a dK / dV workgroup: 32 per wavefront
+constexpr int kBKeys = 64;   // key rows of a dK / dV workgroup: two blocks of 32, four wavefronts each
+constexpr int kBRows = 128;  // query rows of its stages: 32 per wavefront
+constexpr int kMaxSplits = 8;
 constexpr float kInf = __builtin_huge_valf();
 }  // namespace
 
@@ -20,9 +22,9 @@ constexpr float kInf = __builtin_huge_valf();
 // then sees that reads of one stage and DMA into the other touch different
 // objects and does not wait for the DMA in flight.
 template <int D>
-struct PairBytes {  // two tiles of 64 rows, then 2 x 64 binary32 row values
+struct PairBytes {  // two tiles of 64 rows
   static constexpr int kTile = kKRows * 2 * D;
-  static constexpr int kAll = 2 * kTile + 512;
+  static constexpr int kAll = 2 * kTile;
 };
 __shared__ __attribute__((aligned(1024))) char g_a128_st0[PairBytes<128>::kAll];
 __shared__ __attribute__((aligned(1024))) char g_a128_st1[PairBytes<128>::kAll];
@@ -35,14 +37,42 @@ __device__ __forceinline__ lds_char* pair_stage() {
   else return (lds_char*)(P == 0 ? g_a64_st0 : g_a64_st1);
 }
 
-// DMA of 64 rows of two row-major arrays into a stage: wavefront w takes
+// stages of the dK / dV kernel: 128 rows of Q and dO, their lse and delta
+template <int D>
+struct WideBytes {
+  static constexpr int kTile = kBRows * 2 * D;
+  static constexpr int kAll = 2 * kTile + 2 * 4 * kBRows;
+};
+__shared__ __attribute__((aligned(1024))) char g_w128_st0[WideBytes<128>::kAll];
+__shared__ __attribute__((aligned(1024))) char g_w128_st1[WideBytes<128>::kAll];
+__shared__ __attribute__((aligned(1024))) char g_w64_st0[WideBytes<64>::kAll];
+__shared__ __attribute__((aligned(1024))) char g_w64_st1[WideBytes<64>::kAll];
+template <int D, int P>
+__device__ __forceinline__ lds_char* wide_stage() {
+  if constexpr (D == 128) return (lds_char*)(P == 0 ? g_w128_st0 : g_w128_st1);
+  else return (lds_char*)(P == 0 ? g_w64_st0 : g_w64_st1);
+}
+
+// the dK / dV kernel's rows of V, and the operands of K that are not kept in
+// registers: two of D = 128's eight for both blocks of 32 keys
+__shared__ __attribute__((aligned(1024))) char g_v128[kBKeys * 2 * 128];
+__shared__ __attribute__((aligned(1024))) char g_v64[kBKeys * 2 * 64];
+__shared__ __attribute__((aligned(1024))) char g_k128[2 * 2 * 1024];
+template <int D>
+__device__ __forceinline__ lds_char* v_rows() {
+  if constexpr (D == 128) return (lds_char*)g_v128;
+  else return (lds_char*)g_v64;
+}
+
+// DMA of R rows of two row-major arrays into a stage: wavefront w takes
 // kDma consecutive instructions of each.  Rows past `rows` read zeros (the
 // buffer ends there), so what lies behind a sequence, whatever it holds,
 // never reaches a product.
-template <int D>
+template <int D, int R = kKRows, int W = 4>
 struct PairDma {
   typedef Tile<D> T;
-  static constexpr int kDma = kKRows / T::kDmaRows / 4;
+  static constexpr int kDma = R / T::kDmaRows / W;  // instructions of each array and wavefront
+  static_assert(kDma % T::kVariants == 0 || T::kVariants % kDma == 0, "compile-time permutations");
   uint32_t off_a[kDma], off_b[kDma];
   int wave;
   int64_t stride_a, stride_b;
@@ -56,13 +86,13 @@ struct PairDma {
   }
   // a, b: first row's elements; rows >= 1 of them are the sequence's
   __device__ __forceinline__ void issue(lds_char* st, const uint16_t* a, const uint16_t* b, int rows) const {
-    const int n = rows < kKRows ? rows : kKRows;
+    const int n = rows < R ? rows : R;
     const __amdgpu_buffer_rsrc_t ra = rows_rsrc(a, (uint32_t)((n - 1) * (int)stride_a * 2 + 2 * D));
     const __amdgpu_buffer_rsrc_t rb = rows_rsrc(b, (uint32_t)((n - 1) * (int)stride_b * 2 + 2 * D));
 #pragma unroll
     for (int i = 0; i < kDma; ++i) lds_load16(ra, st + 1024 * (wave * kDma + i), off_a[i]);
 #pragma unroll
-    for (int i = 0; i < kDma; ++i) lds_load16(rb, st + PairBytes<D>::kTile + 1024 * (wave * kDma + i), off_b[i]);
+    for (int i = 0; i < kDma; ++i) lds_load16(rb, st + R * T::kRowBytes + 1024 * (wave * kDma + i), off_b[i]);
   }
 };
 
@@ -122,11 +152,12 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
   constexpr int kTile = PairBytes<D>::kTile;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Place pl = place_of(blockIdx.x, a.hq, a.hkv);
+  const int group = a.hq / a.hkv;
+  const Place pl = place_of(blockIdx.x, a.hkv, group);
   const Item it = find_item(a.cu_q, a.batch, a.total_q, kQRows, pl.rank);
   const int seq = __builtin_amdgcn_readfirstlane(it.seq);
   if (seq < 0) return;
-  const int head = pl.head, kvh = head / (a.hq / a.hkv);
+  const int kvh = pl.pair, head = kvh * group + pl.part;
   const Rows qr = seq_rows(a.cu_q, seq, a.total_q), kr = seq_rows(a.cu_k, seq, a.total_k);
   const int q0 = __builtin_amdgcn_readfirstlane(it.level) * kQRows;
   const int off = kr.len - qr.len;
@@ -143,11 +174,12 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
   const PairDma<D> dma(lane, wave, a.k_stride, a.v_stride);
   const uint16_t* kp = a.K + (int64_t)kr.start * a.k_stride + (int64_t)kvh * D;
   const uint16_t* vp = a.V + (int64_t)kr.start * a.v_stride + (int64_t)kvh * D;
-  uint32_t ka[D / 16], va[D / 32];
+  uint32_t ka[D / 16];
+  TrAddr va[D / 32];
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) ka[s] = a_addr<D>(lane, s);
 #pragma unroll
-  for (int t = 0; t < D / 32; ++t) va[t] = kTile + tr_addr<D>(lane, t);
+  for (int t = 0; t < D / 32; ++t) va[t] = tr_addrs<D>(lane, t, kTile);
 
   const float sl = a.scale * kLog2e;
   const int seen = r + off - 4 * (lane >> 5);  // last visible key, minus this lane's row offset
@@ -246,13 +278,15 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
 // delta = sum P dP in binary32 in a sweep of their own and leave it in
 // memory for the dK / dV pass.
 
-// delta and lse * log2 e (+inf where a row sees no key, so P becomes 0), and
-// dO rounded to bf16 where it comes in binary32
+// What the two passes add to their products: -lse / scale to S (-inf where a
+// row sees no key, so P becomes 0) and -delta to dP, as the accumulators'
+// first values; and dO rounded to bf16 where it comes in binary32.
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void attn_delta_kernel(const uint16_t* __restrict__ O, const void* __restrict__ dO,
                                                         const float* __restrict__ lse, int64_t rows, int hq,
-                                                        int64_t total_q, float* __restrict__ delta,
-                                                        float* __restrict__ lse2, uint16_t* __restrict__ dOb) {
+                                                        int64_t total_q, float scale,
+                                                        float* __restrict__ ndelta, float* __restrict__ shift,
+                                                        uint16_t* __restrict__ dOb) {
   constexpr int kLanes = D / 8;
   const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;  // (token, head)
   const int c = threadIdx.x % kLanes;
@@ -275,24 +309,25 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(const uint16_t* __restr
   if (c == 0) {
     const int64_t t = row / hq, at = (row - t * hq) * total_q + t;
     const float e = ld_global(lse + at);
-    st_global(delta + at, s);
-    st_global(lse2 + at, e == -kInf ? kInf : e * kLog2e);
+    st_global(ndelta + at, -s);
+    st_global(shift + at, e == -kInf ? -kInf : -e / scale);
   }
 }
 
 template <int D>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const uint16_t* __restrict__ dO,
-                                                        float* __restrict__ delta,
-                                                        const float* __restrict__ lse2) {
+                                                        float* __restrict__ ndelta,
+                                                        const float* __restrict__ shift) {
   typedef Tile<D> T;
   constexpr int kTile = PairBytes<D>::kTile;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Place pl = place_of(blockIdx.x, a.hq, a.hkv);
+  const int group = a.hq / a.hkv;
+  const Place pl = place_of(blockIdx.x, a.hkv, group);
   const Item it = find_item(a.cu_q, a.batch, a.total_q, kQRows, pl.rank);
   const int seq = __builtin_amdgcn_readfirstlane(it.seq);
   if (seq < 0) return;
-  const int head = pl.head, kvh = head / (a.hq / a.hkv);
+  const int kvh = pl.pair, head = kvh * group + pl.part;
   const Rows qr = seq_rows(a.cu_q, seq, a.total_q), kr = seq_rows(a.cu_k, seq, a.total_k);
   const int q0 = __builtin_amdgcn_readfirstlane(it.level) * kQRows;
   const int off = kr.len - qr.len;
@@ -307,16 +342,17 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const ui
   v8bf qf[D / 16], gf[D / 16];
   load_row_operand<D>(qf, a.Q + row * a.q_stride + (int64_t)head * D, lane, in);
   load_row_operand<D>(gf, dO + (row * a.hq + head) * D, lane, in);
-  float dl = in ? ld_global(delta + (int64_t)head * a.total_q + row) : 0.f;
-  const float le = in ? ld_global(lse2 + (int64_t)head * a.total_q + row) : kInf;
+  float nd = in ? ld_global(ndelta + (int64_t)head * a.total_q + row) : 0.f;
+  const float le = (in ? ld_global(shift + (int64_t)head * a.total_q + row) : -kInf) * (a.scale * kLog2e);
   const PairDma<D> dma(lane, wave, a.k_stride, a.v_stride);
   const uint16_t* kp = a.K + (int64_t)kr.start * a.k_stride + (int64_t)kvh * D;
   const uint16_t* vp = a.V + (int64_t)kr.start * a.v_stride + (int64_t)kvh * D;
-  uint32_t ka[D / 16], kt[D / 32];
+  uint32_t ka[D / 16];
+  TrAddr kt[D / 32];
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) ka[s] = a_addr<D>(lane, s);
 #pragma unroll
-  for (int t = 0; t < D / 32; ++t) kt[t] = tr_addr<D>(lane, t);
+  for (int t = 0; t < D / 32; ++t) kt[t] = tr_addrs<D>(lane, t, 0);
   const float sl = a.scale * kLog2e;
   const int seen = r + off - 4 * (lane >> 5);
   v16f dq[D / 32];
@@ -345,7 +381,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const ui
         g[0] = mfma32(lds_read8(st + kTile + ka[k] + i * 32 * T::kRowBytes), gf[k], g[0]);
       }
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s[0][j] = exp2_hw(fmaf(s[0][j], sl, -le));
+      for (int j = 0; j < 16; ++j) s[0][j] = exp2_hw(fmaf(s[0][j], sl, le));
       if (diagonal) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) s[0][j] = 32 * i + 8 * (j >> 2) + (j & 3) <= x ? s[0][j] : 0.f;
@@ -355,7 +391,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const ui
         for (int j = 0; j < 16; ++j) exact = fmaf(s[0][j], g[0][j], exact);
       } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) s[0][j] *= g[0][j] - dl;
+        for (int j = 0; j < 16; ++j) s[0][j] *= g[0][j] + nd;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const v8bf p = operand_of(s[0], k);
@@ -378,131 +414,270 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const ui
   };
   if (tiles <= kExactTiles) {
     sweep(std::true_type{});
-    dl = half_join(exact, [](float u, float v) { return u + v; });
-    if (in && lane < 32) st_global(delta + (int64_t)head * a.total_q + row, dl);
+    nd = -half_join(exact, [](float u, float v) { return u + v; });
+    if (in && lane < 32) st_global(ndelta + (int64_t)head * a.total_q + row, nd);
     lds_barrier();  // both stages are free for the second sweep
   }
   sweep(std::false_type{});
   store_row<D>(a.dQ + (row * a.hq + head) * D, dq, a.scale, lane, in);
 }
 
-// dK and dV of 128 keys.  Lanes run over keys here: S = Q K^T has a key per
+// dK and dV of 64 keys.  Lanes run over keys here: S = Q K^T has a key per
 // column, so P and dS are again B operands as they stand, of the products
-// over query rows; K and V stay in registers as operands, Q and dO stream
-// through LDS for all query heads of the group.
+// over query rows.  Q and dO stream through LDS in stages of 128 rows, for
+// all query heads of the group; K stays in registers, V in LDS (with V in
+// registers too a wavefront needs more than half of them, and one per SIMD
+// has nothing to run while it waits).  Of the eight wavefronts four share a
+// block of 32 keys, each with 32 rows of the stage; their sums meet through
+// LDS at the end.  (128 keys a workgroup read each stage for twice the keys,
+// but make half as many workgroups, each twice as long: with 8192 tokens in
+// four sequences and 5 key/value heads the longest was 2.3 times the average
+// load of a CU.)
+//
+// `splits` workgroups share a tile where there are few: each takes a part of
+// the (stage, head) steps and leaves binary32 sums in `part`
+// ([split][dK, dV][total_k][hkv][D]), which attn_dkv_join_kernel adds in
+// order.
 template <int D>
-__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnBwdArgs a, const uint16_t* __restrict__ dO,
-                                                         const float* __restrict__ delta,
-                                                         const float* __restrict__ lse2) {
+__global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, const uint16_t* __restrict__ dO,
+                                                         const float* __restrict__ ndelta,
+                                                         const float* __restrict__ shift, int splits,
+                                                         float* __restrict__ part) {
   typedef Tile<D> T;
-  constexpr int kTile = PairBytes<D>::kTile;
+  constexpr int kTile = WideBytes<D>::kTile;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Place pl = place_of(blockIdx.x, a.hkv, a.hkv);
-  const Item it = find_item(a.cu_k, a.batch, a.total_k, kBRows, pl.rank);
+  const int kw = wave & 1, rq = wave >> 1;
+  const Place pl = place_of(blockIdx.x, a.hkv, splits);
+  const Item it = find_item(a.cu_k, a.batch, a.total_k, kBKeys, pl.rank);
   const int seq = __builtin_amdgcn_readfirstlane(it.seq);
   if (seq < 0) return;
-  const int kvh = pl.head, group = a.hq / a.hkv;
+  const int kvh = pl.pair, split = pl.part, group = a.hq / a.hkv;
   const Rows qr = seq_rows(a.cu_q, seq, a.total_q), kr = seq_rows(a.cu_k, seq, a.total_k);
   // the first keys are seen by the most rows: highest level first
-  const int k0 = ((kr.len + kBRows - 1) / kBRows - 1 - __builtin_amdgcn_readfirstlane(it.level)) * kBRows;
+  const int k0 = ((kr.len + kBKeys - 1) / kBKeys - 1 - __builtin_amdgcn_readfirstlane(it.level)) * kBKeys;
   const int off = kr.len - qr.len;
-  const int w0 = k0 + 32 * wave, j = w0 + (lane & 31);
+  const int w0 = k0 + 32 * kw, j = w0 + (lane & 31);
   const bool in = j < kr.len;
-  const int first = (k0 - off > 0 ? k0 - off : 0) / kKRows;  // first row tile that sees a key of this workgroup
-  const int n = (qr.len + kKRows - 1) / kKRows - first;      // row tiles per head
+  const int first = (k0 - off > 0 ? k0 - off : 0) / kBRows;  // first stage with a row that sees a key of these
+  const int n = (qr.len + kBRows - 1) / kBRows - first;      // stages per head
   const int steps = n > 0 ? n * group : 0;
+  const int i0 = (int)((int64_t)steps * split / splits), i1 = (int)((int64_t)steps * (split + 1) / splits);
 
-  v8bf kf[D / 16], vf[D / 16];
-  load_row_operand<D>(kf, a.K + (int64_t)(kr.start + j) * a.k_stride + (int64_t)kvh * D, lane, in);
-  load_row_operand<D>(vf, a.V + (int64_t)(kr.start + j) * a.v_stride + (int64_t)kvh * D, lane, in);
+  {  // V rows k0 .. k0 + 63
+    constexpr int kDma = kBKeys / T::kDmaRows / 8;
+    const int rows = kr.len - k0 < kBKeys ? kr.len - k0 : kBKeys;
+    const __amdgpu_buffer_rsrc_t r = rows_rsrc(a.V + (int64_t)(kr.start + k0) * a.v_stride + (int64_t)kvh * D,
+                                               (uint32_t)((rows - 1) * (int)a.v_stride * 2 + 2 * D));
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) {
+      const int ins = wave * kDma + i;
+      lds_load16(r, v_rows<D>() + 1024 * ins,
+                 dma_offset<D>(lane, ins % T::kVariants, a.v_stride) + (uint32_t)(ins * T::kDmaRows * (int)a.v_stride * 2));
+    }
+  }
+  constexpr int kHeld = D == 128 ? 6 : 4;  // (all eight: 256 registers and spills)
+  typedef __attribute__((address_space(3))) v8bf lds_v8bf;
+  lds_char* const kx = (lds_char*)g_k128 + 2048 * kw + 16 * lane;
+  v8bf kf[kHeld];
+  {
+    v8bf k[D / 16];
+    load_row_operand<D>(k, a.K + (int64_t)(kr.start + j) * a.k_stride + (int64_t)kvh * D, lane, in);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) kf[i] = k[i];
+    if constexpr (kHeld < D / 16) {
+      if (rq == 0) {
+#pragma unroll
+        for (int i = kHeld; i < D / 16; ++i) *reinterpret_cast<lds_v8bf*>(kx + 1024 * (i - kHeld)) = k[i];
+      }
+    }
+  }
   const int64_t g_stride = (int64_t)a.hq * D;
-  const PairDma<D> dma(lane, wave, a.q_stride, g_stride);
-  uint32_t qa[D / 16], qt[D / 32];
-#pragma unroll
-  for (int s = 0; s < D / 16; ++s) qa[s] = a_addr<D>(lane, s);
-#pragma unroll
-  for (int t = 0; t < D / 32; ++t) qt[t] = tr_addr<D>(lane, t);
+  const PairDma<D, kBRows, 8> dma(lane, wave, a.q_stride, g_stride);
+  // LDS addresses: pieces 2s and columns 32t are address bits of their own
+  // (5.. and 6..), so one exclusive or makes each from the first.  They are
+  // made again in every step: kept, they would cost 13 registers.
+  uint32_t qa = a_addr<D>(lane, 0);
+  TrAddr qt = tr_addrs<D>(lane, 0, 32 * rq * T::kRowBytes);
+  const lds_char* const vr = v_rows<D>() + 32 * kw * T::kRowBytes;
   const float sl = a.scale * kLog2e;
   v16f dk[D / 32], dv[D / 32];
   clear<D / 32>(dk);
   clear<D / 32>(dv);
 
   auto issue = [&](lds_char* st, int h, int t) {
-    const int64_t row = qr.start + t * kKRows;
-    const int rows = qr.len - t * kKRows;
+    const int64_t row = qr.start + t * kBRows;
+    const int rows = qr.len - t * kBRows;
     const int64_t head = (int64_t)kvh * group + h;
     dma.issue(st, a.Q + row * a.q_stride + head * D, dO + row * g_stride + head * D, rows);
-    if (wave < 2) {  // the rows' lse (wavefront 0) and delta (wavefront 1); zeros past the sequence
-      const float* p = (wave ? delta : lse2) + head * a.total_q + row;
-      lds_load4(rows_rsrc(p, (uint32_t)((rows < kKRows ? rows : kKRows) * 4)), st + 2 * kTile + 256 * wave,
-                (uint32_t)lane * 4);
+    if (rq < 2) {  // the rows' first values, 64 rows a wavefront; zeros past the sequence (dO is 0 there)
+      const float* p = (rq ? ndelta : shift) + head * a.total_q + row;
+      lds_load4(rows_rsrc(p, (uint32_t)((rows < kBRows ? rows : kBRows) * 4)),
+                st + 2 * kTile + 4 * kBRows * rq + 256 * kw, (uint32_t)(lane + 64 * kw) * 4);
     }
   };
-  int h = 0, t = first;  // of the step being computed
+  // The last rows first, all heads of the group for each stage: workgroups of
+  // different keys that start together then read the same stages together.
+  int t = first + n - 1 - i0 / group, h = i0 % group;  // of the step being computed
   auto step = [&](auto stage, int i) {
     constexpr int P = decltype(stage)::value;
     wait_dma<0>();
     lds_barrier();
-    const int nt = t + 1 < first + n ? t + 1 : first, nh = t + 1 < first + n ? h : h + 1;
-    if (i + 1 < steps) issue(pair_stage<D, P ^ 1>(), nh, nt);
-    const lds_char* st = pair_stage<D, P>();
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int r0 = t * kKRows + 32 * q;  // rows r0 .. r0 + 31
-      if (r0 + 31 + off < w0) continue;    // none of them sees a key of this wavefront
-      v16f s[1], g[1];
-      clear<1>(s);
-      clear<1>(g);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        s[0] = mfma32(lds_read8(st + qa[k] + q * 32 * T::kRowBytes), kf[k], s[0]);
-        g[0] = mfma32(lds_read8(st + kTile + qa[k] + q * 32 * T::kRowBytes), vf[k], g[0]);
-      }
-      v4f le[4], dl[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const lds_char* p = st + 2 * kTile + (32 * q + 8 * u + 4 * (lane >> 5)) * 4;
-        le[u] = *reinterpret_cast<const __attribute__((address_space(3))) v4f*>(p);
-        dl[u] = *reinterpret_cast<const __attribute__((address_space(3))) v4f*>(p + 256);
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[0][e] = exp2_hw(fmaf(s[0][e], sl, -le[e >> 2][e & 3]));
-      if (r0 + off < w0 + 31) {  // the diagonal
-        const int x = j - off - r0 - 4 * (lane >> 5);  // first row that sees this lane's key
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[0][e] = 8 * (e >> 2) + (e & 3) >= x ? s[0][e] : 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const v8bf p = operand_of(s[0], k);
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d)
-          dv[d] = mfma32(tr_operand<D>(st + kTile, qt[d], 32 * q + 16 * k), p, dv[d]);
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[0][e] *= g[0][e] - dl[e >> 2][e & 3];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const v8bf p = operand_of(s[0], k);
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d) dk[d] = mfma32(tr_operand<D>(st, qt[d], 32 * q + 16 * k), p, dk[d]);
-      }
-    }
+    const int nh = h + 1 < group ? h + 1 : 0, nt = nh ? t : t - 1;
+    if (i + 1 < i1) issue(wide_stage<D, P ^ 1>(), nh, nt);
+    const lds_char* st = wide_stage<D, P>();
+    const int r0 = t * kBRows + 32 * rq;  // this wavefront's rows r0 .. r0 + 31
     t = nt;
     h = nh;
+    if (r0 + 31 + off < w0 || r0 >= qr.len) return;  // none of them sees a key of these
+    const lds_char* const sq = st + 32 * rq * T::kRowBytes;
+    asm volatile("" : "+v"(qa), "+v"(qt.near), "+v"(qt.far));
+    v16f s, g;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const lds_char* p = st + 2 * kTile + (32 * rq + 8 * u + 4 * (lane >> 5)) * 4;
+      const v4f x = *reinterpret_cast<const __attribute__((address_space(3))) v4f*>(p);
+      const v4f y = *reinterpret_cast<const __attribute__((address_space(3))) v4f*>(p + 4 * kBRows);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[4 * u + e] = x[e];
+        g[4 * u + e] = y[e];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      s = mfma32(lds_read8(sq + (qa ^ (32 * k))), k < kHeld ? kf[k % kHeld] : lds_read8(kx + 1024 * (k - kHeld)), s);
+      g = mfma32(lds_read8(sq + kTile + (qa ^ (32 * k))), lds_read8(vr + (qa ^ (32 * k))), g);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = exp2_hw(s[e] * sl);
+    if (r0 + off < w0 + 31) {  // the diagonal
+      const int x = j - off - r0 - 4 * (lane >> 5);  // first row that sees this lane's key
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = 8 * (e >> 2) + (e & 3) >= x ? s[e] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const v8bf p = operand_of(s, k);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+        dv[d] = mfma32(tr_operand<D>(st + kTile, TrAddr{qt.near ^ (64 * d), qt.far ^ (64 * d)}, 16 * k), p, dv[d]);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] *= g[e];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const v8bf p = operand_of(s, k);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+        dk[d] = mfma32(tr_operand<D>(st, TrAddr{qt.near ^ (64 * d), qt.far ^ (64 * d)}, 16 * k), p, dk[d]);
+    }
   };
 
-  if (steps > 0) issue(pair_stage<D, 0>(), 0, first);
-  int i = 0;
-  for (; i + 1 < steps; i += 2) {
+  if (i0 < i1) issue(wide_stage<D, 0>(), h, t);
+  int i = i0;
+  for (; i + 1 < i1; i += 2) {
     step(std::integral_constant<int, 0>{}, i);
     step(std::integral_constant<int, 1>{}, i + 1);
   }
-  if (i < steps) step(std::integral_constant<int, 0>{}, i);
+  if (i < i1) step(std::integral_constant<int, 0>{}, i);
+
+  // Join the four wavefronts of a block, ((0 + 2) + (1 + 3)): quarters 2 and 3
+  // leave their sums for 0 and 1, then 0 takes dK and 1 dV from the other.
+  // A box holds D/32 accumulators, 16 bytes per lane and quad of registers.
+  typedef __attribute__((address_space(3))) v4f lds_v4f;
+  constexpr int kBox = D / 32 * 4096;
+  auto box = [&](int at) {  // eight of them, four to a stage
+    return (at < 4 ? wide_stage<D, 0>() : wide_stage<D, 1>()) + kBox * (at & 3);
+  };
+  auto leave = [&](lds_char* to, const v16f* x) {
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<lds_v4f*>(to + 1024 * (4 * d + q) + 16 * lane) =
+            v4f{x[d][4 * q], x[d][4 * q + 1], x[d][4 * q + 2], x[d][4 * q + 3]};
+  };
+  auto add = [&](const lds_char* from, v16f* x) {
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const v4f z = *reinterpret_cast<const lds_v4f*>(from + 1024 * (4 * d + q) + 16 * lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[d][4 * q + e] += z[e];
+      }
+  };
   const int64_t out = ((int64_t)(kr.start + j) * a.hkv + kvh) * D;
-  store_row<D>(a.dK + out, dk, a.scale, lane, in);
-  store_row<D>(a.dV + out, dv, 1.f, lane, in);
+  auto finish = [&](const v16f* x, uint16_t* y, float mul) {
+    if (splits == 1) {
+      store_row<D>(y + out, x, mul, lane, in);
+    } else if (in) {
+      float* p = part + (int64_t)(2 * split + rq) * a.total_k * a.hkv * D + out;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          st_global(reinterpret_cast<v4f*>(p + 32 * d + 8 * q + 4 * (lane >> 5)),
+                    v4f{x[d][4 * q], x[d][4 * q + 1], x[d][4 * q + 2], x[d][4 * q + 3]});
+    }
+  };
+  __syncthreads();  // the stages are free (and no DMA is in flight)
+  if (rq >= 2) {
+    leave(box(2 * (rq - 2) + kw), dk);
+    leave(box(4 + 2 * (rq - 2) + kw), dv);
+  }
+  __syncthreads();
+  if (rq < 2) {
+    add(box(2 * rq + kw), dk);
+    add(box(4 + 2 * rq + kw), dv);
+  }
+  __syncthreads();
+  if (rq == 0) leave(box(kw), dv);
+  if (rq == 1) leave(box(2 + kw), dk);
+  __syncthreads();
+  if (rq == 0) {
+    add(box(2 + kw), dk);
+    finish(dk, a.dK, a.scale);
+  } else if (rq == 1) {
+    add(box(kw), dv);
+    finish(dv, a.dV, 1.f);
+  }
+}
+
+// dK and dV of split tiles: the splits' sums in order, 8 elements a thread
+template <int D>
+__global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnBwdArgs a, int splits,
+                                                           const float* __restrict__ part) {
+  constexpr int kParts = 2 * kBKeys * (D / 8) / 256;  // workgroups of a tile
+  const int tile = blockIdx.x / kParts, which = blockIdx.x % kParts / (kParts / 2);
+  const Item it = find_item(a.cu_k, a.batch, a.total_k, kBKeys, tile / a.hkv);
+  if (it.seq < 0) return;
+  const Rows kr = seq_rows(a.cu_k, it.seq, a.total_k);
+  const int f = blockIdx.x % (kParts / 2) * 256 + threadIdx.x;
+  const int row = it.level * kBKeys + f / (D / 8);
+  if (row >= kr.len) return;
+  const int64_t plane = a.total_k * a.hkv * D;
+  const int64_t at = ((int64_t)(kr.start + row) * a.hkv + tile % a.hkv) * D + 8 * (f % (D / 8));
+  v4f u[kMaxSplits], v[kMaxSplits];
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) {
+    const v4f* p = reinterpret_cast<const v4f*>(part + (2 * (s < splits ? s : 0) + which) * plane + at);
+    u[s] = ld_global(p);
+    v[s] = ld_global(p + 1);
+  }
+  v4f x = u[0], y = v[0];
+#pragma unroll
+  for (int s = 1; s < kMaxSplits; ++s)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] += s < splits ? u[s][i] : 0.f;
+      y[i] += s < splits ? v[s][i] : 0.f;
+    }
+  const float mul = which ? 1.f : a.scale;
+  st_global(reinterpret_cast<u32x4*>((which ? a.dV : a.dK) + at),
+            u32x4{pk_bf16(x[0] * mul, x[1] * mul), pk_bf16(x[2] * mul, x[3] * mul),
+                  pk_bf16(y[0] * mul, y[1] * mul), pk_bf16(y[2] * mul, y[3] * mul)});
 }
 
 // ------------------------------------------------------------------- host
@@ -518,15 +693,29 @@ size_t bwd_row_bytes(int64_t total_q, int64_t hq) { return align256((size_t)tota
 size_t attn_fwd_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
 
 hipError_t launch_attn_fwd(const AttnArgs& a, int64_t d, void*, hipStream_t s) {
-  const unsigned blocks = (unsigned)placed_blocks(most_tiles(a.total_q, a.batch, kQRows), a.hq, a.hkv);
+  const unsigned blocks = (unsigned)placed_blocks(most_tiles(a.total_q, a.batch, kQRows), a.hkv, a.hq / a.hkv);
   if (d == 128) attn_fwd_kernel<128><<<dim3(blocks), 256, 0, s>>>(a);
   else attn_fwd_kernel<64><<<dim3(blocks), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
-// workspace: delta, lse * log2 e ([hq][total_q] each), dO in bf16
-size_t attn_bwd_ws_bytes(int64_t, int64_t total_q, int64_t, int64_t hq, int64_t, int64_t d) {
-  return 2 * bwd_row_bytes(total_q, hq) + align256((size_t)total_q * hq * d * 2);
+// Workgroups that share a dK / dV tile: enough that every CU has one
+// (D = 64: two), by the number of whole tiles the totals make.
+static int dkv_splits(int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d) {
+  const int64_t tiles = (total_k + kBKeys - 1) / kBKeys * hkv, want = d == 128 ? 256 : 512;
+  const int64_t steps = hq / hkv * ((total_q + kBRows - 1) / kBRows);
+  int64_t s = tiles > 0 ? want / tiles : 1;
+  s = s > kMaxSplits ? kMaxSplits : s;
+  s = s > steps ? steps : s;
+  return s < 1 ? 1 : (int)s;
+}
+
+// workspace: delta, lse * log2 e ([hq][total_q] each), dO in bf16, partial
+// dK and dV of split tiles
+size_t attn_bwd_ws_bytes(int64_t, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d) {
+  const int splits = dkv_splits(total_q, total_k, hq, hkv, d);
+  return 2 * bwd_row_bytes(total_q, hq) + align256((size_t)total_q * hq * d * 2) +
+         (splits > 1 ? (size_t)splits * 2 * total_k * hkv * d * 4 : 0);
 }
 
 template <int D>
@@ -535,24 +724,34 @@ static hipError_t bwd_launch(const AttnBwdArgs& a, hipStream_t s) {
   float* delta = reinterpret_cast<float*>(ws);
   float* lse2 = reinterpret_cast<float*>(ws + bwd_row_bytes(a.total_q, a.hq));
   uint16_t* copy = reinterpret_cast<uint16_t*>(ws + 2 * bwd_row_bytes(a.total_q, a.hq));
+  float* part = reinterpret_cast<float*>(ws + 2 * bwd_row_bytes(a.total_q, a.hq) +
+                                         align256((size_t)a.total_q * a.hq * D * 2));
   const uint16_t* dO = a.do_f32 ? copy : static_cast<const uint16_t*>(a.dO);
   if (a.total_q > 0) {
     const int64_t rows = a.total_q * a.hq;
     const dim3 grid((unsigned)((rows * (D / 8) + 255) / 256));
     if (a.do_f32)
-      attn_delta_kernel<D, true><<<grid, 256, 0, s>>>(a.O, a.dO, a.lse, rows, a.hq, a.total_q, delta, lse2, copy);
+      attn_delta_kernel<D, true><<<grid, 256, 0, s>>>(a.O, a.dO, a.lse, rows, a.hq, a.total_q, a.scale, delta, lse2,
+                                                        copy);
     else
-      attn_delta_kernel<D, false><<<grid, 256, 0, s>>>(a.O, a.dO, a.lse, rows, a.hq, a.total_q, delta, lse2, copy);
+      attn_delta_kernel<D, false><<<grid, 256, 0, s>>>(a.O, a.dO, a.lse, rows, a.hq, a.total_q, a.scale, delta, lse2,
+                                                        copy);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attn_dq_kernel<D><<<dim3((unsigned)placed_blocks(most_tiles(a.total_q, a.batch, kQRows), a.hq, a.hkv)), 256, 0, s>>>(
+    attn_dq_kernel<D><<<dim3((unsigned)placed_blocks(most_tiles(a.total_q, a.batch, kQRows), a.hkv, a.hq / a.hkv)), 256, 0, s>>>(
         a, dO, delta, lse2);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.total_k > 0)
-    attn_dkv_kernel<D><<<dim3((unsigned)placed_blocks(most_tiles(a.total_k, a.batch, kBRows), a.hkv, a.hkv)), 256, 0, s>>>(
-        a, dO, delta, lse2);
+  if (a.total_k > 0) {
+    const int splits = dkv_splits(a.total_q, a.total_k, a.hq, a.hkv, D);
+    const int64_t items = most_tiles(a.total_k, a.batch, kBKeys);
+    attn_dkv_kernel<D><<<dim3((unsigned)placed_blocks(items, a.hkv, splits)), 512, 0, s>>>(a, dO, delta, lse2,
+                                                                                       splits, part);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (splits > 1) attn_dkv_join_kernel<D><<<dim3((unsigned)(items * a.hkv * (2 * kBKeys * (D / 8) / 256))), 256, 0, s>>>(a, splits, part);
+  }
   return hipGetLastError();
 }
 hipError_t launch_attn_bwd(const AttnBwdArgs& a, int64_t d, hipStream_t s) {

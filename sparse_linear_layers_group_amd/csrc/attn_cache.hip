@@ -103,11 +103,12 @@ __global__ __launch_bounds__(256, D == 128 ? 1 : 2) void attn_cache_kernel(AttnC
 #pragma unroll
   for (int i = 0; i < kPerGranule; ++i)
     off[i] = dma_offset<D>(lane, i % T::kVariants, stride) + (uint32_t)(i * T::kDmaRows * stride * 2);
-  uint32_t ka[D / 16], va[D / 32];
+  uint32_t ka[D / 16];
+  TrAddr va[D / 32];
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) ka[s] = wave * C::kStage + a_addr<D>(lane, s);
 #pragma unroll
-  for (int t = 0; t < D / 32; ++t) va[t] = wave * C::kStage + C::kBytes + tr_addr<D>(lane, t);
+  for (int t = 0; t < D / 32; ++t) va[t] = tr_addrs<D>(lane, t, wave * C::kStage + C::kBytes);
   const float sl = a.scale * kLog2e;
   const int gpp = (int)(a.page / kGranule);
 
