@@ -36,6 +36,25 @@ __device__ __forceinline__ lds_char* pair_stage() {
   if constexpr (D == 128) return (lds_char*)(P == 0 ? g_a128_st0 : g_a128_st1);
   else return (lds_char*)(P == 0 ? g_a64_st0 : g_a64_st1);
 }
+// the forward's stages: tiles of K and of V apart
+__shared__ __attribute__((aligned(1024))) char g_f128_k0[PairBytes<128>::kTile];
+__shared__ __attribute__((aligned(1024))) char g_f128_k1[PairBytes<128>::kTile];
+__shared__ __attribute__((aligned(1024))) char g_f128_v0[PairBytes<128>::kTile];
+__shared__ __attribute__((aligned(1024))) char g_f128_v1[PairBytes<128>::kTile];
+__shared__ __attribute__((aligned(1024))) char g_f64_k0[PairBytes<64>::kTile];
+__shared__ __attribute__((aligned(1024))) char g_f64_k1[PairBytes<64>::kTile];
+__shared__ __attribute__((aligned(1024))) char g_f64_v0[PairBytes<64>::kTile];
+__shared__ __attribute__((aligned(1024))) char g_f64_v1[PairBytes<64>::kTile];
+template <int D, int P>
+__device__ __forceinline__ lds_char* k_stage() {
+  if constexpr (D == 128) return (lds_char*)(P == 0 ? g_f128_k0 : g_f128_k1);
+  else return (lds_char*)(P == 0 ? g_f64_k0 : g_f64_k1);
+}
+template <int D, int P>
+__device__ __forceinline__ lds_char* v_stage() {
+  if constexpr (D == 128) return (lds_char*)(P == 0 ? g_f128_v0 : g_f128_v1);
+  else return (lds_char*)(P == 0 ? g_f64_v0 : g_f64_v1);
+}
 
 // stages of the dK / dV kernel: 128 rows of Q and dO, their lse and delta
 template <int D>
@@ -64,35 +83,40 @@ __device__ __forceinline__ lds_char* v_rows() {
   else return (lds_char*)g_v64;
 }
 
-// DMA of R rows of two row-major arrays into a stage: wavefront w takes
-// kDma consecutive instructions of each.  Rows past `rows` read zeros (the
-// buffer ends there), so what lies behind a sequence, whatever it holds,
-// never reaches a product.
+// DMA of R rows of a row-major array into a tile: wavefront w takes kDma
+// consecutive instructions.  Rows past `rows` read zeros (the buffer ends
+// there), so what lies behind a sequence, whatever it holds, never reaches a
+// product.
 template <int D, int R = kKRows, int W = 4>
-struct PairDma {
+struct TileDma {
   typedef Tile<D> T;
-  static constexpr int kDma = R / T::kDmaRows / W;  // instructions of each array and wavefront
+  static constexpr int kDma = R / T::kDmaRows / W;
   static_assert(kDma % T::kVariants == 0 || T::kVariants % kDma == 0, "compile-time permutations");
-  uint32_t off_a[kDma], off_b[kDma];
+  uint32_t off[kDma];
   int wave;
-  int64_t stride_a, stride_b;
-  __device__ __forceinline__ PairDma(int lane, int w, int64_t sa, int64_t sb) : wave(w), stride_a(sa), stride_b(sb) {
+  int64_t stride;
+  __device__ __forceinline__ TileDma(int lane, int w, int64_t st) : wave(w), stride(st) {
 #pragma unroll
     for (int i = 0; i < kDma; ++i) {
       const int ins = w * kDma + i;
-      off_a[i] = dma_offset<D>(lane, ins % T::kVariants, sa) + (uint32_t)(ins * T::kDmaRows * (int)sa * 2);
-      off_b[i] = dma_offset<D>(lane, ins % T::kVariants, sb) + (uint32_t)(ins * T::kDmaRows * (int)sb * 2);
+      off[i] = dma_offset<D>(lane, ins % T::kVariants, st) + (uint32_t)(ins * T::kDmaRows * (int)st * 2);
     }
   }
-  // a, b: first row's elements; rows >= 1 of them are the sequence's
-  __device__ __forceinline__ void issue(lds_char* st, const uint16_t* a, const uint16_t* b, int rows) const {
+  // p: first row's elements; rows >= 1 of them are the sequence's
+  __device__ __forceinline__ void issue(lds_char* to, const uint16_t* p, int rows) const {
     const int n = rows < R ? rows : R;
-    const __amdgpu_buffer_rsrc_t ra = rows_rsrc(a, (uint32_t)((n - 1) * (int)stride_a * 2 + 2 * D));
-    const __amdgpu_buffer_rsrc_t rb = rows_rsrc(b, (uint32_t)((n - 1) * (int)stride_b * 2 + 2 * D));
+    const __amdgpu_buffer_rsrc_t r = rows_rsrc(p, (uint32_t)((n - 1) * (int)stride * 2 + 2 * D));
 #pragma unroll
-    for (int i = 0; i < kDma; ++i) lds_load16(ra, st + 1024 * (wave * kDma + i), off_a[i]);
-#pragma unroll
-    for (int i = 0; i < kDma; ++i) lds_load16(rb, st + R * T::kRowBytes + 1024 * (wave * kDma + i), off_b[i]);
+    for (int i = 0; i < kDma; ++i) lds_load16(r, to + 1024 * (wave * kDma + i), off[i]);
+  }
+};
+template <int D, int R = kKRows, int W = 4>
+struct PairDma {  // two arrays, one tile after the other
+  TileDma<D, R, W> a, b;
+  __device__ __forceinline__ PairDma(int lane, int w, int64_t sa, int64_t sb) : a(lane, w, sa), b(lane, w, sb) {}
+  __device__ __forceinline__ void issue(lds_char* st, const uint16_t* x, const uint16_t* y, int rows) const {
+    a.issue(st, x, rows);
+    b.issue(st + R * Tile<D>::kRowBytes, y, rows);
   }
 };
 
@@ -149,7 +173,6 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 template <int D>
 __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
   typedef Tile<D> T;
-  constexpr int kTile = PairBytes<D>::kTile;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.hq / a.hkv;
@@ -171,85 +194,169 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
 
   v8bf qf[D / 16];
   load_row_operand<D>(qf, a.Q + (int64_t)(qr.start + r) * a.q_stride + (int64_t)head * D, lane, in);
-  const PairDma<D> dma(lane, wave, a.k_stride, a.v_stride);
+  const TileDma<D> kd(lane, wave, a.k_stride), vd(lane, wave, a.v_stride);
   const uint16_t* kp = a.K + (int64_t)kr.start * a.k_stride + (int64_t)kvh * D;
   const uint16_t* vp = a.V + (int64_t)kr.start * a.v_stride + (int64_t)kvh * D;
-  uint32_t ka[D / 16];
-  TrAddr va[D / 32];
-#pragma unroll
-  for (int s = 0; s < D / 16; ++s) ka[s] = a_addr<D>(lane, s);
-#pragma unroll
-  for (int t = 0; t < D / 32; ++t) va[t] = tr_addrs<D>(lane, t, kTile);
+  // LDS addresses: pieces 2s and columns 32t are address bits of their own
+  // (5.. and 6..), so one exclusive or makes each from the first.  They are
+  // made again for every tile: kept, they would cost 13 registers.
+  uint32_t ka = a_addr<D>(lane, 0);
+  TrAddr va = tr_addrs<D>(lane, 0, 0);
 
   const float sl = a.scale * kLog2e;
   const int seen = r + off - 4 * (lane >> 5);  // last visible key, minus this lane's row offset
-  v16f o[D / 32];
+  v16f o[D / 32], s[2][2];  // s[t % 2]: the scores of tile t
   clear<D / 32>(o);
-  float m = -kInf, l = 0.f;
+  float m = -kInf, ms = 0.f, l = 0.f;  // ms: m scale log2 e, 0 while m is -inf
 
-  auto step = [&](auto stage, int t) {
-    constexpr int P = decltype(stage)::value;
-    wait_dma<0>();
-    lds_barrier();
-    if (t + 1 < tiles)
-      dma.issue(pair_stage<D, P ^ 1>(), kp + (int64_t)(t + 1) * kKRows * a.k_stride,
-                vp + (int64_t)(t + 1) * kKRows * a.v_stride, kr.len - (t + 1) * kKRows);
-    if (t >= wtiles) return;
-    const lds_char* st = pair_stage<D, P>();
-    v16f s[2];
-    clear<2>(s);
+  auto issue_k = [&](lds_char* to, int t) {
+    if (t < tiles) kd.issue(to, kp + (int64_t)t * kKRows * a.k_stride, kr.len - t * kKRows);
+  };
+  auto issue_v = [&](lds_char* to, int t) {
+    if (t < tiles) vd.issue(to, vp + (int64_t)t * kKRows * a.v_stride, kr.len - t * kKRows);
+  };
+  auto scores = [&](const lds_char* st, v16f* x) {
+    clear<2>(x);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) s[i] = mfma32(lds_read8(st + ka[k] + i * 32 * T::kRowBytes), qf[k], s[i]);
+      for (int i = 0; i < 2; ++i) x[i] = mfma32(lds_read8(st + (ka ^ (32 * k)) + i * 32 * T::kRowBytes), qf[k], x[i]);
+  };
+  auto mask = [&](v16f* x, int t) {
     if (t * kKRows + kKRows > w0 + off + 1) {  // the diagonal
-      const int x = seen - t * kKRows;
+      const int y = seen - t * kKRows;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) s[i][j] = 32 * i + 8 * (j >> 2) + (j & 3) <= x ? s[i][j] : -kInf;
+        for (int j = 0; j < 16; ++j) x[i][j] = 32 * i + 8 * (j >> 2) + (j & 3) <= y ? x[i][j] : -kInf;
     }
-    float mx = s[0][0];
+  };
+  auto most = [&](const v16f* x) {
+    float mx = x[0][0];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[i][j]);
-    mx = half_join(mx, [](float u, float v) { return fmaxf(u, v); });
+      for (int j = 0; j < 16; ++j) mx = fmaxf(mx, x[i][j]);
+    return half_join(mx, [](float u, float v) { return fmaxf(u, v); });
+  };
+  auto raise = [&](float mx) {
     if (__ballot((mx - m) * sl > 8.f)) {  // (NaN where both are -inf: a row that sees no key yet)
-      const float mn = fmaxf(m, mx);
-      const float f = exp2_hw((m - (mn == -kInf ? 0.f : mn)) * sl);
+      const float mn = fmaxf(m, mx), z = mn == -kInf ? 0.f : mn;
+      const float f = exp2_hw((m - z) * sl);
       m = mn;
+      ms = z * sl;
       l *= f;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[d][j] *= f;
     }
-    const float ms = (m == -kInf ? 0.f : m) * sl;
+  };
+  // P of a tile's scores as operands; its sum goes to l
+  auto weights = [&](v16f* x, v8bf* p) {
     float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        s[i][j] = exp2_hw(fmaf(s[i][j], sl, -ms));
-        sum[i] += s[i][j];
-      }
-    l += sum[0] + sum[1];
-#pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const v8bf p = operand_of(s[i >> 1], i & 1);
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) o[d] = mfma32(tr_operand<D>(st, va[d], 16 * i), p, o[d]);
+      for (int j = 8 * (i & 1); j < 8 * (i & 1) + 8; ++j) {
+        x[i >> 1][j] = exp2_hw(fmaf(x[i >> 1][j], sl, -ms));
+        sum[j & 1] += x[i >> 1][j];
+      }
+      p[i] = operand_of(x[i >> 1], i & 1);
     }
+    l += sum[0] + sum[1];
+  };
+  auto values = [&](const lds_char* st, const v8bf* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) o[d] = mfma32(tr_operand<D>(st, TrAddr{va.near ^ (64 * d), va.far ^ (64 * d)}, 16 * i), p[i], o[d]);
+  };
+  // K of tile t + 1 and V of tile t have landed; K of t + 2 and V of t + 1
+  // start on their way, into the places of K of t and V of t - 1
+  auto arrive = [&, &ka = ka, &va = va](auto stage, int t) {
+    constexpr int P = decltype(stage)::value;
+    wait_dma<0>();
+    lds_barrier();
+    issue_k(k_stage<D, P>(), t + 2);
+    issue_v(v_stage<D, P ^ 1>(), t + 1);
+    asm volatile("" : "+v"(ka), "+v"(va.near), "+v"(va.far));
+  };
+  // Tile t, its scores in s[t % 2]: the next tile's scores are computed among
+  // the exponentials of this one, the next maximum among the products with
+  // V, so that the matrix unit has work throughout.  (The empty statements
+  // keep the compiler from moving the exponentials out of that block.)
+  auto step = [&](auto stage, int t) {
+    constexpr int P = decltype(stage)::value;
+    arrive(stage, t);
+    v8bf p[4];
+    asm volatile("" : "+v"(s[P][0]), "+v"(s[P][1]));
+    scores(k_stage<D, P ^ 1>(), s[P ^ 1]);
+    weights(s[P], p);
+    asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]), "+v"(l));
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x402, 1024 / D, 0);
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x402, 1024 / D, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    mask(s[P ^ 1], t + 1);
+    const float mx = most(s[P ^ 1]);
+    values(v_stage<D, P>(), p);
+    __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+    for (int i = 0; i < D / 8 - 3; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x8, 3, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    raise(mx);
+  };
+  auto end = [&](auto stage, int t) {  // this wavefront's last tile
+    constexpr int P = decltype(stage)::value;
+    arrive(stage, t);
+    v8bf p[4];
+    weights(s[P], p);
+    values(v_stage<D, P>(), p);
   };
 
-  if (tiles > 0) dma.issue(pair_stage<D, 0>(), kp, vp, kr.len);
+  typedef std::integral_constant<int, 0> S0;
+  typedef std::integral_constant<int, 1> S1;
   int t = 0;
-  for (; t + 1 < tiles; t += 2) {
-    step(std::integral_constant<int, 0>{}, t);
-    step(std::integral_constant<int, 1>{}, t + 1);
+  if (tiles > 0) {
+    issue_k(k_stage<D, 0>(), 0);
+    wait_dma<0>();
+    lds_barrier();
+    issue_k(k_stage<D, 1>(), 1);
+    issue_v(v_stage<D, 0>(), 0);
   }
-  if (t < tiles) step(std::integral_constant<int, 0>{}, t);
+  if (wtiles > 0) {
+    scores(k_stage<D, 0>(), s[0]);
+    mask(s[0], 0);
+    raise(most(s[0]));
+    for (; t + 2 < wtiles; t += 2) {
+      step(S0{}, t);
+      step(S1{}, t + 1);
+    }
+    if (t + 1 < wtiles) {
+      step(S0{}, t);
+      end(S1{}, t + 1);
+      t += 2;
+    } else {
+      end(S0{}, t);
+      t += 1;
+    }
+  }
+  for (; t < tiles; ++t) {  // the other wavefronts' tiles
+    if (t & 1) arrive(S1{}, t);
+    else arrive(S0{}, t);
+  }
 
   l = half_join(l, [](float u, float v) { return u + v; });
   // a row that sees no key: zeros, and -inf as the logarithm of its sum
