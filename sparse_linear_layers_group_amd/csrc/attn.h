@@ -144,6 +144,26 @@ __device__ __forceinline__ v8bf tr_operand(const lds_char* tile, TrAddr a, int r
   return join(lds_read_tr(tile + a.near + r0 * Tile<D>::kRowBytes), lds_read_tr(tile + a.far + r0 * Tile<D>::kRowBytes));
 }
 
+// acc^T (column = row of the output, registers = its D elements) times mul,
+// as bf16: after an exchange between the half wavefronts every lane stores
+// 16 bytes of its row at a time
+template <int D>
+__device__ __forceinline__ void store_row(uint16_t* row, const v16f* acc, float mul, int lane, bool in) {
+#pragma unroll
+  for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int e = 8 * u;
+      uint32_t a0 = pk_bf16(acc[t][e] * mul, acc[t][e + 1] * mul);
+      uint32_t a1 = pk_bf16(acc[t][e + 2] * mul, acc[t][e + 3] * mul);
+      uint32_t b0 = pk_bf16(acc[t][e + 4] * mul, acc[t][e + 5] * mul);
+      uint32_t b1 = pk_bf16(acc[t][e + 6] * mul, acc[t][e + 7] * mul);
+      half_swap(a0, b0);
+      half_swap(a1, b1);
+      if (in) st_global(reinterpret_cast<u32x4*>(row + 32 * t + 16 * u + 8 * (lane >> 5)), u32x4{a0, a1, b0, b1});
+    }
+}
+
 // ---------------------------------------------------------------------
 // Work items are tiles of the sequences, every sequence cut into
 // ceil(len / rows) of them, numbered so that those with the highest level

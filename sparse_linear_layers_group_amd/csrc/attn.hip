@@ -131,26 +131,6 @@ __device__ __forceinline__ void load_row_operand(v8bf* f, const uint16_t* row, i
   }
 }
 
-// acc^T (column = row of the output, registers = its D elements) times mul,
-// as bf16: after an exchange between the half wavefronts every lane stores
-// 16 bytes of its row at a time
-template <int D>
-__device__ __forceinline__ void store_row(uint16_t* row, const v16f* acc, float mul, int lane, bool in) {
-#pragma unroll
-  for (int t = 0; t < D / 32; ++t)
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int e = 8 * u;
-      uint32_t a0 = pk_bf16(acc[t][e] * mul, acc[t][e + 1] * mul);
-      uint32_t a1 = pk_bf16(acc[t][e + 2] * mul, acc[t][e + 3] * mul);
-      uint32_t b0 = pk_bf16(acc[t][e + 4] * mul, acc[t][e + 5] * mul);
-      uint32_t b1 = pk_bf16(acc[t][e + 6] * mul, acc[t][e + 7] * mul);
-      half_swap(a0, b0);
-      half_swap(a1, b1);
-      if (in) st_global(reinterpret_cast<u32x4*>(row + 32 * t + 16 * u + 8 * (lane >> 5)), u32x4{a0, a1, b0, b1});
-    }
-}
-
 template <int N>
 __device__ __forceinline__ void clear(v16f* acc) {
 #pragma unroll
@@ -170,17 +150,22 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // the unrounded P.  m' only moves when a score passes it by 8 in the
 // exponent of 2: P then stays below 2^8 and the 64 accumulators are
 // rescaled a few times per row instead of once per tile.
+//
+// `splits` workgroups share the keys of a tile of rows where there are few
+// tiles: each leaves its binary32 O, m and l in `part` ([split][hq][total_q]
+// rows of D, then [split][hq][total_q] pairs), and attn_fwd_join_kernel adds
+// them in order.
 template <int D>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int splits, float* __restrict__ part) {
   typedef Tile<D> T;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.hq / a.hkv;
-  const Place pl = place_of(blockIdx.x, a.hkv, group);
+  const Place pl = place_of(blockIdx.x, a.hkv, group * splits);
   const Item it = find_item(a.cu_q, a.batch, a.total_q, kQRows, pl.rank);
   const int seq = __builtin_amdgcn_readfirstlane(it.seq);
   if (seq < 0) return;
-  const int kvh = pl.pair, head = kvh * group + pl.part;
+  const int split = pl.part / group, kvh = pl.pair, head = kvh * group + pl.part - split * group;
   const Rows qr = seq_rows(a.cu_q, seq, a.total_q), kr = seq_rows(a.cu_k, seq, a.total_k);
   const int q0 = __builtin_amdgcn_readfirstlane(it.level) * kQRows;
   const int off = kr.len - qr.len;
@@ -189,8 +174,11 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
   // keys the workgroup's and this wavefront's last rows see
   const int last = q0 + kQRows < qr.len ? q0 + kQRows : qr.len;
   const int wlast = w0 + 32 < qr.len ? w0 + 32 : qr.len;
-  const int tiles = (clampi(last + off, 0, kr.len) + kKRows - 1) / kKRows;
-  const int wtiles = w0 < qr.len ? (clampi(wlast + off, 0, kr.len) + kKRows - 1) / kKRows : 0;
+  const int all = (clampi(last + off, 0, kr.len) + kKRows - 1) / kKRows;
+  const int wall = w0 < qr.len ? (clampi(wlast + off, 0, kr.len) + kKRows - 1) / kKRows : 0;
+  // this workgroup's tiles [first, tiles) of them
+  const int first = (int)((int64_t)all * split / splits), tiles = (int)((int64_t)all * (split + 1) / splits);
+  const int wtiles = wall < tiles ? wall : tiles;
 
   v8bf qf[D / 16];
   load_row_operand<D>(qf, a.Q + (int64_t)(qr.start + r) * a.q_stride + (int64_t)head * D, lane, in);
@@ -205,7 +193,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
 
   const float sl = a.scale * kLog2e;
   const int seen = r + off - 4 * (lane >> 5);  // last visible key, minus this lane's row offset
-  v16f o[D / 32], s[2][2];  // s[t % 2]: the scores of tile t
+  v16f o[D / 32], s[2][2];  // scores of the tiles in stage 0 and 1
   clear<D / 32>(o);
   float m = -kInf, ms = 0.f, l = 0.f;  // ms: m scale log2 e, 0 while m is -inf
 
@@ -282,7 +270,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
     issue_v(v_stage<D, P ^ 1>(), t + 1);
     asm volatile("" : "+v"(ka), "+v"(va.near), "+v"(va.far));
   };
-  // Tile t, its scores in s[t % 2]: the next tile's scores are computed among
+  // Tile t, its scores in the s of its stage: the next tile's scores are computed among
   // the exponentials of this one, the next maximum among the products with
   // V, so that the matrix unit has work throughout.  (The empty statements
   // keep the compiler from moving the exponentials out of that block.)
@@ -328,17 +316,17 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
 
   typedef std::integral_constant<int, 0> S0;
   typedef std::integral_constant<int, 1> S1;
-  int t = 0;
-  if (tiles > 0) {
-    issue_k(k_stage<D, 0>(), 0);
+  int t = first;  // (stages alternate from the first tile on: S0 is its stage)
+  if (first < tiles) {
+    issue_k(k_stage<D, 0>(), first);
     wait_dma<0>();
     lds_barrier();
-    issue_k(k_stage<D, 1>(), 1);
-    issue_v(v_stage<D, 0>(), 0);
+    issue_k(k_stage<D, 1>(), first + 1);
+    issue_v(v_stage<D, 0>(), first);
   }
-  if (wtiles > 0) {
+  if (first < wtiles) {
     scores(k_stage<D, 0>(), s[0]);
-    mask(s[0], 0);
+    mask(s[0], first);
     raise(most(s[0]));
     for (; t + 2 < wtiles; t += 2) {
       step(S0{}, t);
@@ -354,15 +342,69 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
     }
   }
   for (; t < tiles; ++t) {  // the other wavefronts' tiles
-    if (t & 1) arrive(S1{}, t);
+    if ((t - first) & 1) arrive(S1{}, t);
     else arrive(S0{}, t);
   }
 
   l = half_join(l, [](float u, float v) { return u + v; });
+  if (splits > 1) {
+    if (in) {
+      const int64_t rows = (int64_t)a.hq * a.total_q, at = ((int64_t)split * a.hq + head) * a.total_q + qr.start + r;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          st_global(reinterpret_cast<v4f*>(part + at * D + 32 * d + 8 * q + 4 * (lane >> 5)),
+                    v4f{o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]});
+      if (lane < 32) st_global(reinterpret_cast<v2f*>(part + splits * rows * D) + at, v2f{m, l});
+    }
+    return;
+  }
   // a row that sees no key: zeros, and -inf as the logarithm of its sum
   store_row<D>(a.O + ((int64_t)(qr.start + r) * a.hq + head) * D, o, l > 0.f ? 1.f / l : 0.f, lane, in);
   if (a.lse && in && lane < 32)
     st_global(a.lse + (int64_t)head * a.total_q + qr.start + r, l > 0.f ? fmaf(m, sl, log2_hw(l)) * kLn2 : -kInf);
+}
+
+// O and lse of rows whose keys were split: 16 rows of a tile and head per
+// workgroup, 4 elements a thread
+template <int D>
+__global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int splits, const float* __restrict__ part) {
+  constexpr int kRows = 256 / (D / 4);  // rows of a workgroup
+  constexpr int kParts = kQRows / kRows;
+  const int tile = blockIdx.x / kParts, head = tile % a.hq;
+  const Item it = find_item(a.cu_q, a.batch, a.total_q, kQRows, tile / a.hq);
+  if (it.seq < 0) return;
+  const Rows qr = seq_rows(a.cu_q, it.seq, a.total_q);
+  const int r = it.level * kQRows + blockIdx.x % kParts * kRows + threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
+  if (r >= qr.len) return;
+  const int64_t plane = (int64_t)a.hq * a.total_q, at = (int64_t)head * a.total_q + qr.start + r;
+  const float sl = a.scale * kLog2e;
+  v4f x[kMaxSplits];
+  v2f ml[kMaxSplits];
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) {
+    const int64_t i = (s < splits ? s : 0) * plane + at;
+    x[s] = ld_global(reinterpret_cast<const v4f*>(part + i * D) + c);
+    ml[s] = ld_global(reinterpret_cast<const v2f*>(part + splits * plane * D) + i);
+  }
+  float m = -kInf;
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) m = fmaxf(m, ml[s][0]);
+  const float z = m == -kInf ? 0.f : m;
+  v4f y = v4f{0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) {
+    const float w = s < splits ? exp2_hw((ml[s][0] - z) * sl) : 0.f;
+    l = fmaf(ml[s][1], w, l);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = fmaf(x[s][e], w, y[e]);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  st_global(reinterpret_cast<u32x2*>(a.O + ((int64_t)(qr.start + r) * a.hq + head) * D) + c,
+            u32x2{pk_bf16(y[0] * inv, y[1] * inv), pk_bf16(y[2] * inv, y[3] * inv)});
+  if (a.lse && c == 0) st_global(a.lse + at, l > 0.f ? fmaf(m, sl, log2_hw(l)) * kLn2 : -kInf);
 }
 
 // --------------------------------------------------------------- backward
@@ -636,7 +678,9 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, const u
     const int r0 = t * kBRows + 32 * rq;  // this wavefront's rows r0 .. r0 + 31
     t = nt;
     h = nh;
-    if (r0 + 31 + off < w0 || r0 >= qr.len) return;  // none of them sees a key of these
+    // (Rows that see none of these keys are computed too, as zeros: the other
+    // wavefronts of the step take as long, and accumulators that pass through
+    // a branch are copied around it.)
     const lds_char* const sq = st + 32 * rq * T::kRowBytes;
     asm volatile("" : "+v"(qa), "+v"(qt.near), "+v"(qt.far));
     v16f s, g;
@@ -652,32 +696,61 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, const u
       }
     }
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
+    for (int k = 0; k < D / 16; ++k)
       s = mfma32(lds_read8(sq + (qa ^ (32 * k))), k < kHeld ? kf[k % kHeld] : lds_read8(kx + 1024 * (k - kHeld)), s);
-      g = mfma32(lds_read8(sq + kTile + (qa ^ (32 * k))), lds_read8(vr + (qa ^ (32 * k))), g);
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) s[e] = exp2_hw(s[e] * sl);
     if (r0 + off < w0 + 31) {  // the diagonal
       const int x = j - off - r0 - 4 * (lane >> 5);  // first row that sees this lane's key
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s[e] = 8 * (e >> 2) + (e & 3) >= x ? s[e] : 0.f;
+      for (int e = 0; e < 16; ++e) s[e] = 8 * (e >> 2) + (e & 3) >= x ? s[e] : -kInf;
     }
+    // dP among the exponentials, dV among the products P dP, then dK
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" : "+v"(s));
+    v8bf p[2], w[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const v8bf p = operand_of(s, k);
+    for (int k = 0; k < D / 16; ++k)
+      g = mfma32(lds_read8(sq + kTile + (qa ^ (32 * k))), lds_read8(vr + (qa ^ (32 * k))), g);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = exp2_hw(s[e] * sl);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) p[k] = operand_of(s, k);
+    asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(s));
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x402, 640 / D, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
-        dv[d] = mfma32(tr_operand<D>(st + kTile, TrAddr{qt.near ^ (64 * d), qt.far ^ (64 * d)}, 16 * k), p, dv[d]);
-    }
+        dv[d] = mfma32(tr_operand<D>(st + kTile, TrAddr{qt.near ^ (64 * d), qt.far ^ (64 * d)}, 16 * k), p[k], dv[d]);
 #pragma unroll
     for (int e = 0; e < 16; ++e) s[e] *= g[e];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const v8bf p = operand_of(s, k);
+    for (int k = 0; k < 2; ++k) w[k] = operand_of(s, k);
+    asm volatile("" : "+v"(w[0]), "+v"(w[1]));
+    __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x2, 384 / D, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
-        dk[d] = mfma32(tr_operand<D>(st, TrAddr{qt.near ^ (64 * d), qt.far ^ (64 * d)}, 16 * k), p, dk[d]);
+        dk[d] = mfma32(tr_operand<D>(st, TrAddr{qt.near ^ (64 * d), qt.far ^ (64 * d)}, 16 * k), w[k], dk[d]);
+    __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
     }
   };
 
@@ -797,13 +870,37 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t bwd_row_bytes(int64_t total_q, int64_t hq) { return align256((size_t)total_q * hq * 4); }
 }  // namespace
 
-size_t attn_fwd_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+// Workgroups that share the keys of a tile of rows: enough that every CU has
+// two, of at least kMinSplitTiles key tiles each for sequences of the mean
+// length (shorter ones cost more to join than they save).
+constexpr int kMinSplitTiles = 8;
+static int fwd_splits(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq) {
+  const int64_t tiles = (total_q + kQRows - 1) / kQRows * hq;
+  const int64_t keys = total_k / (batch > 0 ? batch : 1) / kKRows;
+  int64_t s = tiles > 0 ? 512 / tiles : 1;
+  s = s > keys / kMinSplitTiles ? keys / kMinSplitTiles : s;
+  s = s > kMaxSplits ? kMaxSplits : s;
+  return s < 1 ? 1 : (int)s;
+}
 
-hipError_t launch_attn_fwd(const AttnArgs& a, int64_t d, void*, hipStream_t s) {
-  const unsigned blocks = (unsigned)placed_blocks(most_tiles(a.total_q, a.batch, kQRows), a.hkv, a.hq / a.hkv);
-  if (d == 128) attn_fwd_kernel<128><<<dim3(blocks), 256, 0, s>>>(a);
-  else attn_fwd_kernel<64><<<dim3(blocks), 256, 0, s>>>(a);
+// workspace: partial O, m and l of split tiles
+size_t attn_fwd_ws_bytes(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t, int64_t d) {
+  const int splits = fwd_splits(batch, total_q, total_k, hq);
+  return splits > 1 ? (size_t)splits * hq * total_q * (d + 2) * 4 : 0;
+}
+
+template <int D>
+static hipError_t fwd_launch(const AttnArgs& a, float* part, hipStream_t s) {
+  const int splits = fwd_splits(a.batch, a.total_q, a.total_k, a.hq);
+  const int64_t items = most_tiles(a.total_q, a.batch, kQRows);
+  attn_fwd_kernel<D><<<dim3((unsigned)placed_blocks(items, a.hkv, a.hq / a.hkv * splits)), 256, 0, s>>>(a, splits, part);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  attn_fwd_join_kernel<D><<<dim3((unsigned)(items * a.hq * (kQRows / (256 / (D / 4))))), 256, 0, s>>>(a, splits, part);
   return hipGetLastError();
+}
+hipError_t launch_attn_fwd(const AttnArgs& a, int64_t d, void* ws, hipStream_t s) {
+  return d == 128 ? fwd_launch<128>(a, static_cast<float*>(ws), s) : fwd_launch<64>(a, static_cast<float*>(ws), s);
 }
 
 // Workgroups that share a dK / dV tile: enough that every CU has one

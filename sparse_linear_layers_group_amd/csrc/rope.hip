@@ -278,23 +278,35 @@ __global__ __launch_bounds__(256) void qk_rope_bwd_kernel(RopeBwdArgs a) {
               (part[0][e / D][e % D] + part[1][e / D][e % D]) + (part[2][e / D][e % D] + part[3][e / D][e % D]));
 }
 
-// dw[e] = sum of the workgroups' partials: 16 columns of 2D by 16 threads
-// each, joined in LDS, all in binary64 and in a fixed order
+// dw[e] = sum of the workgroups' partials: 4 columns of 2D per workgroup, its
+// threads along the rows, joined in LDS, all in binary64 and in a fixed order
 __global__ __launch_bounds__(256) void rope_dw_kernel(const float* __restrict__ part, int rows, int d,
                                                      float* __restrict__ gq, float* __restrict__ gk) {
-  __shared__ double red[16][16];
-  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
-  const int e = blockIdx.x * 16 + c;
-  double s = 0.0;
-  for (int i = r; i < rows; i += 16) s += (double)ld_global(part + (int64_t)i * 2 * d + e);
-  red[r][c] = s;
-  __syncthreads();
-  if (r == 0) {
-    s = 0.0;
+  __shared__ double red[4][4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.x * 4;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += red[i][c];
-    if (e < d) gq[e] = (float)s;
-    else gk[e - d] = (float)s;
+  for (int u = 0; u < kRopeDwRows / 256; ++u) {
+    const int i = threadIdx.x + 256 * u;
+    if (i < rows) {
+      const f32x4 x = ld_global(reinterpret_cast<const f32x4*>(part + (int64_t)i * 2 * d + e));
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[c] += (double)x[c];
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s[c] += __shfl_xor(s[c], o, 64);
+    if (lane == 0) red[wave][c] = s[c];
+  }
+  __syncthreads();
+  if (threadIdx.x < 4) {
+    const int c = threadIdx.x;
+    const float v = (float)((red[0][c] + red[1][c]) + (red[2][c] + red[3][c]));
+    if (e + c < d) gq[e + c] = v;
+    else gk[e + c - d] = v;
   }
 }
 
@@ -336,7 +348,7 @@ static hipError_t rope_bwd_launch(const RopeBwdArgs& a, hipStream_t s) {
     if (blocks > 0) qk_rope_bwd_kernel<D, F32, true><<<dim3((unsigned)blocks), 256, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    rope_dw_kernel<<<dim3(2 * D / 16), 256, 0, s>>>(a.part, (int)blocks, D, a.gqw, a.gkw);
+    rope_dw_kernel<<<dim3(2 * D / 4), 256, 0, s>>>(a.part, (int)blocks, D, a.gqw, a.gkw);
   } else {
     qk_rope_bwd_kernel<D, F32, false><<<dim3((unsigned)blocks), 256, 0, s>>>(a);
   }

@@ -255,3 +255,16 @@ def test_no_rows():
     assert (o == 0).all() and (lse == -math.inf).all()
     dq, _, _ = backward(q, none, none, o, lse, q, [5], [0], 0.125)
     assert (dq == 0).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (6, 2, 128), (8, 1, 128)])
+@pytest.mark.parametrize("q_lens,k_lens", [
+    ([5], [4100]),                       # few rows, many keys: the keys are shared out
+    ([130, 1], [3000, 2500]),
+    ([64, 200, 3], [1700, 200, 4000]),   # one short sequence among them: parts without tiles
+    ([40, 100], [4000, 20]),             # and rows that see no key
+])
+def test_few_rows_with_many_keys(hq, hkv, d, q_lens, k_lens):
+    assert bl.bitlinear_attn_fwd_workspace_bytes(len(q_lens), sum(q_lens), sum(k_lens), hq, hkv, d) > 0
+    q, k, v, do = inputs(q_lens, k_lens, hq, hkv, d, seed=20, extra=3)
+    check(q, k, v, do, q_lens, k_lens)
