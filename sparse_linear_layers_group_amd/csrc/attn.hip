@@ -139,6 +139,7 @@ __device__ __forceinline__ void clear(v16f* acc) {
     for (int i = 0; i < 16; ++i) acc[t][i] = 0.f;
 }
 
+
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
 // ---------------------------------------------------------------- forward
@@ -151,12 +152,22 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // exponent of 2: P then stays below 2^8 and the 64 accumulators are
 // rescaled a few times per row instead of once per tile.
 //
-// `splits` workgroups share the keys of a tile of rows where there are few
-// tiles: each leaves its binary32 O, m and l in `part` ([split][hq][total_q]
+// Where there are few tiles of rows, `splits` workgroups are launched for
+// each, and as many as its keys make parts of about `target` key tiles share
+// them: each leaves its binary32 O, m and l in `part` ([split][hq][total_q]
 // rows of D, then [split][hq][total_q] pairs), and attn_fwd_join_kernel adds
 // them in order.
+__device__ __forceinline__ int parts_of(int tiles, int splits, int target) {
+  const int n = (tiles + target - 1) / target;
+  return n < 1 ? 1 : n < splits ? n : splits;
+}
+__device__ __forceinline__ int key_tiles(const Rows& qr, const Rows& kr, int q0) {  // that rows q0 .. q0 + 127 see
+  const int last = q0 + kQRows < qr.len ? q0 + kQRows : qr.len;
+  return (clampi(last + kr.len - qr.len, 0, kr.len) + kKRows - 1) / kKRows;
+}
 template <int D>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int splits, float* __restrict__ part) {
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int splits, int target,
+                                                         float* __restrict__ part) {
   typedef Tile<D> T;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -171,13 +182,14 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int splits
   const int off = kr.len - qr.len;
   const int w0 = q0 + 32 * wave, r = w0 + (lane & 31);
   const bool in = r < qr.len;
-  // keys the workgroup's and this wavefront's last rows see
-  const int last = q0 + kQRows < qr.len ? q0 + kQRows : qr.len;
+  // key tiles that the workgroup's and this wavefront's last rows see
   const int wlast = w0 + 32 < qr.len ? w0 + 32 : qr.len;
-  const int all = (clampi(last + off, 0, kr.len) + kKRows - 1) / kKRows;
+  const int all = key_tiles(qr, kr, q0);
   const int wall = w0 < qr.len ? (clampi(wlast + off, 0, kr.len) + kKRows - 1) / kKRows : 0;
   // this workgroup's tiles [first, tiles) of them
-  const int first = (int)((int64_t)all * split / splits), tiles = (int)((int64_t)all * (split + 1) / splits);
+  const int parts = parts_of(all, splits, target);
+  if (split >= parts) return;
+  const int first = (int)((int64_t)all * split / parts), tiles = (int)((int64_t)all * (split + 1) / parts);
   const int wtiles = wall < tiles ? wall : tiles;
 
   v8bf qf[D / 16];
@@ -347,7 +359,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int splits
   }
 
   l = half_join(l, [](float u, float v) { return u + v; });
-  if (splits > 1) {
+  if (parts > 1) {
     if (in) {
       const int64_t rows = (int64_t)a.hq * a.total_q, at = ((int64_t)split * a.hq + head) * a.total_q + qr.start + r;
 #pragma unroll
@@ -369,13 +381,16 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int splits
 // O and lse of rows whose keys were split: 16 rows of a tile and head per
 // workgroup, 4 elements a thread
 template <int D>
-__global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int splits, const float* __restrict__ part) {
+__global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int splits, int target,
+                                                           const float* __restrict__ part) {
   constexpr int kRows = 256 / (D / 4);  // rows of a workgroup
   constexpr int kParts = kQRows / kRows;
   const int tile = blockIdx.x / kParts, head = tile % a.hq;
   const Item it = find_item(a.cu_q, a.batch, a.total_q, kQRows, tile / a.hq);
   if (it.seq < 0) return;
   const Rows qr = seq_rows(a.cu_q, it.seq, a.total_q);
+  const int parts = parts_of(key_tiles(qr, seq_rows(a.cu_k, it.seq, a.total_k), it.level * kQRows), splits, target);
+  if (parts == 1) return;  // its workgroup wrote the rows
   const int r = it.level * kQRows + blockIdx.x % kParts * kRows + threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
   if (r >= qr.len) return;
   const int64_t plane = (int64_t)a.hq * a.total_q, at = (int64_t)head * a.total_q + qr.start + r;
@@ -384,7 +399,7 @@ __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int spli
   v2f ml[kMaxSplits];
 #pragma unroll
   for (int s = 0; s < kMaxSplits; ++s) {
-    const int64_t i = (s < splits ? s : 0) * plane + at;
+    const int64_t i = (s < parts ? s : 0) * plane + at;
     x[s] = ld_global(reinterpret_cast<const v4f*>(part + i * D) + c);
     ml[s] = ld_global(reinterpret_cast<const v2f*>(part + splits * plane * D) + i);
   }
@@ -396,7 +411,7 @@ __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int spli
   float l = 0.f;
 #pragma unroll
   for (int s = 0; s < kMaxSplits; ++s) {
-    const float w = s < splits ? exp2_hw((ml[s][0] - z) * sl) : 0.f;
+    const float w = s < parts ? exp2_hw((ml[s][0] - z) * sl) : 0.f;
     l = fmaf(ml[s][1], w, l);
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = fmaf(x[s][e], w, y[e]);
@@ -870,33 +885,42 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t bwd_row_bytes(int64_t total_q, int64_t hq) { return align256((size_t)total_q * hq * 4); }
 }  // namespace
 
-// Workgroups that share the keys of a tile of rows: enough that every CU has
-// two, of at least kMinSplitTiles key tiles each for sequences of the mean
-// length (shorter ones cost more to join than they save).
+// How a forward with few tiles of rows shares out the keys: into parts as
+// long as they can be for all of them to run at once, two workgroups per CU
+// (one more than 512 would start when the others are done: 903 rows behind
+// 11779 keys, 12 heads: 73 us with 528 parts, 54 us with 480), by the mean
+// length (the kernels see the true ones), and at least kMinSplitTiles
+// (shorter parts cost more to join than they save).  splits = 1: not at all.
 constexpr int kMinSplitTiles = 8;
-static int fwd_splits(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq) {
+struct FwdSplit {
+  int splits, target;
+};
+static FwdSplit fwd_split(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq) {
   const int64_t tiles = (total_q + kQRows - 1) / kQRows * hq;
   const int64_t keys = total_k / (batch > 0 ? batch : 1) / kKRows;
-  int64_t s = tiles > 0 ? 512 / tiles : 1;
-  s = s > keys / kMinSplitTiles ? keys / kMinSplitTiles : s;
-  s = s > kMaxSplits ? kMaxSplits : s;
-  return s < 1 ? 1 : (int)s;
+  if (tiles > 256 || keys < 2 * kMinSplitTiles) return FwdSplit{1, 1};
+  // (rows of long prompts see half of the keys on average)
+  const int64_t mean = total_q >= total_k ? (keys + 1) / 2 : keys;
+  const int64_t room = 512 - tiles / 2, target = (tiles * mean + room - 1) / room;  // (a tile ends in half a part)
+  return FwdSplit{kMaxSplits, (int)(target < kMinSplitTiles ? kMinSplitTiles : target)};
 }
 
 // workspace: partial O, m and l of split tiles
 size_t attn_fwd_ws_bytes(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t, int64_t d) {
-  const int splits = fwd_splits(batch, total_q, total_k, hq);
+  const int splits = fwd_split(batch, total_q, total_k, hq).splits;
   return splits > 1 ? (size_t)splits * hq * total_q * (d + 2) * 4 : 0;
 }
 
 template <int D>
 static hipError_t fwd_launch(const AttnArgs& a, float* part, hipStream_t s) {
-  const int splits = fwd_splits(a.batch, a.total_q, a.total_k, a.hq);
+  const FwdSplit p = fwd_split(a.batch, a.total_q, a.total_k, a.hq);
   const int64_t items = most_tiles(a.total_q, a.batch, kQRows);
-  attn_fwd_kernel<D><<<dim3((unsigned)placed_blocks(items, a.hkv, a.hq / a.hkv * splits)), 256, 0, s>>>(a, splits, part);
+  attn_fwd_kernel<D><<<dim3((unsigned)placed_blocks(items, a.hkv, a.hq / a.hkv * p.splits)), 256, 0, s>>>(
+      a, p.splits, p.target, part);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || splits == 1) return e;
-  attn_fwd_join_kernel<D><<<dim3((unsigned)(items * a.hq * (kQRows / (256 / (D / 4))))), 256, 0, s>>>(a, splits, part);
+  if (e != hipSuccess || p.splits == 1) return e;
+  attn_fwd_join_kernel<D><<<dim3((unsigned)(items * a.hq * (kQRows / (256 / (D / 4))))), 256, 0, s>>>(
+      a, p.splits, p.target, part);
   return hipGetLastError();
 }
 hipError_t launch_attn_fwd(const AttnArgs& a, int64_t d, void* ws, hipStream_t s) {
