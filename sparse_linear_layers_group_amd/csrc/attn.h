@@ -179,68 +179,93 @@ __device__ __forceinline__ void store_row(uint16_t* row, const v16f* acc, float 
 constexpr int kOrderedPerLane = 4;
 constexpr int kOrdered = 64 * kOrderedPerLane;
 
-__device__ __forceinline__ int wave_sum_i(int v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+// Sums over the lanes 0 .. lane by DPP moves within the vector unit (rows of
+// 16, then the last lane of a row to the next rows): a tenth of the time of
+// exchanges through LDS, of which finding an item takes dozens one after the
+// other.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int dpp_from(int none, int v) {
+  return __builtin_amdgcn_update_dpp(none, v, kCtrl, kRows, 0xf, false);
+}
+__device__ __forceinline__ int wave_scan_i(int v) {
+  v += dpp_from<0x111, 0xf>(0, v);  // row_shr:1, 2, 4, 8
+  v += dpp_from<0x112, 0xf>(0, v);
+  v += dpp_from<0x114, 0xf>(0, v);
+  v += dpp_from<0x118, 0xf>(0, v);
+  v += dpp_from<0x142, 0xa>(0, v);  // row_bcast:15 into rows 1 and 3
+  v += dpp_from<0x143, 0xc>(0, v);  // row_bcast:31 into rows 2 and 3
   return v;
 }
-__device__ __forceinline__ int wave_max_i(int v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const int u = __shfl_xor(v, o, 64);
-    v = u > v ? u : v;
-  }
-  return v;
-}
-__device__ __forceinline__ int wave_scan_i(int v, int lane) {  // sum over lanes 0..lane
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(v, o, 64);
-    v += lane >= o ? u : 0;
-  }
-  return v;
+__device__ __forceinline__ int wave_sum_i(int v) { return __builtin_amdgcn_readlane(wave_scan_i(v), 63); }
+__device__ __forceinline__ int max_i(int a, int b) { return a > b ? a : b; }
+__device__ __forceinline__ int wave_max_i(int v) {  // of values >= 0
+  v = max_i(v, dpp_from<0x111, 0xf>(0, v));
+  v = max_i(v, dpp_from<0x112, 0xf>(0, v));
+  v = max_i(v, dpp_from<0x114, 0xf>(0, v));
+  v = max_i(v, dpp_from<0x118, 0xf>(0, v));
+  v = max_i(v, dpp_from<0x142, 0xa>(0, v));
+  v = max_i(v, dpp_from<0x143, 0xc>(0, v));
+  return __builtin_amdgcn_readlane(v, 63);
 }
 
 // rows [start, start + len) of sequence b
 struct Rows {
   int start, len;
 };
-__device__ __forceinline__ Rows seq_rows(const int32_t* cu, int b, int64_t total) {
-  int lo = ld_global(cu + b), hi = ld_global(cu + b + 1);
+__device__ __forceinline__ Rows cut_rows(int lo, int hi, int64_t total) {
   lo = lo < 0 ? 0 : lo > total ? (int)total : lo;
   hi = hi < lo ? lo : hi > total ? (int)total : hi;
   return Rows{lo, hi - lo};
 }
+__device__ __forceinline__ Rows seq_rows(const int32_t* cu, int b, int64_t total) {
+  return cut_rows(ld_global(cu + b), ld_global(cu + b + 1), total);
+}
+__device__ __forceinline__ Rows lane_rows(const Rows& r, int lane) {
+  return Rows{__builtin_amdgcn_readlane(r.start, lane), __builtin_amdgcn_readlane(r.len, lane)};
+}
 
+// Item `rank` of the tiles of `rows` rows of the sequences in cu, with the
+// sequence's rows there and in the other offsets (all the same in every lane)
 struct Item {
   int seq, level;  // seq < 0: none
+  Rows mine, other;
 };
-__device__ __forceinline__ Item find_item(const int32_t* cu, int batch, int64_t total, int rows, int rank) {
+__device__ __forceinline__ Item find_item(const int32_t* cu, int64_t total, const int32_t* cu2, int64_t total2,
+                                          int batch, int rows, int rank) {
   const int lane = threadIdx.x & 63;
+  const Item none{-1, 0, {0, 0}, {0, 0}};
   if (batch > kOrdered) {
     int before = 0;
     for (int b0 = 0; b0 < batch; b0 += 64) {
       const int b = b0 + lane;
       const int n = b < batch ? (seq_rows(cu, b, total).len + rows - 1) / rows : 0;
-      const int incl = before + wave_scan_i(n, lane);
+      const int incl = before + wave_scan_i(n);
       const unsigned long long hit = __ballot(incl > rank);
       if (hit) {
-        const int l = __ffsll(hit) - 1;
-        return Item{b0 + l, rank - (__shfl(incl, l, 64) - __shfl(n, l, 64))};
+        const int l = __builtin_amdgcn_readfirstlane(__ffsll(hit) - 1);
+        const int level = rank - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l));
+        const Rows r = seq_rows(cu, b0 + l, total), o = seq_rows(cu2, b0 + l, total2);
+        return Item{b0 + l, level, lane_rows(r, 0), lane_rows(o, 0)};
       }
-      before = __shfl(incl, 63, 64);
+      before = __builtin_amdgcn_readlane(incl, 63);
     }
-    return Item{-1, 0};
+    return none;
   }
+  Rows mine[kOrderedPerLane], other[kOrderedPerLane];
   int n[kOrderedPerLane], most = 0, all = 0;
 #pragma unroll
   for (int i = 0; i < kOrderedPerLane; ++i) {
     const int b = 64 * i + lane;
-    n[i] = b < batch ? (seq_rows(cu, b, total).len + rows - 1) / rows : 0;
-    most = n[i] > most ? n[i] : most;
+    mine[i] = other[i] = Rows{0, 0};
+    if (b < batch) {
+      mine[i] = seq_rows(cu, b, total);
+      other[i] = seq_rows(cu2, b, total2);
+    }
+    n[i] = (mine[i].len + rows - 1) / rows;
+    most = max_i(most, n[i]);
     all += n[i];
   }
-  if (rank >= wave_sum_i(all)) return Item{-1, 0};
+  if (rank >= wave_sum_i(all)) return none;
   // at(L) = items of level L and above; the largest L with at(L) > rank
   const auto at = [&](int L) {
     int c = 0;
@@ -260,12 +285,13 @@ __device__ __forceinline__ Item find_item(const int32_t* cu, int batch, int64_t 
     const unsigned long long m = __ballot(n[i] > lo);
     const int c = __popcll(m);
     if (skip < c) {
-      const bool mine = (m >> lane & 1) && __popcll(m & ((1ull << lane) - 1)) == skip;
-      return Item{64 * i + __ffsll(__ballot(mine)) - 1, lo};
+      const bool mine_is = (m >> lane & 1) && __popcll(m & ((1ull << lane) - 1)) == skip;
+      const int l = __builtin_amdgcn_readfirstlane(__ffsll(__ballot(mine_is)) - 1);
+      return Item{64 * i + l, lo, lane_rows(mine[i], l), lane_rows(other[i], l)};
     }
     skip -= c;
   }
-  return Item{-1, 0};
+  return none;
 }
 
 // Workgroup id -> (item rank, head) for `pairs` key/value heads and `per`

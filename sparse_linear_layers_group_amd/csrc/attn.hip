@@ -173,12 +173,11 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int splits
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.hq / a.hkv;
   const Place pl = place_of(blockIdx.x, a.hkv, group * splits);
-  const Item it = find_item(a.cu_q, a.batch, a.total_q, kQRows, pl.rank);
-  const int seq = __builtin_amdgcn_readfirstlane(it.seq);
-  if (seq < 0) return;
+  const Item it = find_item(a.cu_q, a.total_q, a.cu_k, a.total_k, a.batch, kQRows, pl.rank);
+  if (it.seq < 0) return;
   const int split = pl.part / group, kvh = pl.pair, head = kvh * group + pl.part - split * group;
-  const Rows qr = seq_rows(a.cu_q, seq, a.total_q), kr = seq_rows(a.cu_k, seq, a.total_k);
-  const int q0 = __builtin_amdgcn_readfirstlane(it.level) * kQRows;
+  const Rows qr = it.mine, kr = it.other;
+  const int q0 = it.level * kQRows;
   const int off = kr.len - qr.len;
   const int w0 = q0 + 32 * wave, r = w0 + (lane & 31);
   const bool in = r < qr.len;
@@ -386,10 +385,10 @@ __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int spli
   constexpr int kRows = 256 / (D / 4);  // rows of a workgroup
   constexpr int kParts = kQRows / kRows;
   const int tile = blockIdx.x / kParts, head = tile % a.hq;
-  const Item it = find_item(a.cu_q, a.batch, a.total_q, kQRows, tile / a.hq);
+  const Item it = find_item(a.cu_q, a.total_q, a.cu_k, a.total_k, a.batch, kQRows, tile / a.hq);
   if (it.seq < 0) return;
-  const Rows qr = seq_rows(a.cu_q, it.seq, a.total_q);
-  const int parts = parts_of(key_tiles(qr, seq_rows(a.cu_k, it.seq, a.total_k), it.level * kQRows), splits, target);
+  const Rows qr = it.mine;
+  const int parts = parts_of(key_tiles(qr, it.other, it.level * kQRows), splits, target);
   if (parts == 1) return;  // its workgroup wrote the rows
   const int r = it.level * kQRows + blockIdx.x % kParts * kRows + threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
   if (r >= qr.len) return;
@@ -442,58 +441,24 @@ __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int spli
 // delta = sum P dP in binary32 in a sweep of their own and leave it in
 // memory for the dK / dV pass.
 
-// What the two passes add to their products: -lse / scale to S (-inf where a
-// row sees no key, so P becomes 0) and -delta to dP, as the accumulators'
-// first values; and dO rounded to bf16 where it comes in binary32.
-template <int D, bool F32>
-__global__ __launch_bounds__(256) void attn_delta_kernel(const uint16_t* __restrict__ O, const void* __restrict__ dO,
-                                                        const float* __restrict__ lse, int64_t rows, int hq,
-                                                        int64_t total_q, float scale,
-                                                        float* __restrict__ ndelta, float* __restrict__ shift,
-                                                        uint16_t* __restrict__ dOb) {
-  constexpr int kLanes = D / 8;
-  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;  // (token, head)
-  const int c = threadIdx.x % kLanes;
-  if (row >= rows) return;  // whole groups of kLanes lanes at a time
-  const u32x4 o = ld_global(reinterpret_cast<const u32x4*>(O + row * D) + c);
-  u32x4 g;
-  if constexpr (F32) {
-    const v4f* p = reinterpret_cast<const v4f*>(static_cast<const float*>(dO) + row * D) + 2 * c;
-    const v4f x = ld_global(p), y = ld_global(p + 1);
-    g = u32x4{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(y[0], y[1]), pk_bf16(y[2], y[3])};
-    st_global(reinterpret_cast<u32x4*>(dOb + row * D) + c, g);
-  } else {
-    g = ld_global(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(dO) + row * D) + c);
-  }
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) s = fmaf(bf16_lo(o[i]), bf16_lo(g[i]), fmaf(bf16_hi(o[i]), bf16_hi(g[i]), s));
-#pragma unroll
-  for (int x = 1; x < kLanes; x <<= 1) s += __shfl_xor(s, x, 64);
-  if (c == 0) {
-    const int64_t t = row / hq, at = (row - t * hq) * total_q + t;
-    const float e = ld_global(lse + at);
-    st_global(ndelta + at, -s);
-    st_global(shift + at, e == -kInf ? -kInf : -e / scale);
-  }
-}
-
+// The dQ pass comes first and leaves for the other what it adds to its
+// products as the accumulators' first values, -lse / scale to S (-inf where
+// a row sees no key, so P becomes 0) and -delta to dP, and dO rounded to
+// bf16 where it comes in binary32.
 template <int D>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const uint16_t* __restrict__ dO,
-                                                        float* __restrict__ ndelta,
-                                                        const float* __restrict__ shift) {
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, uint16_t* __restrict__ copy,
+                                                        float* __restrict__ ndelta, float* __restrict__ shift) {
   typedef Tile<D> T;
   constexpr int kTile = PairBytes<D>::kTile;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.hq / a.hkv;
   const Place pl = place_of(blockIdx.x, a.hkv, group);
-  const Item it = find_item(a.cu_q, a.batch, a.total_q, kQRows, pl.rank);
-  const int seq = __builtin_amdgcn_readfirstlane(it.seq);
-  if (seq < 0) return;
+  const Item it = find_item(a.cu_q, a.total_q, a.cu_k, a.total_k, a.batch, kQRows, pl.rank);
+  if (it.seq < 0) return;
   const int kvh = pl.pair, head = kvh * group + pl.part;
-  const Rows qr = seq_rows(a.cu_q, seq, a.total_q), kr = seq_rows(a.cu_k, seq, a.total_k);
-  const int q0 = __builtin_amdgcn_readfirstlane(it.level) * kQRows;
+  const Rows qr = it.mine, kr = it.other;
+  const int q0 = it.level * kQRows;
   const int off = kr.len - qr.len;
   const int w0 = q0 + 32 * wave, r = w0 + (lane & 31);
   const bool in = r < qr.len;
@@ -502,12 +467,43 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const ui
   const int tiles = (clampi(last + off, 0, kr.len) + kKRows - 1) / kKRows;
   const int wtiles = w0 < qr.len ? (clampi(wlast + off, 0, kr.len) + kKRows - 1) / kKRows : 0;
 
-  const int64_t row = qr.start + r;
+  const int64_t row = qr.start + r, at = (row * a.hq + head) * D, sum_at = (int64_t)head * a.total_q + row;
   v8bf qf[D / 16], gf[D / 16];
   load_row_operand<D>(qf, a.Q + row * a.q_stride + (int64_t)head * D, lane, in);
-  load_row_operand<D>(gf, dO + (row * a.hq + head) * D, lane, in);
-  float nd = in ? ld_global(ndelta + (int64_t)head * a.total_q + row) : 0.f;
-  const float le = (in ? ld_global(shift + (int64_t)head * a.total_q + row) : -kInf) * (a.scale * kLog2e);
+  if (a.do_f32) {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      const int64_t e = at + 16 * s + 8 * (lane >> 5);
+      u32x4 g = u32x4{0u, 0u, 0u, 0u};
+      if (in) {
+        const v4f* p = reinterpret_cast<const v4f*>(static_cast<const float*>(a.dO) + e);
+        const v4f x = ld_global(p), y = ld_global(p + 1);
+        g = u32x4{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(y[0], y[1]), pk_bf16(y[2], y[3])};
+        st_global(reinterpret_cast<u32x4*>(copy + e), g);
+      }
+      gf[s] = __builtin_bit_cast(v8bf, g);
+    }
+  } else {
+    load_row_operand<D>(gf, static_cast<const uint16_t*>(a.dO) + at, lane, in);
+  }
+  const float lse = in ? ld_global(a.lse + sum_at) : -kInf;
+  float nd = 0.f;  // -delta, from the row's O
+  {
+    v8bf of[D / 16];
+    load_row_operand<D>(of, a.O + at, lane, in);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      const u32x4 o = __builtin_bit_cast(u32x4, of[s]), g = __builtin_bit_cast(u32x4, gf[s]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) nd = fmaf(-bf16_lo(o[i]), bf16_lo(g[i]), fmaf(-bf16_hi(o[i]), bf16_hi(g[i]), nd));
+    }
+    nd = half_join(nd, [](float u, float v) { return u + v; });
+  }
+  if (in && lane < 32) {
+    st_global(ndelta + sum_at, nd);
+    st_global(shift + sum_at, lse == -kInf ? -kInf : -lse / a.scale);
+  }
+  const float le = lse == -kInf ? -kInf : -lse * kLog2e;
   const PairDma<D> dma(lane, wave, a.k_stride, a.v_stride);
   const uint16_t* kp = a.K + (int64_t)kr.start * a.k_stride + (int64_t)kvh * D;
   const uint16_t* vp = a.V + (int64_t)kr.start * a.v_stride + (int64_t)kvh * D;
@@ -579,11 +575,11 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, const ui
   if (tiles <= kExactTiles) {
     sweep(std::true_type{});
     nd = -half_join(exact, [](float u, float v) { return u + v; });
-    if (in && lane < 32) st_global(ndelta + (int64_t)head * a.total_q + row, nd);
+    if (in && lane < 32) st_global(ndelta + sum_at, nd);
     lds_barrier();  // both stages are free for the second sweep
   }
   sweep(std::false_type{});
-  store_row<D>(a.dQ + (row * a.hq + head) * D, dq, a.scale, lane, in);
+  store_row<D>(a.dQ + at, dq, a.scale, lane, in);
 }
 
 // dK and dV of 64 keys.  Lanes run over keys here: S = Q K^T has a key per
@@ -613,13 +609,12 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, const u
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = wave & 1, rq = wave >> 1;
   const Place pl = place_of(blockIdx.x, a.hkv, splits);
-  const Item it = find_item(a.cu_k, a.batch, a.total_k, kBKeys, pl.rank);
-  const int seq = __builtin_amdgcn_readfirstlane(it.seq);
-  if (seq < 0) return;
+  const Item it = find_item(a.cu_k, a.total_k, a.cu_q, a.total_q, a.batch, kBKeys, pl.rank);
+  if (it.seq < 0) return;
   const int kvh = pl.pair, split = pl.part, group = a.hq / a.hkv;
-  const Rows qr = seq_rows(a.cu_q, seq, a.total_q), kr = seq_rows(a.cu_k, seq, a.total_k);
+  const Rows qr = it.other, kr = it.mine;
   // the first keys are seen by the most rows: highest level first
-  const int k0 = ((kr.len + kBKeys - 1) / kBKeys - 1 - __builtin_amdgcn_readfirstlane(it.level)) * kBKeys;
+  const int k0 = ((kr.len + kBKeys - 1) / kBKeys - 1 - it.level) * kBKeys;
   const int off = kr.len - qr.len;
   const int w0 = k0 + 32 * kw, j = w0 + (lane & 31);
   const bool in = j < kr.len;
@@ -846,9 +841,9 @@ __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnBwdArgs a, int s
                                                            const float* __restrict__ part) {
   constexpr int kParts = 2 * kBKeys * (D / 8) / 256;  // workgroups of a tile
   const int tile = blockIdx.x / kParts, which = blockIdx.x % kParts / (kParts / 2);
-  const Item it = find_item(a.cu_k, a.batch, a.total_k, kBKeys, tile / a.hkv);
+  const Item it = find_item(a.cu_k, a.total_k, a.cu_q, a.total_q, a.batch, kBKeys, tile / a.hkv);
   if (it.seq < 0) return;
-  const Rows kr = seq_rows(a.cu_k, it.seq, a.total_k);
+  const Rows kr = it.mine;
   const int f = blockIdx.x % (kParts / 2) * 256 + threadIdx.x;
   const int row = it.level * kBKeys + f / (D / 8);
   if (row >= kr.len) return;
@@ -938,7 +933,7 @@ static int dkv_splits(int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv,
   return s < 1 ? 1 : (int)s;
 }
 
-// workspace: delta, lse * log2 e ([hq][total_q] each), dO in bf16, partial
+// workspace: -delta, -lse / scale ([hq][total_q] each), dO in bf16, partial
 // dK and dV of split tiles
 size_t attn_bwd_ws_bytes(int64_t, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d) {
   const int splits = dkv_splits(total_q, total_k, hq, hkv, d);
@@ -950,31 +945,21 @@ template <int D>
 static hipError_t bwd_launch(const AttnBwdArgs& a, hipStream_t s) {
   char* ws = static_cast<char*>(a.ws);
   float* delta = reinterpret_cast<float*>(ws);
-  float* lse2 = reinterpret_cast<float*>(ws + bwd_row_bytes(a.total_q, a.hq));
+  float* shift = reinterpret_cast<float*>(ws + bwd_row_bytes(a.total_q, a.hq));
   uint16_t* copy = reinterpret_cast<uint16_t*>(ws + 2 * bwd_row_bytes(a.total_q, a.hq));
   float* part = reinterpret_cast<float*>(ws + 2 * bwd_row_bytes(a.total_q, a.hq) +
                                          align256((size_t)a.total_q * a.hq * D * 2));
   const uint16_t* dO = a.do_f32 ? copy : static_cast<const uint16_t*>(a.dO);
   if (a.total_q > 0) {
-    const int64_t rows = a.total_q * a.hq;
-    const dim3 grid((unsigned)((rows * (D / 8) + 255) / 256));
-    if (a.do_f32)
-      attn_delta_kernel<D, true><<<grid, 256, 0, s>>>(a.O, a.dO, a.lse, rows, a.hq, a.total_q, a.scale, delta, lse2,
-                                                        copy);
-    else
-      attn_delta_kernel<D, false><<<grid, 256, 0, s>>>(a.O, a.dO, a.lse, rows, a.hq, a.total_q, a.scale, delta, lse2,
-                                                        copy);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
     attn_dq_kernel<D><<<dim3((unsigned)placed_blocks(most_tiles(a.total_q, a.batch, kQRows), a.hkv, a.hq / a.hkv)), 256, 0, s>>>(
-        a, dO, delta, lse2);
-    e = hipGetLastError();
+        a, copy, delta, shift);
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.total_k > 0) {
     const int splits = dkv_splits(a.total_q, a.total_k, a.hq, a.hkv, D);
     const int64_t items = most_tiles(a.total_k, a.batch, kBKeys);
-    attn_dkv_kernel<D><<<dim3((unsigned)placed_blocks(items, a.hkv, splits)), 512, 0, s>>>(a, dO, delta, lse2,
+    attn_dkv_kernel<D><<<dim3((unsigned)placed_blocks(items, a.hkv, splits)), 512, 0, s>>>(a, dO, delta, shift,
                                                                                        splits, part);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

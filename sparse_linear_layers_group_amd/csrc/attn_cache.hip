@@ -100,7 +100,7 @@ __device__ __forceinline__ CacheRange cache_range(const AttnCacheArgs& a, int un
   const int lane = threadIdx.x & 63;
   int n = 0;
   for (int i = lane; i < a.batch; i += 64) n += cache_tiles<F>(cache_len(a, i));
-  const int all = __builtin_amdgcn_readfirstlane(wave_sum_i(n) * units);
+  const int all = wave_sum_i(n) * units;
   const int per = range_tiles<F>(all);
   CacheRange r{0, 0, a.batch, 0};
   if ((int64_t)blockIdx.x * per >= all) return r;
@@ -109,15 +109,15 @@ __device__ __forceinline__ CacheRange cache_range(const AttnCacheArgs& a, int un
   int before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
     const int c = b0 + lane < a.batch ? cache_tiles<F>(cache_len(a, b0 + lane)) * units : 0;
-    const int incl = before + wave_scan_i(c, lane);
+    const int incl = before + wave_scan_i(c);
     const unsigned long long hit = __ballot(incl > r.g0);
     if (hit) {
-      const int l = __ffsll(hit) - 1;
-      r.b = __builtin_amdgcn_readfirstlane(b0 + l);
-      r.before = __builtin_amdgcn_readfirstlane(__shfl(incl, l, 64) - __shfl(c, l, 64));
+      const int l = __builtin_amdgcn_readfirstlane(__ffsll(hit) - 1);
+      r.b = b0 + l;
+      r.before = __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(c, l);
       break;
     }
-    before = __shfl(incl, 63, 64);
+    before = __builtin_amdgcn_readlane(incl, 63);
   }
   return r;
 }
@@ -272,9 +272,6 @@ __global__ __launch_bounds__(256, D == 128 ? 1 : 2) void attn_cache_kernel(AttnC
     }
     const int kvh = (g - before) / nt, t0 = (g - before) - kvh * nt;
     const int t1 = nt - t0 < range.g1 - g ? nt : t0 + range.g1 - g;
-    v8bf qf[D / 16];
-    QRow<D> q;
-    q.load(a, qf, b, kvh, lane & 31, lane);
     const int ctx = len - a.draft;  // rows before the drafted ones (may be below 0)
     const uint16_t* kp = a.K + (int64_t)kvh * D;
     const uint16_t* vp = a.V + (int64_t)kvh * D;
@@ -296,9 +293,16 @@ __global__ __launch_bounds__(256, D == 128 ? 1 : 2) void attn_cache_kernel(AttnC
       }
       return missing;
     };
+    int gone = 0;  // granules of the tile being computed that hold no rows
+    if (w0 < w1) {
+      pages.at(a, b, len, 2 * w0, lane);
+      gone = issue(cache_stage<D, false, 0>(), w0);
+    }
+    v8bf qf[D / 16];
+    QRow<D> q;
+    q.load(a, qf, b, kvh, lane & 31, lane);
     Running<D> acc;
     acc.clear();
-    int gone = 0;  // granules of the tile being computed that hold no rows
 
     auto step = [&](auto stage, int t) {
       constexpr int P = decltype(stage)::value;
@@ -329,10 +333,6 @@ __global__ __launch_bounds__(256, D == 128 ? 1 : 2) void attn_cache_kernel(AttnC
       gone = next;
     };
 
-    if (w0 < w1) {
-      pages.at(a, b, len, 2 * w0, lane);
-      gone = issue(cache_stage<D, false, 0>(), w0);
-    }
     int t = w0;
     for (; t + 1 < w1; t += 2) {
       step(std::integral_constant<int, 0>{}, t);
@@ -437,9 +437,6 @@ __global__ __launch_bounds__(256, 2) void attn_cache_wide_kernel(AttnCacheArgs a
     const int t1 = nt - t0 < range.g1 - g ? nt : t0 + range.g1 - g;
     const int kvh = u / cols, block = (u - kvh * cols) * nc + wave;  // this wavefront's 32 rows of Q
     const bool busy = wave < nc && block < blocks;
-    v8bf qf[D / 16];
-    QRow<D> q;
-    q.load(a, qf, b, kvh, busy ? block * kCols + (lane & 31) : blocks * kCols, lane);
     const int ctx = len - a.draft;
     const uint16_t* kp = a.K + (int64_t)kvh * D;
     const uint16_t* vp = a.V + (int64_t)kvh * D;
@@ -456,9 +453,13 @@ __global__ __launch_bounds__(256, 2) void attn_cache_wide_kernel(AttnCacheArgs a
       dma.issue(to, to + F::kBytes, kp, vp, at, len - (t * F::kRows + wave * kGranule));
       return missing;
     };
+    pages.at(a, b, len, 4 * t0, lane);
+    int gone = issue(cache_stage<D, true, 0>(), t0);  // granules of the next tile that hold no rows
+    v8bf qf[D / 16];
+    QRow<D> q;
+    q.load(a, qf, b, kvh, busy ? block * kCols + (lane & 31) : blocks * kCols, lane);
     Running<D> acc;
     acc.clear();
-    int gone;
 
     auto step = [&](auto stage, int t) {
       constexpr int P = decltype(stage)::value;
@@ -490,8 +491,6 @@ __global__ __launch_bounds__(256, 2) void attn_cache_wide_kernel(AttnCacheArgs a
         for (int d = 0; d < D / 32; ++d) acc.o[d] = mfma32(tr_operand<D>(st, va[d], 16 * k), p, acc.o[d]);
       }
     };
-    pages.at(a, b, len, 4 * t0, lane);
-    gone = issue(cache_stage<D, true, 0>(), t0);
     int t = t0;
     for (; t + 1 < t1; t += 2) {
       step(std::integral_constant<int, 0>{}, t);
@@ -530,7 +529,7 @@ __global__ __launch_bounds__(256) void attn_cache_join_kernel(AttnCacheArgs a) {
   typedef CacheForm<D, WIDE> F;
   constexpr int kGroups = 256 / (D / 4);
   __shared__ v4f sum[kGroups][D / 4];
-  __shared__ float lsum[kGroups];
+  __shared__ float msum[kGroups], lsum[kGroups];
   const int lane = threadIdx.x & 63;
   const int64_t row = blockIdx.x;  // (sequence, drafted token, head)
   const int64_t bt = row / a.hq;
@@ -561,40 +560,56 @@ __global__ __launch_bounds__(256) void attn_cache_join_kernel(AttnCacheArgs a) {
   const int r = c % kCols;
   const float* ws = static_cast<const float*>(a.ws) + (int64_t)(c / kCols % nc) * kPart<D>;
   auto part = [&](int p) { return ws + ((int64_t)p * 2 + (p > p0 || s0 == p0 * per ? 0 : 1)) * nc * kPart<D>; };
-  float mt = -kInf;
-  for (int p = p0 + lane; p <= p1; p += 64) mt = fmaxf(mt, ld_global(part(p) + kCols * D + r));
-  mt = wave_max(mt);
-  const float mz = mt == -kInf ? 0.f : mt;
+  // each group's running maximum, sum and row, then those of the groups
   v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
-  float lt = 0.f;
+  float mt = -kInf, lt = 0.f;
   for (int p = p0 + at; p <= p1; p += 4 * kGroups) {
     v4f x[4];
     float m[4], l[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const float* q = part(p + u * kGroups <= p1 ? p + u * kGroups : p);
+      const bool is = p + u * kGroups <= p1;
+      const float* q = part(is ? p + u * kGroups : p);
       x[u] = ld_global(reinterpret_cast<const v4f*>(q + r * D) + d);
       m[u] = ld_global(q + kCols * D + r);
       l[u] = ld_global(q + kCols * D + kCols + r);
+      m[u] = is ? m[u] : -kInf;
     }
+    const float old = mt;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) mt = fmaxf(mt, m[u]);
+    const float mz = mt == -kInf ? 0.f : mt, f = exp2_hw((old - mz) * sl);
+    lt *= f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] *= f;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const float w = p + u * kGroups <= p1 ? exp2_hw((m[u] - mz) * sl) : 0.f;
+      const float w = exp2_hw((m[u] - mz) * sl);
       lt = fmaf(l[u], w, lt);
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[u][e], w, acc[e]);
     }
   }
   sum[at][d] = acc;
-  if (d == 0) lsum[at] = lt;
+  if (d == 0) {
+    msum[at] = mt;
+    lsum[at] = lt;
+  }
   __syncthreads();
   if (at) return;
+  mt = -kInf;
 #pragma unroll
-  for (int g = 1; g < kGroups; ++g) {
+  for (int g = 0; g < kGroups; ++g) mt = fmaxf(mt, msum[g]);
+  const float mz = mt == -kInf ? 0.f : mt;
+  acc = v4f{0.f, 0.f, 0.f, 0.f};
+  lt = 0.f;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const float w = exp2_hw((msum[g] - mz) * sl);
     const v4f x = sum[g][d];
-    lt += lsum[g];
+    lt = fmaf(lsum[g], w, lt);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] += x[e];
+    for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[e], w, acc[e]);
   }
   const float inv = lt > 0.f ? 1.f / lt : 0.f;
   st_global(reinterpret_cast<u32x2*>(out) + d,
