@@ -1299,8 +1299,8 @@ int bitlinear_attn_cache(const uint16_t* Q, int64_t q_stride, const uint16_t* K,
     return fail(BL_ESHAPE, "max_pages must be >= 1 and max_pages*page below 2^31 (got %lld)", (long long)max_pages);
   if (cache_rows < 0 || cache_rows >= kLimit)
     return fail(BL_ESHAPE, "cache_rows must be in [0, 2^31) (got %lld)", (long long)cache_rows);
-  {  // tiles of the whole call are counted in 32 bits
-    const int64_t tiles = batch * ((max_pages * page + 31) / 32), units = hkv * ((draft * (hq / hkv) + 31) / 32);
+  {  // tiles of the whole call are counted in 32 bits (with up to 8 more for each unit)
+    const int64_t tiles = batch * ((max_pages * page + 31) / 32 + 8), units = hkv * ((draft * (hq / hkv) + 31) / 32);
     if (tiles >= kLimit || tiles * units >= kLimit)
       return fail(BL_ESHAPE, "too many cache tiles for one call (batch %lld, %lld rows each)", (long long)batch,
                   (long long)(max_pages * page));

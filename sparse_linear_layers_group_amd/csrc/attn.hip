@@ -120,15 +120,14 @@ struct PairDma {  // two arrays, one tile after the other
   }
 };
 
-// a row's elements as B operands: 16s + 8(l/32) .. +7 for s = 0 .. D/16-1
+// a row's elements as B operands: 16s + 8(l/32) .. +7 for s = 0 .. D/16-1.
+// Lanes past the last row take that row's (their results are not stored): a
+// condition around the loads would make each wait for the one before it.
 template <int D>
-__device__ __forceinline__ void load_row_operand(v8bf* f, const uint16_t* row, int lane, bool in) {
+__device__ __forceinline__ void load_row_operand(v8bf* f, const uint16_t* row, int lane) {
 #pragma unroll
-  for (int s = 0; s < D / 16; ++s) {
-    u32x4 v = u32x4{0u, 0u, 0u, 0u};
-    if (in) v = ld_global(reinterpret_cast<const u32x4*>(row + 16 * s + 8 * (lane >> 5)));
-    f[s] = __builtin_bit_cast(v8bf, v);
-  }
+  for (int s = 0; s < D / 16; ++s)
+    f[s] = __builtin_bit_cast(v8bf, ld_global(reinterpret_cast<const u32x4*>(row + 16 * s + 8 * (lane >> 5))));
 }
 
 template <int N>
@@ -192,7 +191,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int splits
   const int wtiles = wall < tiles ? wall : tiles;
 
   v8bf qf[D / 16];
-  load_row_operand<D>(qf, a.Q + (int64_t)(qr.start + r) * a.q_stride + (int64_t)head * D, lane, in);
+  load_row_operand<D>(qf, a.Q + (int64_t)(qr.start + (in ? r : qr.len - 1)) * a.q_stride + (int64_t)head * D, lane);
   const TileDma<D> kd(lane, wave, a.k_stride), vd(lane, wave, a.v_stride);
   const uint16_t* kp = a.K + (int64_t)kr.start * a.k_stride + (int64_t)kvh * D;
   const uint16_t* vp = a.V + (int64_t)kr.start * a.v_stride + (int64_t)kvh * D;
@@ -330,10 +329,12 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int splits
   int t = first;  // (stages alternate from the first tile on: S0 is its stage)
   if (first < tiles) {
     issue_k(k_stage<D, 0>(), first);
-    wait_dma<0>();
-    lds_barrier();
-    issue_k(k_stage<D, 1>(), first + 1);
     issue_v(v_stage<D, 0>(), first);
+    issue_k(k_stage<D, 1>(), first + 1);
+    // the first K has landed; the rest may be on its way
+    if (first + 1 < tiles) wait_dma<2 * TileDma<D>::kDma>();
+    else wait_dma<TileDma<D>::kDma>();
+    lds_barrier();
   }
   if (first < wtiles) {
     scores(k_stage<D, 0>(), s[0]);
@@ -467,38 +468,37 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, uint16_t
   const int tiles = (clampi(last + off, 0, kr.len) + kKRows - 1) / kKRows;
   const int wtiles = w0 < qr.len ? (clampi(wlast + off, 0, kr.len) + kKRows - 1) / kKRows : 0;
 
-  const int64_t row = qr.start + r, at = (row * a.hq + head) * D, sum_at = (int64_t)head * a.total_q + row;
-  v8bf qf[D / 16], gf[D / 16];
-  load_row_operand<D>(qf, a.Q + row * a.q_stride + (int64_t)head * D, lane, in);
+  const int64_t row = qr.start + (in ? r : qr.len - 1), at = (row * a.hq + head) * D;
+  const int64_t sum_at = (int64_t)head * a.total_q + row;
+  v8bf qf[D / 16], gf[D / 16], of[D / 16];
+  load_row_operand<D>(qf, a.Q + row * a.q_stride + (int64_t)head * D, lane);
+  load_row_operand<D>(of, a.O + at, lane);
+  const float lse = ld_global(a.lse + sum_at);
   if (a.do_f32) {
+    const v4f* p = reinterpret_cast<const v4f*>(static_cast<const float*>(a.dO) + at + 8 * (lane >> 5));
+    v4f x[D / 16][2];
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) x[s][i] = ld_global(p + 4 * s + i);
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
-      const int64_t e = at + 16 * s + 8 * (lane >> 5);
-      u32x4 g = u32x4{0u, 0u, 0u, 0u};
-      if (in) {
-        const v4f* p = reinterpret_cast<const v4f*>(static_cast<const float*>(a.dO) + e);
-        const v4f x = ld_global(p), y = ld_global(p + 1);
-        g = u32x4{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(y[0], y[1]), pk_bf16(y[2], y[3])};
-        st_global(reinterpret_cast<u32x4*>(copy + e), g);
-      }
+      const v4f y = x[s][0], z = x[s][1];
+      const u32x4 g = u32x4{pk_bf16(y[0], y[1]), pk_bf16(y[2], y[3]), pk_bf16(z[0], z[1]), pk_bf16(z[2], z[3])};
+      if (in) st_global(reinterpret_cast<u32x4*>(copy + at + 16 * s + 8 * (lane >> 5)), g);
       gf[s] = __builtin_bit_cast(v8bf, g);
     }
   } else {
-    load_row_operand<D>(gf, static_cast<const uint16_t*>(a.dO) + at, lane, in);
+    load_row_operand<D>(gf, static_cast<const uint16_t*>(a.dO) + at, lane);
   }
-  const float lse = in ? ld_global(a.lse + sum_at) : -kInf;
   float nd = 0.f;  // -delta, from the row's O
-  {
-    v8bf of[D / 16];
-    load_row_operand<D>(of, a.O + at, lane, in);
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      const u32x4 o = __builtin_bit_cast(u32x4, of[s]), g = __builtin_bit_cast(u32x4, gf[s]);
+  for (int s = 0; s < D / 16; ++s) {
+    const u32x4 o = __builtin_bit_cast(u32x4, of[s]), g = __builtin_bit_cast(u32x4, gf[s]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) nd = fmaf(-bf16_lo(o[i]), bf16_lo(g[i]), fmaf(-bf16_hi(o[i]), bf16_hi(g[i]), nd));
-    }
-    nd = half_join(nd, [](float u, float v) { return u + v; });
+    for (int i = 0; i < 4; ++i) nd = fmaf(-bf16_lo(o[i]), bf16_lo(g[i]), fmaf(-bf16_hi(o[i]), bf16_hi(g[i]), nd));
   }
+  nd = half_join(nd, [](float u, float v) { return u + v; });
   if (in && lane < 32) {
     st_global(ndelta + sum_at, nd);
     st_global(shift + sum_at, lse == -kInf ? -kInf : -lse / a.scale);
@@ -641,7 +641,7 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, const u
   v8bf kf[kHeld];
   {
     v8bf k[D / 16];
-    load_row_operand<D>(k, a.K + (int64_t)(kr.start + j) * a.k_stride + (int64_t)kvh * D, lane, in);
+    load_row_operand<D>(k, a.K + (int64_t)(kr.start + (in ? j : kr.len - 1)) * a.k_stride + (int64_t)kvh * D, lane);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) kf[i] = k[i];
     if constexpr (kHeld < D / 16) {

@@ -22,7 +22,9 @@ constexpr int kGranule = 16;  // rows that share a page
 // between workgroups leaves partial results (O, max, sum) in the workspace,
 // which the second kernel joins in a fixed order.  The ranges follow from
 // the lengths in device memory, so a captured graph may be replayed with
-// others.
+// others.  Starting on a unit (its pages, the first loads, the join) takes as
+// long as several tiles, so each counts as kStart tiles more than it has:
+// otherwise a workgroup with a handful of short sequences ends last.
 //
 // Up to 32 rows (decoding): each of the four wavefronts takes a quarter of a
 // unit's tiles of 32 keys and streams them through two LDS stages of its
@@ -30,18 +32,23 @@ constexpr int kGranule = 16;  // rows that share a page
 // The wavefronts meet in LDS at the end of the unit or the range.
 //
 // More rows (drafted trees): up to 128 in a unit, 32 for each wavefront, on
-// common tiles of 64 keys.  (The first form with several blocks of 32 rows
-// per wavefront ran out of registers; with units of 32 rows it read K and V
-// once for each: 24 tokens of 4 heads behind 38,000 rows, 113 us.)
+// common tiles of 64 keys in four stages, three of them in flight.  One
+// workgroup per CU with deep prefetch rather than two with less: a range that
+// is half as long leaves twice as many partial results, which at 96 rows are
+// a quarter of the bytes of K and V already.  (The first form with several
+// blocks of 32 rows per wavefront ran out of registers; with units of 32 rows
+// it read K and V once for each: 24 tokens of 4 heads behind 38,000 rows took
+// 113 us, with two stages and two workgroups per CU 41 us.)
 // ---------------------------------------------------------------------
 template <int D, bool WIDE>
 struct CacheForm {
   static constexpr int kRows = WIDE ? 64 : 32;           // keys of a tile
   static constexpr int kBytes = kRows * 2 * D;           // K or V of a tile
   static constexpr int kStage = WIDE ? 2 * kBytes : 8 * kBytes;  // of the workgroup
-  static constexpr int kBlocks = D == 128 && !WIDE ? 256 : 512;  // workgroups: 1 or 2 per CU by LDS
+  static constexpr int kBlocks = D == 128 ? 256 : 512;   // workgroups: 1 or 2 per CU by LDS
   static constexpr int kUnitBlocks = WIDE ? 4 : 1;       // blocks of 32 rows of Q in a unit, at most
   static constexpr int kMinTiles = WIDE ? 1 : 4;         // tiles of a workgroup's range, at least
+  static constexpr int kStart = 6;                       // tiles that starting on a unit counts as
   static constexpr int kRowF32 = D + 4;                  // padded row when wavefronts are joined
 };
 template <int D>
@@ -54,13 +61,17 @@ __shared__ __attribute__((aligned(1024))) char g_c64_st1[CacheForm<64, false>::k
 __shared__ float g_cred[9 * 32];  // [4][32] maxima, [4][32] sums, [32] joined sums
 __shared__ __attribute__((aligned(1024))) char g_d128_st0[CacheForm<128, true>::kStage];
 __shared__ __attribute__((aligned(1024))) char g_d128_st1[CacheForm<128, true>::kStage];
+__shared__ __attribute__((aligned(1024))) char g_d128_st2[CacheForm<128, true>::kStage];
+__shared__ __attribute__((aligned(1024))) char g_d128_st3[CacheForm<128, true>::kStage];
 __shared__ __attribute__((aligned(1024))) char g_d64_st0[CacheForm<64, true>::kStage];
 __shared__ __attribute__((aligned(1024))) char g_d64_st1[CacheForm<64, true>::kStage];
+__shared__ __attribute__((aligned(1024))) char g_d64_st2[CacheForm<64, true>::kStage];
+__shared__ __attribute__((aligned(1024))) char g_d64_st3[CacheForm<64, true>::kStage];
 template <int D, bool WIDE, int P>
 __device__ __forceinline__ lds_char* cache_stage() {
   if constexpr (WIDE) {
-    if constexpr (D == 128) return (lds_char*)(P == 0 ? g_d128_st0 : g_d128_st1);
-    else return (lds_char*)(P == 0 ? g_d64_st0 : g_d64_st1);
+    if constexpr (D == 128) return (lds_char*)(P == 0 ? g_d128_st0 : P == 1 ? g_d128_st1 : P == 2 ? g_d128_st2 : g_d128_st3);
+    else return (lds_char*)(P == 0 ? g_d64_st0 : P == 1 ? g_d64_st1 : P == 2 ? g_d64_st2 : g_d64_st3);
   } else {
     if constexpr (D == 128) return (lds_char*)(P == 0 ? g_c128_st0 : g_c128_st1);
     else return (lds_char*)(P == 0 ? g_c64_st0 : g_c64_st1);
@@ -75,6 +86,10 @@ __device__ __forceinline__ int cache_len(const AttnCacheArgs& a, int b) {
 template <class F>
 __device__ __forceinline__ int cache_tiles(int len) {
   return (len + F::kRows - 1) / F::kRows;
+}
+template <class F>
+__device__ __forceinline__ int unit_places(int tiles) {  // in the row of all units' tiles
+  return tiles > 0 ? tiles + F::kStart : 0;
 }
 // blocks of 32 rows of Q, and those of a unit: as few units as possible,
 // then equal ones
@@ -99,7 +114,7 @@ template <class F>
 __device__ __forceinline__ CacheRange cache_range(const AttnCacheArgs& a, int units) {
   const int lane = threadIdx.x & 63;
   int n = 0;
-  for (int i = lane; i < a.batch; i += 64) n += cache_tiles<F>(cache_len(a, i));
+  for (int i = lane; i < a.batch; i += 64) n += unit_places<F>(cache_tiles<F>(cache_len(a, i)));
   const int all = wave_sum_i(n) * units;
   const int per = range_tiles<F>(all);
   CacheRange r{0, 0, a.batch, 0};
@@ -108,7 +123,7 @@ __device__ __forceinline__ CacheRange cache_range(const AttnCacheArgs& a, int un
   r.g1 = r.g0 + per < all ? r.g0 + per : all;
   int before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    const int c = b0 + lane < a.batch ? cache_tiles<F>(cache_len(a, b0 + lane)) * units : 0;
+    const int c = b0 + lane < a.batch ? unit_places<F>(cache_tiles<F>(cache_len(a, b0 + lane))) * units : 0;
     const int incl = before + wave_scan_i(c);
     const unsigned long long hit = __ballot(incl > r.g0);
     if (hit) {
@@ -170,31 +185,32 @@ struct QRow {
   int token, head;
   bool in;
   uint64_t seen;  // drafted tokens it sees
+  // (rows past the last take that one's: a condition around the loads would
+  // make each wait for the one before it)
   __device__ __forceinline__ void load(const AttnCacheArgs& a, v8bf* f, int b, int kvh, int c, int lane) {
-    const int group = a.hq / a.hkv;
+    const int group = a.hq / a.hkv, rows = group * a.draft;
+    in = c < rows;
+    c = in ? c : rows - 1;
     token = c / group;
     head = c - token * group;
-    in = c < group * a.draft;
     const uint16_t* q = a.Q + ((int64_t)b * a.draft + token) * a.q_stride + (int64_t)(kvh * group + head) * D;
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      u32x4 v = u32x4{0u, 0u, 0u, 0u};
-      if (in) v = ld_global(reinterpret_cast<const u32x4*>(q + 16 * s + 8 * (lane >> 5)));
-      f[s] = __builtin_bit_cast(v8bf, v);
-    }
-    seen = 0;
-    if (in) seen = a.tree ? ld_global(a.tree + (int64_t)b * a.draft + token) : (2ull << token) - 1;
+    for (int s = 0; s < D / 16; ++s)
+      f[s] = __builtin_bit_cast(v8bf, ld_global(reinterpret_cast<const u32x4*>(q + 16 * s + 8 * (lane >> 5))));
+    seen = a.tree ? ld_global(a.tree + (int64_t)b * a.draft + token) : (2ull << token) - 1;
     if (a.draft < 64) seen &= (1ull << a.draft) - 1;
   }
-  // scores of 32 keys: row0 is the first one's place behind the context,
-  // gone: which of the two granules hold no rows
+  // scores of 32 keys: row0 is the first one's place behind the context
+  // (below 0: in it), gone: which of the two granules hold no rows
   __device__ __forceinline__ void mask(v16f& s, int row0, int gone, int lane) const {
+    uint32_t v = 0;  // bit r: key r is seen
+    if (row0 <= -32) v = ~0u;
+    else if (row0 < 0) v = (uint32_t)(seen << -row0) | ((1u << -row0) - 1);
+    else if (row0 < 64) v = (uint32_t)(seen >> row0);
+    v &= (gone & 1 ? 0u : 0xffffu) | (gone & 2 ? 0u : 0xffff0000u);
+    v >>= 4 * (lane >> 5);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int e = row0 + 8 * (j >> 2) + (j & 3) + 4 * (lane >> 5);  // drafted token, below 0: context
-      const bool v = (e < 0 || (e < 64 && (seen >> (e & 63) & 1))) && !(gone >> (j >> 3) & 1);
-      s[j] = v ? s[j] : -kInf;
-    }
+    for (int j = 0; j < 16; ++j) s[j] = v & (1u << (8 * (j >> 2) + (j & 3))) ? s[j] : -kInf;
   }
 };
 
@@ -264,13 +280,18 @@ __global__ __launch_bounds__(256, D == 128 ? 1 : 2) void attn_cache_kernel(AttnC
   for (int g = range.g0; g < range.g1 && b < a.batch;) {
     // key/value head kvh of sequence b, tiles [t0, t1) of it
     const int len = __builtin_amdgcn_readfirstlane(cache_len(a, b));
-    const int nt = cache_tiles<F>(len);
-    if (g - before >= nt * units) {  // next sequence (also past empty ones)
-      before += nt * units;
+    const int nt = cache_tiles<F>(len), places = unit_places<F>(nt);
+    if (g - before >= places * units) {  // next sequence (also past empty ones)
+      before += places * units;
       ++b;
       continue;
     }
-    const int kvh = (g - before) / nt, t0 = (g - before) - kvh * nt;
+    const int kvh = (g - before) / places, t0 = (g - before) - kvh * places;
+    const int end = g - t0 + places;  // where the next unit starts
+    if (t0 >= nt) {
+      g = end;
+      continue;
+    }
     const int t1 = nt - t0 < range.g1 - g ? nt : t0 + range.g1 - g;
     const int ctx = len - a.draft;  // rows before the drafted ones (may be below 0)
     const uint16_t* kp = a.K + (int64_t)kvh * D;
@@ -333,12 +354,12 @@ __global__ __launch_bounds__(256, D == 128 ? 1 : 2) void attn_cache_kernel(AttnC
       gone = next;
     };
 
-    int t = w0;
-    for (; t + 1 < w1; t += 2) {
+    for (int t = w0; t < w1;) {
       step(std::integral_constant<int, 0>{}, t);
-      step(std::integral_constant<int, 1>{}, t + 1);
+      if (++t == w1) break;
+      step(std::integral_constant<int, 1>{}, t);
+      ++t;
     }
-    if (t < w1) step(std::integral_constant<int, 0>{}, t);
     acc.l = half_join(acc.l, [](float x, float y) { return x + y; });
 
     // join the wavefronts: common maximum, then the scaled sums through LDS
@@ -400,12 +421,12 @@ __global__ __launch_bounds__(256, D == 128 ? 1 : 2) void attn_cache_kernel(AttnC
       }
     }
     __syncthreads();  // the stages are free again
-    g += t1 - t0;
+    g = t1 == nt ? end : g + t1 - t0;
   }
 }
 
 template <int D>
-__global__ __launch_bounds__(256, 2) void attn_cache_wide_kernel(AttnCacheArgs a) {
+__global__ __launch_bounds__(256, D == 128 ? 1 : 2) void attn_cache_wide_kernel(AttnCacheArgs a) {
   typedef CacheForm<D, true> F;
   typedef Tile<D> T;
   const int lane = threadIdx.x & 63;
@@ -427,13 +448,18 @@ __global__ __launch_bounds__(256, 2) void attn_cache_wide_kernel(AttnCacheArgs a
   for (int g = range.g0; g < range.g1 && b < a.batch;) {
     // unit u of sequence b, tiles [t0, t1) of it
     const int len = __builtin_amdgcn_readfirstlane(cache_len(a, b));
-    const int nt = cache_tiles<F>(len);
-    if (g - before >= nt * units) {
-      before += nt * units;
+    const int nt = cache_tiles<F>(len), places = unit_places<F>(nt);
+    if (g - before >= places * units) {
+      before += places * units;
       ++b;
       continue;
     }
-    const int u = (g - before) / nt, t0 = (g - before) - u * nt;
+    const int u = (g - before) / places, t0 = (g - before) - u * places;
+    const int end = g - t0 + places;
+    if (t0 >= nt) {
+      g = end;
+      continue;
+    }
     const int t1 = nt - t0 < range.g1 - g ? nt : t0 + range.g1 - g;
     const int kvh = u / cols, block = (u - kvh * cols) * nc + wave;  // this wavefront's 32 rows of Q
     const bool busy = wave < nc && block < blocks;
@@ -441,32 +467,40 @@ __global__ __launch_bounds__(256, 2) void attn_cache_wide_kernel(AttnCacheArgs a
     const uint16_t* kp = a.K + (int64_t)kvh * D;
     const uint16_t* vp = a.V + (int64_t)kvh * D;
     Lookup pages;
-    // this wavefront's granule of tile t; returns which of the four hold no rows
-    auto issue = [&](lds_char* st, int t) {
+    // this wavefront's granule of tile t (t1 and on: nothing is read, but as
+    // many instructions are issued, so the waits below can count them);
+    // returns which of the tile's four hold no rows
+    auto issue = [&](auto stage, int t) {
       if (4 * t - pages.base >= 64) pages.at(a, b, len, 4 * t, lane);
       int missing = 0;
 #pragma unroll
       for (int h = 0; h < 4; ++h)
         missing |= __builtin_amdgcn_readlane(pages.where, 4 * t - pages.base + h) < 0 ? 1 << h : 0;
-      const int at = __builtin_amdgcn_readlane(pages.where, 4 * t - pages.base + wave);
-      lds_char* to = st + wave * kGranule * T::kRowBytes;
+      const int at = t < t1 ? __builtin_amdgcn_readlane(pages.where, 4 * t - pages.base + wave) : -1;
+      lds_char* to = cache_stage<D, true, decltype(stage)::value>() + wave * kGranule * T::kRowBytes;
       dma.issue(to, to + F::kBytes, kp, vp, at, len - (t * F::kRows + wave * kGranule));
       return missing;
     };
+    typedef std::integral_constant<int, 0> S0;
+    typedef std::integral_constant<int, 1> S1;
+    typedef std::integral_constant<int, 2> S2;
+    typedef std::integral_constant<int, 3> S3;
     pages.at(a, b, len, 4 * t0, lane);
-    int gone = issue(cache_stage<D, true, 0>(), t0);  // granules of the next tile that hold no rows
+    int gone0 = issue(S0{}, t0), gone1 = issue(S1{}, t0 + 1), gone2 = issue(S2{}, t0 + 2);  // of the next three tiles
     v8bf qf[D / 16];
     QRow<D> q;
     q.load(a, qf, b, kvh, busy ? block * kCols + (lane & 31) : blocks * kCols, lane);
     Running<D> acc;
     acc.clear();
 
-    auto step = [&](auto stage, int t) {
+    auto step = [&](auto stage, auto last, int t) {
       constexpr int P = decltype(stage)::value;
-      wait_dma<0>();
+      wait_dma<2 * 2 * GranuleDma<D>::kDma>();
       lds_barrier();
-      const int now = gone;
-      if (t + 1 < t1) gone = issue(cache_stage<D, true, P ^ 1>(), t + 1);
+      const int now = gone0;
+      gone0 = gone1;
+      gone1 = gone2;
+      gone2 = issue(last, t + 3);
       const lds_char* st = cache_stage<D, true, P>();
       v16f s[2];
 #pragma unroll
@@ -491,12 +525,19 @@ __global__ __launch_bounds__(256, 2) void attn_cache_wide_kernel(AttnCacheArgs a
         for (int d = 0; d < D / 32; ++d) acc.o[d] = mfma32(tr_operand<D>(st, va[d], 16 * k), p, acc.o[d]);
       }
     };
-    int t = t0;
-    for (; t + 1 < t1; t += 2) {
-      step(std::integral_constant<int, 0>{}, t);
-      step(std::integral_constant<int, 1>{}, t + 1);
+    // (leaving between the stages keeps one copy of each: with copies for the
+    // last tiles the code no longer fitted the instruction cache)
+    for (int t = t0;;) {
+      step(S0{}, S3{}, t);
+      if (++t == t1) break;
+      step(S1{}, S0{}, t);
+      if (++t == t1) break;
+      step(S2{}, S1{}, t);
+      if (++t == t1) break;
+      step(S3{}, S2{}, t);
+      if (++t == t1) break;
     }
-    if (t < t1) step(std::integral_constant<int, 0>{}, t);
+    wait_dma<0>();
     acc.l = half_join(acc.l, [](float x, float y) { return x + y; });
     if (t0 == 0 && t1 == nt) {
       const float inv = acc.l > 0.f ? 1.f / acc.l : 0.f;
@@ -516,39 +557,55 @@ __global__ __launch_bounds__(256, 2) void attn_cache_wide_kernel(AttnCacheArgs a
                     v4f{acc.o[d][4 * e], acc.o[d][4 * e + 1], acc.o[d][4 * e + 2], acc.o[d][4 * e + 3]});
     }
     lds_barrier();  // the stages are free again (all reads have been used)
-    g += t1 - t0;
+    g = t1 == nt ? end : g + t1 - t0;
   }
 }
 
-// Rows of units that were cut: one workgroup per row of Q joins the partial
-// results of its unit (weights 2^(m - max)): its groups of D/4 threads take
-// every kGroups-th of them and meet in LDS, in a fixed order.  Rows of empty
+// Rows of units that were cut are joined from the partial results of their
+// unit (weights 2^(m - max)) by groups of D/4 threads, each of which takes
+// every so-manieth part with a running maximum; the groups then meet in a
+// fixed order.  WIDE: one wavefront per row, 2 or 4 groups (many rows, few
+// parts); otherwise one workgroup per row, 8 or 16 groups (few rows, many
+// parts: one per workgroup that shared a long sequence).  Rows of empty
 // sequences become zeros; rows that one workgroup had all of are written.
+struct Joined {
+  v4f acc;
+  float m, l;
+  __device__ __forceinline__ void add(const v4f& x, float mx, float lx, float sl) {
+    const float mn = fmaxf(m, mx), z = mn == -kInf ? 0.f : mn;
+    const float f = exp2_hw((m - z) * sl), w = exp2_hw((mx - z) * sl);
+    m = mn;
+    l = fmaf(lx, w, l * f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[e], w, acc[e] * f);
+  }
+};
 template <int D, bool WIDE>
 __global__ __launch_bounds__(256) void attn_cache_join_kernel(AttnCacheArgs a) {
   typedef CacheForm<D, WIDE> F;
-  constexpr int kGroups = 256 / (D / 4);
-  __shared__ v4f sum[kGroups][D / 4];
+  constexpr int kGroups = (WIDE ? 64 : 256) / (D / 4);
+  __shared__ v4f sum[WIDE ? 1 : kGroups][D / 4];
   __shared__ float msum[kGroups], lsum[kGroups];
-  const int lane = threadIdx.x & 63;
-  const int64_t row = blockIdx.x;  // (sequence, drafted token, head)
+  const int lane = threadIdx.x & 63, thread = WIDE ? lane : threadIdx.x;
+  const int64_t row = WIDE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;  // (sequence, token, head)
   const int64_t bt = row / a.hq;
   const int head = (int)(row - bt * a.hq), b = (int)(bt / a.draft), i = (int)(bt - (int64_t)b * a.draft);
+  if (b >= a.batch) return;
   const int group = a.hq / a.hkv, blocks = col_blocks(group * a.draft), nc = unit_blocks<F>(blocks);
   const int cols = (blocks + nc - 1) / nc, units = a.hkv * cols;
   const int kvh = head / group, c = i * group + head - kvh * group;
+  const int nt = cache_tiles<F>(cache_len(a, b));
   int all = 0, before = 0;
   for (int s = lane; s < a.batch; s += 64) {
-    const int n = cache_tiles<F>(cache_len(a, s));
+    const int n = unit_places<F>(cache_tiles<F>(cache_len(a, s)));
     all += n;
     before += s < b ? n : 0;
   }
-  const int nt = cache_tiles<F>(cache_len(a, b));
   all = wave_sum_i(all) * units;
   before = wave_sum_i(before) * units;
   const int per = range_tiles<F>(all);
-  const int s0 = before + (kvh * cols + c / (nc * kCols)) * nt, s1 = s0 + nt;  // the unit's tiles
-  const int at = threadIdx.x / (D / 4), d = threadIdx.x % (D / 4);
+  const int s0 = before + (kvh * cols + c / (nc * kCols)) * unit_places<F>(nt), s1 = s0 + nt;  // the unit's tiles
+  const int at = thread / (D / 4), d = thread % (D / 4);
   uint16_t* out = a.O + (bt * a.hq + head) * D;
   if (nt == 0) {
     if (at == 0) st_global(reinterpret_cast<u32x2*>(out) + d, u32x2{0u, 0u});
@@ -560,9 +617,7 @@ __global__ __launch_bounds__(256) void attn_cache_join_kernel(AttnCacheArgs a) {
   const int r = c % kCols;
   const float* ws = static_cast<const float*>(a.ws) + (int64_t)(c / kCols % nc) * kPart<D>;
   auto part = [&](int p) { return ws + ((int64_t)p * 2 + (p > p0 || s0 == p0 * per ? 0 : 1)) * nc * kPart<D>; };
-  // each group's running maximum, sum and row, then those of the groups
-  v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
-  float mt = -kInf, lt = 0.f;
+  Joined y{v4f{0.f, 0.f, 0.f, 0.f}, -kInf, 0.f};
   for (int p = p0 + at; p <= p1; p += 4 * kGroups) {
     v4f x[4];
     float m[4], l[4];
@@ -575,45 +630,32 @@ __global__ __launch_bounds__(256) void attn_cache_join_kernel(AttnCacheArgs a) {
       l[u] = ld_global(q + kCols * D + kCols + r);
       m[u] = is ? m[u] : -kInf;
     }
-    const float old = mt;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) mt = fmaxf(mt, m[u]);
-    const float mz = mt == -kInf ? 0.f : mt, f = exp2_hw((old - mz) * sl);
-    lt *= f;
+    for (int u = 0; u < 4; ++u) y.add(x[u], m[u], l[u], sl);
+  }
+  if constexpr (WIDE) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] *= f;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float w = exp2_hw((m[u] - mz) * sl);
-      lt = fmaf(l[u], w, lt);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[u][e], w, acc[e]);
+    for (int o = D / 4; o < 64; o <<= 1) {  // lower and upper halves, so every lane adds in the same order
+      Joined x{v4f{__shfl_xor(y.acc[0], o, 64), __shfl_xor(y.acc[1], o, 64), __shfl_xor(y.acc[2], o, 64),
+                   __shfl_xor(y.acc[3], o, 64)},
+               __shfl_xor(y.m, o, 64), __shfl_xor(y.l, o, 64)};
+      y.add(x.acc, x.m, x.l, sl);
     }
-  }
-  sum[at][d] = acc;
-  if (d == 0) {
-    msum[at] = mt;
-    lsum[at] = lt;
-  }
-  __syncthreads();
-  if (at) return;
-  mt = -kInf;
+    if (at) return;
+  } else {
+    sum[at][d] = y.acc;
+    if (d == 0) {
+      msum[at] = y.m;
+      lsum[at] = y.l;
+    }
+    __syncthreads();
+    if (at) return;
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) mt = fmaxf(mt, msum[g]);
-  const float mz = mt == -kInf ? 0.f : mt;
-  acc = v4f{0.f, 0.f, 0.f, 0.f};
-  lt = 0.f;
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    const float w = exp2_hw((msum[g] - mz) * sl);
-    const v4f x = sum[g][d];
-    lt = fmaf(lsum[g], w, lt);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[e], w, acc[e]);
+    for (int g = 1; g < kGroups; ++g) y.add(sum[g][d], msum[g], lsum[g], sl);
   }
-  const float inv = lt > 0.f ? 1.f / lt : 0.f;
+  const float inv = y.l > 0.f ? 1.f / y.l : 0.f;
   st_global(reinterpret_cast<u32x2*>(out) + d,
-            u32x2{pk_bf16(acc[0] * inv, acc[1] * inv), pk_bf16(acc[2] * inv, acc[3] * inv)});
+            u32x2{pk_bf16(y.acc[0] * inv, y.acc[1] * inv), pk_bf16(y.acc[2] * inv, y.acc[3] * inv)});
 }
 
 // ------------------------------------------------------------------- host
@@ -631,14 +673,14 @@ size_t attn_cache_ws_bytes(int64_t, int64_t draft, int64_t hq, int64_t hkv, int6
 
 template <int D>
 static hipError_t cache_launch(const AttnCacheArgs& a, hipStream_t s) {
-  const dim3 rows((unsigned)((int64_t)a.batch * a.draft * a.hq));
+  const int64_t rows = (int64_t)a.batch * a.draft * a.hq;
   const bool wide = a.hq / a.hkv * a.draft > kCols;
   if (wide) attn_cache_wide_kernel<D><<<dim3(CacheForm<D, true>::kBlocks), 256, 0, s>>>(a);
   else attn_cache_kernel<D><<<dim3(CacheForm<D, false>::kBlocks), 256, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (wide) attn_cache_join_kernel<D, true><<<rows, 256, 0, s>>>(a);
-  else attn_cache_join_kernel<D, false><<<rows, 256, 0, s>>>(a);
+  if (wide) attn_cache_join_kernel<D, true><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, s>>>(a);
+  else attn_cache_join_kernel<D, false><<<dim3((unsigned)rows), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 hipError_t launch_attn_cache(const AttnCacheArgs& a, int64_t d, hipStream_t s) {
