@@ -643,7 +643,8 @@ int bitlinear_qk_rope_bwd(const void *Q, const void *K, int x_type, int64_t q_st
  *   ws         bitlinear_attn_fwd_workspace_bytes() bytes, 256-byte
  *              aligned, clobbered; may be NULL when that is 0.  Calls that
  *              overlap on one workspace race.
- * batch 1..65535, scale finite and > 0; total_q == 0 is a no-op. */
+ * batch 1..65535, total_q and total_k at most 2^31 - 1024, scale finite and
+ * > 0; total_q == 0 is a no-op. */
 size_t bitlinear_attn_fwd_workspace_bytes(int64_t batch, int64_t total_q, int64_t total_k,
                                           int64_t hq, int64_t hkv, int64_t d);
 int bitlinear_attn_fwd(const uint16_t *Q, const uint16_t *K, const uint16_t *V, int64_t q_stride,

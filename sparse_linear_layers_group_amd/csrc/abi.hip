@@ -1187,8 +1187,9 @@ constexpr int64_t kStrideLimit = (int64_t)1 << 22;  // a 64-row tile's offsets s
 int check_attn(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d, float scale) {
   TRY(check_heads(hq, hkv, d));
   if (batch < 1 || batch > 65535) return fail(BL_ESHAPE, "batch must be in 1..65535 (got %lld)", (long long)batch);
-  if (total_q < 0 || total_k < 0 || total_q >= kLimit || total_k >= kLimit)
-    return fail(BL_ESHAPE, "total_q and total_k must be in [0, 2^31)");
+  // (room for a tile behind the last row in 32 bits)
+  if (total_q < 0 || total_k < 0 || total_q > kLimit - 1024 || total_k > kLimit - 1024)
+    return fail(BL_ESHAPE, "total_q and total_k must be in [0, 2^31 - 1024]");
   // workgroups of a launch (tiles of at least 32 rows, and 16 bytes a thread)
   if ((total_q / 32 + batch + 8) * hq >= kLimit || total_k / 32 * hkv >= kLimit ||
       total_q * hq * (d / 8) / 256 >= kLimit - 1)

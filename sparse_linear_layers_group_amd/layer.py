@@ -117,6 +117,78 @@ class LatentWeights:
         bl.bitlinear_latent_update(self.master, dW, self.master.numel(), lr, self.W, stream=stream)
 
 
+class BlockAttention:
+    """What stands between a block's q, k, v BitLinears and its o BitLinear:
+    head norms with the rotation, and causal attention over packed sequences
+    (prompts and training) or over a paged cache (serving).  Owns the rotation
+    table; outputs and workspaces are allocated per call on torch's current
+    stream, as torch's own operators do."""
+
+    def __init__(self, hq, hkv, d, max_pos, base=10000.0, q_weight=None, k_weight=None, eps=1e-6, scale=None,
+                 device="cuda"):
+        self.hq, self.hkv, self.d, self.eps = int(hq), int(hkv), int(d), float(eps)
+        self.q_weight, self.k_weight = q_weight, k_weight
+        self.scale = float(scale) if scale is not None else self.d ** -0.5
+        self.device = device
+        self.table = torch.empty(max_pos, self.d // 2, 2, dtype=torch.float32, device=device)
+        bl.bitlinear_rope_table(max_pos, self.d, base, self.table)
+
+    def _bf16(self, rows, heads):
+        return torch.empty(rows, heads * self.d, dtype=torch.bfloat16, device=self.device)
+
+    def _scratch(self, nbytes):
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
+
+    def rotate(self, Q, K, V, pos, cache=None, slots=None):
+        """(Qr, Kr, Vr) of the projections' rows; with a cache (K, V) and the
+        tokens' slots in it, K and V rows go there instead."""
+        n = pos.numel()
+        Qr = self._bf16(n, self.hq)
+        Kr, Vr = cache if cache is not None else (self._bf16(n, self.hkv), self._bf16(n, self.hkv))
+        bl.bitlinear_qk_rope(Q, K, V, n, self.hq, self.hkv, self.d, self.q_weight, self.k_weight, self.eps, self.table,
+                             pos, Qr, Kr, Vr, slots=slots)
+        return Qr, Kr, Vr
+
+    def rotate_bwd(self, Q, K, pos, dQr, dKr):
+        """(dQ, dK, dq_weight, dk_weight); the last two None without norms."""
+        n, norms = pos.numel(), self.q_weight is not None
+        dQ, dK = self._bf16(n, self.hq), self._bf16(n, self.hkv)
+        gq = torch.empty(self.d, device=self.device) if norms else None
+        gk = torch.empty(self.d, device=self.device) if norms else None
+        ws = self._scratch(bl.bitlinear_qk_rope_bwd_workspace_bytes(self.d)) if norms else None
+        bl.bitlinear_qk_rope_bwd(Q if norms else None, K if norms else None, n, self.hq, self.hkv, self.d,
+                                 self.q_weight, self.k_weight, self.eps, self.table, pos, dQr, dKr, dQ, dK, gq, gk, ws=ws)
+        return dQ, dK, gq, gk
+
+    def attend(self, Qr, Kr, Vr, cu_q, cu_k):
+        """(O, lse) of packed sequences."""
+        tq, tk, b = Qr.shape[0], Kr.shape[0], cu_q.numel() - 1
+        O, lse = self._bf16(tq, self.hq), torch.empty(self.hq, tq, device=self.device)
+        ws = self._scratch(bl.bitlinear_attn_fwd_workspace_bytes(b, tq, tk, self.hq, self.hkv, self.d))
+        bl.bitlinear_attn_fwd(Qr, Kr, Vr, cu_q, cu_k, b, self.hq, self.hkv, self.d, self.scale, O, lse, ws=ws)
+        return O, lse
+
+    def attend_bwd(self, Qr, Kr, Vr, O, lse, dO, cu_q, cu_k):
+        """(dQr, dKr, dV) for dO in bfloat16 or float32 (the o BitLinear's dX)."""
+        tq, tk, b = Qr.shape[0], Kr.shape[0], cu_q.numel() - 1
+        dQ, dK, dV = self._bf16(tq, self.hq), self._bf16(tk, self.hkv), self._bf16(tk, self.hkv)
+        ws = self._scratch(bl.bitlinear_attn_bwd_workspace_bytes(b, tq, tk, self.hq, self.hkv, self.d))
+        bl.bitlinear_attn_bwd(Qr, Kr, Vr, O, lse, dO, cu_q, cu_k, b, self.hq, self.hkv, self.d, self.scale, dQ, dK, dV,
+                              ws=ws)
+        return dQ, dK, dV
+
+    def attend_cache(self, Qr, cache, pages, page, lens, tree=None):
+        """O of each sequence's newest tokens (lens.numel() * draft rows of Qr)
+        over its cache of pages."""
+        b = lens.numel()
+        draft = Qr.shape[0] // b
+        O = self._bf16(b * draft, self.hq)
+        ws = self._scratch(bl.bitlinear_attn_cache_workspace_bytes(b, draft, self.hq, self.hkv, self.d))
+        bl.bitlinear_attn_cache(Qr, cache[0], cache[1], pages, page, lens, tree, b, draft, self.hq, self.hkv, self.d,
+                                self.scale, O, ws=ws)
+        return O
+
+
 def dense_to_sparse(step, switch_step, n, m):
     """N:M pattern of a dense-to-sparse schedule: dense (8:8) before
     switch_step, n:m from it on."""

@@ -268,3 +268,38 @@ def test_few_rows_with_many_keys(hq, hkv, d, q_lens, k_lens):
     assert bl.bitlinear_attn_fwd_workspace_bytes(len(q_lens), sum(q_lens), sum(k_lens), hq, hkv, d) > 0
     q, k, v, do = inputs(q_lens, k_lens, hq, hkv, d, seed=20, extra=3)
     check(q, k, v, do, q_lens, k_lens)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_other_sequences_may_hold_anything(d):
+    """Not-a-number rows of one sequence stay in it, forward and backward."""
+    lens = [70, 33, 190]
+    q, k, v, do = inputs(lens, lens, 4, 2, d, seed=21)
+    do = do.to(BF)
+    clean = forward(q, k, v, lens, lens, 0.1)
+    grads = backward(q, k, v, *clean, do, lens, lens, 0.1)
+    q2, k2, v2, do2 = (t.clone() for t in (q, k, v, do))
+    for t in (q2, k2, v2, do2):
+        t[70:103] = float("nan")
+    o, lse = forward(q2, k2, v2, lens, lens, 0.1)
+    keep = torch.ones(sum(lens), dtype=torch.bool, device="cuda")
+    keep[70:103] = False
+    assert torch.equal(o[keep], clean[0][keep]) and torch.equal(lse[:, keep], clean[1][:, keep])
+    for x, y in zip(backward(q2, k2, v2, o, lse, do2, lens, lens, 0.1), grads):
+        assert torch.equal(x[keep], y[keep])
+
+
+def test_two_streams_at_once():
+    """Two calls of different sizes, each with its own buffers."""
+    a, b = [300, 40], [129, 513, 7]
+    qa, qb = inputs(a, a, 4, 2, 128, seed=22), inputs(b, b, 4, 2, 128, seed=23)
+    want = [forward(*q[:3], n, n, 0.1) for q, n in ((qa, a), (qb, b))]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for st, q, n in zip(streams, (qa, qb), (a, b)):
+        with torch.cuda.stream(st):
+            got.append(forward(*q[:3], n, n, 0.1))
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
