@@ -294,25 +294,30 @@ __device__ __forceinline__ Item find_item(const int32_t* cu, int64_t total, cons
   return none;
 }
 
-// Workgroup id -> (item rank, head) for `pairs` key/value heads and `per`
-// workgroups of each.  Consecutive workgroups go to different XCDs, whose L2
-// caches are separate.  Eight ranks at a time are dealt so that an XCD's
-// workgroups have the fewest possible key/value heads among them (8 * pairs
-// (head, rank) pairs in that order, `pairs` to each XCD): they read the same
-// rows at about the same time, and those reads meet in its L2.  Odd blocks
-// of ranks run backwards, so no XCD always has the longer items.
+// Workgroup id -> (item rank, head) for `items` ranks, `pairs` key/value
+// heads and `per` workgroups of each.  Consecutive workgroups go to different
+// XCDs, whose L2 caches are separate.  Eight ranks at a time are dealt so
+// that an XCD's workgroups have the fewest possible key/value heads among
+// them (8 * pairs (head, rank) pairs in that order, `pairs` to each XCD):
+// they read the same rows at about the same time, and those reads meet in its
+// L2.  Odd blocks of ranks run backwards, so no XCD always has the longer
+// items.  Fewer than eight ranks are simply numbered: padded to eight, most
+// workgroups of a small call would have nothing to do.
 struct Place {
   int rank, pair, part;
 };
-__device__ __forceinline__ Place place_of(int id, int pairs, int per) {
+__device__ __forceinline__ Place place_of(int id, int items, int pairs, int per) {
+  if (items < 8) {
+    const int s = id / per, rank = s / pairs;
+    return Place{rank, s - rank * pairs, id - s * per};
+  }
   const int xcd = id & 7, slot = id >> 3;
   const int s = slot / per, block = s / pairs;
   const int at = xcd * pairs + (s - block * pairs);
   const int r = at & 7;
   return Place{block * 8 + (block & 1 ? 7 - r : r), at >> 3, slot - s * per};
 }
-inline int64_t placed_blocks(int64_t items, int64_t pairs, int64_t per) {
-  return (items + 7) / 8 * 8 * pairs * per;
-}
+inline int64_t placed_items(int64_t items) { return items < 8 ? items : (items + 7) / 8 * 8; }
+inline int64_t placed_blocks(int64_t items, int64_t pairs, int64_t per) { return placed_items(items) * pairs * per; }
 
 }  // namespace bl

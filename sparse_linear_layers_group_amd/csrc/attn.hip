@@ -11,7 +11,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kQRows = 128;  // query rows of a forward / dQ workgroup: 32 per wavefront
 constexpr int kKRows = 64;   // key rows of a tile in LDS
-constexpr int kExactTiles = 4;  // dQ workgroups with at most this many key tiles form delta from P dP
+constexpr int kExactTiles = 2;  // dQ workgroups with at most this many key tiles form delta from P dP
 constexpr int kBKeys = 64;   // key rows of a dK / dV workgroup: two blocks of 32, four wavefronts each
 constexpr int kBRows = 128;  // query rows of its stages: 32 per wavefront
 constexpr int kMaxSplits = 8;
@@ -165,13 +165,13 @@ __device__ __forceinline__ int key_tiles(const Rows& qr, const Rows& kr, int q0)
   return (clampi(last + kr.len - qr.len, 0, kr.len) + kKRows - 1) / kKRows;
 }
 template <int D>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int splits, int target,
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int items, int splits, int target,
                                                          float* __restrict__ part) {
   typedef Tile<D> T;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.hq / a.hkv;
-  const Place pl = place_of(blockIdx.x, a.hkv, group * splits);
+  const Place pl = place_of(blockIdx.x, items, a.hkv, group * splits);
   const Item it = find_item(a.cu_q, a.total_q, a.cu_k, a.total_k, a.batch, kQRows, pl.rank);
   if (it.seq < 0) return;
   const int split = pl.part / group, kvh = pl.pair, head = kvh * group + pl.part - split * group;
@@ -443,22 +443,23 @@ __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int spli
 // see few keys make up most of the gradients' norm: there it raised the
 // relative error of dQ and dK from 2.4e-3 to 2.7e-3 (bf16 outputs alone:
 // 1.7e-3).  Workgroups of at most kExactTiles key tiles therefore form
-// delta = sum P dP in binary32 in a sweep of their own and leave it in
-// memory for the dK / dV pass.
+// delta = sum P dP in binary32 in a sweep of their own over tiles that stay
+// in LDS, and leave it in memory for the dK / dV pass (four tiles instead of
+// two gain another 1 % of the error and double the time of small calls).
 
 // The dQ pass comes first and leaves for the other what it adds to its
 // products as the accumulators' first values, -lse / scale to S (-inf where
 // a row sees no key, so P becomes 0) and -delta to dP, and dO rounded to
 // bf16 where it comes in binary32.
 template <int D>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, uint16_t* __restrict__ copy,
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, int items, uint16_t* __restrict__ copy,
                                                         float* __restrict__ ndelta, float* __restrict__ shift) {
   typedef Tile<D> T;
   constexpr int kTile = PairBytes<D>::kTile;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.hq / a.hkv;
-  const Place pl = place_of(blockIdx.x, a.hkv, group);
+  const Place pl = place_of(blockIdx.x, items, a.hkv, group);
   const Item it = find_item(a.cu_q, a.total_q, a.cu_k, a.total_k, a.batch, kQRows, pl.rank);
   if (it.seq < 0) return;
   const int kvh = pl.pair, head = kvh * group + pl.part;
@@ -471,6 +472,19 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, uint16_t
   const int wlast = w0 + 32 < qr.len ? w0 + 32 : qr.len;
   const int tiles = (clampi(last + off, 0, kr.len) + kKRows - 1) / kKRows;
   const int wtiles = w0 < qr.len ? (clampi(wlast + off, 0, kr.len) + kKRows - 1) / kKRows : 0;
+
+  // the first tiles are on their way before anything is waited for; few keys:
+  // both of them, and they stay
+  const bool few = tiles <= kExactTiles;
+  const PairDma<D> dma(lane, wave, a.k_stride, a.v_stride);
+  const uint16_t* kp = a.K + (int64_t)kr.start * a.k_stride + (int64_t)kvh * D;
+  const uint16_t* vp = a.V + (int64_t)kr.start * a.v_stride + (int64_t)kvh * D;
+  auto issue = [&](lds_char* st, int t) {
+    if (t < tiles)
+      dma.issue(st, kp + (int64_t)t * kKRows * a.k_stride, vp + (int64_t)t * kKRows * a.v_stride, kr.len - t * kKRows);
+  };
+  issue(pair_stage<D, 0>(), 0);
+  if (few) issue(pair_stage<D, 1>(), 1);
 
   const int64_t row = qr.start + (in ? r : qr.len - 1), at = (row * a.hq + head) * D;
   const int64_t sum_at = (int64_t)head * a.total_q + row;
@@ -508,9 +522,6 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, uint16_t
     st_global(shift + sum_at, lse == -kInf ? -kInf : -lse / a.scale);
   }
   const float le = lse == -kInf ? -kInf : -lse * kLog2e;
-  const PairDma<D> dma(lane, wave, a.k_stride, a.v_stride);
-  const uint16_t* kp = a.K + (int64_t)kr.start * a.k_stride + (int64_t)kvh * D;
-  const uint16_t* vp = a.V + (int64_t)kr.start * a.v_stride + (int64_t)kvh * D;
   uint32_t ka[D / 16];
   TrAddr kt[D / 32];
 #pragma unroll
@@ -521,68 +532,74 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, uint16_t
   const int seen = r + off - 4 * (lane >> 5);
   v16f dq[D / 32];
   clear<D / 32>(dq);
-  float exact = 0.f;  // this lane's share of sum P dP
 
-  auto step = [&](auto stage, auto sums, int t) {
-    constexpr int P = decltype(stage)::value;
-    wait_dma<0>();
-    lds_barrier();
-    if (t + 1 < tiles)
-      dma.issue(pair_stage<D, P ^ 1>(), kp + (int64_t)(t + 1) * kKRows * a.k_stride,
-                vp + (int64_t)(t + 1) * kKRows * a.v_stride, kr.len - (t + 1) * kKRows);
-    if (t >= wtiles) return;
-    const lds_char* st = pair_stage<D, P>();
-    const bool diagonal = t * kKRows + kKRows > w0 + off + 1;
-    const int x = seen - t * kKRows;
+  // P and dP of 32 keys
+  auto probs = [&](const lds_char* st, int t, int i, v16f* s, v16f* g) {
+    clear<1>(s);
+    clear<1>(g);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      s[0] = mfma32(lds_read8(st + ka[k] + i * 32 * T::kRowBytes), qf[k], s[0]);
+      g[0] = mfma32(lds_read8(st + kTile + ka[k] + i * 32 * T::kRowBytes), gf[k], g[0]);
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) s[0][j] = exp2_hw(fmaf(s[0][j], sl, le));
+    if (t * kKRows + kKRows > w0 + off + 1) {  // the diagonal
+      const int x = seen - t * kKRows;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[0][j] = 32 * i + 8 * (j >> 2) + (j & 3) <= x ? s[0][j] : 0.f;
+    }
+  };
+  auto grads = [&](auto stage, int t) {
+    const lds_char* st = pair_stage<D, decltype(stage)::value>();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       v16f s[1], g[1];
-      clear<1>(s);
-      clear<1>(g);
+      probs(st, t, i, s, g);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        s[0] = mfma32(lds_read8(st + ka[k] + i * 32 * T::kRowBytes), qf[k], s[0]);
-        g[0] = mfma32(lds_read8(st + kTile + ka[k] + i * 32 * T::kRowBytes), gf[k], g[0]);
+      for (int j = 0; j < 16; ++j) s[0][j] *= g[0][j] + nd;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const v8bf p = operand_of(s[0], k);
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) dq[d] = mfma32(tr_operand<D>(st, kt[d], 32 * i + 16 * k), p, dq[d]);
       }
+    }
+  };
+  typedef std::integral_constant<int, 0> S0;
+  typedef std::integral_constant<int, 1> S1;
+  if (few) {
+    wait_dma<0>();
+    lds_barrier();
+    float exact = 0.f;  // this lane's share of sum P dP
+    auto sums = [&](auto stage, int t) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s[0][j] = exp2_hw(fmaf(s[0][j], sl, le));
-      if (diagonal) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) s[0][j] = 32 * i + 8 * (j >> 2) + (j & 3) <= x ? s[0][j] : 0.f;
-      }
-      if constexpr (decltype(sums)::value) {
+      for (int i = 0; i < 2; ++i) {
+        v16f s[1], g[1];
+        probs(pair_stage<D, decltype(stage)::value>(), t, i, s, g);
 #pragma unroll
         for (int j = 0; j < 16; ++j) exact = fmaf(s[0][j], g[0][j], exact);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) s[0][j] *= g[0][j] + nd;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const v8bf p = operand_of(s[0], k);
-#pragma unroll
-          for (int d = 0; d < D / 32; ++d) dq[d] = mfma32(tr_operand<D>(st, kt[d], 32 * i + 16 * k), p, dq[d]);
-        }
       }
-    }
-  };
-  auto sweep = [&](auto sums) {
-    typedef std::integral_constant<int, 0> S0;
-    typedef std::integral_constant<int, 1> S1;
-    if (tiles > 0) dma.issue(pair_stage<D, 0>(), kp, vp, kr.len);
-    int t = 0;
-    for (; t + 1 < tiles; t += 2) {
-      step(S0{}, sums, t);
-      step(S1{}, sums, t + 1);
-    }
-    if (t < tiles) step(S0{}, sums, t);
-  };
-  if (tiles <= kExactTiles) {
-    sweep(std::true_type{});
+    };
+    if (wtiles > 0) sums(S0{}, 0);
+    if (wtiles > 1) sums(S1{}, 1);
     nd = -half_join(exact, [](float u, float v) { return u + v; });
     if (in && lane < 32) st_global(ndelta + sum_at, nd);
-    lds_barrier();  // both stages are free for the second sweep
   }
-  sweep(std::false_type{});
+  auto step = [&](auto stage, int t) {
+    if (!few) {  // (few: both tiles are there)
+      wait_dma<0>();
+      lds_barrier();
+      issue(pair_stage<D, decltype(stage)::value ^ 1>(), t + 1);
+    }
+    if (t < wtiles) grads(stage, t);
+  };
+  int t = 0;
+  for (; t + 1 < tiles; t += 2) {
+    step(S0{}, t);
+    step(S1{}, t + 1);
+  }
+  if (t < tiles) step(S0{}, t);
   store_row<D>(a.dQ + at, dq, a.scale, lane, in);
 }
 
@@ -603,7 +620,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, uint16_t
 // ([split][dK, dV][total_k][hkv][D]), which attn_dkv_join_kernel adds in
 // order.
 template <int D>
-__global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, const uint16_t* __restrict__ dO,
+__global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, int items, const uint16_t* __restrict__ dO,
                                                          const float* __restrict__ ndelta,
                                                          const float* __restrict__ shift, int splits,
                                                          float* __restrict__ part) {
@@ -612,7 +629,7 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, const u
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = wave & 1, rq = wave >> 1;
-  const Place pl = place_of(blockIdx.x, a.hkv, splits);
+  const Place pl = place_of(blockIdx.x, items, a.hkv, splits);
   const Item it = find_item(a.cu_k, a.total_k, a.cu_q, a.total_q, a.batch, kBKeys, pl.rank);
   if (it.seq < 0) return;
   const int kvh = pl.pair, split = pl.part, group = a.hq / a.hkv;
@@ -639,6 +656,23 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, const u
                  dma_offset<D>(lane, ins % T::kVariants, a.v_stride) + (uint32_t)(ins * T::kDmaRows * (int)a.v_stride * 2));
     }
   }
+  const int64_t g_stride = (int64_t)a.hq * D;
+  const PairDma<D, kBRows, 8> dma(lane, wave, a.q_stride, g_stride);
+  auto issue = [&](lds_char* st, int h, int t) {
+    const int64_t row = qr.start + t * kBRows;
+    const int rows = qr.len - t * kBRows;
+    const int64_t head = (int64_t)kvh * group + h;
+    dma.issue(st, a.Q + row * a.q_stride + head * D, dO + row * g_stride + head * D, rows);
+    if (rq < 2) {  // the rows' first values, 64 rows a wavefront; zeros past the sequence (dO is 0 there)
+      const float* p = (rq ? ndelta : shift) + head * a.total_q + row;
+      lds_load4(rows_rsrc(p, (uint32_t)((rows < kBRows ? rows : kBRows) * 4)),
+                st + 2 * kTile + 4 * kBRows * rq + 256 * kw, (uint32_t)(lane + 64 * kw) * 4);
+    }
+  };
+  // The last rows first, all heads of the group for each stage: workgroups of
+  // different keys that start together then read the same stages together.
+  int t = first + n - 1 - i0 / group, h = i0 % group;  // of the step being computed
+  if (i0 < i1) issue(wide_stage<D, 0>(), h, t);
   constexpr int kHeld = D == 128 ? 6 : 4;  // (all eight: 256 registers and spills)
   typedef __attribute__((address_space(3))) v8bf lds_v8bf;
   lds_char* const kx = (lds_char*)g_k128 + 2048 * kw + 16 * lane;
@@ -655,8 +689,6 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, const u
       }
     }
   }
-  const int64_t g_stride = (int64_t)a.hq * D;
-  const PairDma<D, kBRows, 8> dma(lane, wave, a.q_stride, g_stride);
   // LDS addresses: pieces 2s and columns 32t are address bits of their own
   // (5.. and 6..), so one exclusive or makes each from the first.  They are
   // made again in every step: kept, they would cost 13 registers.
@@ -668,20 +700,6 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, const u
   clear<D / 32>(dk);
   clear<D / 32>(dv);
 
-  auto issue = [&](lds_char* st, int h, int t) {
-    const int64_t row = qr.start + t * kBRows;
-    const int rows = qr.len - t * kBRows;
-    const int64_t head = (int64_t)kvh * group + h;
-    dma.issue(st, a.Q + row * a.q_stride + head * D, dO + row * g_stride + head * D, rows);
-    if (rq < 2) {  // the rows' first values, 64 rows a wavefront; zeros past the sequence (dO is 0 there)
-      const float* p = (rq ? ndelta : shift) + head * a.total_q + row;
-      lds_load4(rows_rsrc(p, (uint32_t)((rows < kBRows ? rows : kBRows) * 4)),
-                st + 2 * kTile + 4 * kBRows * rq + 256 * kw, (uint32_t)(lane + 64 * kw) * 4);
-    }
-  };
-  // The last rows first, all heads of the group for each stage: workgroups of
-  // different keys that start together then read the same stages together.
-  int t = first + n - 1 - i0 / group, h = i0 % group;  // of the step being computed
   auto step = [&](auto stage, int i) {
     constexpr int P = decltype(stage)::value;
     wait_dma<0>();
@@ -768,7 +786,6 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, const u
     }
   };
 
-  if (i0 < i1) issue(wide_stage<D, 0>(), h, t);
   int i = i0;
   for (; i + 1 < i1; i += 2) {
     step(std::integral_constant<int, 0>{}, i);
@@ -902,7 +919,10 @@ static FwdSplit fwd_split(int64_t batch, int64_t total_q, int64_t total_k, int64
   // (rows of long prompts see half of the keys on average)
   const int64_t mean = total_q >= total_k ? (keys + 1) / 2 : keys;
   const int64_t room = 512 - tiles / 2, target = (tiles * mean + room - 1) / room;  // (a tile ends in half a part)
-  return FwdSplit{kMaxSplits, (int)(target < kMinSplitTiles ? kMinSplitTiles : target)};
+  const int64_t t = target < kMinSplitTiles ? kMinSplitTiles : target;
+  const int64_t most = (2 * mean + t - 1) / t;  // parts of a sequence of twice the mean length
+  if (most < 2) return FwdSplit{1, 1};
+  return FwdSplit{most > kMaxSplits ? kMaxSplits : (int)most, (int)t};
 }
 
 // workspace: partial O, m and l of split tiles
@@ -916,7 +936,7 @@ static hipError_t fwd_launch(const AttnArgs& a, float* part, hipStream_t s) {
   const FwdSplit p = fwd_split(a.batch, a.total_q, a.total_k, a.hq);
   const int64_t items = most_tiles(a.total_q, a.batch, kQRows);
   attn_fwd_kernel<D><<<dim3((unsigned)placed_blocks(items, a.hkv, a.hq / a.hkv * p.splits)), 256, 0, s>>>(
-      a, p.splits, p.target, part);
+      a, (int)items, p.splits, p.target, part);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   attn_fwd_join_kernel<D><<<dim3((unsigned)(items * a.hq * (kQRows / (256 / (D / 4))))), 256, 0, s>>>(
@@ -927,10 +947,10 @@ hipError_t launch_attn_fwd(const AttnArgs& a, int64_t d, void* ws, hipStream_t s
   return d == 128 ? fwd_launch<128>(a, static_cast<float*>(ws), s) : fwd_launch<64>(a, static_cast<float*>(ws), s);
 }
 
-// Workgroups that share a dK / dV tile: enough that every CU has one
-// (D = 64: two), by the number of whole tiles the totals make.
-static int dkv_splits(int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d) {
-  const int64_t tiles = (total_k + kBKeys - 1) / kBKeys * hkv, want = d == 128 ? 256 : 512;
+// Workgroups that share a dK / dV tile: as many as the chip runs at once, one
+// per CU (D = 64: two).  (A workgroup without steps still waits for a place.)
+static int dkv_splits(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d) {
+  const int64_t tiles = placed_items(most_tiles(total_k, batch, kBKeys)) * hkv, want = d == 128 ? 256 : 512;
   const int64_t steps = hq / hkv * ((total_q + kBRows - 1) / kBRows);
   int64_t s = tiles > 0 ? want / tiles : 1;
   s = s > kMaxSplits ? kMaxSplits : s;
@@ -940,8 +960,8 @@ static int dkv_splits(int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv,
 
 // workspace: -delta, -lse / scale ([hq][total_q] each), dO in bf16, partial
 // dK and dV of split tiles
-size_t attn_bwd_ws_bytes(int64_t, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d) {
-  const int splits = dkv_splits(total_q, total_k, hq, hkv, d);
+size_t attn_bwd_ws_bytes(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d) {
+  const int splits = dkv_splits(batch, total_q, total_k, hq, hkv, d);
   return 2 * bwd_row_bytes(total_q, hq) + align256((size_t)total_q * hq * d * 2) +
          (splits > 1 ? (size_t)splits * 2 * total_k * hkv * d * 4 : 0);
 }
@@ -956,15 +976,16 @@ static hipError_t bwd_launch(const AttnBwdArgs& a, hipStream_t s) {
                                          align256((size_t)a.total_q * a.hq * D * 2));
   const uint16_t* dO = a.do_f32 ? copy : static_cast<const uint16_t*>(a.dO);
   if (a.total_q > 0) {
-    attn_dq_kernel<D><<<dim3((unsigned)placed_blocks(most_tiles(a.total_q, a.batch, kQRows), a.hkv, a.hq / a.hkv)), 256, 0, s>>>(
-        a, copy, delta, shift);
+    const int64_t items = most_tiles(a.total_q, a.batch, kQRows);
+    attn_dq_kernel<D><<<dim3((unsigned)placed_blocks(items, a.hkv, a.hq / a.hkv)), 256, 0, s>>>(a, (int)items, copy,
+                                                                                               delta, shift);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.total_k > 0) {
-    const int splits = dkv_splits(a.total_q, a.total_k, a.hq, a.hkv, D);
+    const int splits = dkv_splits(a.batch, a.total_q, a.total_k, a.hq, a.hkv, D);
     const int64_t items = most_tiles(a.total_k, a.batch, kBKeys);
-    attn_dkv_kernel<D><<<dim3((unsigned)placed_blocks(items, a.hkv, splits)), 512, 0, s>>>(a, dO, delta, shift,
+    attn_dkv_kernel<D><<<dim3((unsigned)placed_blocks(items, a.hkv, splits)), 512, 0, s>>>(a, (int)items, dO, delta, shift,
                                                                                        splits, part);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
