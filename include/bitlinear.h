@@ -563,7 +563,9 @@ int bitlinear_bwd_tiles(int tiles);
  * have that many elements between rows (a multiple of 16 bytes, at least the
  * row), so slices of one fused projection are taken as they are; every
  * other array is contiguous.  Offsets are formed in 64 bits: only row
- * counts have to stay below 2^31.  Rows of inputs that belong to no
+ * counts have to stay below 2^31, and the threads of one launch below 2^32
+ * (limits given below).  Outputs and workspaces must not alias inputs or each
+ * other.  Rows of inputs that belong to no
  * sequence may hold anything, infinities and NaN included; in rows that do,
  * values are finite. */
 #define BL_TYPE_F32   0
@@ -572,7 +574,7 @@ int bitlinear_bwd_tiles(int tiles);
 /* Table of the rotation: table[p*(d/2) + i] = (cos a, sin a) with
  * a = p * base^(-2i/d), formed in binary64 and rounded once to binary32.
  *   table  device float [max_pos][d/2][2], written.  max_pos >= 1, base > 0
- * finite.  A caller with scaled positions fills its own table. */
+ * finite, max_pos * d/2 at most 2^32 - 256.  A caller with scaled positions fills its own table. */
 int bitlinear_rope_table(int64_t max_pos, int64_t d, double base, float *table, void *stream);
 
 /* Head norms of queries and keys with the position rotation, in one pass.
@@ -593,7 +595,7 @@ int bitlinear_rope_table(int64_t max_pos, int64_t d, double base, float *table, 
  *              skipped (padding), and the others must be distinct.
  *   kv_rows    rows of Kr and Vr (without slots: at least tokens).
  *   Qr         device bf16 [tokens][hq*d]; Kr, Vr  device bf16 [kv_rows][hkv*d].
- * Outputs must not alias inputs.  tokens == 0 is a no-op. */
+ * tokens * ceil((hq + 2 hkv) d / 2048) below 2^26 - 3.  tokens == 0 is a no-op. */
 int bitlinear_qk_rope(const void *Q, const void *K, const void *V, int x_type, int64_t q_stride,
                       int64_t k_stride, int64_t v_stride, int64_t tokens, int64_t hq, int64_t hkv,
                       int64_t d, const float *q_weight, const float *k_weight, float eps,
@@ -643,8 +645,9 @@ int bitlinear_qk_rope_bwd(const void *Q, const void *K, int x_type, int64_t q_st
  *   ws         bitlinear_attn_fwd_workspace_bytes() bytes, 256-byte
  *              aligned, clobbered; may be NULL when that is 0.  Calls that
  *              overlap on one workspace race.
- * batch 1..65535, total_q and total_k at most 2^31 - 1024, scale finite and
- * > 0; total_q == 0 is a no-op. */
+ * batch 1..65535, total_q and total_k at most 2^31 - 1024, (total_q / 128 +
+ * batch + 8) * hq below 2^24, (total_k / 64 + batch + 8) * hkv below 2^23,
+ * scale finite and > 0; total_q == 0 is a no-op. */
 size_t bitlinear_attn_fwd_workspace_bytes(int64_t batch, int64_t total_q, int64_t total_k,
                                           int64_t hq, int64_t hkv, int64_t d);
 int bitlinear_attn_fwd(const uint16_t *Q, const uint16_t *K, const uint16_t *V, int64_t q_stride,
@@ -697,7 +700,8 @@ int bitlinear_attn_bwd(const uint16_t *Q, const uint16_t *K, const uint16_t *V, 
  * Formulas and roundings as for bitlinear_attn_fwd.  Lengths, pages and tree
  * are read by the kernels: a captured graph may be replayed with others.
  * page a multiple of 16, draft 1..64, batch 1..65535, max_pages * page and
- * cache_rows below 2^31, and batch * (ceil(max_pages * page / 32) + 8) *
+ * cache_rows below 2^31, batch * draft * hq below 2^24 (below 2^26 where
+ * draft * (hq/hkv) > 32), and batch * (ceil(max_pages * page / 32) + 8) *
  * hkv * ceil(draft * (hq/hkv) / 32) below 2^31. */
 size_t bitlinear_attn_cache_workspace_bytes(int64_t batch, int64_t draft, int64_t hq, int64_t hkv,
                                             int64_t d);

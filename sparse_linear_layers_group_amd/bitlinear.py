@@ -605,6 +605,8 @@ def bitlinear_qk_rope(Q, K, V, tokens, hq, hkv, d, q_weight, k_weight, eps, tabl
     k, ks, _ = _rows(K, _FLOATS, hkv * d, "K", dev, tokens)
     v, vs, _ = _rows(V, _FLOATS, hkv * d, "V", dev, tokens) if V is not None else (None, 0, 0)
     kr = _arg(Kr, _BF16, None, "Kr", dev)
+    if min(hkv, d) < 1:
+        raise ValueError(f"hkv and d must be positive (got {hkv}, {d})")
     kv_rows = Kr.numel() // (hkv * d)
     if kv_rows * hkv * d != Kr.numel():
         raise ValueError(f"Kr must hold rows of {hkv * d} elements")
@@ -697,6 +699,8 @@ def bitlinear_attn_cache(Q, K, V, pages, page, lens, tree, batch, draft, hq, hkv
     dev = torch.cuda.current_device()
     q, qs, _ = _rows(Q, _BF16, hq * d, "Q", dev, batch * draft)
     k = _arg(K, _BF16, None, "K", dev)
+    if min(batch, hkv, d) < 1:
+        raise ValueError(f"batch, hkv and d must be positive (got {batch}, {hkv}, {d})")
     rows, width = K.numel() // (hkv * d), pages.numel() // batch
     if rows * hkv * d != K.numel():
         raise ValueError(f"K must hold rows of {hkv * d} elements")

@@ -1059,6 +1059,8 @@ int bitlinear_bwd(const uint16_t* dY, const int8_t* xq, const float* x_scale, co
 
 // ------------------------------------------------ head norms and rotation
 namespace {
+constexpr int64_t kMaxBlocks = (int64_t)1 << 24;  // of 256 threads: a launch holds fewer than 2^32
+
 int check_heads(int64_t hq, int64_t hkv, int64_t d) {
   if (d != 64 && d != 128) return fail(BL_ESHAPE, "head size must be 64 or 128 (got %lld)", (long long)d);
   if (hq < 1 || hkv < 1 || hq > 4096 || hq % hkv != 0)
@@ -1084,8 +1086,9 @@ int check_type(int type, const char* name) {
 int check_rope(int64_t tokens, const float* qw, const float* kw, float eps, const float* table, int64_t max_pos,
                const int32_t* pos, int64_t hq, int64_t hkv, int64_t d) {
   if (tokens < 0 || tokens >= kLimit) return fail(BL_ESHAPE, "tokens must be in [0, 2^31) (got %lld)", (long long)tokens);
-  // wavefronts of the launch: at least 16 head rows each
-  if (tokens * ((hq + 2 * hkv + 15) / 16) >= 4 * (kLimit - 1))
+  // wavefronts of the launch: 2048 / d head rows of a token each
+  const int64_t rows = 2048 / d;
+  if (tokens * ((hq + 2 * hkv + rows - 1) / rows) > 4 * (kMaxBlocks - 1))
     return fail(BL_ESHAPE, "too many head rows for one call (%lld tokens)", (long long)tokens);
   if (max_pos < 1 || max_pos >= kLimit) return fail(BL_ESHAPE, "max_pos must be in [1, 2^31) (got %lld)", (long long)max_pos);
   if ((qw == nullptr) != (kw == nullptr)) return fail(BL_EINVAL, "q_weight and k_weight: both or neither");
@@ -1102,6 +1105,7 @@ int check_rope(int64_t tokens, const float* qw, const float* kw, float eps, cons
 int bitlinear_rope_table(int64_t max_pos, int64_t d, double base, float* table, void* stream) {
   TRY(check_heads(1, 1, d));
   if (max_pos < 1 || max_pos >= kLimit) return fail(BL_ESHAPE, "max_pos must be in [1, 2^31) (got %lld)", (long long)max_pos);
+  if (max_pos * (d / 2) > 256 * (kMaxBlocks - 1)) return fail(BL_ESHAPE, "max_pos too large for one call");
   if (!(base > 0.0 && base < 1e300)) return fail(BL_EINVAL, "base must be finite and > 0");
   TRY(check_ptr(table, 16, "table"));
   return hip_status(bl::launch_rope_table(table, max_pos, d, base, reinterpret_cast<hipStream_t>(stream)),
@@ -1187,13 +1191,13 @@ constexpr int64_t kStrideLimit = (int64_t)1 << 22;  // a 64-row tile's offsets s
 int check_attn(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d, float scale) {
   TRY(check_heads(hq, hkv, d));
   if (batch < 1 || batch > 65535) return fail(BL_ESHAPE, "batch must be in 1..65535 (got %lld)", (long long)batch);
-  // (room for a tile behind the last row in 32 bits)
-  if (total_q < 0 || total_k < 0 || total_q > kLimit - 1024 || total_k > kLimit - 1024)
-    return fail(BL_ESHAPE, "total_q and total_k must be in [0, 2^31 - 1024]");
-  // workgroups of a launch (tiles of at least 32 rows, and 16 bytes a thread)
-  if ((total_q / 32 + batch + 8) * hq >= kLimit || total_k / 32 * hkv >= kLimit ||
-      total_q * hq * (d / 8) / 256 >= kLimit - 1)
-    return fail(BL_ESHAPE, "too many rows for one call");
+  if (total_q < 0 || total_k < 0) return fail(BL_ESHAPE, "total_q and total_k must not be negative");
+  // room for a tile behind the last row in 32 bits, and the workgroups of a
+  // launch: 256 threads for 128 query rows, 512 for 64 keys
+  if (total_q > kLimit - 1024 || total_k > kLimit - 1024 || (total_q / 128 + batch + 8) * hq >= kMaxBlocks ||
+      (total_k / 64 + batch + 8) * hkv >= kMaxBlocks / 2)
+    return fail(BL_ESHAPE, "too many rows for one call (total_q %lld, total_k %lld, batch %lld)", (long long)total_q,
+                (long long)total_k, (long long)batch);
   if (!(scale > 0.f && scale <= 3.0e38f)) return fail(BL_EINVAL, "scale must be finite and > 0");
   return BL_OK;
 }
@@ -1279,7 +1283,10 @@ int check_cache(int64_t batch, int64_t draft, int64_t hq, int64_t hkv, int64_t d
   TRY(check_heads(hq, hkv, d));
   if (batch < 1 || batch > 65535) return fail(BL_ESHAPE, "batch must be in 1..65535 (got %lld)", (long long)batch);
   if (draft < 1 || draft > 64) return fail(BL_ESHAPE, "draft must be in 1..64 (got %lld)", (long long)draft);
-  if (batch * draft * hq >= kLimit) return fail(BL_ESHAPE, "batch*draft*hq must stay below 2^31");
+  // the join's workgroups: one per row, or a wavefront per row
+  const int bits = draft * (hq / hkv) > 32 ? 26 : 24;
+  if (batch * draft * hq >= (int64_t)1 << bits)
+    return fail(BL_ESHAPE, "batch*draft*hq must stay below 2^%d (got %lld)", bits, (long long)(batch * draft * hq));
   return BL_OK;
 }
 }  // namespace

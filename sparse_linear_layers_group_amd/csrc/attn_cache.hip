@@ -120,7 +120,7 @@ __device__ __forceinline__ CacheRange cache_range(const AttnCacheArgs& a, int un
   CacheRange r{0, 0, a.batch, 0};
   if ((int64_t)blockIdx.x * per >= all) return r;
   r.g0 = blockIdx.x * per;
-  r.g1 = r.g0 + per < all ? r.g0 + per : all;
+  r.g1 = per < all - r.g0 ? r.g0 + per : all;
   int before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
     const int c = b0 + lane < a.batch ? unit_places<F>(cache_tiles<F>(cache_len(a, b0 + lane))) * units : 0;

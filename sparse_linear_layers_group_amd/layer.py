@@ -181,6 +181,8 @@ class BlockAttention:
         """O of each sequence's newest tokens (lens.numel() * draft rows of Qr)
         over its cache of pages."""
         b = lens.numel()
+        if b < 1 or Qr.shape[0] % b:
+            raise ValueError(f"{Qr.shape[0]} query rows for {b} sequences")
         draft = Qr.shape[0] // b
         O = self._bf16(b * draft, self.hq)
         ws = self._scratch(bl.bitlinear_attn_cache_workspace_bytes(b, draft, self.hq, self.hkv, self.d))

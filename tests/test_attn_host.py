@@ -151,3 +151,21 @@ def test_workspace_sizes_of_refused_shapes_are_zero(L):
     assert bl.bitlinear_attn_bwd_workspace_bytes(1, 10, 10, 3, 2, 128) == 0
     assert bl.bitlinear_attn_fwd_workspace_bytes(0, 10, 10, 4, 2, 128) == 0
     assert bl.bitlinear_attn_cache_workspace_bytes(1, 65, 4, 2, 128) == 0
+
+
+def test_more_workgroups_than_a_launch_holds(L):
+    """2^32 threads: refused by size, not left to the launch."""
+    assert rope(L, n=(1 << 26) - 3, rows=(1 << 26) - 3) == bl.BL_ESHAPE
+    assert "too many head rows" in bl.bitlinear_last_error()
+    assert rope_bwd(L, n=1 << 26, qw=None, kw=None) == bl.BL_ESHAPE
+    assert L.bitlinear_rope_table(1 << 26, 128, 1e4, A, None) == bl.BL_ESHAPE
+    assert "max_pos" in bl.bitlinear_last_error()
+    for f in (attn_fwd, attn_bwd):
+        for bad in (dict(b=65535, hq=256, hkv=1, qs=256 * 128), dict(b=65535, hq=128, hkv=128, qs=128 * 128),
+                    dict(tq=1 << 30, hq=2, hkv=1), dict(tk=1 << 29, hq=1, hkv=1)):
+            assert f(L, **bad) == bl.BL_ESHAPE
+            assert "too many rows" in bl.bitlinear_last_error()
+    assert cache(L, b=1 << 15, t=16, hq=32, hkv=16, mp=1) == bl.BL_ESHAPE
+    assert "2^24" in bl.bitlinear_last_error()
+    assert cache(L, b=1 << 15, t=64, hq=32, hkv=16, mp=1) == bl.BL_ESHAPE
+    assert "2^26" in bl.bitlinear_last_error()
