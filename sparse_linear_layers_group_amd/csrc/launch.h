@@ -395,7 +395,7 @@ struct RopeBwdArgs {
   float *gqw, *gkw;
   float* part;  // kRopeDwRows rows of 2d partial sums
 };
-constexpr int kRopeDwRows = 1024;  // workgroups of the backward with norms, at most
+constexpr int kRopeDwRows = 768;  // workgroups of the backward with norms, at most: as many as run at once
 inline size_t rope_bwd_ws_bytes(int64_t d) { return (size_t)kRopeDwRows * 2 * d * 4; }
 hipError_t launch_qk_rope(const RopeArgs& a, int64_t d, bool f32, hipStream_t s);
 hipError_t launch_qk_rope_bwd(const RopeBwdArgs& a, int64_t d, bool f32, hipStream_t s);

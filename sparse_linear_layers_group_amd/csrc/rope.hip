@@ -171,12 +171,17 @@ __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a) {
 // Backward of one row, with g = R(pos)^T dy and n = x / rms(x):
 //   dw += g n,   a = w g,   dx = (a - n mean(a n)) / rms(x)
 // (without norms dx = g).  With norms each workgroup walks over units and
-// keeps its share of dw in registers (one sum per lane and element, fewer
-// than a few hundred terms each), joins them in LDS in a fixed order and
+// keeps its share of dw in registers (a binary32 sum per lane and element, over
+// every 3072nd unit of a large call), joins them in LDS in a fixed order and
 // writes one row of partial sums; rope_dw_kernel adds those in binary64.
 // No atomics: reruns give the same bits.
+// Bound by HBM: x and dy are read and dx is written once.  The sums take the
+// registers to 162 - 168, so three workgroups fit a CU and kRopeDwRows of them are
+// launched, which walk side by side to the end (1024, a third more than fit:
+// 64.6 us in place of 52.1 at 8192 tokens of 20 + 5 heads of 128 in binary32,
+// 210 MB, 4.0 TB/s; 512: 54.9 us).
 template <int D, bool F32, bool NORM>
-__global__ __launch_bounds__(256) void qk_rope_bwd_kernel(RopeBwdArgs a) {
+__global__ __launch_bounds__(256, NORM ? 3 : 4) void qk_rope_bwd_kernel(RopeBwdArgs a) {
   typedef RopeMap<D> M;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int heads = a.hq + a.hkv;
