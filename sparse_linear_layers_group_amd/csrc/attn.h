@@ -18,12 +18,13 @@ typedef __attribute__((address_space(3))) void lds_void;
 // B[8(l/32) .. +7][l%32]; register i of its result is element
 // [8(i/4) + 4(l/32) + i%4][l%32].
 //
-// All three kernels keep the softmax's row along the lanes: with S^T = K Q^T
-// a lane holds one query's scores (column l%32) and after exp two
-// consecutive groups of four registers are, as they stand, the B operand of
-// the product over keys: its slots 0-3 and 4-7 are then keys 4(l/32) + 0..3
+// The forward, dQ and cache kernels keep the softmax's row along the lanes:
+// with S^T = K Q^T a lane holds one query's scores (column l%32) and after exp
+// two consecutive groups of four registers are, as they stand, the B operand
+// of the product over keys: its slots 0-3 and 4-7 are then keys 4(l/32) + 0..3
 // and 8 + 4(l/32) + 0..3 of 16, and A is read from LDS in the same order.
-// The probabilities never leave the registers.
+// (The dK / dV kernel does the same with keys along the lanes and sums over
+// rows.)  The probabilities never leave the registers.
 __device__ __forceinline__ v16f mfma32(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -302,7 +303,8 @@ __device__ __forceinline__ Item find_item(const int32_t* cu, int64_t total, cons
 // they read the same rows at about the same time, and those reads meet in its
 // L2.  Odd blocks of ranks run backwards, so no XCD always has the longer
 // items.  Fewer than eight ranks are simply numbered: padded to eight, most
-// workgroups of a small call would have nothing to do.
+// workgroups of a small call would have nothing to do (two sequences of 64 and
+// 100 tokens, 16 + 2 heads, forward and backward: 36.2 us padded, 35.1 us).
 struct Place {
   int rank, pair, part;
 };

@@ -14,7 +14,7 @@ constexpr int kKRows = 64;   // key rows of a tile in LDS
 constexpr int kExactTiles = 2;  // dQ workgroups with at most this many key tiles form delta from P dP
 constexpr int kBKeys = 64;   // key rows of a dK / dV workgroup: two blocks of 32, four wavefronts each
 constexpr int kBRows = 128;  // query rows of its stages: 32 per wavefront
-constexpr int kMaxSplits = 8;
+constexpr int kMaxSplits = 8;  // (16 made every join 1 - 2 us longer and saved 2 us in a few calls)
 constexpr float kInf = __builtin_huge_valf();
 }  // namespace
 
@@ -138,7 +138,6 @@ __device__ __forceinline__ void clear(v16f* acc) {
     for (int i = 0; i < 16; ++i) acc[t][i] = 0.f;
 }
 
-
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
 // ---------------------------------------------------------------- forward
@@ -150,6 +149,18 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // the unrounded P.  m' only moves when a score passes it by 8 in the
 // exponent of 2: P then stays below 2^8 and the 64 accumulators are
 // rescaled a few times per row instead of once per tile.
+//
+// Bound by the matrix unit and, beside it, the exponentials: one tile of a
+// wavefront is 32 matrix instructions (1024 clocks) and about 200 others, which
+// two wavefronts per SIMD overlap in part.  128 rows a workgroup (32 in each
+// wavefront: their O, scores and Q take 250 registers) and two workgroups per
+// CU; K and V in two stages each, so a load has a whole tile's time.  16384
+// tokens, 16 + 2 heads of 128: 1022 us, 1076 TFLOP/s of the products below the
+// diagonal, the matrix unit busy 53 % of the clocks; without the exponentials
+// 750 us.  8192 tokens in seven sequences, 20 + 5 heads: 125 us, 39 % busy (the
+// longest rows of one sequence are as long as a CU's mean share).
+// Tried without gain: two heads of a group in a workgroup of eight wavefronts
+// (half the loads, 5 % slower at 16384 tokens), priorities by length.
 //
 // Where there are few tiles of rows, `splits` workgroups are launched for
 // each, and as many as its keys make parts of about `target` key tiles share
@@ -382,8 +393,9 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int items,
     st_global(a.lse + (int64_t)head * a.total_q + qr.start + r, l > 0.f ? fmaf(m, sl, log2_hw(l)) * kLn2 : -kInf);
 }
 
-// O and lse of rows whose keys were split: 16 rows of a tile and head per
-// workgroup, 4 elements a thread
+// O and lse of rows whose keys were split: 8 (D = 128) or 16 rows of a tile and
+// head per workgroup, 4 elements a thread, all parts loaded before the first is
+// used.  Bound by the binary32 parts: 480 of 128 rows (31 MB) take 7.2 us.
 template <int D>
 __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int splits, int target,
                                                            const float* __restrict__ part) {
@@ -431,11 +443,11 @@ __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int spli
 //   delta = rowsum(dO O),  dV = P^T dO,  dP = dO V^T,  dS = P (dP - delta),
 //   dQ = scale dS K,  dK = scale dS^T Q
 // in two passes without atomics: one workgroup per 128 query rows walks the
-// keys for dQ, one per 128 keys walks the rows of all query heads of its
+// keys for dQ, one per 64 keys walks the rows of all query heads of its
 // group for dK and dV.  S and dP are computed in both, 7 products in place
 // of 5; the alternative, dQ added up in memory by the workgroups of all key
-// tiles, writes and reads binary32 dQ once per 128 keys and leaves the order
-// of the sums to chance.  P and dS are rounded to bf16 for the products,
+// tiles, writes and reads binary32 dQ once per tile of keys and leaves the
+// order of the sums to chance.  P and dS are rounded to bf16 for the products,
 // every sum is binary32.
 //
 // delta from the bf16 O carries O's rounding into every dS of its row.  Over
@@ -451,6 +463,13 @@ __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int spli
 // products as the accumulators' first values, -lse / scale to S (-inf where
 // a row sees no key, so P becomes 0) and -delta to dP, and dO rounded to
 // bf16 where it comes in binary32.
+//
+// Bound by the matrix unit with LDS beside it (every operand from LDS, 1 KiB
+// per instruction, serves one product): 8192 tokens in four sequences, 20 + 5
+// heads of 128: 178 us, 1015 TFLOP/s of its three products, the matrix unit
+// busy 50 % of the clocks.  Two workgroups per CU (220 registers), K and V
+// tiles in two stages.  Small calls are a chain of latencies (finding the item,
+// the rows, the tiles, the exact sums): 512 tokens, 14 + 2 heads of 64: 10 us.
 template <int D>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, int items, uint16_t* __restrict__ copy,
                                                         float* __restrict__ ndelta, float* __restrict__ shift) {
@@ -613,7 +632,15 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, int item
 // LDS at the end.  (128 keys a workgroup read each stage for twice the keys,
 // but make half as many workgroups, each twice as long: with 8192 tokens in
 // four sequences and 5 key/value heads the longest was 2.3 times the average
-// load of a CU.)
+// load of a CU.  Four wavefronts with both blocks of keys each, which read an
+// operand from LDS for two products, need 512 registers: 382 us in place of
+// 300, one wavefront per SIMD and moves between the two register files.)
+//
+// Bound by the matrix unit with LDS beside it: 8192 tokens in four sequences,
+// 20 + 5 heads of 128: 300 us, 803 TFLOP/s of its four products, the matrix unit
+// busy 40 % of the clocks, LDS 32 %; each CU runs 15 % of the time with one
+// wavefront per SIMD or none (the tile of a sequence's first keys is as long as
+// a CU's mean share).  512 tokens, 14 + 2 heads of 64: 10 us and 3.5 us to join.
 //
 // `splits` workgroups share a tile where there are few: each takes a part of
 // the (stage, head) steps and leaves binary32 sums in `part`
@@ -857,7 +884,8 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, int ite
   }
 }
 
-// dK and dV of split tiles: the splits' sums in order, 8 elements a thread
+// dK and dV of split tiles: the splits' sums in order, 8 elements a thread,
+// all loaded before the first is used (bound by latency: 3.5 us)
 template <int D>
 __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnBwdArgs a, int splits,
                                                            const float* __restrict__ part) {
@@ -905,21 +933,25 @@ size_t bwd_row_bytes(int64_t total_q, int64_t hq) { return align256((size_t)tota
 // How a forward with few tiles of rows shares out the keys: into parts as
 // long as they can be for all of them to run at once, two workgroups per CU
 // (one more than 512 would start when the others are done: 903 rows behind
-// 11779 keys, 12 heads: 73 us with 528 parts, 54 us with 480), by the mean
-// length (the kernels see the true ones), and at least kMinSplitTiles
-// (shorter parts cost more to join than they save).  splits = 1: not at all.
-constexpr int kMinSplitTiles = 8;
+// 11779 keys, 12 heads: 73 us with 528 parts, 54 us with 480, 166 us unsplit),
+// by the mean length (the kernels see the true ones), and not shorter than
+// is worth a join: four tiles for rows behind a longer context (16 rows, 2048
+// keys, 16 heads: 43.6 us unsplit, 18.7 with parts of eight tiles, 13.5 of four,
+// 13.8 of two), six for whole prompts, whose rows see half of the keys on
+// average (1900 tokens, 8 heads: 45.3 us unsplit, 32.7 with eight, 32.3 with six,
+// 35.7 with four).  splits = 1: not at all.
 struct FwdSplit {
   int splits, target;
 };
 static FwdSplit fwd_split(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq) {
   const int64_t tiles = (total_q + kQRows - 1) / kQRows * hq;
   const int64_t keys = total_k / (batch > 0 ? batch : 1) / kKRows;
-  if (tiles > 256 || keys < 2 * kMinSplitTiles) return FwdSplit{1, 1};
-  // (rows of long prompts see half of the keys on average)
-  const int64_t mean = total_q >= total_k ? (keys + 1) / 2 : keys;
+  const bool prompts = total_q >= total_k;
+  const int64_t least = prompts ? 6 : 4;
+  if (tiles > 256 || keys < 2 * least) return FwdSplit{1, 1};
+  const int64_t mean = prompts ? (keys + 1) / 2 : keys;
   const int64_t room = 512 - tiles / 2, target = (tiles * mean + room - 1) / room;  // (a tile ends in half a part)
-  const int64_t t = target < kMinSplitTiles ? kMinSplitTiles : target;
+  const int64_t t = target < least ? least : target;
   const int64_t most = (2 * mean + t - 1) / t;  // parts of a sequence of twice the mean length
   if (most < 2) return FwdSplit{1, 1};
   return FwdSplit{most > kMaxSplits ? kMaxSplits : (int)most, (int)t};
@@ -949,6 +981,8 @@ hipError_t launch_attn_fwd(const AttnArgs& a, int64_t d, void* ws, hipStream_t s
 
 // Workgroups that share a dK / dV tile: as many as the chip runs at once, one
 // per CU (D = 64: two).  (A workgroup without steps still waits for a place.)
+// 512 tokens in three sequences, 14 + 2 heads of 64: 27.3 us unsplit, 10.6 and
+// 3.7 for the join.
 static int dkv_splits(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d) {
   const int64_t tiles = placed_items(most_tiles(total_k, batch, kBKeys)) * hkv, want = d == 128 ? 256 : 512;
   const int64_t steps = hq / hkv * ((total_q + kBRows - 1) / kBRows);

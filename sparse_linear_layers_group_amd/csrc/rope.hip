@@ -92,7 +92,10 @@ __device__ __forceinline__ void store8(uint16_t* p, const float* y) {
 }
 
 // y = R(pos) (w * x / rms(x)) for rows of q and k, V rows copied; all
-// rounded once to bf16.
+// rounded once to bf16.  Bound by HBM where there is much to move (6001 tokens,
+// 14 + 2 + 2 heads of 64, bf16: 28 MB in 8.4 us, 3.3 TB/s of which 2 us are the
+// launch), by three loads one after another (position, table, weights) in a
+// serving step (64 tokens: 3.6 us).
 template <int D, bool F32, bool NORM>
 __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a) {
   typedef RopeMap<D> M;
@@ -285,6 +288,7 @@ __global__ __launch_bounds__(256, NORM ? 3 : 4) void qk_rope_bwd_kernel(RopeBwdA
 
 // dw[e] = sum of the workgroups' partials: 4 columns of 2D per workgroup, its
 // threads along the rows, joined in LDS, all in binary64 and in a fixed order
+// (768 rows of 256 columns: 4.2 us, latency)
 __global__ __launch_bounds__(256) void rope_dw_kernel(const float* __restrict__ part, int rows, int d,
                                                      float* __restrict__ gq, float* __restrict__ gk) {
   __shared__ double red[4][4];
@@ -316,7 +320,8 @@ __global__ __launch_bounds__(256) void rope_dw_kernel(const float* __restrict__ 
 }
 
 // cos and sin of p * base^(-2i/d), formed in binary64 (a binary32 product
-// would lose the angle of far positions) and rounded once
+// would lose the angle of far positions) and rounded once.  Made once for a
+// model; bound by the binary64 power and sine.
 __global__ __launch_bounds__(256) void rope_table_kernel(float* __restrict__ table, int64_t pairs, int half,
                                                         double base) {
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
