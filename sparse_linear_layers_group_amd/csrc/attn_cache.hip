@@ -44,10 +44,11 @@ constexpr int kGranule = 16;  // rows that share a page
 // blocks of 32 rows per wavefront ran out of registers; with units of 32 rows
 // it read K and V once for each: 24 tokens of 4 heads behind 38,000 rows took
 // 113 us, with two stages and two workgroups per CU 41 us of this kernel, now
-// 35.)  Those 38,000 rows in eight sequences, 5 key/value heads (99 MB), are
-// 40 us with the join: bound by the chain of a tile at one wavefront per SIMD
-// (scores, maximum, exponentials, products: 25 tiles of a workgroup in 25 us),
-// then by the 13 MB of partial results.
+// 33.)  Those 38,000 rows in eight sequences, 5 key/value heads (99 MB), are
+// 39 us with the join: 3 to find the ranges, 7 to start on one or two units
+// each, 14 for a workgroup's 12 tiles (their loads alone 10), 6 to write 13 MB
+// of partial results and 6.5 to join them.  (The next tile's scores among the
+// exponentials, as in the forward, gained nothing here.)
 // ---------------------------------------------------------------------
 template <int D, bool WIDE>
 struct CacheForm {
@@ -493,10 +494,12 @@ __global__ __launch_bounds__(256, D == 128 ? 1 : 2) void attn_cache_wide_kernel(
     typedef std::integral_constant<int, 2> S2;
     typedef std::integral_constant<int, 3> S3;
     pages.at(a, b, len, 4 * t0, lane);
-    int gone0 = issue(S0{}, t0), gone1 = issue(S1{}, t0 + 1), gone2 = issue(S2{}, t0 + 2);  // of the next three tiles
+    // (before the tiles: loads return in order, and a wait for these rows would
+    // be one for three tiles)
     v8bf qf[D / 16];
     QRow<D> q;
     q.load(a, qf, b, kvh, busy ? block * kCols + (lane & 31) : blocks * kCols, lane);
+    int gone0 = issue(S0{}, t0), gone1 = issue(S1{}, t0 + 1), gone2 = issue(S2{}, t0 + 2);  // of the next three tiles
     Running<D> acc;
     acc.clear();
 
