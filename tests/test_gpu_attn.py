@@ -303,3 +303,93 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for x, y in zip(got, want):
         assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+@pytest.mark.parametrize("q_lens,k_lens", [([1] * 40, [300] * 40), ([1] * 300, [40] * 300), ([3] * 16, [800] * 16)])
+def test_a_few_rows_of_many_sequences(q_lens, k_lens):
+    q, k, v, do = inputs(q_lens, k_lens, 4, 2, 64, seed=24)
+    check(q, k, v, do, q_lens, k_lens)
+
+
+@pytest.mark.parametrize("hq,hkv", [(300, 1), (96, 96), (520, 4)])
+def test_many_heads(hq, hkv):
+    lens = [5, 70]
+    q, k, v, do = inputs(lens, lens, hq, hkv, 64, seed=25)
+    check(q, k, v, do, lens, lens)
+
+
+def test_captured_graph_of_shared_out_keys():
+    """Few rows, many keys: parts, their join and the backward's splits, with
+    lengths that change what is split; eager work between the replays."""
+    hq, hkv, d, tq, tk, s = 4, 2, 128, 70, 4000, 0.1
+    q, k, v, do = inputs([tq], [tk], hq, hkv, d, seed=26)
+    do = do.to(BF)
+    cq, ck = cu([30, 40]), cu([1000, 3000])
+    nf = bl.bitlinear_attn_fwd_workspace_bytes(2, tq, tk, hq, hkv, d)
+    assert nf > 0
+    wf = torch.full((nf,), 255, dtype=torch.uint8, device="cuda")
+    wb = torch.full((bl.bitlinear_attn_bwd_workspace_bytes(2, tq, tk, hq, hkv, d),), 255, dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(hq, tq, device="cuda")
+    g = [torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)]
+
+    def step():
+        bl.bitlinear_attn_fwd(q, k, v, cq, ck, 2, hq, hkv, d, s, o, lse, ws=wf)
+        bl.bitlinear_attn_bwd(q, k, v, o, lse, do, cq, ck, 2, hq, hkv, d, s, *g, ws=wb)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for ql, kl in (([30, 40], [1000, 3000]), ([1, 69], [4000, 0]), ([70, 0], [20, 3980]), ([35, 35], [2000, 2000])):
+        cq.copy_(cu(ql))
+        ck.copy_(cu(kl))
+        for x in (o, lse, *g):
+            x.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (o, lse, *g)]
+        ref = R.attention(q, k, v, ql, kl, s, do)
+        R.assert_within(got[0], ref["o"], ref["o_err"], "O")
+        for x, n in zip(got[2:], ("dq", "dk", "dv")):
+            R.assert_within(x, ref[n], ref[n + "_err"], n)
+        step()
+        torch.cuda.synchronize()
+        for x, y in zip(got, (o, lse, *g)):
+            assert torch.equal(x, y)
+
+
+def test_two_graphs_with_workspaces_of_their_own():
+    """Replayed in turn, each keeps its results."""
+    runs = []
+    for seed, lens in ((27, [200, 56]), (28, [100, 300])):
+        q, k, v, do = inputs(lens, lens, 4, 2, 64, seed=seed)
+        do = do.to(BF)
+        b, t = len(lens), sum(lens)
+        c = cu(lens)
+        o, lse = torch.empty_like(q), torch.empty(4, t, device="cuda")
+        g = [torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)]
+        ws = ws_for(bl.bitlinear_attn_bwd_workspace_bytes, b, t, t, 4, 2, 64)
+
+        def step(q=q, k=k, v=v, do=do, c=c, o=o, lse=lse, g=g, ws=ws, b=b):
+            bl.bitlinear_attn_fwd(q, k, v, c, c, b, 4, 2, 64, 0.125, o, lse)
+            bl.bitlinear_attn_bwd(q, k, v, o, lse, do, c, c, b, 4, 2, 64, 0.125, *g, ws=ws)
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.synchronize()
+        want = [x.clone() for x in (o, lse, *g)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        runs.append((graph, want, (o, lse, *g), step))  # (step holds the inputs and the workspace)
+    for _ in range(3):
+        for graph, _, outs, _ in runs:
+            for x in outs:
+                x.fill_(3.0)
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, want, outs, _ in runs:
+            for x, y in zip(want, outs):
+                assert torch.equal(x, y)

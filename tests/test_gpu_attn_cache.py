@@ -221,3 +221,49 @@ def test_captured_graph_replays_with_other_lengths():
         assert torch.equal(got, run(q, k, v, pages, page, lens, None, batch, 1, 0.1))
         want, err = reference(q, k, v, [r[:m] for r, m in zip(rows, lens)], lens, None, 1, 0.1)
         R.assert_within(got, want, err, "O")
+
+
+def test_captured_graph_of_drafted_trees():
+    """The kernel for more than 32 rows of Q, with lengths, pages and trees that change."""
+    page, hq, hkv, d, batch, draft = 16, 20, 5, 128, 3, 12
+    k, v, pages, rows = cache([700, 700, 700], page, hkv, d, seed=11)
+    q = queries(batch, draft, hq, d, 11)
+    tree = trees(batch, draft, 11)
+    n = torch.tensor([12, 20, 30], dtype=torch.int32, device="cuda")
+    o = torch.empty_like(q)
+    ws = torch.full((bl.bitlinear_attn_cache_workspace_bytes(batch, draft, hq, hkv, d),), 255, dtype=torch.uint8, device="cuda")
+
+    def step():
+        bl.bitlinear_attn_cache(q, k, v, pages, page, n, tree, batch, draft, hq, hkv, d, 0.1, o, ws=ws)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed, lens in ((12, [700, 12, 77]), (13, [0, 699, 13]), (14, [700, 700, 700])):
+        n.copy_(torch.tensor(lens, dtype=torch.int32))
+        tree.copy_(trees(batch, draft, seed))
+        pages.copy_(pages.flip(0).contiguous())
+        rows = rows[::-1]
+        o.fill_(4.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = o.clone()
+        assert torch.equal(got, run(q, k, v, pages, page, lens, tree, batch, draft, 0.1))
+        want, err = reference(q, k, v, [r[:m] for r, m in zip(rows, lens)], lens, tree, draft, 0.1)
+        R.assert_within(got, want, err, "O")
+
+
+@pytest.mark.parametrize("draft", [1, 9])
+def test_more_sequences_than_lanes(draft):
+    """More than 64 sequences, empty ones among them, some long."""
+    lens = [0 if i % 7 == 2 else (i * 13) % 40 + draft + (500 if i % 31 == 5 else 0) for i in range(150)]
+    check(lens, 16, draft, 8, 2, 64, False, seed=15)
+
+
+@pytest.mark.parametrize("hq,hkv,draft", [(64, 1, 3), (128, 1, 1), (48, 24, 2), (200, 1, 8)])
+def test_many_heads(hq, hkv, draft):
+    """Groups of many heads: several units read the same tiles."""
+    check([draft, 90, 1000], 32, draft, hq, hkv, 64, True, seed=16)

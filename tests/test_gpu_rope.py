@@ -178,3 +178,41 @@ def test_no_tokens():
     ws = torch.empty(bl.bitlinear_qk_rope_bwd_workspace_bytes(d), dtype=torch.uint8, device="cuda")
     bl.bitlinear_qk_rope_bwd(e, e, 0, 1, 1, d, w, w, EPS, table, pos, eb, eb, eb, eb, gq, gk, ws=ws)
     assert (gq == 0).all() and (gk == 0).all()
+
+
+def test_captured_graph_and_another_stream():
+    tokens, hq, hkv, d = 70, 4, 2, 64
+    table = table_of(4096, d)
+    q, k, v, pos, (qw, kw) = case(tokens, hq, hkv, d, torch.float32, True, seed=20)
+    outs = [torch.empty(tokens, h * d, dtype=BF, device="cuda") for h in (hq, hkv, hkv)]
+    grads = [torch.empty(tokens, h * d, dtype=BF, device="cuda") for h in (hq, hkv)]
+    gw = [torch.empty(d, device="cuda") for _ in range(2)]
+    ws = torch.full((bl.bitlinear_qk_rope_bwd_workspace_bytes(d),), 255, dtype=torch.uint8, device="cuda")
+
+    def step():
+        bl.bitlinear_qk_rope(q, k, v, tokens, hq, hkv, d, qw, kw, EPS, table, pos, *outs)
+        bl.bitlinear_qk_rope_bwd(q, k, tokens, hq, hkv, d, qw, kw, EPS, table, pos, outs[0], outs[1], *grads, *gw, ws=ws)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in range(3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        pos.copy_(torch.randint(0, 4096, (tokens,), generator=g, device="cuda", dtype=torch.int32))
+        q.normal_(generator=g)
+        for x in (*outs, *grads, *gw):
+            x.fill_(2.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (*outs, *grads, *gw)]
+        step()
+        torch.cuda.synchronize()
+        for x, y in zip(got, (*outs, *grads, *gw)):
+            assert torch.equal(x, y)
+        c, s = angles(table, pos)
+        y, err = R.rope(q.view(tokens, hq, d), c, s, qw, EPS)
+        R.assert_within(got[0].view(tokens, hq, d), y, err, "q")
