@@ -470,31 +470,41 @@ __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int spli
 // busy 50 % of the clocks.  Two workgroups per CU (220 registers), K and V
 // tiles in two stages.  Small calls are a chain of latencies (finding the item,
 // the rows, the tiles, the exact sums): 512 tokens, 14 + 2 heads of 64: 10 us.
+//
+// Keys are shared out as in the forward: parts leave binary32 sums in `part`
+// ([split][hq][total_q] rows of D), which attn_dq_join_kernel adds in order (2452
+// tokens, 12 heads: 70 us unsplit, 50 and 11 to join; 300 rows behind 3000 keys,
+// 16 heads: 79 us, 26 and 6).
 template <int D>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, int items, uint16_t* __restrict__ copy,
-                                                        float* __restrict__ ndelta, float* __restrict__ shift) {
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, int items, int splits, int target,
+                                                        uint16_t* __restrict__ copy, float* __restrict__ ndelta,
+                                                        float* __restrict__ shift, float* __restrict__ part) {
   typedef Tile<D> T;
   constexpr int kTile = PairBytes<D>::kTile;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.hq / a.hkv;
-  const Place pl = place_of(blockIdx.x, items, a.hkv, group);
+  const Place pl = place_of(blockIdx.x, items, a.hkv, group * splits);
   const Item it = find_item(a.cu_q, a.total_q, a.cu_k, a.total_k, a.batch, kQRows, pl.rank);
   if (it.seq < 0) return;
-  const int kvh = pl.pair, head = kvh * group + pl.part;
+  const int split = pl.part / group, kvh = pl.pair, head = kvh * group + pl.part - split * group;
   const Rows qr = it.mine, kr = it.other;
   const int q0 = it.level * kQRows;
   const int off = kr.len - qr.len;
   const int w0 = q0 + 32 * wave, r = w0 + (lane & 31);
   const bool in = r < qr.len;
-  const int last = q0 + kQRows < qr.len ? q0 + kQRows : qr.len;
   const int wlast = w0 + 32 < qr.len ? w0 + 32 : qr.len;
-  const int tiles = (clampi(last + off, 0, kr.len) + kKRows - 1) / kKRows;
-  const int wtiles = w0 < qr.len ? (clampi(wlast + off, 0, kr.len) + kKRows - 1) / kKRows : 0;
+  const int all = key_tiles(qr, kr, q0);
+  const int wall = w0 < qr.len ? (clampi(wlast + off, 0, kr.len) + kKRows - 1) / kKRows : 0;
+  // this workgroup's tiles [first, tiles) of them
+  const int parts = parts_of(all, splits, target);
+  if (split >= parts) return;
+  const int first = (int)((int64_t)all * split / parts), tiles = (int)((int64_t)all * (split + 1) / parts);
+  const int wtiles = wall < tiles ? wall : tiles;
 
-  // the first tiles are on their way before anything is waited for; few keys:
-  // both of them, and they stay
-  const bool few = tiles <= kExactTiles;
+  // the first tiles are on their way before anything is waited for; few keys
+  // (less than a part): both of them, and they stay
+  const bool few = all <= kExactTiles;
   const PairDma<D> dma(lane, wave, a.k_stride, a.v_stride);
   const uint16_t* kp = a.K + (int64_t)kr.start * a.k_stride + (int64_t)kvh * D;
   const uint16_t* vp = a.V + (int64_t)kr.start * a.v_stride + (int64_t)kvh * D;
@@ -502,7 +512,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, int item
     if (t < tiles)
       dma.issue(st, kp + (int64_t)t * kKRows * a.k_stride, vp + (int64_t)t * kKRows * a.v_stride, kr.len - t * kKRows);
   };
-  issue(pair_stage<D, 0>(), 0);
+  issue(pair_stage<D, 0>(), first);
   if (few) issue(pair_stage<D, 1>(), 1);
 
   const int64_t row = qr.start + (in ? r : qr.len - 1), at = (row * a.hq + head) * D;
@@ -522,7 +532,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, int item
     for (int s = 0; s < D / 16; ++s) {
       const v4f y = x[s][0], z = x[s][1];
       const u32x4 g = u32x4{pk_bf16(y[0], y[1]), pk_bf16(y[2], y[3]), pk_bf16(z[0], z[1]), pk_bf16(z[2], z[3])};
-      if (in) st_global(reinterpret_cast<u32x4*>(copy + at + 16 * s + 8 * (lane >> 5)), g);
+      if (in && split == 0) st_global(reinterpret_cast<u32x4*>(copy + at + 16 * s + 8 * (lane >> 5)), g);
       gf[s] = __builtin_bit_cast(v8bf, g);
     }
   } else {
@@ -536,7 +546,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, int item
     for (int i = 0; i < 4; ++i) nd = fmaf(-bf16_lo(o[i]), bf16_lo(g[i]), fmaf(-bf16_hi(o[i]), bf16_hi(g[i]), nd));
   }
   nd = half_join(nd, [](float u, float v) { return u + v; });
-  if (in && lane < 32) {
+  if (in && split == 0 && lane < 32) {
     st_global(ndelta + sum_at, nd);
     st_global(shift + sum_at, lse == -kInf ? -kInf : -lse / a.scale);
   }
@@ -613,13 +623,52 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, int item
     }
     if (t < wtiles) grads(stage, t);
   };
-  int t = 0;
+  int t = first;
   for (; t + 1 < tiles; t += 2) {
     step(S0{}, t);
     step(S1{}, t + 1);
   }
   if (t < tiles) step(S0{}, t);
-  store_row<D>(a.dQ + at, dq, a.scale, lane, in);
+  if (parts == 1) {
+    store_row<D>(a.dQ + at, dq, a.scale, lane, in);
+  } else if (in) {
+    float* p = part + ((int64_t)split * a.hq * a.total_q + sum_at) * D;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        st_global(reinterpret_cast<v4f*>(p + 32 * d + 8 * q + 4 * (lane >> 5)),
+                  v4f{dq[d][4 * q], dq[d][4 * q + 1], dq[d][4 * q + 2], dq[d][4 * q + 3]});
+  }
+}
+
+// dQ of rows whose keys were split: the parts' sums in order, 4 elements a
+// thread (see attn_fwd_join_kernel)
+template <int D>
+__global__ __launch_bounds__(256) void attn_dq_join_kernel(AttnBwdArgs a, int splits, int target,
+                                                          const float* __restrict__ part) {
+  constexpr int kRows = 256 / (D / 4);  // rows of a workgroup
+  constexpr int kParts = kQRows / kRows;
+  const int tile = blockIdx.x / kParts, head = tile % a.hq;
+  const Item it = find_item(a.cu_q, a.total_q, a.cu_k, a.total_k, a.batch, kQRows, tile / a.hq);
+  if (it.seq < 0) return;
+  const Rows qr = it.mine;
+  const int parts = parts_of(key_tiles(qr, it.other, it.level * kQRows), splits, target);
+  if (parts == 1) return;  // its workgroup wrote the rows
+  const int r = it.level * kQRows + blockIdx.x % kParts * kRows + threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
+  if (r >= qr.len) return;
+  const int64_t plane = (int64_t)a.hq * a.total_q, at = (int64_t)head * a.total_q + qr.start + r;
+  v4f x[kMaxSplits];
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s)
+    x[s] = ld_global(reinterpret_cast<const v4f*>(part + ((s < parts ? s : 0) * plane + at) * D) + c);
+  v4f y = x[0];
+#pragma unroll
+  for (int s = 1; s < kMaxSplits; ++s)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] += s < parts ? x[s][e] : 0.f;
+  st_global(reinterpret_cast<u32x2*>(a.dQ + ((int64_t)(qr.start + r) * a.hq + head) * D) + c,
+            u32x2{pk_bf16(y[0] * a.scale, y[1] * a.scale), pk_bf16(y[2] * a.scale, y[3] * a.scale)});
 }
 
 // dK and dV of 64 keys.  Lanes run over keys here: S = Q K^T has a key per
@@ -982,25 +1031,41 @@ hipError_t launch_attn_fwd(const AttnArgs& a, int64_t d, void* ws, hipStream_t s
   return d == 128 ? fwd_launch<128>(a, static_cast<float*>(ws), s) : fwd_launch<64>(a, static_cast<float*>(ws), s);
 }
 
-// Workgroups that share a dK / dV tile: as many as the chip runs at once, one
-// per CU (D = 64: two).  (A workgroup without steps still waits for a place.)
-// 512 tokens in three sequences, 14 + 2 heads of 64: 27.3 us unsplit, 10.6 and
-// 3.7 for the join.
+// Workgroups that share a dK / dV tile: as many as the chip runs at once (one
+// per CU, at D = 64 two).  At D = 128 twice as many for whole prompts whose parts
+// stay long: with one workgroup per CU and tiles of unequal length a second
+// round evens them out (3945 tokens in six sequences, 12 + 2 heads: 113 us unsplit, 66 with
+// two, 51 with three, 55 with four, joins 7 - 8 more; 8192 in four, 16 + 2 heads:
+// 252 and 169; but 1259 in six, 20 + 5 heads, steps that are few: 36 unsplit, 26
+// with two, 28 with three and four; 300 rows behind 3000 keys, 16 + 2 heads, tiles
+// of equal length: 35 with two, 41 with five).  D = 64: 512 tokens in three sequences, 14 +
+// 2 heads: 27 unsplit, 11 with eight; 4136 in three, 8 + 8 heads, as many tiles
+// as places: 32 unsplit, 46 with two.
 static int dkv_splits(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d) {
-  const int64_t tiles = placed_items(most_tiles(total_k, batch, kBKeys)) * hkv, want = d == 128 ? 256 : 512;
-  const int64_t steps = hq / hkv * ((total_q + kBRows - 1) / kBRows);
-  int64_t s = tiles > 0 ? want / tiles : 1;
+  const int64_t full = (total_k + kBKeys - 1) / kBKeys, each = batch < total_k ? batch : total_k;
+  const int64_t tiles = (full > each ? full : each) * hkv, group = hq / hkv;
+  if (tiles == 0) return 1;
+  const int64_t places = d == 128 ? 256 : 512;
+  int64_t s = places / tiles;
+  // steps of a tile of the mean prompt, whose rows see half of the keys
+  const int64_t mean = (total_q / (batch > 0 ? batch : 1) + kBRows - 1) / kBRows * group / 2;
+  if (d == 128 && total_q >= total_k && mean / 3 * tiles >= 2 * places) s = 2 * places / tiles;
+  const int64_t steps = group * ((total_q + kBRows - 1) / kBRows);
   s = s > kMaxSplits ? kMaxSplits : s;
   s = s > steps ? steps : s;
   return s < 1 ? 1 : (int)s;
 }
 
-// workspace: -delta, -lse / scale ([hq][total_q] each), dO in bf16, partial
-// dK and dV of split tiles
+// workspace: -delta, -lse / scale ([hq][total_q] each), dO in bf16, and the
+// partial sums of one pass after the other: dQ, then dK and dV
+static size_t bwd_part_bytes(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d) {
+  const int q = fwd_split(batch, total_q, total_k, hq).splits, k = dkv_splits(batch, total_q, total_k, hq, hkv, d);
+  const size_t nq = q > 1 ? (size_t)q * total_q * hq * d * 4 : 0, nk = k > 1 ? (size_t)k * 2 * total_k * hkv * d * 4 : 0;
+  return nq > nk ? nq : nk;
+}
 size_t attn_bwd_ws_bytes(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d) {
-  const int splits = dkv_splits(batch, total_q, total_k, hq, hkv, d);
   return 2 * bwd_row_bytes(total_q, hq) + align256((size_t)total_q * hq * d * 2) +
-         (splits > 1 ? (size_t)splits * 2 * total_k * hkv * d * 4 : 0);
+         bwd_part_bytes(batch, total_q, total_k, hq, hkv, d);
 }
 
 template <int D>
@@ -1014,10 +1079,17 @@ static hipError_t bwd_launch(const AttnBwdArgs& a, hipStream_t s) {
   const uint16_t* dO = a.do_f32 ? copy : static_cast<const uint16_t*>(a.dO);
   if (a.total_q > 0) {
     const int64_t items = most_tiles(a.total_q, a.batch, kQRows);
-    attn_dq_kernel<D><<<dim3((unsigned)placed_blocks(items, a.hkv, a.hq / a.hkv)), 256, 0, s>>>(a, (int)items, copy,
-                                                                                               delta, shift);
+    const FwdSplit p = fwd_split(a.batch, a.total_q, a.total_k, a.hq);
+    attn_dq_kernel<D><<<dim3((unsigned)placed_blocks(items, a.hkv, a.hq / a.hkv * p.splits)), 256, 0, s>>>(
+        a, (int)items, p.splits, p.target, copy, delta, shift, part);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (p.splits > 1) {
+      attn_dq_join_kernel<D><<<dim3((unsigned)(items * a.hq * (kQRows / (256 / (D / 4))))), 256, 0, s>>>(
+          a, p.splits, p.target, part);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
   }
   if (a.total_k > 0) {
     const int splits = dkv_splits(a.batch, a.total_q, a.total_k, a.hq, a.hkv, D);
