@@ -647,7 +647,7 @@ int bitlinear_qk_rope_bwd(const void *Q, const void *K, int x_type, int64_t q_st
  *              overlap on one workspace race.
  * batch 1..65535, total_q and total_k at most 2^31 - 1024, (total_q / 128 +
  * batch + 8) * hq below 2^24, (total_k / 64 + batch + 8) * hkv below 2^23,
- * scale finite and > 0; total_q == 0 is a no-op. */
+ * scale in [1e-30, 1e30]; total_q == 0 is a no-op. */
 size_t bitlinear_attn_fwd_workspace_bytes(int64_t batch, int64_t total_q, int64_t total_k,
                                           int64_t hq, int64_t hkv, int64_t d);
 int bitlinear_attn_fwd(const uint16_t *Q, const uint16_t *K, const uint16_t *V, int64_t q_stride,
@@ -697,7 +697,7 @@ int bitlinear_attn_bwd(const uint16_t *Q, const uint16_t *K, const uint16_t *V, 
  *   O        device bf16 [batch * draft][hq*d], written.
  *   ws       bitlinear_attn_cache_workspace_bytes() bytes, 256-byte
  *            aligned, clobbered; calls that overlap on it race.
- * Formulas and roundings as for bitlinear_attn_fwd.  Lengths, pages and tree
+ * Formulas, roundings and scale as for bitlinear_attn_fwd.  Lengths, pages and tree
  * are read by the kernels: a captured graph may be replayed with others.
  * page a multiple of 16, draft 1..64, batch 1..65535, max_pages * page and
  * cache_rows below 2^31, batch * draft * hq below 2^24 (below 2^26 where

@@ -1188,6 +1188,12 @@ int bitlinear_qk_rope_bwd(const void* Q, const void* K, int x_type, int64_t q_st
 namespace {
 constexpr int64_t kStrideLimit = (int64_t)1 << 22;  // a 64-row tile's offsets stay below 2^31 bytes
 
+// (far outside, scale log2 e or -lse / scale would leave binary32)
+int check_scale(float scale) {
+  if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(BL_EINVAL, "scale must be in [1e-30, 1e30] (got %g)", (double)scale);
+  return BL_OK;
+}
+
 int check_attn(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int64_t hkv, int64_t d, float scale) {
   TRY(check_heads(hq, hkv, d));
   if (batch < 1 || batch > 65535) return fail(BL_ESHAPE, "batch must be in 1..65535 (got %lld)", (long long)batch);
@@ -1198,7 +1204,7 @@ int check_attn(int64_t batch, int64_t total_q, int64_t total_k, int64_t hq, int6
       (total_k / 64 + batch + 8) * hkv >= kMaxBlocks / 2)
     return fail(BL_ESHAPE, "too many rows for one call (total_q %lld, total_k %lld, batch %lld)", (long long)total_q,
                 (long long)total_k, (long long)batch);
-  if (!(scale > 0.f && scale <= 3.0e38f)) return fail(BL_EINVAL, "scale must be finite and > 0");
+  TRY(check_scale(scale));
   return BL_OK;
 }
 
@@ -1313,7 +1319,7 @@ int bitlinear_attn_cache(const uint16_t* Q, int64_t q_stride, const uint16_t* K,
       return fail(BL_ESHAPE, "too many cache tiles for one call (batch %lld, %lld rows each)", (long long)batch,
                   (long long)(max_pages * page));
   }
-  if (!(scale > 0.f && scale <= 3.0e38f)) return fail(BL_EINVAL, "scale must be finite and > 0");
+  TRY(check_scale(scale));
   TRY(check_stride(q_stride, hq * d, 8, kLimit, "q_stride"));
   TRY(check_ptr(Q, 16, "Q"));
   if (cache_rows >= page) {

@@ -169,3 +169,10 @@ def test_more_workgroups_than_a_launch_holds(L):
     assert "2^24" in bl.bitlinear_last_error()
     assert cache(L, b=1 << 15, t=64, hq=32, hkv=16, mp=1) == bl.BL_ESHAPE
     assert "2^26" in bl.bitlinear_last_error()
+
+
+@pytest.mark.parametrize("scale,status", [(9e-31, bl.BL_EINVAL), (1.1e30, bl.BL_EINVAL), (1e-45, bl.BL_EINVAL)])
+def test_scales_that_leave_binary32(L, scale, status):
+    for f in (attn_fwd, attn_bwd, cache):
+        assert f(L, scale=scale) == status
+        assert "scale" in bl.bitlinear_last_error()

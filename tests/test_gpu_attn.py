@@ -393,3 +393,16 @@ def test_two_graphs_with_workspaces_of_their_own():
         for _, want, outs, _ in runs:
             for x, y in zip(want, outs):
                 assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-12])
+def test_scales_that_flatten_every_row(scale):
+    """Scores that vanish: the mean of the visible V, and its gradients."""
+    lens = [70, 200]
+    q, k, v, do = inputs(lens, lens, 2, 1, 64, seed=29)
+    do = do.to(BF)
+    o, lse = forward(q, k, v, lens, lens, scale)
+    ref = R.attention(q, k, v, lens, lens, scale, do)
+    R.assert_within(o, ref["o"], ref["o_err"], "O")
+    _, _, dv = backward(q, k, v, o, lse, do, lens, lens, scale)
+    R.assert_within(dv, ref["dv"], ref["dv_err"], "dv")
