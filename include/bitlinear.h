@@ -699,10 +699,10 @@ int bitlinear_attn_bwd(const uint16_t *Q, const uint16_t *K, const uint16_t *V, 
  *            aligned, clobbered; calls that overlap on it race.
  * Formulas, roundings and scale as for bitlinear_attn_fwd.  Lengths, pages and tree
  * are read by the kernels: a captured graph may be replayed with others.
- * page a multiple of 16, draft 1..64, batch 1..65535, max_pages * page and
- * cache_rows below 2^31, batch * draft * hq below 2^24 (below 2^26 where
- * draft * (hq/hkv) > 32), and batch * (ceil(max_pages * page / 32) + 8) *
- * hkv * ceil(draft * (hq/hkv) / 32) below 2^31. */
+ * page a multiple of 16, draft 1..64, batch 1..65535, max_pages * page at
+ * most 2^31 - 1024, cache_rows below 2^31, batch * draft * hq below 2^24
+ * (below 2^26 where draft * (hq/hkv) > 32), and batch * (ceil(max_pages *
+ * page / 32) + 8) * hkv * ceil(draft * (hq/hkv) / 32) at most 2^31 - 1024. */
 size_t bitlinear_attn_cache_workspace_bytes(int64_t batch, int64_t draft, int64_t hq, int64_t hkv,
                                             int64_t d);
 int bitlinear_attn_cache(const uint16_t *Q, int64_t q_stride, const uint16_t *K,

@@ -1309,13 +1309,16 @@ int bitlinear_attn_cache(const uint16_t* Q, int64_t q_stride, const uint16_t* K,
   TRY(check_cache(batch, draft, hq, hkv, d));
   if (page < 16 || page % 16 != 0 || page >= kLimit)
     return fail(BL_ESHAPE, "page must be a positive multiple of 16 (got %lld)", (long long)page);
-  if (max_pages < 1 || max_pages >= kLimit || max_pages * page >= kLimit)
-    return fail(BL_ESHAPE, "max_pages must be >= 1 and max_pages*page below 2^31 (got %lld)", (long long)max_pages);
+  // (the kernels count rows and tiles in 32 bits and round both up: to tiles of
+  // up to 64 rows, three of them beyond the last, and to 512 equal ranges)
+  if (max_pages < 1 || max_pages >= kLimit || max_pages * page > kLimit - 1024)
+    return fail(BL_ESHAPE, "max_pages must be >= 1 and max_pages*page at most 2^31 - 1024 (got %lld)",
+                (long long)max_pages);
   if (cache_rows < 0 || cache_rows >= kLimit)
     return fail(BL_ESHAPE, "cache_rows must be in [0, 2^31) (got %lld)", (long long)cache_rows);
   {  // tiles of the whole call are counted in 32 bits (with up to 8 more for each unit)
     const int64_t tiles = batch * ((max_pages * page + 31) / 32 + 8), units = hkv * ((draft * (hq / hkv) + 31) / 32);
-    if (tiles >= kLimit || tiles * units >= kLimit)
+    if (tiles >= kLimit || tiles * units > kLimit - 1024)
       return fail(BL_ESHAPE, "too many cache tiles for one call (batch %lld, %lld rows each)", (long long)batch,
                   (long long)(max_pages * page));
   }
