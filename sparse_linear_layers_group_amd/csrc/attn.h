@@ -49,6 +49,9 @@ __device__ __forceinline__ v8bf operand_of(const v16f& x, int s) {
 }
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }
+// Largest |m scale log2 e| whose rounding may stay in the exponents of a
+// softmax: 2^-12 of an exponent, 2^-12 of P, a sixteenth of P's rounding to bf16
+constexpr float kSteep = 4096.f;
 // the other half wavefront's value of the same column, combined with `f`
 template <class F>
 __device__ __forceinline__ float half_join(float v, F f) {

@@ -150,6 +150,12 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // exponent of 2: P then stays below 2^8 and the 64 accumulators are
 // rescaled a few times per row instead of once per tile.
 //
+// The exponent is one fma, S scale log2 e - ms with ms = m scale log2 e rounded:
+// the rounding of ms (2^-24 of it) turns up in every P of the row alike, and
+// differs only between tiles of different m.  Where |ms| passes kSteep that is no
+// longer small (at 2^31 it leaves the range of P altogether), and the tile's
+// scores are made differences S - m before their exponents are taken.
+//
 // Bound by the matrix unit and, beside it, the exponentials: one tile of a
 // wavefront is 32 matrix instructions (1024 clocks) and about 200 others, which
 // two wavefronts per SIMD overlap in part.  128 rows a workgroup (32 in each
@@ -216,7 +222,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int items,
   const int seen = r + off - 4 * (lane >> 5);  // last visible key, minus this lane's row offset
   v16f o[D / 32], s[2][2];  // scores of the tiles in stage 0 and 1
   clear<D / 32>(o);
-  float m = -kInf, ms = 0.f, l = 0.f;  // ms: m scale log2 e, 0 while m is -inf
+  float m = -kInf, ms = 0.f, l = 0.f;  // ms: m scale log2 e, 0 while m is -inf, and while steep
+  bool steep = false;                  // some row's |m scale log2 e| > kSteep (the same in all lanes)
 
   auto issue_k = [&](lds_char* to, int t) {
     if (t < tiles) kd.issue(to, kp + (int64_t)t * kKRows * a.k_stride, kr.len - t * kKRows);
@@ -248,17 +255,26 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int items,
       for (int j = 0; j < 16; ++j) mx = fmaxf(mx, x[i][j]);
     return half_join(mx, [](float u, float v) { return fmaxf(u, v); });
   };
-  auto raise = [&](float mx) {
+  auto raise = [&](float mx, v16f* x) {
     if (__ballot((mx - m) * sl > 8.f)) {  // (NaN where both are -inf: a row that sees no key yet)
       const float mn = fmaxf(m, mx), z = mn == -kInf ? 0.f : mn;
       const float f = exp2_hw((m - z) * sl);
       m = mn;
       ms = z * sl;
+      steep = __ballot(fabsf(ms) > kSteep) != 0;
+      if (steep) ms = 0.f;
       l *= f;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[d][j] *= f;
+    }
+    if (steep) {
+      const float z = m == -kInf ? 0.f : m;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[i][j] -= z;
     }
   };
   // P of a tile's scores as operands; its sum goes to l
@@ -325,7 +341,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int items,
     }
     __builtin_amdgcn_sched_group_barrier(0x8, 3, 0);
     __builtin_amdgcn_sched_barrier(0);
-    raise(mx);
+    raise(mx, s[P ^ 1]);
   };
   auto end = [&](auto stage, int t) {  // this wavefront's last tile
     constexpr int P = decltype(stage)::value;
@@ -354,7 +370,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int items,
   if (first < wtiles) {
     scores(k_stage<D, 0>(), s[0]);
     mask(s[0], first);
-    raise(most(s[0]));
+    raise(most(s[0]), s[0]);
     for (; t + 2 < wtiles; t += 2) {
       step(S0{}, t);
       step(S1{}, t + 1);
