@@ -227,6 +227,7 @@ template <int D>
 struct Running {
   v16f o[D / 32];
   float m, l;
+  bool steep;  // some row's |m scale log2 e| > kSteep (the same in all lanes)
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
@@ -234,6 +235,7 @@ struct Running {
       for (int j = 0; j < 16; ++j) o[d][j] = 0.f;
     m = -kInf;
     l = 0.f;
+    steep = false;
   }
   __device__ __forceinline__ void raise(float mx, float sl) {
     mx = half_join(mx, [](float p, float q) { return fmaxf(p, q); });
@@ -241,6 +243,7 @@ struct Running {
       const float mn = fmaxf(m, mx);
       const float f = exp2_hw((m - (mn == -kInf ? 0.f : mn)) * sl);
       m = mn;
+      steep = __ballot((mn == -kInf ? 0.f : fabsf(mn)) * sl > kSteep) != 0;
       l *= f;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
@@ -249,7 +252,11 @@ struct Running {
     }
   }
   __device__ __forceinline__ void weigh(v16f& s, float sl) {
-    const float ms = (m == -kInf ? 0.f : m) * sl;
+    const float z = m == -kInf ? 0.f : m, ms = steep ? 0.f : z * sl;
+    if (steep) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[j] -= z;
+    }
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
