@@ -663,7 +663,10 @@ int bitlinear_attn_fwd(const uint16_t *Q, const uint16_t *K, const uint16_t *V, 
  *   dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO
  * dK and dV are sums over the query heads of a group.  P, dS and (from
  * binary32) dO are rounded to bf16 for the products, all sums are binary32,
- * and the order of every sum is fixed: reruns give the same bits.
+ * and the order of every sum is fixed: reruns give the same bits.  P is formed
+ * from lse, whose binary32 rounding makes it wrong by up to some 2^-22 |lse|,
+ * relative: a row with |lse| above 65536 gets NaN in its dQ and in the dK and
+ * dV of the keys it sees.
  *   dO   device [total_q][hq*d], bf16 or binary32 (do_type; binary32 is
  *        what bitlinear_bwd of the o BitLinear writes).
  *   dQ   device bf16 [total_q][hq*d]; dK, dV  device bf16 [total_k][hkv*d];

@@ -12,6 +12,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kQRows = 128;  // query rows of a forward / dQ workgroup: 32 per wavefront
 constexpr int kKRows = 64;   // key rows of a tile in LDS
 constexpr int kExactTiles = 2;  // dQ workgroups with at most this many key tiles form delta from P dP
+constexpr float kMostLse = 65536.f;  // largest |lse| of a row with gradients
 constexpr int kBKeys = 64;   // key rows of a dK / dV workgroup: two blocks of 32, four wavefronts each
 constexpr int kBRows = 128;  // query rows of its stages: 32 per wavefront
 constexpr int kMaxSplits = 8;  // (16 made every join 1 - 2 us longer and saved 2 us in a few calls)
@@ -474,6 +475,11 @@ __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int spli
 // delta = sum P dP in binary32 in a sweep of their own over tiles that stay
 // in LDS, and leave it in memory for the dK / dV pass (four tiles instead of
 // two gain another 1 % of the error and double the time of small calls).
+//
+// lse is binary32, and so is -lse / scale that S is added to: P carries their
+// rounding, two to five half steps of lse (measured with exact scores: 0.4 % at |lse|
+// = 1e4, 1 - 2 % at 1e5, 27 % at 2.5e6).  Rows beyond kMostLse, where that passes the
+// rounding of P to bf16 several times over, get NaN in place of wrong gradients.
 
 // The dQ pass comes first and leaves for the other what it adds to its
 // products as the accumulators' first values, -lse / scale to S (-inf where
@@ -536,7 +542,9 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, int item
   v8bf qf[D / 16], gf[D / 16], of[D / 16];
   load_row_operand<D>(qf, a.Q + row * a.q_stride + (int64_t)head * D, lane);
   load_row_operand<D>(of, a.O + at, lane);
-  const float lse = ld_global(a.lse + sum_at);
+  const float given = ld_global(a.lse + sum_at);
+  const bool wild = given != -kInf && !(fabsf(given) <= kMostLse);
+  const float lse = wild ? __builtin_nanf("") : given;
   if (a.do_f32) {
     const v4f* p = reinterpret_cast<const v4f*>(static_cast<const float*>(a.dO) + at + 8 * (lane >> 5));
     v4f x[D / 16][2];
@@ -629,7 +637,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnBwdArgs a, int item
     if (wtiles > 0) sums(S0{}, 0);
     if (wtiles > 1) sums(S1{}, 1);
     nd = -half_join(exact, [](float u, float v) { return u + v; });
-    if (in && lane < 32) st_global(ndelta + sum_at, nd);
+    // (a row of NaN keeps its finite delta there: 0 times that is 0 at the keys it does not see)
+    if (in && lane < 32 && !wild) st_global(ndelta + sum_at, nd);
   }
   auto step = [&](auto stage, int t) {
     if (!few) {  // (few: both tiles are there)
