@@ -404,10 +404,11 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int items,
     }
     return;
   }
-  // a row that sees no key: zeros, and -inf as the logarithm of its sum
+  // a row that sees no key: zeros, and -inf as the logarithm of its sum (NaN
+  // scores make l NaN, and lse with it)
   store_row<D>(a.O + ((int64_t)(qr.start + r) * a.hq + head) * D, o, l > 0.f ? 1.f / l : 0.f, lane, in);
   if (a.lse && in && lane < 32)
-    st_global(a.lse + (int64_t)head * a.total_q + qr.start + r, l > 0.f ? fmaf(m, sl, log2_hw(l)) * kLn2 : -kInf);
+    st_global(a.lse + (int64_t)head * a.total_q + qr.start + r, l == 0.f ? -kInf : fmaf(m, sl, log2_hw(l)) * kLn2);
 }
 
 // O and lse of rows whose keys were split: 8 (D = 128) or 16 rows of a tile and
@@ -452,7 +453,7 @@ __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int spli
   const float inv = l > 0.f ? 1.f / l : 0.f;
   st_global(reinterpret_cast<u32x2*>(a.O + ((int64_t)(qr.start + r) * a.hq + head) * D) + c,
             u32x2{pk_bf16(y[0] * inv, y[1] * inv), pk_bf16(y[2] * inv, y[3] * inv)});
-  if (a.lse && c == 0) st_global(a.lse + at, l > 0.f ? fmaf(m, sl, log2_hw(l)) * kLn2 : -kInf);
+  if (a.lse && c == 0) st_global(a.lse + at, l == 0.f ? -kInf : fmaf(m, sl, log2_hw(l)) * kLn2);
 }
 
 // --------------------------------------------------------------- backward
