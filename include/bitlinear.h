@@ -586,7 +586,8 @@ int bitlinear_rope_table(int64_t max_pos, int64_t d, double base, float *table, 
  *              the BitLinears' Y, or BL_TYPE_BF16, their bf16 Y).  V and Vr
  *              may both be NULL.
  *   q_weight, k_weight  device float [d], both or neither (no norms).
- *   eps        finite, >= 0.
+ *   eps        finite, >= 0.  Rows of any finite size are normed (one of
+ *              zeros with eps = 0 gives NaN).
  *   pos        device int32 [tokens]; a position outside [0, max_pos) gives
  *              NaN in that token's q and k rows.
  *   slots      NULL, or device int64 [tokens]: the row of Kr and Vr that

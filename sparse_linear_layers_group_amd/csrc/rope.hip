@@ -55,6 +55,13 @@ struct Vec8<true> {
   }
   __device__ __forceinline__ void zero() { a = b = f32x4{0.f, 0.f, 0.f, 0.f}; }
   __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i & 3] : b[i & 3]; }
+  __device__ __forceinline__ void scale(float k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] *= k;
+      b[i] *= k;
+    }
+  }
 };
 template <>
 struct Vec8<false> {
@@ -66,7 +73,35 @@ struct Vec8<false> {
   __device__ __forceinline__ float get(int i) const {
     return (i & 1) ? bf16_hi(a[(i >> 1) & 3]) : bf16_lo(a[(i >> 1) & 3]);
   }
+  __device__ __forceinline__ void scale(float k) {  // by a power of two
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = pack_bf16(bf16_lo(a[i]) * k, bf16_hi(a[i]) * k);
+  }
 };
+
+// 1 / sqrt(mean(x^2) + eps) of the row that D/16 lanes hold.  Where the squares
+// leave binary32 (from some 1e18 on: an infinite mean made the row zeros; below
+// 2^-50 with an eps as small) the row is first scaled by a power of two, in
+// place: the result is then that of the scaled row, and `by` the scale.  The
+// branch is taken for a whole wavefront and no ordinary row takes it.
+template <int D, bool F32>
+__device__ __forceinline__ float row_scale(Vec8<F32>& lo, Vec8<F32>& hi, float eps, float& by) {
+  auto mean = [&](float e) {
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq = fmaf(lo.get(i), lo.get(i), fmaf(hi.get(i), hi.get(i), sq));
+    return fmaf(row_sum<D>(sq), 1.f / D, e);
+  };
+  float m = mean(eps);
+  by = 1.f;
+  if (__ballot(!(m >= 0x1p-100f && m <= 0x1p127f))) {
+    by = m > 0x1p127f ? 0x1p-70f : m < 0x1p-100f ? 0x1p96f : 1.f;
+    lo.scale(by);
+    hi.scale(by);
+    m = mean(eps * by * by);
+  }
+  return rsq(m);
+}
 
 // cosines and sines of a lane's 8 pairs at one position; a position outside
 // the table gives NaN, so a wrong one shows in the outputs
@@ -130,18 +165,16 @@ __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a) {
 #pragma unroll
   for (int r = 0; r < kRowsHeld; ++r) {
     const int h = h0 + r * M::kGroups;
-    float x[8], y[8];
+    const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
+    float x[8], y[8], rs = 1.f, by;
+    Vec8<F32> xl = lo[r], xh = hi[r];
+    if (NORM) rs = row_scale<D>(xl, xh, a.eps, by);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      x[i] = lo[r].get(i);
-      y[i] = hi[r].get(i);
+      x[i] = is_v ? lo[r].get(i) : xl.get(i);
+      y[i] = is_v ? hi[r].get(i) : xh.get(i);
     }
-    const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
     if (NORM) {
-      float sq = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], fmaf(y[i], y[i], sq));
-      const float rs = rsq(fmaf(row_sum<D>(sq), 1.f / D, a.eps));
       if (!is_v) {
         const float* w = is_q ? a.qw : a.kw;
         Vec8<true> wl, wh;
@@ -233,10 +266,8 @@ __global__ __launch_bounds__(256, NORM ? 3 : 4) void qk_rope_bwd_kernel(RopeBwdA
         q[i] = fmaf(v, turn.c[i], -(u * turn.s[i]));
       }
       if (NORM) {
-        float sq = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(xl[r].get(i), xl[r].get(i), fmaf(xh[r].get(i), xh[r].get(i), sq));
-        const float rs = rsq(fmaf(row_sum<D>(sq), 1.f / D, a.eps));
+        float by;
+        const float rs = row_scale<D>(xl[r], xh[r], a.eps, by);
         const float* w = is_q ? a.qw : a.kw;
         Vec8<true> wl, wh;
         wl.load(w, i0);
@@ -256,10 +287,11 @@ __global__ __launch_bounds__(256, NORM ? 3 : 4) void qk_rope_bwd_kernel(RopeBwdA
           dot = fmaf(p[i], nl, fmaf(q[i], nh, dot));
         }
         dot = row_sum<D>(dot) * (1.f / D);
+        const float rx = rs * by;  // of the row as it was
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          p[i] = rs * fmaf(-(xl[r].get(i) * rs), dot, p[i]);
-          q[i] = rs * fmaf(-(xh[r].get(i) * rs), dot, q[i]);
+          p[i] = rx * fmaf(-(xl[r].get(i) * rs), dot, p[i]);
+          q[i] = rx * fmaf(-(xh[r].get(i) * rs), dot, q[i]);
         }
       }
       if (h >= heads) continue;
