@@ -610,7 +610,8 @@ int bitlinear_qk_rope(const void *Q, const void *K, const void *V, int x_type, i
  * (dx = g without weights; x, x_type and eps are then not read and Q, K may
  * be NULL).  dx is rounded once to bf16 (the dY of the q and k BitLinears'
  * bitlinear_bwd); dw is summed in binary32 per wavefront and binary64 over
- * workgroups, in a fixed order.
+ * workgroups, in a fixed order, over all tokens: padding among them needs
+ * finite x, a position in the table, and zeros in dQr and dKr.
  *   dQr, dKr   device bf16 [tokens][hq*d], [tokens][hkv*d].
  *   dQ, dK     device bf16, the same shapes, written.
  *   dq_weight, dk_weight  device float [d], written; NULL without weights.

@@ -122,7 +122,13 @@ class BlockAttention:
     head norms with the rotation, and causal attention over packed sequences
     (prompts and training) or over a paged cache (serving).  Owns the rotation
     table; outputs and workspaces are allocated per call on torch's current
-    stream, as torch's own operators do."""
+    stream, as torch's own operators do.
+
+    A packed batch may be padded: rows of no sequence come back as zeros from
+    attend and attend_bwd, since whatever is further on sums over all tokens
+    (rotate_bwd for the norms' weights, the BitLinears' dW).  A program whose
+    sequences fill their rows may pass padded=False, which spares filling the
+    outputs (8192 tokens, 20 + 5 heads of 128: 105 MB over both calls)."""
 
     def __init__(self, hq, hkv, d, max_pos, base=10000.0, q_weight=None, k_weight=None, eps=1e-6, scale=None,
                  device="cuda"):
@@ -133,8 +139,9 @@ class BlockAttention:
         self.table = torch.empty(max_pos, self.d // 2, 2, dtype=torch.float32, device=device)
         bl.bitlinear_rope_table(max_pos, self.d, base, self.table)
 
-    def _bf16(self, rows, heads):
-        return torch.empty(rows, heads * self.d, dtype=torch.bfloat16, device=self.device)
+    def _bf16(self, rows, heads, zeros=False):
+        new = torch.zeros if zeros else torch.empty
+        return new(rows, heads * self.d, dtype=torch.bfloat16, device=self.device)
 
     def _scratch(self, nbytes):
         return torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
@@ -160,18 +167,18 @@ class BlockAttention:
                                  self.q_weight, self.k_weight, self.eps, self.table, pos, dQr, dKr, dQ, dK, gq, gk, ws=ws)
         return dQ, dK, gq, gk
 
-    def attend(self, Qr, Kr, Vr, cu_q, cu_k):
-        """(O, lse) of packed sequences."""
+    def attend(self, Qr, Kr, Vr, cu_q, cu_k, padded=True):
+        """(O, lse) of packed sequences; lse of rows of no sequence is undefined."""
         tq, tk, b = Qr.shape[0], Kr.shape[0], cu_q.numel() - 1
-        O, lse = self._bf16(tq, self.hq), torch.empty(self.hq, tq, device=self.device)
+        O, lse = self._bf16(tq, self.hq, padded), torch.empty(self.hq, tq, device=self.device)
         ws = self._scratch(bl.bitlinear_attn_fwd_workspace_bytes(b, tq, tk, self.hq, self.hkv, self.d))
         bl.bitlinear_attn_fwd(Qr, Kr, Vr, cu_q, cu_k, b, self.hq, self.hkv, self.d, self.scale, O, lse, ws=ws)
         return O, lse
 
-    def attend_bwd(self, Qr, Kr, Vr, O, lse, dO, cu_q, cu_k):
+    def attend_bwd(self, Qr, Kr, Vr, O, lse, dO, cu_q, cu_k, padded=True):
         """(dQr, dKr, dV) for dO in bfloat16 or float32 (the o BitLinear's dX)."""
         tq, tk, b = Qr.shape[0], Kr.shape[0], cu_q.numel() - 1
-        dQ, dK, dV = self._bf16(tq, self.hq), self._bf16(tk, self.hkv), self._bf16(tk, self.hkv)
+        dQ, dK, dV = (self._bf16(n, h, padded) for n, h in ((tq, self.hq), (tk, self.hkv), (tk, self.hkv)))
         ws = self._scratch(bl.bitlinear_attn_bwd_workspace_bytes(b, tq, tk, self.hq, self.hkv, self.d))
         bl.bitlinear_attn_bwd(Qr, Kr, Vr, O, lse, dO, cu_q, cu_k, b, self.hq, self.hkv, self.d, self.scale, dQ, dK, dV,
                               ws=ws)
