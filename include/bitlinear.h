@@ -636,7 +636,7 @@ int bitlinear_qk_rope_bwd(const void *Q, const void *K, int x_type, int64_t q_st
  *   lse = ln sum exp S
  * A row that sees no key has O = 0 and lse = -infinity.  Products are bf16
  * with binary32 sums, the softmax is binary32, P is rounded to bf16 for the
- * product with V (relative 2^-9 per key) and O once more.  Scores may be of
+ * product with V (up to 2^-8 relative per key) and O once more.  Scores may be of
  * any size as long as q.k and scale q.k are finite in binary32: exponents are
  * formed from differences to the row's maximum.
  *   Q, K, V    device bf16 rows, strides below 2^22.

@@ -145,9 +145,9 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // O = softmax(scale Q K^T) V in one pass over the keys: per 64-key tile
 //   S^T = K Q^T,  m' = max(m, max S),  P = 2^((S - m') scale log2 e),
 //   l = l 2^((m - m') ..) + sum P,  O^T = O^T 2^(..) + V^T P^T
-// with m, l, O in binary32; P is rounded to bf16 (half a step, 2^-9
-// relative, averaged over the keys) for the second product, the sum l is of
-// the unrounded P.  m' only moves when a score passes it by 8 in the
+// with m, l, O in binary32; P is rounded to bf16 (half a step, at most 2^-8
+// relative; its sign differs from key to key) for the second product, the sum
+// l is of the unrounded P.  m' only moves when a score passes it by 8 in the
 // exponent of 2: P then stays below 2^8 and the 64 accumulators are
 // rescaled a few times per row instead of once per tile.
 //
