@@ -113,9 +113,16 @@ def lib():
     return _lib
 
 
+# The current stream's handle itself: making a Stream object for it takes 2.5 us
+# a call.  (A private name of torch; without it the object is made.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:  # the handle itself: making a Stream object for it takes 2.5 us a call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
