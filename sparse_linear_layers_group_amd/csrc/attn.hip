@@ -162,9 +162,9 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // two wavefronts per SIMD overlap in part.  128 rows a workgroup (32 in each
 // wavefront: their O, scores and Q take 250 registers) and two workgroups per
 // CU; K and V in two stages each, so a load has a whole tile's time.  16384
-// tokens, 16 + 2 heads of 128: 1022 us, 1076 TFLOP/s of the products below the
+// tokens, 16 + 2 heads of 128: 1049 us, 1048 TFLOP/s of the products below the
 // diagonal, the matrix unit busy 53 % of the clocks; without the exponentials
-// 750 us.  8192 tokens in seven sequences, 20 + 5 heads: 125 us, 39 % busy (the
+// 750 us.  8192 tokens in seven sequences, 20 + 5 heads: 127 us, 39 % busy (the
 // longest rows of one sequence are as long as a CU's mean share).
 // Tried without gain: two heads of a group in a workgroup of eight wavefronts
 // (half the loads, 5 % slower at 16384 tokens), priorities by length.
@@ -413,7 +413,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int items,
 
 // O and lse of rows whose keys were split: 8 (D = 128) or 16 rows of a tile and
 // head per workgroup, 4 elements a thread, all parts loaded before the first is
-// used.  Bound by the binary32 parts: 480 of 128 rows (31 MB) take 7.2 us.
+// used.  Bound by the binary32 parts: 480 of 128 rows (31 MB) take 7.9 us.
 template <int D>
 __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int splits, int target,
                                                            const float* __restrict__ part) {
@@ -489,10 +489,10 @@ __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int spli
 //
 // Bound by the matrix unit with LDS beside it (every operand from LDS, 1 KiB
 // per instruction, serves one product): 8192 tokens in four sequences, 20 + 5
-// heads of 128: 178 us, 1015 TFLOP/s of its three products, the matrix unit
-// busy 50 % of the clocks.  Two workgroups per CU (220 registers), K and V
-// tiles in two stages.  Small calls are a chain of latencies (finding the item,
-// the rows, the tiles, the exact sums): 512 tokens, 14 + 2 heads of 64: 10 us.
+// heads of 128: 196 us (average of 20 runs; the shortest 181), 924 TFLOP/s of
+// its three products, the matrix unit busy 51 % of the clocks.  Two workgroups
+// per CU (224 registers), K and V tiles in two stages.  Small calls are a chain of latencies (finding the item,
+// the rows, the tiles, the exact sums): 512 tokens, 14 + 2 heads of 64: 11 us.
 //
 // Keys are shared out as in the forward: parts leave binary32 sums in `part`
 // ([split][hq][total_q] rows of D), which attn_dq_join_kernel adds in order (2452
@@ -712,10 +712,11 @@ __global__ __launch_bounds__(256) void attn_dq_join_kernel(AttnBwdArgs a, int sp
 // 300, one wavefront per SIMD and moves between the two register files.)
 //
 // Bound by the matrix unit with LDS beside it: 8192 tokens in four sequences,
-// 20 + 5 heads of 128: 300 us, 803 TFLOP/s of its four products, the matrix unit
-// busy 40 % of the clocks, LDS 32 %; each CU runs 15 % of the time with one
+// 20 + 5 heads of 128: 336 us (average of 20 runs; the shortest 306), 718
+// TFLOP/s of its four products, the matrix unit busy 40 % of the clocks, LDS
+// 32 %; each CU runs 15 % of the time with one
 // wavefront per SIMD or none (the tile of a sequence's first keys is as long as
-// a CU's mean share).  512 tokens, 14 + 2 heads of 64: 10 us and 3.5 us to join.
+// a CU's mean share).  512 tokens, 14 + 2 heads of 64: 11 us and 3.8 us to join.
 //
 // `splits` workgroups share a tile where there are few: each takes a part of
 // the (stage, head) steps and leaves binary32 sums in `part`
@@ -960,7 +961,7 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnBwdArgs a, int ite
 }
 
 // dK and dV of split tiles: the splits' sums in order, 8 elements a thread,
-// all loaded before the first is used (bound by latency: 3.5 us)
+// all loaded before the first is used (bound by latency: 3.8 us)
 template <int D>
 __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnBwdArgs a, int splits,
                                                            const float* __restrict__ part) {

@@ -32,7 +32,7 @@ constexpr int kGranule = 16;  // rows that share a page
 // unit's tiles of 32 keys and streams them through two LDS stages of its
 // own; no barriers, one tile in flight while one is computed (64 KiB per CU).
 // The wavefronts meet in LDS at the end of the unit or the range.  64
-// sequences of 1024 - 8192 rows, 16 + 2 heads of 128 (301 MB): 64.6 us with the
+// sequences of 1024 - 8192 rows, 16 + 2 heads of 128 (301 MB): 64.5 us with the
 // join, 4.7 TB/s, as fast as a large copy; one of 32768 rows, 20 + 5 heads
 // (84 MB): 22.6 us, of which the join takes 4.5 and the first loads 3.
 //
@@ -44,8 +44,8 @@ constexpr int kGranule = 16;  // rows that share a page
 // blocks of 32 rows per wavefront ran out of registers; with units of 32 rows
 // it read K and V once for each: 24 tokens of 4 heads behind 38,000 rows took
 // 113 us, with two stages and two workgroups per CU 41 us of this kernel, now
-// 33.)  Those 38,000 rows in eight sequences, 5 key/value heads (99 MB), are
-// 39 us with the join: 3 to find the ranges, 7 to start on one or two units
+// 35.)  Those 38,000 rows in eight sequences, 5 key/value heads (99 MB), are
+// 40 us with the join: 3 to find the ranges, 7 to start on one or two units
 // each, 14 for a workgroup's 12 tiles (their loads alone 10), 6 to write 13 MB
 // of partial results and 6.5 to join them.  (The next tile's scores among the
 // exponentials, as in the forward, gained nothing here.)

@@ -128,9 +128,9 @@ __device__ __forceinline__ void store8(uint16_t* p, const float* y) {
 
 // y = R(pos) (w * x / rms(x)) for rows of q and k, V rows copied; all
 // rounded once to bf16.  Bound by HBM where there is much to move (6001 tokens,
-// 14 + 2 + 2 heads of 64, bf16: 28 MB in 8.4 us, 3.3 TB/s of which 2 us are the
+// 14 + 2 + 2 heads of 64, bf16: 28 MB in 9.0 us, 3.1 TB/s of which 2 us are the
 // launch), by three loads one after another (position, table, weights) in a
-// serving step (64 tokens: 3.6 us).
+// serving step (64 tokens: 4.1 us).
 template <int D, bool F32, bool NORM>
 __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a) {
   typedef RopeMap<D> M;
@@ -214,8 +214,8 @@ __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a) {
 // Bound by HBM: x and dy are read and dx is written once.  The sums take the
 // registers to 162 - 168, so three workgroups fit a CU and kRopeDwRows of them are
 // launched, which walk side by side to the end (1024, a third more than fit:
-// 64.6 us in place of 52.1 at 8192 tokens of 20 + 5 heads of 128 in binary32,
-// 210 MB, 4.0 TB/s; 512: 54.9 us).
+// 64.6 us in place of 52.1 at 8192 tokens of 20 + 5 heads of 128 in binary32;
+// 512: 54.9 us; now 51.3 us for 210 MB, 4.1 TB/s).
 template <int D, bool F32, bool NORM>
 __global__ __launch_bounds__(256, NORM ? 3 : 4) void qk_rope_bwd_kernel(RopeBwdArgs a) {
   typedef RopeMap<D> M;
@@ -320,7 +320,7 @@ __global__ __launch_bounds__(256, NORM ? 3 : 4) void qk_rope_bwd_kernel(RopeBwdA
 
 // dw[e] = sum of the workgroups' partials: 4 columns of 2D per workgroup, its
 // threads along the rows, joined in LDS, all in binary64 and in a fixed order
-// (768 rows of 256 columns: 4.2 us, latency)
+// (768 rows of 256 columns: 4.6 us, latency)
 __global__ __launch_bounds__(256) void rope_dw_kernel(const float* __restrict__ part, int rows, int d,
                                                      float* __restrict__ gq, float* __restrict__ gk) {
   __shared__ double red[4][4];
