@@ -57,3 +57,42 @@ def test_padded_batch(d, norm):
         assert (dx[i][used:] == 0).all()
         if norm:
             R.assert_within(dx[2 + i], dw, dwe, "norm weight")
+
+
+@pytest.mark.parametrize("q_total,k_total", [(200, 200), (60, 3000)])
+def test_padded_batch_in_a_graph(q_total, k_total):
+    """Captured with one set of lengths, replayed with others: rows that were a
+    sequence's before are padding now, and zeros."""
+    hq, hkv, d = 4, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)  # noqa: E731
+    att = BlockAttention(hq, hkv, d, 256)
+    q, k, v, do = n(q_total, hq * d), n(k_total, hkv * d), n(k_total, hkv * d), n(q_total, hq * d)
+    cq, ck = (torch.tensor([0, t // 2, t], dtype=torch.int32, device="cuda") for t in (q_total, k_total))
+
+    def step():
+        o, lse = att.attend(q, k, v, cq, ck)
+        return o, *att.attend_bwd(q, k, v, o, lse, do, cq, ck)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for used in ((1.0, 1.0), (0.3, 0.5), (0.1, 0.9), (1.0, 0.4)):
+        ql = [int(q_total * used[0] * 0.5), int(q_total * used[0] * 0.4)]
+        kl = [int(k_total * used[1] * 0.4), int(k_total * used[1] * 0.5)]
+        for c, l in ((cq, ql), (ck, kl)):
+            c.copy_(torch.tensor([0, l[0], sum(l)], dtype=torch.int32))
+        poison(q_total * hq * d, k_total * hkv * d)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in outs]
+        ref = R.attention(*(t.view(t.shape[0], -1, d) for t in (q, k, v)), ql, kl, att.scale, do.view(q_total, hq, d))
+        for x, name, rows in zip(got, ("o", "dq", "dk", "dv"), (sum(ql), sum(ql), sum(kl), sum(kl))):
+            R.assert_within(x.view(x.shape[0], -1, d), ref[name], ref[name + "_err"], name)
+            assert (x[rows:] == 0).all()
+        for x, y in zip(got, step()):
+            assert torch.equal(x, y)
