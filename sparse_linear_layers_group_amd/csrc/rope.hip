@@ -208,7 +208,7 @@ __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a) {
 //   dw += g n,   a = w g,   dx = (a - n mean(a n)) / rms(x)
 // (without norms dx = g).  With norms each workgroup walks over units and
 // keeps its share of dw in registers (a binary32 sum per lane and element, over
-// every 3072nd unit of a large call), joins them in LDS in a fixed order and
+// one unit of every 4 kRopeDwRows of a large call), joins them in LDS in a fixed order and
 // writes one row of partial sums; rope_dw_kernel adds those in binary64.
 // No atomics: reruns give the same bits.
 // Bound by HBM: x and dy are read and dx is written once.  The sums take the

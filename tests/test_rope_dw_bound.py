@@ -29,9 +29,9 @@ def test_mistakes_do_not_pass(tokens, h, hkv, d):
     t = terms(x, dy, c, s, torch.float32)
     right = t.double().sum((0, 1))
     assert ((right - dw).abs() <= err).all()
-    lanes = t.reshape(-1, d)  # 3072 sums in binary32, added in binary64
-    pad = torch.zeros(-lanes.shape[0] % 3072, d)
-    parts = torch.cat((lanes, pad)).view(-1, 3072, d)
+    lanes = t.reshape(-1, d)  # a sum in binary32 for each wavefront, added in binary64
+    pad = torch.zeros(-lanes.shape[0] % W.WAVES, d)
+    parts = torch.cat((lanes, pad)).view(-1, W.WAVES, d)
     in_lanes = parts[0].clone()
     for p in parts[1:]:
         in_lanes += p
