@@ -719,6 +719,135 @@ int bitlinear_attn_cache(const uint16_t *Q, int64_t q_stride, const uint16_t *K,
                          int64_t hkv, int64_t d, float scale, uint16_t *O, void *ws,
                          size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------
+ * The feed-forward side of a block: layer norm, the gated feed-forward's two
+ * projections with the activation and the product, and 8-bit checkpoints of
+ * activations, which both of the others write and read.  The pages describe
+ * BitNet's feed-forward (2B4T article §一: squared ReLU, gated) and give no
+ * formulas for norms or checkpoints; those below are the operators'
+ * definitions here. */
+#define BL_TYPE_Q8  2  /* int8 codes with one binary32 scale per block of a row */
+
+/* 8-bit checkpoint of rows of n values: blocks of 64 consecutive values of a
+ * row (the last block of a row may be shorter) share one scale.  With a the
+ * largest |x| of a block, in binary32:
+ *   code = the integer nearest to x * RN(127 / a) (ties to even),
+ *   scale = RN(a / 127),  and a value comes back as RN(code * scale),
+ * at most a/254 (and its roundings) away.  A block whose a is below 2^-100
+ * comes back as zeros, one that holds an infinity or a NaN as NaN.
+ *   X       device rows, binary32 or bf16 (x_type), x_stride elements apart.
+ *   codes   device int8 [rows][n], 16-byte aligned.
+ *   scales  device float [rows][ceil(n / 64)].
+ *   Y       device [rows][n], binary32 or bf16 (rounded once).
+ * n a positive multiple of 16, rows * ceil(n / 64) at most 2^29 - 32;
+ * rows == 0 is a no-op. */
+int bitlinear_ckpt_pack(const void *X, int x_type, int64_t x_stride, int64_t rows, int64_t n,
+                        int8_t *codes, float *scales, void *stream);
+int bitlinear_ckpt_unpack(const int8_t *codes, const float *scales, int64_t rows, int64_t n,
+                          void *Y, int y_type, void *stream);
+
+/* Layer norm of rows of n values:
+ *   mu = mean(x) (0 unless center),  rstd = 1 / sqrt(mean((x - mu)^2) + eps),
+ *   y = (x - mu) rstd weight + bias
+ * in binary32, rounded once.  With center = 0 it is the root-mean-square norm.
+ * The row stays in registers: the variance is formed from the differences.
+ * A row whose variance leaves binary32 (from some 1e19 on) gives NaN.
+ *   X       device rows, binary32 or bf16 (x_type), x_stride elements apart.
+ *   weight, bias  device float [n]; each may be NULL (1 and 0).
+ *   Y       device [rows][n], bf16 (a BitLinear's X) or binary32 (y_type).
+ *   mean, rstd  device float [rows] or NULL: for the backward.
+ *   codes, scales  NULL, or where a checkpoint of X goes (BL_TYPE_Q8, as
+ *           bitlinear_ckpt_pack writes it; n then a multiple of 16).
+ * n a multiple of 8 from 8 to 16384, rows below 2^23, eps finite and >= 0.
+ * rows == 0 is a no-op. */
+int bitlinear_layernorm(const void *X, int x_type, int64_t x_stride, int64_t rows, int64_t n,
+                        const float *weight, const float *bias, float eps, int center, void *Y,
+                        int y_type, float *mean, float *rstd, int8_t *codes, float *scales,
+                        void *stream);
+
+/* Its backward, from X or X's checkpoint.  With nx = (x - mu) rstd (mu and
+ * rstd those of the forward) and a = weight dy:
+ *   dx = rstd (a - mean(a) - nx mean(a nx)) + dr   (no mean(a) if not centred),
+ *   dweight = sum over rows of dy nx,  dbias = sum over rows of dy
+ * in binary32; the sums over rows are binary32 over the rows of one
+ * wavefront's or workgroup's share and binary64 over the shares, in a fixed
+ * order: reruns give the same bits.
+ *   X, x_type, x_stride  as in the forward, or its codes with BL_TYPE_Q8
+ *           (x_stride then n, x_scales their scales; otherwise x_scales NULL).
+ *   mean    what the forward wrote, or NULL for a norm that is not centred.
+ *   dY      device [rows][n], binary32 or bf16 (dy_type).
+ *   dR      NULL, or device [rows][n] of dX's type: the gradient that reaches X
+ *           past the norm (a residual's), added before the one rounding.
+ *   dX      device [rows][n], binary32 or bf16 (dx_type), written.
+ *   dweight, dbias  device float [n], each may be NULL.
+ *   ws      bitlinear_layernorm_bwd_workspace_bytes(n) bytes, 16-byte aligned,
+ *           clobbered; NULL without dweight and dbias.  Calls that overlap on
+ *           one workspace race.
+ * rows == 0 zeroes dweight and dbias. */
+size_t bitlinear_layernorm_bwd_workspace_bytes(int64_t n);
+int bitlinear_layernorm_bwd(const void *X, int x_type, const float *x_scales, int64_t x_stride,
+                            int64_t rows, int64_t n, const float *weight, const float *mean,
+                            const float *rstd, const void *dY, int dy_type, const void *dR,
+                            void *dX, int dx_type, float *dweight, float *dbias, void *ws,
+                            size_t ws_bytes, void *stream);
+
+/* The gated feed-forward's first half in one kernel: both projections, the
+ * activation and the product.  BitNet b1.58 2B4T article §一 (squared ReLU,
+ * gated, in place of SwiGLU; both are here).
+ *   G = acc_gate * gate_gamma * s_t,  U = acc_up * up_gamma * s_t
+ *       (binary32, exactly bitlinear_contract's Y of the two layers),
+ *   h = act(G) * U in binary32, rounded once to bf16: the down BitLinear's X.
+ * BL_ACT_RELU2: act(g) = max(g, 0)^2, products rounded as bitlinear_relu2_gate
+ * rounds them; BL_ACT_SILU: act(g) = g / (1 + exp(-g)).
+ *   xq, x_scale  device int8 [tokens x k] and float [tokens], as
+ *           bitlinear_act_quant writes them.
+ *   gate, up     device packed codes of two [n_out x k] layers under n:m;
+ *   gate_gamma, up_gamma  their scales.
+ *   H       device bf16 [tokens x n_out], written.
+ *   G, U    both NULL, or device [tokens x n_out] in save_type, for the
+ *           backward: BL_TYPE_F32, BL_TYPE_BF16, or BL_TYPE_Q8 (checkpoints as
+ *           bitlinear_ckpt_pack writes them, scales to G_scales and U_scales,
+ *           float [tokens x n_out / 64]; otherwise those are NULL).
+ *   ws      bitlinear_glu_workspace_bytes() bytes, 256-byte aligned,
+ *           clobbered; NULL where that is 0.
+ * n_out a positive multiple of 128 (the next BitLinear's k); other sizes as
+ * for bitlinear_contract.  tokens == 0 is a no-op. */
+#define BL_ACT_RELU2  0
+#define BL_ACT_SILU   1
+size_t bitlinear_glu_workspace_bytes(int64_t tokens, int64_t k, int64_t n_out);
+int bitlinear_glu(const int8_t *xq, const float *x_scale, int64_t tokens, int64_t k,
+                  const void *gate, const double *gate_gamma, const void *up,
+                  const double *up_gamma, int64_t n_out, int n, int m, int act, uint16_t *H,
+                  int save_type, void *G, float *G_scales, void *U, float *U_scales, void *ws,
+                  size_t ws_bytes, void *stream);
+
+/* Its backward, with the dual straight-through gradients of both layers
+ * (Sparse-BitNet article §三 and §六), from G and U as the forward kept them
+ * (g, u: the values they come back as):
+ *   dU = dh act(g),  dG = dh u act'(g)     (act' of squared ReLU is 2 max(g, 0))
+ *   dX = gate_gamma dG codes_gate + up_gamma dU codes_up
+ *   dW_gate = sum_t dG s_t x_q,  dW_up = sum_t dU s_t x_q   (masked weights too)
+ * The operands dG gate_gamma, dU up_gamma, dG s_t and dU s_t are formed in
+ * binary32 and rounded once to bf16 (up to 2^-8 relative each) for the matrix
+ * products, whose sums are binary32; the order of every sum is fixed.
+ *   dH      device [tokens x n_out], binary32 or bf16 (dh_type): the down
+ *           BitLinear's dX.
+ *   G, G_scales, U, U_scales, save_type, act  as in the forward.
+ *   dX      device [tokens x k] or NULL; dW_gate, dW_up  device [n_out x k],
+ *           both or neither; all binary32 or all bf16 (grad_type).
+ *   ws      bitlinear_glu_bwd_workspace_bytes() bytes, 256-byte aligned,
+ *           clobbered.
+ * tokens rounded up to 64, times n_out, and n_out * k below 2^29; tokens * k
+ * below 2^30.  tokens == 0 zeroes dW_gate and dW_up. */
+size_t bitlinear_glu_bwd_workspace_bytes(int64_t tokens, int64_t k, int64_t n_out);
+int bitlinear_glu_bwd(const void *dH, int dh_type, int save_type, const void *G,
+                      const float *G_scales, const void *U, const float *U_scales,
+                      const int8_t *xq, const float *x_scale, const void *gate,
+                      const double *gate_gamma, const void *up, const double *up_gamma,
+                      int64_t tokens, int64_t k, int64_t n_out, int n, int m, int act,
+                      int grad_type, void *dX, void *dW_gate, void *dW_up, void *ws,
+                      size_t ws_bytes, void *stream);
+
 /* Static text for a status code. */
 const char *bitlinear_status_string(int status);
 

@@ -85,6 +85,17 @@ _SIGS = {
     "bitlinear_attn_cache_workspace_bytes": (_sz, [_i64] * 5),
     "bitlinear_attn_cache": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _vp, _vp] + [_i64] * 5 + [_f32, _vp, _vp,
                                                                                                    _sz, _vp]),
+    "bitlinear_ckpt_pack": (_int, [_vp, _int] + [_i64] * 3 + [_vp] * 3),
+    "bitlinear_ckpt_unpack": (_int, [_vp, _vp, _i64, _i64, _vp, _int, _vp]),
+    "bitlinear_layernorm": (_int, [_vp, _int] + [_i64] * 3 + [_vp, _vp, _f32, _int, _vp, _int] + [_vp] * 5),
+    "bitlinear_layernorm_bwd_workspace_bytes": (_sz, [_i64]),
+    "bitlinear_layernorm_bwd": (_int, [_vp, _int, _vp] + [_i64] * 3 + [_vp] * 4 + [_int, _vp, _vp, _int] + [_vp] * 3 +
+                                [_sz, _vp]),
+    "bitlinear_glu_workspace_bytes": (_sz, [_i64] * 3),
+    "bitlinear_glu": (_int, [_vp, _vp, _i64, _i64] + [_vp] * 4 + [_i64, _int, _int, _int, _vp, _int] + [_vp] * 5 +
+                      [_sz, _vp]),
+    "bitlinear_glu_bwd_workspace_bytes": (_sz, [_i64] * 3),
+    "bitlinear_glu_bwd": (_int, [_vp, _int, _int] + [_vp] * 10 + [_i64] * 3 + [_int] * 4 + [_vp] * 4 + [_sz, _vp]),
     "bitlinear_status_string": (ctypes.c_char_p, [_int]),
     "bitlinear_last_error": (ctypes.c_char_p, []),
 }
@@ -719,3 +730,143 @@ def bitlinear_attn_cache(Q, K, V, pages, page, lens, tree, batch, draft, hq, hkv
         _arg(lens, _I32T, batch, "lens", dev), _opt(tree, (torch.int64, torch.uint64), batch * draft, "tree", dev),
         batch, draft, hq, hkv, d, scale, _arg(O, _BF16, batch * draft * hq * d, "O", dev), w, wn, _stream(stream))
     _check(st, "bitlinear_attn_cache")
+
+
+BL_TYPE_Q8 = 2
+BL_ACT_RELU2, BL_ACT_SILU = 0, 1
+CKPT_BLOCK = 64  # values of a row that share a checkpoint's scale
+_I8T, _F64T = (torch.int8,), (torch.float64,)
+
+
+def _blocks(n):
+    return -(-n // CKPT_BLOCK)
+
+
+def _kind(t, name):
+    """BL_TYPE_* of one float32 or bfloat16 tensor."""
+    return _type_of(name, t)
+
+
+def bitlinear_ckpt_pack(X, rows, n, codes, scales, stream=None):
+    """8-bit checkpoint of rows of n values: int8 codes [rows, n] and float32
+    scales [rows, ceil(n / 64)].  X: float32 or bfloat16 rows, any row stride."""
+    dev = torch.cuda.current_device()
+    x, xs, _ = _rows(X, _FLOATS, n, "X", dev, rows)
+    st = lib().bitlinear_ckpt_pack(
+        x, _kind(X, "X"), xs, rows, n, _arg(codes, _I8T, rows * n, "codes", dev),
+        _arg(scales, _F32T, rows * _blocks(n), "scales", dev), _stream(stream))
+    _check(st, "bitlinear_ckpt_pack")
+
+
+def bitlinear_ckpt_unpack(codes, scales, rows, n, Y, stream=None):
+    """The values a checkpoint holds: Y, float32 or bfloat16 [rows, n]."""
+    dev = torch.cuda.current_device()
+    st = lib().bitlinear_ckpt_unpack(
+        _arg(codes, _I8T, rows * n, "codes", dev), _arg(scales, _F32T, rows * _blocks(n), "scales", dev), rows, n,
+        _arg(Y, _FLOATS, rows * n, "Y", dev), _kind(Y, "Y"), _stream(stream))
+    _check(st, "bitlinear_ckpt_unpack")
+
+
+def bitlinear_layernorm(X, rows, n, weight, bias, eps, center, Y, mean=None, rstd=None, codes=None, scales=None,
+                        stream=None):
+    """Layer norm of rows (root-mean-square norm with center False): bfloat16
+    or float32 Y; mean, rstd (float32 [rows]) and a checkpoint of X where
+    given.  X: float32 or bfloat16 rows, any row stride."""
+    dev = torch.cuda.current_device()
+    x, xs, _ = _rows(X, _FLOATS, n, "X", dev, rows)
+    st = lib().bitlinear_layernorm(
+        x, _kind(X, "X"), xs, rows, n, _opt(weight, _F32T, n, "weight", dev), _opt(bias, _F32T, n, "bias", dev), eps,
+        int(bool(center)), _arg(Y, _FLOATS, rows * n, "Y", dev), _kind(Y, "Y"), _opt(mean, _F32T, rows, "mean", dev),
+        _opt(rstd, _F32T, rows, "rstd", dev), _opt(codes, _I8T, rows * n, "codes", dev),
+        _opt(scales, _F32T, rows * _blocks(n), "scales", dev), _stream(stream))
+    _check(st, "bitlinear_layernorm")
+
+
+def bitlinear_layernorm_bwd_workspace_bytes(n):
+    return int(lib().bitlinear_layernorm_bwd_workspace_bytes(int(n)))
+
+
+def bitlinear_layernorm_bwd(X, x_scales, rows, n, weight, mean, rstd, dY, dX, dweight=None, dbias=None, dR=None, ws=None,
+                            ws_bytes=None, stream=None):
+    """Backward of bitlinear_layernorm from X (x_scales None) or from the
+    checkpoint (X its int8 codes); mean None for a norm that is not centred.
+    dX: float32 or bfloat16, dR (a residual's gradient, added) of its type."""
+    dev = torch.cuda.current_device()
+    if getattr(X, "dtype", None) == torch.int8:
+        x, xs, x_type = _arg(X, _I8T, rows * n, "X", dev), n, BL_TYPE_Q8
+    else:
+        x, xs, _ = _rows(X, _FLOATS, n, "X", dev, rows)
+        x_type = _kind(X, "X")
+    dx_type = _type_of("dX and dR", dX, dR)
+    w, wn = _ws(ws, ws_bytes, dev)
+    st = lib().bitlinear_layernorm_bwd(
+        x, x_type, _opt(x_scales, _F32T, rows * _blocks(n), "x_scales", dev), xs, rows, n,
+        _opt(weight, _F32T, n, "weight", dev), _opt(mean, _F32T, rows, "mean", dev), _arg(rstd, _F32T, rows, "rstd", dev),
+        _arg(dY, _FLOATS, rows * n, "dY", dev), _kind(dY, "dY"), _opt(dR, _FLOATS, rows * n, "dR", dev),
+        _arg(dX, _FLOATS, rows * n, "dX", dev), dx_type, _opt(dweight, _F32T, n, "dweight", dev),
+        _opt(dbias, _F32T, n, "dbias", dev), w, wn, _stream(stream))
+    _check(st, "bitlinear_layernorm_bwd")
+
+
+def _saved(G, G_scales, U, U_scales, tokens, n_out, dev):
+    """(save_type, pointers) of G and U as they are kept: float32, bfloat16 or
+    int8 codes with their scales."""
+    kind = getattr(G, "dtype", None)
+    types = {torch.float32: BL_TYPE_F32, torch.bfloat16: BL_TYPE_BF16, torch.int8: BL_TYPE_Q8}
+    if kind not in types or getattr(U, "dtype", None) != kind:
+        raise TypeError("G and U must both be float32, bfloat16 or int8 tensors")
+    n, ns = tokens * n_out, tokens * _blocks(n_out)
+    return (types[kind], _arg(G, (kind,), n, "G", dev), _opt(G_scales, _F32T, ns, "G_scales", dev),
+            _arg(U, (kind,), n, "U", dev), _opt(U_scales, _F32T, ns, "U_scales", dev))
+
+
+def bitlinear_glu_workspace_bytes(tokens, k, n_out):
+    return int(lib().bitlinear_glu_workspace_bytes(int(tokens), int(k), int(n_out)))
+
+
+def bitlinear_glu(xq, x_scale, tokens, k, gate, gate_gamma, up, up_gamma, n_out, n, m, act, H, G=None, G_scales=None,
+                  U=None, U_scales=None, ws=None, ws_bytes=None, stream=None):
+    """bfloat16 H = act(G) * U of two packed layers that read the same
+    activations; G and U are kept in the type of the tensors given for them
+    (float32, bfloat16, or int8 with float32 scales)."""
+    dev = torch.cuda.current_device()
+    saved = (BL_TYPE_F32, None, None, None, None)
+    if G is not None or U is not None:
+        saved = _saved(G, G_scales, U, U_scales, tokens, n_out, dev)
+    w, wn = _ws(ws, ws_bytes, dev)
+    st = lib().bitlinear_glu(
+        _arg(xq, _I8T, tokens * k, "xq", dev), _arg(x_scale, _F32T, tokens, "x_scale", dev), tokens, k,
+        _packed(gate, n_out, k, n, m, "gate", dev), _arg(gate_gamma, _F64T, 1, "gate_gamma", dev),
+        _packed(up, n_out, k, n, m, "up", dev), _arg(up_gamma, _F64T, 1, "up_gamma", dev), n_out, n, m, act,
+        _arg(H, _BF16, tokens * n_out, "H", dev), *saved, w, wn, _stream(stream))
+    _check(st, "bitlinear_glu")
+
+
+def _packed(t, n_out, k, n, m, name, dev):
+    """Packed codes of an [n_out, k] layer (an unsupported layer is refused by
+    the call itself)."""
+    return _arg(t, _U8T, bitlinear_packed_bytes(n_out, k, n, m) or None, name, dev)
+
+
+def bitlinear_glu_bwd_workspace_bytes(tokens, k, n_out):
+    return int(lib().bitlinear_glu_bwd_workspace_bytes(int(tokens), int(k), int(n_out)))
+
+
+def bitlinear_glu_bwd(dH, G, G_scales, U, U_scales, xq, x_scale, gate, gate_gamma, up, up_gamma, tokens, k, n_out, n, m,
+                      act, dX, dW_gate, dW_up, ws=None, ws_bytes=None, stream=None):
+    """Backward of bitlinear_glu from G and U as they were kept: dX and the two
+    weight gradients, all float32 or all bfloat16 (dX, or both dW, may be
+    None).  dH: float32 or bfloat16."""
+    dev = torch.cuda.current_device()
+    save_type, g, gs, u, us = _saved(G, G_scales, U, U_scales, tokens, n_out, dev)
+    grads = [t for t in (dX, dW_gate, dW_up) if t is not None]
+    grad_type = _type_of("dX, dW_gate and dW_up", *grads) if grads else BL_TYPE_F32
+    w, wn = _ws(ws, ws_bytes, dev)
+    st = lib().bitlinear_glu_bwd(
+        _arg(dH, _FLOATS, tokens * n_out, "dH", dev), _kind(dH, "dH"), save_type, g, gs, u, us,
+        _arg(xq, _I8T, tokens * k, "xq", dev), _arg(x_scale, _F32T, tokens, "x_scale", dev),
+        _packed(gate, n_out, k, n, m, "gate", dev), _arg(gate_gamma, _F64T, 1, "gate_gamma", dev),
+        _packed(up, n_out, k, n, m, "up", dev), _arg(up_gamma, _F64T, 1, "up_gamma", dev), tokens, k, n_out, n, m, act,
+        grad_type, _opt(dX, _FLOATS, tokens * k, "dX", dev), _opt(dW_gate, _FLOATS, n_out * k, "dW_gate", dev),
+        _opt(dW_up, _FLOATS, n_out * k, "dW_up", dev), w, wn, _stream(stream))
+    _check(st, "bitlinear_glu_bwd")

@@ -26,7 +26,8 @@ CFLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", os.path.join(ROOT, "include"),
 ]
-SOURCES = ["abi.hip", "quant.hip", "gemv.hip", "gemm.hip", "bwd.hip", "rope.hip", "attn.hip", "attn_cache.hip"]
+SOURCES = ["abi.hip", "quant.hip", "gemv.hip", "gemm.hip", "bwd.hip", "rope.hip", "attn.hip", "attn_cache.hip",
+           "norm.hip", "glu.hip"]
 
 
 def _compile(src):

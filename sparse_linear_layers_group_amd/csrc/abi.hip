@@ -18,6 +18,7 @@
 #include "common.h"
 #include "bwd_group.h"
 #include "gemm_group.h"
+#include "glu.h"
 #include "launch.h"
 
 namespace {
@@ -1337,6 +1338,243 @@ int bitlinear_attn_cache(const uint16_t* Q, int64_t q_stride, const uint16_t* K,
   const bl::AttnCacheArgs a{Q, q_stride, K, V, cache_rows / page, pages, max_pages, page, lens, tree,
                             (int)batch, (int)draft, (int)hq, (int)hkv, scale, O, ws};
   return hip_status(bl::launch_attn_cache(a, d, reinterpret_cast<hipStream_t>(stream)), "cache attention launch");
+}
+
+// ----------------------------------------------- layer norm and checkpoints
+namespace {
+static_assert(BL_TYPE_F32 == 0 && BL_TYPE_BF16 == 1 && BL_TYPE_Q8 == 2, "the kernels' row types");
+
+int check_saved_type(int type, const char* name) {
+  if (type != BL_TYPE_F32 && type != BL_TYPE_BF16 && type != BL_TYPE_Q8)
+    return fail(BL_EINVAL, "%s must be BL_TYPE_F32, BL_TYPE_BF16 or BL_TYPE_Q8 (got %d)", name, type);
+  return BL_OK;
+}
+
+int check_norm(int64_t rows, int64_t n) {
+  if (n < 8 || n > bl::kNormMaxWidth || n % 8 != 0)
+    return fail(BL_ESHAPE, "n must be a multiple of 8 in 8..%lld (got %lld)", (long long)bl::kNormMaxWidth, (long long)n);
+  if (rows < 0 || rows >= (int64_t)1 << 23) return fail(BL_ESHAPE, "rows must be in [0, 2^23) (got %lld)", (long long)rows);
+  return BL_OK;
+}
+
+int check_ckpt_shape(int64_t rows, int64_t n) {
+  if (n < 16 || n % 16 != 0 || n >= kLimit)
+    return fail(BL_ESHAPE, "n must be a positive multiple of 16 below 2^31 (got %lld)", (long long)n);
+  const int64_t blocks = (n + bl::kCkptBlock - 1) / bl::kCkptBlock;
+  if (rows < 0 || rows > (((int64_t)1 << 29) - 32) / blocks)
+    return fail(BL_ESHAPE, "rows must be >= 0 with at most 2^29 - 32 blocks of %d values (got %lld rows)", bl::kCkptBlock,
+                (long long)rows);
+  return BL_OK;
+}
+
+int64_t piece_of(int type) { return type == BL_TYPE_F32 ? 4 : 8; }
+}  // namespace
+
+int bitlinear_ckpt_pack(const void* X, int x_type, int64_t x_stride, int64_t rows, int64_t n, int8_t* codes,
+                        float* scales, void* stream) {
+  TRY(check_type(x_type, "x_type"));
+  TRY(check_ckpt_shape(rows, n));
+  if (rows == 0) return ok();
+  TRY(check_stride(x_stride, n, piece_of(x_type), kLimit, "x_stride"));
+  TRY(check_ptr(X, 16, "X"));
+  TRY(check_ptr(codes, 16, "codes"));
+  TRY(check_ptr(scales, 4, "scales"));
+  return hip_status(bl::launch_ckpt_pack(X, x_type, x_stride, rows, n, codes, scales, reinterpret_cast<hipStream_t>(stream)),
+                    "checkpoint launch");
+}
+
+int bitlinear_ckpt_unpack(const int8_t* codes, const float* scales, int64_t rows, int64_t n, void* Y, int y_type,
+                          void* stream) {
+  TRY(check_type(y_type, "y_type"));
+  TRY(check_ckpt_shape(rows, n));
+  if (rows == 0) return ok();
+  TRY(check_ptr(codes, 16, "codes"));
+  TRY(check_ptr(scales, 4, "scales"));
+  TRY(check_ptr(Y, 16, "Y"));
+  return hip_status(bl::launch_ckpt_unpack(codes, scales, rows, n, Y, y_type, reinterpret_cast<hipStream_t>(stream)),
+                    "checkpoint launch");
+}
+
+int bitlinear_layernorm(const void* X, int x_type, int64_t x_stride, int64_t rows, int64_t n, const float* weight,
+                        const float* bias, float eps, int center, void* Y, int y_type, float* mean, float* rstd,
+                        int8_t* codes, float* scales, void* stream) {
+  TRY(check_type(x_type, "x_type"));
+  TRY(check_type(y_type, "y_type"));
+  TRY(check_norm(rows, n));
+  if (!(eps >= 0.f && eps <= 3.0e38f)) return fail(BL_EINVAL, "eps must be finite and >= 0");
+  if ((codes == nullptr) != (scales == nullptr) && rows > 0) return fail(BL_EINVAL, "codes and scales: both or neither");
+  if (codes) TRY(check_ckpt_shape(rows, n));
+  if (rows == 0) return ok();
+  TRY(check_stride(x_stride, n, piece_of(x_type), kLimit, "x_stride"));
+  TRY(check_ptr(X, 16, "X"));
+  TRY(check_opt_ptr(weight, 16, "weight"));
+  TRY(check_opt_ptr(bias, 16, "bias"));
+  TRY(check_ptr(Y, 16, "Y"));
+  TRY(check_opt_ptr(mean, 4, "mean"));
+  TRY(check_opt_ptr(rstd, 4, "rstd"));
+  TRY(check_opt_ptr(codes, 16, "codes"));
+  TRY(check_opt_ptr(scales, 4, "scales"));
+  const bl::NormArgs a{X, x_stride, rows, n, weight, bias, eps, center != 0, Y, y_type, mean, rstd, codes, scales};
+  return hip_status(bl::launch_layernorm(a, x_type, reinterpret_cast<hipStream_t>(stream)), "layer norm launch");
+}
+
+size_t bitlinear_layernorm_bwd_workspace_bytes(int64_t n) {
+  return n >= 8 && n <= bl::kNormMaxWidth && n % 8 == 0 ? bl::norm_bwd_ws_bytes(n) : 0;
+}
+
+int bitlinear_layernorm_bwd(const void* X, int x_type, const float* x_scales, int64_t x_stride, int64_t rows, int64_t n,
+                            const float* weight, const float* mean, const float* rstd, const void* dY, int dy_type,
+                            const void* dR, void* dX, int dx_type, float* dweight, float* dbias, void* ws,
+                            size_t ws_bytes, void* stream) {
+  TRY(check_saved_type(x_type, "x_type"));
+  TRY(check_type(dy_type, "dy_type"));
+  TRY(check_type(dx_type, "dx_type"));
+  TRY(check_norm(rows, n));
+  const bool q8 = x_type == BL_TYPE_Q8, sums = dweight || dbias;
+  if (q8) TRY(check_ckpt_shape(rows, n));
+  TRY(check_opt_ptr(dweight, 16, "dweight"));
+  TRY(check_opt_ptr(dbias, 16, "dbias"));
+  if (rows == 0 && !sums) return ok();
+  if (rows > 0) {
+    if (q8 && x_stride != n) return fail(BL_ESHAPE, "x_stride of a checkpoint must be n (got %lld)", (long long)x_stride);
+    if (!q8) TRY(check_stride(x_stride, n, piece_of(x_type), kLimit, "x_stride"));
+    if (!q8 && x_scales) return fail(BL_EINVAL, "x_scales belong to BL_TYPE_Q8");
+    TRY(check_ptr(X, 16, "X"));
+    if (q8) TRY(check_ptr(x_scales, 4, "x_scales"));
+    TRY(check_opt_ptr(weight, 16, "weight"));
+    TRY(check_opt_ptr(mean, 4, "mean"));
+    TRY(check_ptr(rstd, 4, "rstd"));
+    TRY(check_ptr(dY, 16, "dY"));
+    TRY(check_opt_ptr(dR, 16, "dR"));
+    TRY(check_ptr(dX, 16, "dX"));
+    if (sums) {
+      const size_t need = bl::norm_bwd_ws_bytes(n);
+      if (!ws || ws_bytes < need)
+        return fail(BL_EWORKSPACE, "layer norm backward workspace needs %zu bytes (got %zu)", need, ws ? ws_bytes : (size_t)0);
+      TRY(check_ptr(ws, 16, "ws"));
+    }
+  }
+  const bl::NormBwdArgs a{X, x_scales, x_stride, rows, n, weight, mean, rstd, dY, dy_type, dR, dX, dx_type, dweight,
+                          dbias, sums ? static_cast<float*>(ws) : nullptr};
+  return hip_status(bl::launch_layernorm_bwd(a, x_type, reinterpret_cast<hipStream_t>(stream)),
+                    "layer norm backward launch");
+}
+
+// ------------------------------------------------- the gated feed-forward
+namespace {
+static_assert(BL_ACT_RELU2 == bl::kActRelu2 && BL_ACT_SILU == bl::kActSilu, "the kernels' activations");
+
+int check_glu(int64_t tokens, int64_t k, int64_t n_out, int n, int m, int act) {
+  TRY(check_nm(n, m));
+  TRY(check_layer(n_out, k));
+  if (n_out % 128 != 0)
+    return fail(BL_ESHAPE, "n_out must be a positive multiple of 128 (got %lld)", (long long)n_out);
+  if (act != BL_ACT_RELU2 && act != BL_ACT_SILU)
+    return fail(BL_EINVAL, "act must be BL_ACT_RELU2 or BL_ACT_SILU (got %d)", act);
+  if (tokens < 0 || tokens >= kLimit || tokens * k >= kLimit || tokens * n_out >= kLimit)
+    return fail(BL_ESHAPE, "tokens must be >= 0 with tokens*k and tokens*n_out below 2^31");
+  return BL_OK;
+}
+
+int check_saved(int type, const void* G, const float* Gs, const void* U, const float* Us) {
+  TRY(check_saved_type(type, "save_type"));
+  TRY(check_ptr(G, 16, "G"));
+  TRY(check_ptr(U, 16, "U"));
+  if (type == BL_TYPE_Q8) {
+    TRY(check_ptr(Gs, 4, "G_scales"));
+    TRY(check_ptr(Us, 4, "U_scales"));
+  } else if (Gs || Us) {
+    return fail(BL_EINVAL, "G_scales and U_scales belong to BL_TYPE_Q8");
+  }
+  return BL_OK;
+}
+
+bool glu_bwd_fits(int64_t tokens, int64_t k, int64_t n_out) {
+  const int64_t tp = bl::bwd_tokens_padded(tokens);
+  return tp * n_out < kLimit / 4 && n_out * k < kLimit / 4 && tp * k < kLimit / 2;
+}
+}  // namespace
+
+size_t bitlinear_glu_workspace_bytes(int64_t tokens, int64_t k, int64_t n_out) {
+  if (check_glu(tokens, k, n_out, 8, 8, BL_ACT_RELU2) != BL_OK || tokens == 0) return 0;
+  return bl::glu_ws_bytes(tokens, k, n_out);
+}
+
+int bitlinear_glu(const int8_t* xq, const float* x_scale, int64_t tokens, int64_t k, const void* gate,
+                  const double* gate_gamma, const void* up, const double* up_gamma, int64_t n_out, int n, int m,
+                  int act, uint16_t* H, int save_type, void* G, float* G_scales, void* U, float* U_scales, void* ws,
+                  size_t ws_bytes, void* stream) {
+  TRY(check_glu(tokens, k, n_out, n, m, act));
+  if (tokens == 0) return ok();
+  TRY(check_ptr(xq, 16, "xq"));
+  TRY(check_ptr(x_scale, 4, "x_scale"));
+  TRY(check_ptr(gate, 16, "gate"));
+  TRY(check_ptr(gate_gamma, 8, "gate_gamma"));
+  TRY(check_ptr(up, 16, "up"));
+  TRY(check_ptr(up_gamma, 8, "up_gamma"));
+  TRY(check_ptr(H, 16, "H"));
+  if (!G && !U && (G_scales || U_scales)) return fail(BL_EINVAL, "G_scales and U_scales belong to G and U");
+  if (G || U) TRY(check_saved(save_type, G, G_scales, U, U_scales));
+  const size_t need = bl::glu_ws_bytes(tokens, k, n_out);
+  if (need) {
+    if (!ws || ws_bytes < need)
+      return fail(BL_EWORKSPACE, "gated feed-forward workspace needs %zu bytes (got %zu)", need, ws ? ws_bytes : (size_t)0);
+    TRY(check_ptr(ws, 256, "ws"));
+  }
+  const bl::GluArgs a{xq, x_scale, tokens, k, n_out, gate, up, gate_gamma, up_gamma, act, H,
+                      G ? save_type : bl::kSaveNone, G, U, G_scales, U_scales};
+  return hip_status(bl::launch_glu(a, bl::s_of(n, m), ws, reinterpret_cast<hipStream_t>(stream)),
+                    "gated feed-forward launch");
+}
+
+size_t bitlinear_glu_bwd_workspace_bytes(int64_t tokens, int64_t k, int64_t n_out) {
+  if (check_glu(tokens, k, n_out, 8, 8, BL_ACT_RELU2) != BL_OK || tokens == 0 || !glu_bwd_fits(tokens, k, n_out)) return 0;
+  return bl::glu_bwd_layout(tokens, k, n_out).bytes;
+}
+
+int bitlinear_glu_bwd(const void* dH, int dh_type, int save_type, const void* G, const float* G_scales, const void* U,
+                      const float* U_scales, const int8_t* xq, const float* x_scale, const void* gate,
+                      const double* gate_gamma, const void* up, const double* up_gamma, int64_t tokens, int64_t k,
+                      int64_t n_out, int n, int m, int act, int grad_type, void* dX, void* dW_gate, void* dW_up,
+                      void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_glu(tokens, k, n_out, n, m, act));
+  TRY(check_type(dh_type, "dh_type"));
+  TRY(check_type(grad_type, "grad_type"));
+  if ((dW_gate == nullptr) != (dW_up == nullptr)) return fail(BL_EINVAL, "dW_gate and dW_up: both or neither");
+  TRY(check_opt_ptr(dX, 16, "dX"));
+  TRY(check_opt_ptr(dW_gate, 16, "dW_gate"));
+  TRY(check_opt_ptr(dW_up, 16, "dW_up"));
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (tokens == 0) {
+    // no tokens: dX is empty and the weights' gradients are all zeros (two bf16 zeros fill a binary32's place)
+    const int64_t count = grad_type == BL_TYPE_F32 ? n_out * k : n_out * k / 2;
+    for (void* dW : {dW_gate, dW_up}) {
+      const hipError_t e = dW ? bl::launch_zero(static_cast<float*>(dW), count, s) : hipSuccess;
+      if (e != hipSuccess) return hip_status(e, "weight gradient clear");
+    }
+    return ok();
+  }
+  if (!dX && !dW_gate) return ok();
+  if (!glu_bwd_fits(tokens, k, n_out))
+    return fail(BL_ESHAPE, "the backward needs tokens*n_out and n_out*k below 2^29 and tokens*k below 2^30");
+  const size_t need = bl::glu_bwd_layout(tokens, k, n_out).bytes;
+  if (!ws || ws_bytes < need)
+    return fail(BL_EWORKSPACE, "gated feed-forward backward workspace needs %zu bytes (got %zu)", need,
+                ws ? ws_bytes : (size_t)0);
+  TRY(check_ptr(ws, 256, "ws"));
+  TRY(check_ptr(dH, 16, "dH"));
+  TRY(check_saved(save_type, G, G_scales, U, U_scales));
+  TRY(check_ptr(x_scale, 4, "x_scale"));
+  if (dX) {
+    TRY(check_ptr(gate, 16, "gate"));
+    TRY(check_ptr(gate_gamma, 8, "gate_gamma"));
+    TRY(check_ptr(up, 16, "up"));
+    TRY(check_ptr(up_gamma, 8, "up_gamma"));
+  }
+  if (dW_gate) TRY(check_ptr(xq, 16, "xq"));
+  const bl::GluBwdArgs a{dH, dh_type, save_type, act, G, U, G_scales, U_scales, xq, x_scale, gate, up, gate_gamma,
+                         up_gamma, tokens, k, n_out, grad_type, dX, dW_gate, dW_up, static_cast<char*>(ws)};
+  return hip_status(bl::launch_glu_bwd(a, bl::s_of(n, m), s), "gated feed-forward backward launch");
 }
 
 const char* bitlinear_status_string(int status) {

@@ -17,7 +17,9 @@
 // transposed (exact).  Every conversion happens once per element, so the
 // product kernel is a plain copy-to-LDS and MFMA loop.
 #include "bwd_group.h"
+#include "bitlinear.h"
 #include "common.h"
+#include "glu.h"
 #include "launch.h"
 
 #include <algorithm>
@@ -285,6 +287,9 @@ struct NtProblem {
   const float* U = nullptr;
   uint16_t* dG = nullptr;
   uint16_t* dU = nullptr;
+  // with Cb set, C is not written but rounded to bf16 into Cb, laid out like C
+  // (256-row kernel and split sums only; N even)
+  uint16_t* Cb = nullptr;
 };
 
 // the products of one launch of the 256-row kernel (its tiles dealt over
@@ -757,6 +762,31 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
     }
     return;
   }
+  if (pr.Cb) {
+    uint16_t* __restrict__ Cb = pr.Cb;
+    // lanes l16 and l16 ^ 1 share their columns' pairs as in the gated epilogue
+    const bool odd = (l16 & 1) != 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t h[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[q] = f32_to_bf16_rne(scaled ? (float)((double)c[i][j][q] * g) : c[i][j][q]);
+        const uint32_t p0 = h[0] | h[1] << 16, p1 = h[2] | h[3] << 16;
+        const uint32_t x0 = lane_xor1(p0), x1 = lane_xor1(p1);
+        const int64_t col = n0 + wn * 64 + j * 16 + (l16 & ~1);
+        if (col >= N) continue;
+        const int64_t ra = m0 + wm * 128 + i * 16 + 4 * lg + (odd ? 1 : 0);
+        if (ra < M)
+          st_stream(reinterpret_cast<uint32_t*>(Cb + ra * ldc + col),
+                    odd ? (x0 >> 16) | (p0 & 0xffff0000u) : (p0 & 0xffffu) | (x0 << 16));
+        if (ra + 2 < M)
+          st_stream(reinterpret_cast<uint32_t*>(Cb + (ra + 2) * ldc + col),
+                    odd ? (x1 >> 16) | (p1 & 0xffff0000u) : (p1 & 0xffffu) | (x1 << 16));
+      }
+    return;
+  }
   if (m0 + kBigM <= M && n0 + T::N <= N) {
     float* cb = C + (m0 + wm * 128 + 4 * lg) * ldc + n0 + wn * 64 + l16;
 #pragma unroll
@@ -784,10 +814,11 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
     }
 }
 
-// C = alpha * (sum of the split planes, in order), binary32 sums
+// C = alpha * (sum of the split planes, in order), binary32 sums; to Cb in bf16
+// where that is given
 __global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict__ P, int splits,
                                                        int64_t n4, const double* __restrict__ alpha,
-                                                       float* __restrict__ C) {
+                                                       float* __restrict__ C, uint16_t* __restrict__ Cb) {
   const double g = alpha ? *alpha : 1.0;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
     v4f acc = ld_global(reinterpret_cast<const v4f*>(P) + i);
@@ -800,7 +831,8 @@ __global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict_
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = (float)((double)acc[e] * g);
     }
-    st_global(reinterpret_cast<v4f*>(C) + i, acc);
+    if (Cb) st_global(reinterpret_cast<u32x2*>(Cb) + i, bf16x4(acc));
+    else st_global(reinterpret_cast<v4f*>(C) + i, acc);
   }
 }
 
@@ -820,8 +852,10 @@ static hipError_t gemm_nt_split(NtProblem p, float* partials, hipStream_t s) {
   const int64_t klen = bwd_split_len(p.K, splits);
   const int used = (int)((p.K + klen - 1) / klen);
   float* C = p.C;
+  uint16_t* Cb = p.Cb;
   const double* alpha = p.alpha;
   p.C = partials;
+  p.Cb = nullptr;
   p.ldc = p.N;
   p.alpha = nullptr;
   p.klen = klen;
@@ -831,7 +865,7 @@ static hipError_t gemm_nt_split(NtProblem p, float* partials, hipStream_t s) {
   gemm_nt_bf16_kernel<<<dim3(gx, (unsigned)used), 256, 0, s>>>(p, none);
   const int64_t n4 = p.M * p.N / 4;
   const int64_t blocks = (n4 + 255) / 256;
-  split_sum_kernel<<<(unsigned)(blocks < 2048 ? blocks : 2048), 256, 0, s>>>(partials, used, n4, alpha, C);
+  split_sum_kernel<<<(unsigned)(blocks < 2048 ? blocks : 2048), 256, 0, s>>>(partials, used, n4, alpha, C, Cb);
   return hipGetLastError();
 }
 
@@ -1048,6 +1082,62 @@ hipError_t launch_bwd_gate(const uint16_t* dY, const int8_t* xq, const float* sc
     if (e != hipSuccess) return e;
   }
   return hipGetLastError();
+}
+
+hipError_t launch_zero(float* p, int64_t n, hipStream_t s) {
+  zero_f32_kernel<<<1024, 256, 0, s>>>(p, n);
+  return hipGetLastError();
+}
+
+// The products of the gated feed-forward's backward.  dX is one product of
+// depth 2 n_out: dG gate_gamma and dU up_gamma stand side by side in dgu and so do the two
+// layers' codes in codes_t, so it is written once, and its tiles (twice as
+// deep as the weights') start first.
+hipError_t launch_glu_products(const GluBwdArgs& a, int S, hipStream_t s) {
+  const GluBwdLayout l = glu_bwd_layout(a.tokens, a.k, a.n_out);
+  const int64_t tp = bwd_tokens_padded(a.tokens), nkb = a.k / kBlockK, strips = a.n_out / kStripRows, n2 = 2 * a.n_out;
+  uint16_t* const xq_t = reinterpret_cast<uint16_t*>(a.ws + l.xq_t);
+  uint16_t* const codes_t = reinterpret_cast<uint16_t*>(a.ws + l.codes_t);
+  float* const partials = reinterpret_cast<float*>(a.ws + l.partials);
+  PrepList L;
+  NtProblem probs[3];
+  int np = 0;
+  const bool b16 = a.grad_type == BL_TYPE_BF16;
+  const auto add = [&](NtProblem p, void* out) {
+    p.C = b16 ? nullptr : static_cast<float*>(out);
+    p.Cb = b16 ? static_cast<uint16_t*>(out) : nullptr;
+    probs[np++] = p;
+  };
+  if (a.dX) {
+    const int32_t jobs = (int32_t)((strips * nkb + 3) / 4);
+    L.t.push_back(PrepTask{a.gate, nullptr, codes_t, nkb, strips, n2, kPrepCodes, jobs});
+    L.t.push_back(PrepTask{a.up, nullptr, codes_t + a.n_out, nkb, strips, n2, kPrepCodes, jobs});
+    add(NtProblem{reinterpret_cast<const uint16_t*>(a.ws + l.dgu), codes_t, nullptr, nullptr, n2, n2, a.k, a.tokens,
+                  a.k, n2, n2}, a.dX);
+  }
+  if (a.dWg) {
+    L.t.push_back(PrepTask{a.xq, nullptr, xq_t, a.tokens, a.k, tp, kPrepXq, (int32_t)((tp / 64) * (a.k / 64))});
+    add(NtProblem{reinterpret_cast<const uint16_t*>(a.ws + l.dgs_t), xq_t, nullptr, nullptr, tp, tp, a.k, a.n_out,
+                  a.k, tp, tp}, a.dWg);
+    add(NtProblem{reinterpret_cast<const uint16_t*>(a.ws + l.dus_t), xq_t, nullptr, nullptr, tp, tp, a.k, a.n_out,
+                  a.k, tp, tp}, a.dWu);
+  }
+  hipError_t e = L.launch(S, s);
+  if (e != hipSuccess) return e;
+  std::stable_sort(probs, probs + np, [](const NtProblem& x, const NtProblem& y) { return x.K > y.K; });
+  NtSet set{};
+  for (int i = 0; i < np; ++i)
+    if (bwd_splits(probs[i].M, probs[i].N, probs[i].K) == 1) set.p[set.n++] = probs[i];
+  if (set.n) {
+    e = launch_big(set, big_kind(set), s);
+    if (e != hipSuccess) return e;
+  }
+  for (int i = 0; i < np; ++i)
+    if (bwd_splits(probs[i].M, probs[i].N, probs[i].K) > 1) {
+      e = gemm_nt_split(probs[i], partials, s);
+      if (e != hipSuccess) return e;
+    }
+  return hipSuccess;
 }
 
 hipError_t launch_bwd_group(const BwdItem* items, int count, int64_t tokens, int S, void* ws, int phase,

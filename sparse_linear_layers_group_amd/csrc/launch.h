@@ -322,7 +322,7 @@ hipError_t launch_gemm_sp24(const void* packed, const int8_t* xq, const float* s
 // Backward.  Workspace (bf16 operands of the two products, each region
 // 256-byte aligned): (dY * s)^T [n_out x tp], x_q^T [k x tp] with tp the
 // token count rounded up to 64, and codes^T [k x 64 * strips].
-inline int64_t bwd_tokens_padded(int64_t tokens) { return (tokens + 63) / 64 * 64; }
+__host__ __device__ inline int64_t bwd_tokens_padded(int64_t tokens) { return (tokens + 63) / 64 * 64; }
 inline size_t bwd_align(size_t b) { return (b + 255) & ~(size_t)255; }
 inline size_t bwd_dys_offset(int64_t, int64_t, int64_t) { return 0; }
 inline size_t bwd_xq_offset(int64_t tokens, int64_t, int64_t n_out) {
@@ -452,5 +452,42 @@ struct AttnCacheArgs {
 };
 size_t attn_cache_ws_bytes(int64_t batch, int64_t draft, int64_t hq, int64_t hkv, int64_t d);
 hipError_t launch_attn_cache(const AttnCacheArgs& a, int64_t d, hipStream_t s);
+
+// ---------------------------------------------------------- norm.hip
+constexpr int kCkptBlock = 64;          // values of a row that share a checkpoint's scale
+constexpr int64_t kNormMaxWidth = 16384;
+constexpr int kNormParts = 512;         // workgroups of the norm's backward, at most
+struct NormArgs {
+  const void* X;  // rows of n, x_stride elements apart
+  int64_t x_stride, rows, n;
+  const float *weight, *bias;  // [n] or NULL
+  float eps;
+  int center;
+  void* Y;
+  int y_type;
+  float *mean, *rstd;  // [rows] or NULL
+  int8_t* codes;       // checkpoint of X, or NULL
+  float* scales;
+};
+struct NormBwdArgs {
+  const void* X;
+  const float* x_scales;  // with 8-bit X
+  int64_t x_stride, rows, n;
+  const float *weight, *mean, *rstd;  // mean NULL: not centred
+  const void* dY;
+  int dy_type;
+  const void* dR;  // rows of dX's type, or NULL
+  void* dX;
+  int dx_type;
+  float *dweight, *dbias;  // either may be NULL
+  float* part;             // rows of 2n partial sums; NULL with both NULL
+};
+inline size_t norm_bwd_ws_bytes(int64_t n) { return (size_t)kNormParts * 2 * n * 4; }
+hipError_t launch_layernorm(const NormArgs& a, int x_type, hipStream_t s);
+hipError_t launch_layernorm_bwd(const NormBwdArgs& a, int x_type, hipStream_t s);
+hipError_t launch_ckpt_pack(const void* X, int x_type, int64_t x_stride, int64_t rows, int64_t n, int8_t* codes,
+                            float* scales, hipStream_t s);
+hipError_t launch_ckpt_unpack(const int8_t* codes, const float* scales, int64_t rows, int64_t n, void* Y, int y_type,
+                              hipStream_t s);
 
 }  // namespace bl

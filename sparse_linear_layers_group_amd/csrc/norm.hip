@@ -1,0 +1,372 @@
+// norm.hip -- layer norm of rows (with or without centring), forward and
+// backward with the sums over rows of the parameters' gradients, and 8-bit
+// checkpoints of rows, which both directions take part in.
+#include "ckpt.h"
+#include "common.h"
+#include "launch.h"
+
+namespace bl {
+
+// A row of n values is held by kThreads threads, kV runs of eight consecutive
+// values each: run i of thread t is run i * kThreads + t of the row, so
+// neighbouring threads read neighbouring 16 or 32 bytes.  The whole row stays in
+// registers between its sums and its outputs: every input is read once.
+template <int kThreads>
+struct RowSums {
+  static constexpr int kWaves = kThreads / 64;
+  // sum over the row's threads; `slot`: a different one for each sum between two
+  // barriers that all of the workgroup passes
+  __device__ static __forceinline__ float sum(float v, float (*red)[8], int slot) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+    if constexpr (kWaves > 1) {
+      if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = v;
+      __syncthreads();
+      v = red[slot][0];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v += red[slot][w];
+    }
+    return v;
+  }
+};
+
+// mean and 1 / sqrt(variance + eps); a variance outside binary32 gives NaN, not
+// rows of zeros
+__device__ __forceinline__ float rstd_of(float var, float eps) {
+  const float v = var + eps;
+  return v < __builtin_inff() ? __builtin_amdgcn_rsqf(v) : __builtin_nanf("");
+}
+
+template <int T, int kThreads, int kV>
+__global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void layernorm_kernel(NormArgs a) {
+  constexpr int kRows = kThreads < 256 ? 256 / kThreads : 1;  // rows of a workgroup
+  __shared__ float red[2][8];
+  const int tid = kRows > 1 ? threadIdx.x % kThreads : threadIdx.x, lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * kRows + (kRows > 1 ? threadIdx.x / kThreads : 0);
+  if (row >= a.rows) return;  // whole wavefronts, and no barrier follows where a workgroup has several rows
+  Raw8<T> raw[kV];
+  bool in[kV];
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    const int64_t e = 8 * ((int64_t)i * kThreads + tid);
+    in[i] = e < a.n;
+    raw[i].zero();
+    if (in[i]) raw[i].load(a.X, row * a.x_stride + e);
+  }
+  float mean = 0.f;
+  const float inv_n = 1.f / (float)a.n;
+  if (a.center) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += raw[i].get(j, 0.f);
+    mean = RowSums<kThreads>::sum(s, red, 0) * inv_n;
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < kV; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float d = raw[i].get(j, 0.f) - mean;
+      q = in[i] ? fmaf(d, d, q) : q;
+    }
+  const float rstd = rstd_of(RowSums<kThreads>::sum(q, red, 1) * inv_n, a.eps);
+  if (tid == 0) {
+    if (a.mean) st_global(a.mean + row, mean);
+    if (a.rstd) st_global(a.rstd + row, rstd);
+  }
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    const int64_t e = 8 * ((int64_t)i * kThreads + tid);
+    float x[8], y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = raw[i].get(j, 0.f);
+    if (a.codes)
+      ckpt_store8(x, in[i], lane, a.codes + row * a.n + e,
+                  a.scales + row * ((a.n + kCkptBlock - 1) / kCkptBlock) + e / kCkptBlock);
+    if (!in[i]) continue;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = (x[j] - mean) * rstd;
+    if (a.weight) {
+      Raw8<kRowF32> w;
+      w.load(a.weight, e);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] *= w.get(j, 0.f);
+    }
+    if (a.bias) {
+      Raw8<kRowF32> b;
+      b.load(a.bias, e);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] += b.get(j, 0.f);
+    }
+    store_row8(a.Y, a.y_type, row * a.n + e, y);
+  }
+}
+
+// Backward of rows: with n = (x - mean) rstd and a = w dy,
+//   dx = rstd (a - mean(a) - n mean(a n)) (+ dR),  dw = sum dy n,  db = sum dy
+// (no mean(a) without centring).  Each group of kThreads walks over rows and
+// keeps its share of dw and db in registers; a workgroup's groups are joined in
+// LDS in a fixed order, and each workgroup writes one row of partial sums, which
+// norm_dw_kernel adds in binary64.  No atomics: reruns give the same bits.
+template <int T, int kThreads, int kV>
+__global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void layernorm_bwd_kernel(NormBwdArgs a) {
+  constexpr int kRows = kThreads < 256 ? 256 / kThreads : 1;
+  __shared__ float red[4][8];
+  const int tid = kRows > 1 ? threadIdx.x % kThreads : threadIdx.x;
+  const int group = kRows > 1 ? threadIdx.x / kThreads : 0;
+  const float inv_n = 1.f / (float)a.n;
+  const int64_t blocks = (a.n + kCkptBlock - 1) / kCkptBlock;
+  float gw[kV][8], gb[kV][8];
+#pragma unroll
+  for (int i = 0; i < kV; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) gw[i][j] = gb[i][j] = 0.f;
+  int slot = 0;
+  for (int64_t row = (int64_t)blockIdx.x * kRows + group; row < a.rows; row += (int64_t)gridDim.x * kRows) {
+    Raw8<T> rx[kV];
+    float xs[kV];
+    Raw8<kRowF32> rd[kV];  // binary32 dy, or bf16 in the first half
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const int64_t e = 8 * ((int64_t)i * kThreads + tid);
+      rx[i].zero();
+      rd[i].zero();
+      xs[i] = 0.f;
+      if (e < a.n) {
+        rx[i].load(a.X, row * a.x_stride + e);
+        if (T == kRowQ8) xs[i] = ld_global(a.x_scales + row * blocks + e / kCkptBlock);
+        if (a.dy_type == kRowF32) {
+          rd[i].load(a.dY, row * a.n + e);
+        } else {
+          Raw8<kRowBf16> b;
+          b.load(a.dY, row * a.n + e);
+          rd[i].a = __builtin_bit_cast(f32x4_t, b.a);
+        }
+      }
+    }
+    const float mean = a.mean ? ld_global(a.mean + row) : 0.f, rstd = ld_global(a.rstd + row);
+    float sa = 0.f, sn = 0.f;
+    float x[kV][8], d[kV][8];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const int64_t e = 8 * ((int64_t)i * kThreads + tid);
+      Raw8<kRowF32> w;
+      if (a.weight && e < a.n) w.load(a.weight, e);
+      else w.a = w.b = f32x4_t{1.f, 1.f, 1.f, 1.f};
+      const u32x4 half = __builtin_bit_cast(u32x4, rd[i].a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // threads past the row hold dy = 0, so whatever n they form counts nothing
+        const float n = e < a.n ? (rx[i].get(j, xs[i]) - mean) * rstd : 0.f;
+        const float dy = a.dy_type == kRowF32 ? rd[i].get(j, 0.f) : (j & 1) ? bf16_hi(half[j >> 1]) : bf16_lo(half[j >> 1]);
+        gw[i][j] = fmaf(dy, n, gw[i][j]);
+        gb[i][j] += dy;
+        x[i][j] = n;
+        d[i][j] = dy * w.get(j, 0.f);
+        sa += d[i][j];
+        sn = fmaf(d[i][j], n, sn);
+      }
+    }
+    sn = RowSums<kThreads>::sum(sn, red, slot) * inv_n;
+    sa = a.mean ? RowSums<kThreads>::sum(sa, red, slot + 1) * inv_n : 0.f;
+    slot ^= 2;  // a row's sums are read before the barriers of the next row's, which use the other slots
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const int64_t e = 8 * ((int64_t)i * kThreads + tid);
+      if (e >= a.n) continue;
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = rstd * fmaf(-x[i][j], sn, d[i][j] - sa);
+      if (a.dR) {
+        if (a.dx_type == kRowF32) {
+          Raw8<kRowF32> r;
+          r.load(a.dR, row * a.n + e);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] += r.get(j, 0.f);
+        } else {
+          Raw8<kRowBf16> r;
+          r.load(a.dR, row * a.n + e);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] += r.get(j, 0.f);
+        }
+      }
+      store_row8(a.dX, a.dx_type, row * a.n + e, y);
+    }
+  }
+  if (!a.part) return;
+  if constexpr (kRows == 1) {
+    float* out = a.part + (int64_t)blockIdx.x * 2 * a.n;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const int64_t e = 8 * ((int64_t)i * kThreads + tid);
+      if (e >= a.n) continue;
+      store_row8(out, kRowF32, e, gw[i]);
+      store_row8(out, kRowF32, a.n + e, gb[i]);
+    }
+  } else {
+    __shared__ __attribute__((aligned(16))) float join[kRows][kThreads * 8];
+    // one run at a time: group g's values beside each other, then summed in order
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) join[group][j * kThreads + tid] = s ? gb[i][j] : gw[i][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < kThreads * 8; c += 256) {
+          const int64_t e = 8 * ((int64_t)i * kThreads + c % kThreads) + c / kThreads;
+          if (e >= a.n) continue;
+          float v = join[0][c];
+#pragma unroll
+          for (int g = 1; g < kRows; ++g) v += join[g][c];
+          st_global(a.part + (int64_t)blockIdx.x * 2 * a.n + s * a.n + e, v);
+        }
+      }
+  }
+}
+
+// dw and db: sums of the workgroups' rows of partials, 64 columns of [dw | db] a
+// workgroup, its 16 wavefronts a share of the rows each, joined in LDS; binary64,
+// fixed order
+__global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__ part, int rows, int64_t n,
+                                                       float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ double red[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  double s = 0.0;
+  if (c < 2 * n)
+    for (int r = wave; r < rows; r += 16) s += (double)ld_global(part + (int64_t)r * 2 * n + c);
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < 2 * n) {
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += red[w][lane];
+    float* out = c < n ? dw : db;
+    if (out) st_global(out + (c < n ? c : c - n), (float)s);
+  }
+}
+
+__global__ void norm_zero_kernel(float* __restrict__ dw, float* __restrict__ db, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  if (dw) st_global(dw + i, 0.f);
+  if (db) st_global(db + i, 0.f);
+}
+
+// ------------------------------------------------------- 8-bit checkpoints
+// Eight lanes hold a block of 64 values, eight each, as the norm's rows do.
+template <int T>
+__global__ __launch_bounds__(256) void ckpt_pack_kernel(const void* __restrict__ X, int64_t x_stride, int64_t units,
+                                                        int64_t n, int8_t* __restrict__ codes,
+                                                        float* __restrict__ scales) {
+  const int lane = threadIdx.x & 63;
+  const int64_t blocks = (n + kCkptBlock - 1) / kCkptBlock;
+  const int64_t u = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+  const int64_t row = u / blocks, b = u - row * blocks, e = b * kCkptBlock + 8 * (lane & 7);
+  const bool in = u < units && e < n;
+  Raw8<T> raw;
+  raw.zero();
+  if (in) raw.load(X, row * x_stride + e);
+  float x[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = raw.get(j, 0.f);
+  ckpt_store8(x, in, lane, codes + row * n + e, scales + u);
+}
+
+__global__ __launch_bounds__(256) void ckpt_unpack_kernel(const int8_t* __restrict__ codes,
+                                                          const float* __restrict__ scales, int64_t units, int64_t n,
+                                                          void* __restrict__ Y, int y_type) {
+  const int64_t blocks = (n + kCkptBlock - 1) / kCkptBlock;
+  const int64_t u = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+  const int64_t row = u / blocks, b = u - row * blocks, e = b * kCkptBlock + 8 * (threadIdx.x & 7);
+  if (u >= units || e >= n) return;
+  Raw8<kRowQ8> raw;
+  raw.load(codes, row * n + e);
+  const float s = ld_global(scales + u);
+  float y[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = raw.get(j, s);
+  store_row8(Y, y_type, row * n + e, y);
+}
+
+// ------------------------------------------------------------------ host
+// Threads of a row: one wavefront up to 2560 values (five runs of eight a lane:
+// no barriers, and the backward's sums fit its registers), then four, then eight.
+template <int T, int kThreads, int kV>
+static hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
+  constexpr int kRows = kThreads < 256 ? 256 / kThreads : 1;
+  layernorm_kernel<T, kThreads, kV>
+      <<<(unsigned)((a.rows + kRows - 1) / kRows), kThreads < 256 ? 256 : kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <int T>
+static hipError_t norm_pick(const NormArgs& a, hipStream_t s) {
+  const int64_t runs = (a.n + 7) / 8;
+  if (runs <= 64) return norm_launch<T, 64, 1>(a, s);
+  if (runs <= 128) return norm_launch<T, 64, 2>(a, s);
+  if (runs <= 192) return norm_launch<T, 64, 3>(a, s);
+  if (runs <= 256) return norm_launch<T, 64, 4>(a, s);
+  if (runs <= 320) return norm_launch<T, 64, 5>(a, s);
+  if (runs <= 512) return norm_launch<T, 256, 2>(a, s);
+  if (runs <= 768) return norm_launch<T, 256, 3>(a, s);
+  if (runs <= 1024) return norm_launch<T, 256, 4>(a, s);
+  if (runs <= 1536) return norm_launch<T, 512, 3>(a, s);
+  return norm_launch<T, 512, 4>(a, s);
+}
+hipError_t launch_layernorm(const NormArgs& a, int x_type, hipStream_t s) {
+  return x_type == kRowF32 ? norm_pick<kRowF32>(a, s) : norm_pick<kRowBf16>(a, s);
+}
+
+template <int T, int kThreads, int kV>
+static hipError_t norm_bwd_launch(const NormBwdArgs& a, hipStream_t s) {
+  constexpr int kRows = kThreads < 256 ? 256 / kThreads : 1;
+  int64_t blocks = (a.rows + kRows - 1) / kRows;
+  if (blocks > kNormParts) blocks = kNormParts;
+  layernorm_bwd_kernel<T, kThreads, kV><<<(unsigned)blocks, kThreads < 256 ? 256 : kThreads, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.part) return e;
+  norm_dw_kernel<<<(unsigned)((2 * a.n + 63) / 64), 1024, 0, s>>>(a.part, (int)blocks, a.n, a.dweight, a.dbias);
+  return hipGetLastError();
+}
+template <int T>
+static hipError_t norm_bwd_pick(const NormBwdArgs& a, hipStream_t s) {
+  const int64_t runs = (a.n + 7) / 8;
+  if (runs <= 64) return norm_bwd_launch<T, 64, 1>(a, s);
+  if (runs <= 128) return norm_bwd_launch<T, 64, 2>(a, s);
+  if (runs <= 192) return norm_bwd_launch<T, 64, 3>(a, s);
+  if (runs <= 256) return norm_bwd_launch<T, 64, 4>(a, s);
+  if (runs <= 320) return norm_bwd_launch<T, 64, 5>(a, s);
+  if (runs <= 512) return norm_bwd_launch<T, 256, 2>(a, s);
+  if (runs <= 768) return norm_bwd_launch<T, 256, 3>(a, s);
+  if (runs <= 1024) return norm_bwd_launch<T, 256, 4>(a, s);
+  if (runs <= 1536) return norm_bwd_launch<T, 512, 3>(a, s);
+  return norm_bwd_launch<T, 512, 4>(a, s);
+}
+hipError_t launch_layernorm_bwd(const NormBwdArgs& a, int x_type, hipStream_t s) {
+  if (a.rows == 0) {
+    norm_zero_kernel<<<(unsigned)((a.n + 255) / 256), 256, 0, s>>>(a.dweight, a.dbias, a.n);
+    return hipGetLastError();
+  }
+  if (x_type == kRowF32) return norm_bwd_pick<kRowF32>(a, s);
+  return x_type == kRowBf16 ? norm_bwd_pick<kRowBf16>(a, s) : norm_bwd_pick<kRowQ8>(a, s);
+}
+
+hipError_t launch_ckpt_pack(const void* X, int x_type, int64_t x_stride, int64_t rows, int64_t n, int8_t* codes,
+                            float* scales, hipStream_t s) {
+  const int64_t units = rows * ((n + kCkptBlock - 1) / kCkptBlock);
+  const unsigned grid = (unsigned)((units + 31) / 32);
+  if (x_type == kRowF32) ckpt_pack_kernel<kRowF32><<<grid, 256, 0, s>>>(X, x_stride, units, n, codes, scales);
+  else ckpt_pack_kernel<kRowBf16><<<grid, 256, 0, s>>>(X, x_stride, units, n, codes, scales);
+  return hipGetLastError();
+}
+hipError_t launch_ckpt_unpack(const int8_t* codes, const float* scales, int64_t rows, int64_t n, void* Y, int y_type,
+                              hipStream_t s) {
+  const int64_t units = rows * ((n + kCkptBlock - 1) / kCkptBlock);
+  ckpt_unpack_kernel<<<(unsigned)((units + 31) / 32), 256, 0, s>>>(codes, scales, units, n, Y, y_type);
+  return hipGetLastError();
+}
+
+}  // namespace bl

@@ -198,6 +198,84 @@ class BlockAttention:
         return O
 
 
+class BlockFeedForward:
+    """The feed-forward side of a block: the norm, the gate and up BitLinears
+    with the gating in one kernel, and the down BitLinear, over rows of a
+    residual stream (float32 or bfloat16).  The three BitLinearWeights are the
+    caller's (quantised before a forward, once per training step).
+
+    `keep` is what a training forward keeps G and U in for the backward:
+    torch.int8 (the default: 8-bit checkpoints, and one of the stream's rows as
+    well, so the rows themselves may be overwritten), torch.bfloat16 or
+    torch.float32 (the stream's rows are then kept as they are).  Outputs and
+    workspaces are allocated per call on torch's current stream."""
+
+    def __init__(self, gate, up, down, act=bl.BL_ACT_RELU2, norm_weight=None, norm_bias=None, eps=1e-6, center=False,
+                 keep=torch.int8):
+        if (gate.k, gate.n_out, gate.n, gate.m) != (up.k, up.n_out, up.n, up.m):
+            raise ValueError("gate and up must have one shape and one N:M pattern")
+        if (down.k, down.n_out) != (gate.n_out, gate.k):
+            raise ValueError(f"down must be {gate.k} x {gate.n_out} (got {down.n_out} x {down.k})")
+        if keep not in (torch.int8, torch.bfloat16, torch.float32):
+            raise ValueError(f"keep must be torch.int8, torch.bfloat16 or torch.float32 (got {keep})")
+        self.gate, self.up, self.down, self.act, self.keep = gate, up, down, act, keep
+        self.norm_weight, self.norm_bias, self.eps, self.center = norm_weight, norm_bias, float(eps), bool(center)
+        self.k, self.n_out, self.device = gate.k, gate.n_out, gate.device
+
+    def _new(self, *shape, dtype=torch.float32):
+        return torch.empty(*shape, dtype=dtype, device=self.device)
+
+    def _kept(self, rows, n, dtype):
+        """Values and (8-bit) scales that rows of n are kept in."""
+        scales = self._new(rows, -(-n // bl.CKPT_BLOCK)) if dtype == torch.int8 else None
+        return self._new(rows, n, dtype=dtype), scales
+
+    def fwd(self, X, train=True):
+        """(Y, kept): float32 Y = down(gating(norm(X))) and, with train, what bwd
+        needs; X [tokens, k]."""
+        t, k, n = X.shape[0], self.k, self.n_out
+        kept, norm, gu = None, {}, {}
+        if train:
+            kept = {"rstd": self._new(t), "mean": self._new(t) if self.center else None, "X": (X, None)}
+            norm = {"rstd": kept["rstd"], "mean": kept["mean"]}
+            if self.keep == torch.int8:
+                kept["X"] = norm["codes"], norm["scales"] = self._kept(t, k, torch.int8)
+            kept["G"], kept["U"] = self._kept(t, n, self.keep), self._kept(t, n, self.keep)
+            gu = {"G": kept["G"][0], "G_scales": kept["G"][1], "U": kept["U"][0], "U_scales": kept["U"][1]}
+        N = self._new(t, k, dtype=torch.bfloat16)
+        bl.bitlinear_layernorm(X, t, k, self.norm_weight, self.norm_bias, self.eps, self.center, N, **norm)
+        xq, x_scale = self._new(t, k, dtype=torch.int8), self._new(t)
+        bl.bitlinear_act_quant(N, t, k, xq, x_scale)
+        H = self._new(t, n, dtype=torch.bfloat16)
+        ws = bl.bitlinear_glu_workspace_bytes(t, k, n)
+        bl.bitlinear_glu(xq, x_scale, t, k, self.gate.packed, self.gate.gamma, self.up.packed, self.up.gamma, n,
+                         self.gate.n, self.gate.m, self.act, H, ws=self._new(ws, dtype=torch.uint8) if ws else None, **gu)
+        bufs = self.down.fwd(H, t)
+        if train:
+            kept.update(xq=xq, x_scale=x_scale, hq=bufs["xq"], h_scale=bufs["x_scale"])
+        return bufs["Y"].view(t, k), kept
+
+    def bwd(self, dY, kept, dR=None):
+        """Gradients for bfloat16 dY [tokens, k] of Y: a dict of X (of dR's type,
+        or float32; dR, the gradient that reaches X past this side of the block,
+        is added), gate, up, down (float32), norm_weight and norm_bias (float32,
+        None without the parameter)."""
+        t, k, n = dY.shape[0], self.k, self.n_out
+        dH, dWd = self.down.bwd(dY, kept["hq"], kept["h_scale"], t)
+        dN, dWg, dWu = self._new(t, k), self._new(n, k), self._new(n, k)
+        ws = bl.bitlinear_glu_bwd_workspace_bytes(t, k, n)
+        bl.bitlinear_glu_bwd(dH, *kept["G"], *kept["U"], kept["xq"], kept["x_scale"], self.gate.packed, self.gate.gamma,
+                             self.up.packed, self.up.gamma, t, k, n, self.gate.n, self.gate.m, self.act, dN, dWg, dWu,
+                             ws=self._new(ws, dtype=torch.uint8) if ws else None)
+        dX = self._new(t, k, dtype=dR.dtype if dR is not None else torch.float32)
+        dw = self._new(k) if self.norm_weight is not None else None
+        db = self._new(k) if self.norm_bias is not None else None
+        ws = self._new(bl.bitlinear_layernorm_bwd_workspace_bytes(k), dtype=torch.uint8)
+        bl.bitlinear_layernorm_bwd(*kept["X"], t, k, self.norm_weight, kept["mean"], kept["rstd"], dN, dX, dw, db, dR=dR,
+                                   ws=ws)
+        return {"X": dX, "gate": dWg, "up": dWu, "down": dWd.view(k, n), "norm_weight": dw, "norm_bias": db}
+
+
 def dense_to_sparse(step, switch_step, n, m):
     """N:M pattern of a dense-to-sparse schedule: dense (8:8) before
     switch_step, n:m from it on."""

@@ -1,0 +1,221 @@
+"""The gated feed-forward on the GPU: forward bit for bit where its steps are
+exact or rounded one by one (G, U, squared ReLU, checkpoints), within bounds for
+SiLU; backward within bounds derived from its roundings."""
+import numpy as np
+import pytest
+import torch
+
+import _ffn_ref as R
+from _gpu_ffn import TYPES, activations, dev, empty, host, kept, weight
+from sparse_linear_layers_group_amd import bitlinear as bl
+
+pytestmark = pytest.mark.gpu
+ACT = {"relu2": bl.BL_ACT_RELU2, "silu": bl.BL_ACT_SILU}
+PATTERNS = [(8, 8), (6, 8), (4, 8), (3, 8), (2, 8), (2, 4)]
+
+
+def layers(k, n_out, n, m, seed=0):
+    return [weight(n_out, k, n, m, seed + i) for i in range(2)]
+
+
+def scratch(nbytes):
+    return torch.empty(nbytes, dtype=torch.uint8, device="cuda") if nbytes else None
+
+
+def forward(xq, xs, pair, k, n_out, act, H, G=None, U=None, stream=None):
+    (gate, _), (up, _) = pair
+    t = xq.shape[0]
+    more = {} if G is None else {"G": G[0], "G_scales": G[1], "U": U[0], "U_scales": U[1]}
+    bl.bitlinear_glu(xq, xs, t, k, gate.packed, gate.gamma, up.packed, up.gamma, n_out, gate.n, gate.m, ACT[act], H,
+                     ws=scratch(bl.bitlinear_glu_workspace_bytes(t, k, n_out)), stream=stream, **more)
+
+
+def gammas(pair):
+    return [float(lw.gamma.item()) for lw, _ in pair]
+
+
+def projections(xq, xs, pair):
+    return [R.project(host(xq), host(xs), c, g) for (_, c), g in zip(pair, gammas(pair))]
+
+
+def check_h(H, g, u, act):
+    if act == "relu2":
+        assert np.array_equal(host(H), R.relu2_h(g, u))
+        return
+    want = R.act(g, act)[0] * u
+    # exp(-g): the argument's rounding is |g| log2 e 2^-24 of an exponent, exp2 and the division 1 - 2 ulp each;
+    # then two products, and bf16's half step
+    tol = (R.UBF + (np.abs(g) + 8) * 2 * R.U24) * np.abs(want)
+    assert np.all(np.abs(host(H) - want) <= tol + 1e-37)
+
+
+@pytest.mark.parametrize("act", ["relu2", "silu"])
+@pytest.mark.parametrize("t,k,n_out,nm", [
+    (1, 128, 128, (6, 8)), (2, 256, 384, (8, 8)), (7, 896, 128, (2, 4)), (16, 1152, 256, (3, 8)), (17, 384, 640, (2, 8)),
+    (31, 1024, 128, (4, 8)), (33, 640, 256, (6, 8)), (64, 2560, 128, (6, 8)), (65, 128, 512, (8, 8)), (130, 1536, 384, (4, 8)),
+    (257, 512, 1152, (6, 8)), (300, 896, 640, (2, 4)), (520, 640, 256, (2, 8)), (1025, 256, 384, (3, 8))])
+def test_forward(t, k, n_out, nm, act):
+    pair = layers(k, n_out, *nm, seed=t)
+    xq, xs = activations(t, k, t)
+    g, u = projections(xq, xs, pair)
+    H0 = empty(t, n_out, dtype=torch.bfloat16)
+    forward(xq, xs, pair, k, n_out, act, H0)
+    check_h(H0, g, u, act)
+    for keep in ("f32", "bf16", "q8"):
+        H = empty(t + 1, n_out, dtype=torch.bfloat16, fill=9.0)
+        G, U = kept(t, n_out, keep), kept(t, n_out, keep)
+        forward(xq, xs, pair, k, n_out, act, H[:t], G, U)
+        assert torch.equal(H[:t], H0) and (H[t:] == 9).all()
+        for (v, s), want in ((G, g), (U, u)):
+            if keep == "q8":
+                c, sc = R.ckpt(want)
+                assert np.array_equal(host(v), c) and np.array_equal(host(s), sc)
+            else:
+                assert np.array_equal(host(v), want if keep == "f32" else R.bf16(want))
+
+
+@pytest.mark.parametrize("t", [1, 16, 40, 200, 700])
+def test_forward_equals_the_layers_one_by_one(t):
+    """The existing path: two contractions, then the gating with its own pass."""
+    k, n_out = 1280, 640
+    pair = layers(k, n_out, 6, 8)
+    xq, xs = activations(t, k, 3)
+    Y = []
+    for lw, _ in pair:
+        Y.append(empty(t, n_out))
+        nb = bl.bitlinear_fwd_workspace_bytes(t, k, n_out)
+        bl.bitlinear_contract(xq, xs, t, k, lw.packed, n_out, 6, 8, lw.gamma, Y[-1],
+                              ws=torch.zeros(nb, dtype=torch.uint8, device="cuda") if nb else None)
+    H1, hq, hs = empty(t, n_out, dtype=torch.bfloat16), empty(t, n_out, dtype=torch.int8), empty(t)
+    bl.bitlinear_relu2_gate(*Y, t, n_out, H1, hq, hs)
+    H, G, U = empty(t, n_out, dtype=torch.bfloat16), kept(t, n_out, "f32"), kept(t, n_out, "f32")
+    forward(xq, xs, pair, k, n_out, "relu2", H, G, U)
+    assert torch.equal(H, H1) and torch.equal(G[0], Y[0]) and torch.equal(U[0], Y[1])
+
+
+def test_zero_rows_and_zero_weights():
+    """Tokens whose scale is 0, and layers without a nonzero code, give zeros
+    (an all-zero block's scale is 0)."""
+    t, k, n_out = 20, 256, 128
+    pair = layers(k, n_out, 6, 8)
+    xq, xs = activations(t, k, 1)
+    xq[3], xs[3] = 0, 0
+    H, G, U = empty(t, n_out, dtype=torch.bfloat16), kept(t, n_out, "q8"), kept(t, n_out, "q8")
+    forward(xq, xs, pair, k, n_out, "silu", H, G, U)
+    assert not H[3].any() and not G[0][3].any() and (G[1][3] == 0).all()
+    pair[0][0].packed.zero_()
+    pair[0][0].gamma.zero_()
+    forward(xq, xs, pair, k, n_out, "silu", H, G, U)
+    assert not H.any() and U[0].any()
+
+
+def backward_case(t, k, n_out, nm, act, keep, dh, grad, seed=0, stream=None):
+    pair = layers(k, n_out, *nm, seed=seed)
+    xq, xs = activations(t, k, seed)
+    H, G, U = empty(t, n_out, dtype=torch.bfloat16), kept(t, n_out, keep), kept(t, n_out, keep)
+    forward(xq, xs, pair, k, n_out, act, H, G, U)
+    gen = torch.Generator(device="cuda").manual_seed(seed + 9)
+    dH = torch.randn(t, n_out, generator=gen, device="cuda").to(TYPES[dh])
+    out = [empty(t, k, dtype=TYPES[grad]), empty(n_out, k, dtype=TYPES[grad]), empty(n_out, k, dtype=TYPES[grad])]
+    return pair, xq, xs, G, U, dH, out
+
+
+def backward(pair, xq, xs, G, U, dH, out, k, n_out, act, stream=None, ws=None):
+    (gate, _), (up, _) = pair
+    t = xq.shape[0]
+    if ws is None:
+        ws = scratch(bl.bitlinear_glu_bwd_workspace_bytes(t, k, n_out))
+    bl.bitlinear_glu_bwd(dH, *G, *U, xq, xs, gate.packed, gate.gamma, up.packed, up.gamma, t, k, n_out, gate.n, gate.m,
+                         ACT[act], *out, ws=ws, stream=stream)
+
+
+def values(kept_pair):
+    v, s = kept_pair
+    return host(v) if s is None else R.ckpt_values(host(v), host(s))
+
+
+@pytest.mark.parametrize("t,k,n_out,nm,act,keep,dh,grad", [
+    (1, 128, 128, (6, 8), "relu2", "q8", "f32", "f32"), (5, 256, 384, (8, 8), "silu", "f32", "bf16", "bf16"),
+    (63, 384, 256, (2, 4), "relu2", "bf16", "bf16", "f32"), (64, 640, 128, (4, 8), "silu", "q8", "f32", "bf16"),
+    (65, 128, 1152, (3, 8), "relu2", "f32", "f32", "bf16"), (200, 1024, 2048, (2, 8), "silu", "bf16", "bf16", "f32"),
+    (300, 896, 1280, (6, 8), "relu2", "q8", "bf16", "bf16"), (515, 1280, 640, (6, 8), "silu", "q8", "f32", "f32"),
+    (2100, 256, 384, (6, 8), "relu2", "q8", "bf16", "f32"), (1030, 2304, 2560, (4, 8), "relu2", "f32", "f32", "bf16")])
+def test_backward(t, k, n_out, nm, act, keep, dh, grad):
+    pair, xq, xs, G, U, dH, out = backward_case(t, k, n_out, nm, act, keep, dh, grad, seed=t)
+    backward(pair, xq, xs, G, U, dH, out, k, n_out, act)
+    g, u, d, gm = values(G), values(U), host(dH), gammas(pair)
+    codes = [c for _, c in pair]
+    x, s = host(xq), host(xs)
+    half = torch.finfo(TYPES[grad]).eps / 2
+    ref = R.glu_bwd(d, g, u, act, x, s, codes, gm)
+    depth = (2 * n_out, t, t)
+    for got, (want, sizes), K in zip(out, ref, depth):
+        # operands: a half step of bf16 after at most four binary32 products (and act, act' of SiLU: see check_h); sums:
+        # K + 8 half steps of the sizes (matrix instructions and the planes of a split product)
+        slack = 8 * R.U24 if act == "relu2" else (np.abs(g).max() + 16) * 4 * R.U24
+        tol = (R.UBF + slack + (K + 8) * R.U24) * sizes + half * np.abs(want)
+        assert np.all(np.abs(host(got) - want) <= tol * 1.01 + 1e-30)
+    if act == "relu2":
+        # the operands as they are rounded, and then only the sums' error
+        o = [v.astype(np.float64) for v in R.relu2_operands(d, g, u, s, gm)]
+        c = [v.astype(np.float64) for v in codes]
+        want = (o[0] @ c[0] + o[1] @ c[1], o[2].T @ x.astype(np.float64), o[3].T @ x.astype(np.float64))
+        a = [np.abs(v) for v in o]
+        size = (a[0] @ np.abs(c[0]) + a[1] @ np.abs(c[1]), a[2].T @ np.abs(x.astype(np.float64)), a[3].T @ np.abs(x.astype(np.float64)))
+        for got, w, z, K in zip(out, want, size, depth):
+            tol = (K + 8) * R.U24 * z + half * np.abs(w)
+            assert np.all(np.abs(host(got) - w) <= tol * 1.01 + 1e-30)
+    # reruns give the same bits; a gradient does not depend on which others are asked for
+    again = [torch.empty_like(v) for v in out]
+    backward(pair, xq, xs, G, U, dH, [again[0], None, None], k, n_out, act)
+    backward(pair, xq, xs, G, U, dH, [None, again[1], again[2]], k, n_out, act)
+    assert all(torch.equal(a, b) for a, b in zip(out, again))
+
+
+def test_backward_of_zero_tokens_and_of_zeros():
+    k, n_out = 256, 128
+    pair = layers(k, n_out, 6, 8)
+    for grad in ("f32", "bf16"):
+        out = [empty(0, k, dtype=TYPES[grad]), empty(n_out, k, dtype=TYPES[grad], fill=3.0),
+               empty(n_out, k, dtype=TYPES[grad], fill=3.0)]
+        G, U = kept(0, n_out, "q8"), kept(0, n_out, "q8")
+        backward(pair, empty(0, k, dtype=torch.int8), empty(0), G, U, empty(0, n_out), out, k, n_out, "relu2",
+                 ws=scratch(256))
+        assert not out[1].any() and not out[2].any()
+
+
+def test_neighbours_stay():
+    """Rows behind the tokens and gradients beside the weights' are not written."""
+    t, k, n_out = 70, 256, 384
+    pair, xq, xs, G, U, dH, _ = backward_case(t, k, n_out, (6, 8), "relu2", "q8", "f32", "f32")
+    for dtype in (torch.float32, torch.bfloat16):
+        big = [empty(t + 3, k, dtype=dtype, fill=5.0), empty(n_out + 2, k, dtype=dtype, fill=5.0), empty(n_out + 2, k, dtype=dtype, fill=5.0)]
+        need = bl.bitlinear_glu_bwd_workspace_bytes(t, k, n_out)
+        ws = torch.full((need + 512,), 171, dtype=torch.uint8, device="cuda")
+        backward(pair, xq, xs, G, U, dH, [big[0][:t], big[1][:n_out], big[2][:n_out]], k, n_out, "relu2", ws=ws[:need])
+        assert (big[0][t:] == 5).all() and (big[1][n_out:] == 5).all() and (big[2][n_out:] == 5).all()
+        assert (ws[need:] == 171).all()
+
+
+def test_refusals_of_tensors():
+    t, k, n_out = 4, 256, 128
+    pair, xq, xs, G, U, dH, out = backward_case(t, k, n_out, (6, 8), "relu2", "bf16", "f32", "f32")
+    (gate, _), (up, _) = pair
+    H = empty(t, n_out, dtype=torch.bfloat16)
+    ok = (xq, xs, t, k, gate.packed, gate.gamma, up.packed, up.gamma, n_out, 6, 8, 0, H)
+    with pytest.raises(TypeError):
+        bl.bitlinear_glu(*ok, G=G[0], U=U[0].float())
+    with pytest.raises(TypeError):
+        bl.bitlinear_glu(*ok, G=G[0])
+    with pytest.raises(ValueError):
+        bl.bitlinear_glu(*ok[:4], gate.packed[:-32], *ok[5:])
+    with pytest.raises(ValueError):
+        bl.bitlinear_glu(*ok[:12], H.cpu())
+    with pytest.raises(bl.BitLinearError):
+        bl.bitlinear_glu(*ok[:9], 5, *ok[10:])
+    with pytest.raises(TypeError):
+        backward(pair, xq, xs, G, U, dH, [out[0].bfloat16(), out[1], out[2]], k, n_out, "relu2")
+    with pytest.raises(bl.BitLinearError):
+        backward(pair, xq, xs, G, U, dH, out, k, n_out, "relu2", ws=scratch(256))
+    with pytest.raises(bl.BitLinearError):
+        backward(pair, xq, xs, G, U, dH, [out[0], out[1], None], k, n_out, "relu2")
