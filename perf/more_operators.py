@@ -288,10 +288,12 @@ def _own(s):
     act = bl.BL_ACT_RELU2 if s["act"] == "relu2" else bl.BL_ACT_SILU
     weights = (gate["packed"], gate["gamma"], up["packed"], up["gamma"])
     if s["kind"] == "glu":
-        bl.bitlinear_glu(s["xq"], s["xs"], s["tokens"], s["k"], *weights, s["n_out"], s["n"], s["m"], act, s["h"])
+        need = bl.bitlinear_glu_workspace_bytes(s["tokens"], s["k"], s["n_out"])
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+        bl.bitlinear_glu(s["xq"], s["xs"], s["tokens"], s["k"], *weights, s["n_out"], s["n"], s["m"], act, s["h"], ws=ws)
         return {"h": s["h"]}
     bl.bitlinear_glu(s["xq"], s["xs"], s["tokens"], s["k"], *weights, s["n_out"], s["n"], s["m"], act, s["h"], G=s["g"],
-                     G_scales=s["gs"], U=s["u"], U_scales=s["us"])
+                     G_scales=s["gs"], U=s["u"], U_scales=s["us"], ws=s["ws"])
     bl.bitlinear_glu_bwd(s["dh"], s["g"], s["gs"], s["u"], s["us"], s["xq"], s["xs"], *weights, s["tokens"], s["k"],
                          s["n_out"], s["n"], s["m"], act, s["dx"], s["dwg"], s["dwu"], ws=s["ws"])
     return {"h": s["h"], "dx": s["dx"], "dwg": s["dwg"], "dwu": s["dwu"]}
