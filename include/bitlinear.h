@@ -810,8 +810,8 @@ int bitlinear_layernorm_bwd(const void *X, int x_type, const float *x_scales, in
  *           float [tokens x n_out / 64]; otherwise those are NULL).
  *   ws      bitlinear_glu_workspace_bytes() bytes, 256-byte aligned,
  *           clobbered; NULL where that is 0.
- * n_out a positive multiple of 128 (the next BitLinear's k); other sizes as
- * for bitlinear_contract.  tokens == 0 is a no-op. */
+ * n_out a positive multiple of 128 (the next BitLinear's k), k below 2^22;
+ * other sizes as for bitlinear_contract.  tokens == 0 is a no-op. */
 #define BL_ACT_RELU2  0
 #define BL_ACT_SILU   1
 size_t bitlinear_glu_workspace_bytes(int64_t tokens, int64_t k, int64_t n_out);

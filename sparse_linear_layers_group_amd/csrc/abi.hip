@@ -1469,6 +1469,7 @@ int check_glu(int64_t tokens, int64_t k, int64_t n_out, int n, int m, int act) {
   TRY(check_layer(n_out, k));
   if (n_out % 128 != 0)
     return fail(BL_ESHAPE, "n_out must be a positive multiple of 128 (got %lld)", (long long)n_out);
+  if (k >= (int64_t)1 << 22) return fail(BL_ESHAPE, "k must be below 2^22 (got %lld)", (long long)k);
   if (act != BL_ACT_RELU2 && act != BL_ACT_SILU)
     return fail(BL_EINVAL, "act must be BL_ACT_RELU2 or BL_ACT_SILU (got %d)", act);
   if (tokens < 0 || tokens >= kLimit || tokens * k >= kLimit || tokens * n_out >= kLimit)

@@ -6,6 +6,8 @@
 #include "glu.h"
 #include "launch.h"
 
+#include <type_traits>
+
 namespace bl {
 
 // ---------------------------------------------------------------- the gating
@@ -187,6 +189,281 @@ __global__ __launch_bounds__(1024) void glu_small_kernel(GluArgs a) {
   }
 }
 
+// ------------------------------------------------------ forward, many tokens
+// Both layers' codes are decoded once into int8 (a pass over the weights, some 6%
+// of the products' time at 4096 tokens), and an int8 product runs on tiles of
+// 128 outputs (256 rows: for each 64 outputs their gate rows, then their up
+// rows) x 64 kWN tokens.  A wavefront computes 64 outputs of both layers
+// (128 rows) x 64 tokens, so a lane holds g and u of the same outputs and the
+// gating needs no exchange.  Tiles stream through kGluStages LDS stages of 64 k
+// filled by LDS DMA; a step's fragments are read from LDS while the matrix
+// instructions of the step before run, so a stage is refilled as soon as its
+// fragments are in registers.
+//
+// A row's 64 bytes of a stage are four 16-byte pieces, piece c at place
+// c ^ ((row >> 2) & 3): the 16 lanes that LDS serves at a time (16 rows of one
+// piece) then read each of a 256-byte line's places once.  The decoded codes lie
+// in memory in that order: 8 KiB for each (64 outputs, 64 k), a wavefront's DMA
+// instruction a whole KiB of it.
+constexpr int kGluRows = 256;                 // rows of a tile: 128 outputs
+constexpr int kGluK = 64;                     // k of a stage
+constexpr int kGluABytes = kGluRows * kGluK;  // 16 KiB
+constexpr int kPairBytes = 128 * kGluK;       // decoded codes of 64 outputs, 64 k
+constexpr int kGluStages = 3;
+__device__ __forceinline__ int glu_place(int row, int piece) { return piece ^ ((row >> 2) & 3); }
+
+// One packed superblock (64 rows x 128 k) per wavefront: lane c = r + 16 q holds, as
+// the operand (i, h), the codes of row 16 i + r at k = 64 h + 16 q .. + 15, one piece.
+template <int S>
+__global__ __launch_bounds__(256) void glu_decode_kernel(const char* __restrict__ gate, const char* __restrict__ up,
+                                                        int64_t superblocks, int nkb, char* __restrict__ out) {
+  __shared__ __attribute__((aligned(16))) uint32_t lut[512 * kSmallCopies];
+  const int tid = threadIdx.x, lane = tid & 63;
+#pragma unroll
+  for (int r = 0; r < 512 * kSmallCopies / 4 / 256; ++r) {
+    const uint32_t v = ld_global(&kHalfCodeTable.v[(tid + 256 * r) / (kSmallCopies / 4)]);
+    reinterpret_cast<u32x4*>(lut)[tid + 256 * r] = u32x4{v, v, v, v};
+  }
+  const uint32_t* lut_lane = lut + (lane & (kSmallCopies - 1));
+  __syncthreads();
+  // 2 superblocks: gate's of all strips, then up's
+  for (int64_t j = (int64_t)blockIdx.x * 4 + (tid >> 6); j < 2 * superblocks; j += (int64_t)gridDim.x * 4) {
+    const int side = j >= superblocks;
+    const int64_t sb = side ? j - superblocks : j, strip = sb / nkb, kb = sb - strip * nkb;
+    constexpr int kBytes = block_bytes(S);
+    uint32_t w[kBytes / 4];
+    const uint32_t* src = reinterpret_cast<const uint32_t*>((side ? up : gate) + (sb * kStripRows + lane) * kBytes);
+#pragma unroll
+    for (int i = 0; i < kBytes / 4; ++i) w[i] = ld_global(src + i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v4i c = chunk_operand<S>(w, 2 * i + h, lut_lane);
+        const int row = 64 * side + 16 * i + (lane & 15);
+        char* dst = out + (strip * (2 * nkb) + 2 * kb + h) * kPairBytes + row * kGluK + 16 * glu_place(row, lane >> 4);
+        st_global(reinterpret_cast<v4i*>(dst), c);
+      }
+  }
+}
+
+typedef __attribute__((address_space(3))) char glu_lds_char;
+typedef __attribute__((address_space(3))) void glu_lds_void;
+__device__ __forceinline__ void glu_dma16(__amdgpu_buffer_rsrc_t r, glu_lds_char* dst, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (glu_lds_void*)dst, 16, off, 0, 0, 0);
+}
+template <int N, bool kLds = false>
+__device__ __forceinline__ void glu_wait() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | ((kLds ? 0 : 15) << 8));
+}
+
+// LDS of the stages: separate objects, so that the compiler sees that reads of one
+// stage and DMA into the others touch different memory (namespace scope: a
+// __shared__ array inside a template made the host pass drop the kernel's stub)
+template <int kWN>
+struct GluTile {
+  static constexpr int kTokens = 64 * kWN;
+  static constexpr int kWaves = 2 * kWN;
+  static constexpr int kStageBytes = kGluABytes + kTokens * kGluK;
+  static constexpr int kAInstr = 16 / kWaves;  // DMA instructions of A per wavefront and step
+  static constexpr int kPerStep = kAInstr + 2;
+};
+__shared__ __attribute__((aligned(1024))) char g_glu2_st0[GluTile<2>::kStageBytes];
+__shared__ __attribute__((aligned(1024))) char g_glu2_st1[GluTile<2>::kStageBytes];
+__shared__ __attribute__((aligned(1024))) char g_glu2_st2[GluTile<2>::kStageBytes];
+__shared__ __attribute__((aligned(1024))) char g_glu4_st0[GluTile<4>::kStageBytes];
+__shared__ __attribute__((aligned(1024))) char g_glu4_st1[GluTile<4>::kStageBytes];
+__shared__ __attribute__((aligned(1024))) char g_glu4_st2[GluTile<4>::kStageBytes];
+template <int kWN, int P>
+__device__ __forceinline__ char* glu_stage() {
+  static_assert(kGluStages == 3 && (kWN == 2 || kWN == 4), "the stages above");
+  if constexpr (kWN == 2) return P == 0 ? g_glu2_st0 : P == 1 ? g_glu2_st1 : g_glu2_st2;
+  else return P == 0 ? g_glu4_st0 : P == 1 ? g_glu4_st1 : g_glu4_st2;
+}
+
+struct GluFrags {
+  v4i a[8], b[4];
+};
+
+template <int kWN, int kAct>
+__global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs a, const char* __restrict__ codes, int row_tiles,
+                                                       int token_tiles) {
+  typedef GluTile<kWN> T;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / kWN, wn = wave % kWN;
+  const int l16 = lane & 15, lg = lane >> 4;
+  // Workgroup (XCD x, slot) takes the slot-th tile of XCD x's contiguous eighth of
+  // an order in groups of four token tiles, row tiles within a group: an XCD's
+  // workgroups run a compact block and share its operands in their L2.
+  int rt, tt;
+  {
+    const int tiles = row_tiles * token_tiles, per = (tiles + 7) / 8, full = tiles - (per - 1) * 8;
+    const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+    if (slot >= (xcd < full ? per : per - 1)) return;
+    const int t = xcd < full ? xcd * per + slot : full * per + (xcd - full) * (per - 1) + slot;
+    const int g = t / (4 * row_tiles), r = t - g * 4 * row_tiles;
+    const int gm = token_tiles - 4 * g < 4 ? token_tiles - 4 * g : 4;
+    tt = 4 * g + r % gm;
+    rt = r / gm;
+  }
+  const int64_t t0 = (int64_t)tt * T::kTokens;
+  const int nks = (int)(a.k / kGluK);
+  // A: two pairs of 64 outputs, each nks pieces of 8 KiB, in order
+  const __amdgpu_buffer_rsrc_t ar = glu_rsrc(codes + (int64_t)rt * 2 * nks * kPairBytes, (int64_t)2 * nks * kPairBytes);
+  const __amdgpu_buffer_rsrc_t br = glu_rsrc(a.xq, a.tokens * a.k);
+  uint32_t a_off[T::kAInstr], b_off[2];
+#pragma unroll
+  for (int q = 0; q < T::kAInstr; ++q) {
+    const int at = T::kAInstr * wave + q;  // KiB of the stage's 16
+    a_off[q] = (uint32_t)((at >> 3) * nks * kPairBytes + (at & 7) * 1024 + 16 * lane);
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int row = 32 * wave + 16 * q + (lane >> 2);
+    const int64_t t = t0 + row;
+    b_off[q] = t < a.tokens ? (uint32_t)(t * a.k + 16 * glu_place(row, lane & 3)) : kGluOOB;
+  }
+  // past the last step the same instructions read zeros into a stage that nobody
+  // reads, so the waits can count them
+  auto dma = [&](auto stage, int ks) {
+    constexpr int P = decltype(stage)::value;
+    glu_lds_char* st = (glu_lds_char*)glu_stage<kWN, P>();
+    const bool in = ks < nks;
+#pragma unroll
+    for (int q = 0; q < T::kAInstr; ++q)
+      glu_dma16(ar, st + 1024 * (T::kAInstr * wave + q), in ? a_off[q] + (uint32_t)(ks * kPairBytes) : kGluOOB);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      glu_dma16(br, st + kGluABytes + 1024 * (2 * wave + q),
+                in && b_off[q] != kGluOOB ? b_off[q] + (uint32_t)(ks * kGluK) : kGluOOB);
+  };
+  v4i c[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[i][j] = v4i{0, 0, 0, 0};
+  const uint32_t frag = (uint32_t)(l16 * kGluK + 16 * glu_place(l16, lg));
+  const uint32_t a_base = (uint32_t)(wm * 128 * kGluK) + frag, b_base = (uint32_t)(kGluABytes + wn * 64 * kGluK) + frag;
+  auto read = [&](auto stage, GluFrags& f) {
+    constexpr int P = decltype(stage)::value;
+    const glu_lds_char* st = (const glu_lds_char*)glu_stage<kWN, P>();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      f.b[j] = *reinterpret_cast<const __attribute__((address_space(3))) v4i*>(st + b_base + j * 16 * kGluK);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      f.a[i] = *reinterpret_cast<const __attribute__((address_space(3))) v4i*>(st + a_base + i * 16 * kGluK);
+  };
+  // Step ks: its fragments are in `now` (read in step ks - 1).  Once every wavefront
+  // is here, stage ks % 3 is free and takes step ks + 3; step ks + 1, whose DMA has
+  // landed for all, is read into `next`.
+  auto step = [&](auto stage, int ks, GluFrags& now, GluFrags& next) {
+    constexpr int P = decltype(stage)::value;
+    glu_wait<T::kPerStep, true>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    dma(std::integral_constant<int, P>{}, ks + 3);
+    read(std::integral_constant<int, (P + 1) % 3>{}, next);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[i][j] = mfma_i8(now.a[i], now.b[j], c[i][j]);
+  };
+  using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, 1>;
+  using S2 = std::integral_constant<int, 2>;
+  GluFrags f0, f1;
+  dma(S0{}, 0);
+  dma(S1{}, 1);
+  dma(S2{}, 2);
+  glu_wait<2 * T::kPerStep>();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  read(S0{}, f0);
+  int ks = 0;
+  for (; ks + 5 < nks; ks += 6) {  // three stages x two fragment sets
+    step(S0{}, ks, f0, f1);
+    step(S1{}, ks + 1, f1, f0);
+    step(S2{}, ks + 2, f0, f1);
+    step(S0{}, ks + 3, f1, f0);
+    step(S1{}, ks + 4, f0, f1);
+    step(S2{}, ks + 5, f1, f0);
+  }
+  if (ks < nks) step(S0{}, ks, f0, f1);
+  if (ks + 1 < nks) step(S1{}, ks + 1, f1, f0);
+  if (ks + 2 < nks) step(S2{}, ks + 2, f0, f1);
+  if (ks + 3 < nks) step(S0{}, ks + 3, f1, f0);
+  if (ks + 4 < nks) step(S1{}, ks + 4, f0, f1);
+  glu_wait<0, true>();  // no DMA outlives the workgroup, no read its stage
+
+  // Lane: outputs n0 + 16 i + 4 lg + q (i < 4: gate, i + 4: up) of token
+  // t0 + 64 wn + 16 j + l16
+  const double gg = ld_global(a.gate_gamma), gu = ld_global(a.up_gamma);
+  const int64_t n0 = (int64_t)rt * 128 + wm * 64;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t token = t0 + 64 * wn + 16 * j + l16;
+    const bool in = token < a.tokens;
+    const float s = in ? ld_global(a.x_scale + token) : 0.f;
+    const float sg = out_scale(gg, s), su = out_scale(gu, s);
+    float g[16], u[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        g[4 * i + q] = out_value(c[i][j][q], sg);
+        u[4 * i + q] = out_value(c[i + 4][j][q], su);
+      }
+    const int64_t e = token * a.n_out + n0 + 4 * lg;
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float h[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[q] = act_value<kAct>(g[4 * i + q]) * u[4 * i + q];
+        st_global(reinterpret_cast<u32x2*>(a.H + e + 16 * i), u32x2{pair_bf16(h[0], h[1]), pair_bf16(h[2], h[3])});
+      }
+    }
+    if (a.save == kSaveNone) continue;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const float* x = z ? u : g;
+      void* out = z ? a.U : a.G;
+      if (a.save == kRowQ8) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = max_u(top, abs_bits(x[i]));
+        top = max_u(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+        top = max_u(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+        const CkptScale cs = ckpt_scale(top);
+        if (!in) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) w |= ckpt_code(x[4 * i + q], cs.inv) << (8 * q);
+          st_global(reinterpret_cast<uint32_t*>(static_cast<int8_t*>(out) + e + 16 * i), w);
+        }
+        if (lg == 0) st_global((z ? a.Us : a.Gs) + (token * a.n_out + n0) / kCkptBlock, cs.scale);
+      } else if (in) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (a.save == kRowF32)
+            st_global(reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + e + 16 * i),
+                      f32x4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
+          else
+            st_global(reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + e + 16 * i),
+                      u32x2{pair_bf16(x[4 * i], x[4 * i + 1]), pair_bf16(x[4 * i + 2], x[4 * i + 3])});
+        }
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------- backward, the gating
 // dU = dh act(g) and dG = dh u act'(g) of a 64 x 64 tile (tokens x columns) in
 // binary32, and from them the four bf16 operands of the products, each rounded
@@ -277,27 +554,50 @@ __global__ __launch_bounds__(256) void glu_gate_bwd_kernel(GluBwdArgs a, GluBwdL
 }
 
 // ------------------------------------------------------------------ host
-size_t glu_ws_bytes(int64_t, int64_t, int64_t) { return 0; }
+// From kGluManyTokens tokens on the codes are decoded once for all.
+constexpr int64_t kGluManyTokens = 192;
+size_t glu_ws_bytes(int64_t tokens, int64_t k, int64_t n_out) {
+  return tokens < kGluManyTokens ? 0 : (size_t)(2 * n_out * k);
+}
 
 template <int S, int kAct>
-static hipError_t glu_launch(const GluArgs& a, hipStream_t s) {
-  const unsigned strips = (unsigned)(a.n_out / kStripRows);
-  const int tiles = a.tokens <= 16 ? 1 : a.tokens <= 32 ? 2 : 4;
-  const dim3 grid(strips, (unsigned)((a.tokens + 16 * tiles - 1) / (16 * tiles)));
-  if (tiles == 1) glu_small_kernel<S, kAct, 1><<<grid, 1024, 0, s>>>(a);
-  else if (tiles == 2) glu_small_kernel<S, kAct, 2><<<grid, 1024, 0, s>>>(a);
-  else glu_small_kernel<S, kAct, 4><<<grid, 1024, 0, s>>>(a);
+static hipError_t glu_launch(const GluArgs& a, void* ws, hipStream_t s) {
+  if (a.tokens < kGluManyTokens) {
+    const unsigned strips = (unsigned)(a.n_out / kStripRows);
+    const int tiles = a.tokens <= 16 ? 1 : a.tokens <= 32 ? 2 : 4;
+    const dim3 grid(strips, (unsigned)((a.tokens + 16 * tiles - 1) / (16 * tiles)));
+    if (tiles == 1) glu_small_kernel<S, kAct, 1><<<grid, 1024, 0, s>>>(a);
+    else if (tiles == 2) glu_small_kernel<S, kAct, 2><<<grid, 1024, 0, s>>>(a);
+    else glu_small_kernel<S, kAct, 4><<<grid, 1024, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const int nkb = (int)(a.k / kBlockK);
+  const int64_t superblocks = a.n_out / kStripRows * nkb;
+  const int64_t blocks = (2 * superblocks + 3) / 4;
+  glu_decode_kernel<S><<<(unsigned)(blocks < 1024 ? blocks : 1024), 256, 0, s>>>(
+      static_cast<const char*>(a.gate), static_cast<const char*>(a.up), superblocks, nkb, static_cast<char*>(ws));
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int row_tiles = (int)(a.n_out / 128);
+#ifndef GLU_WN
+#define GLU_WN 2
+#endif
+  typedef GluTile<GLU_WN> T;
+  const int token_tiles = (int)((a.tokens + T::kTokens - 1) / T::kTokens);
+  const int64_t tiles = (int64_t)row_tiles * token_tiles;
+  glu_gemm_kernel<GLU_WN, kAct><<<(unsigned)((tiles + 7) / 8 * 8), 64 * T::kWaves, 0, s>>>(a, static_cast<const char*>(ws),
+                                                                                          row_tiles, token_tiles);
   return hipGetLastError();
 }
 template <int S>
-static hipError_t glu_launch_s(const GluArgs& a, hipStream_t s) {
-  return a.act == kActRelu2 ? glu_launch<S, kActRelu2>(a, s) : glu_launch<S, kActSilu>(a, s);
+static hipError_t glu_launch_s(const GluArgs& a, void* ws, hipStream_t s) {
+  return a.act == kActRelu2 ? glu_launch<S, kActRelu2>(a, ws, s) : glu_launch<S, kActSilu>(a, ws, s);
 }
-hipError_t launch_glu(const GluArgs& a, int S, void*, hipStream_t s) {
-  if (S == 8) return glu_launch_s<8>(a, s);
-  if (S == 6) return glu_launch_s<6>(a, s);
-  if (S == 2) return glu_launch_s<2>(a, s);
-  return glu_launch_s<4>(a, s);
+hipError_t launch_glu(const GluArgs& a, int S, void* ws, hipStream_t s) {
+  if (S == 8) return glu_launch_s<8>(a, ws, s);
+  if (S == 6) return glu_launch_s<6>(a, ws, s);
+  if (S == 2) return glu_launch_s<2>(a, ws, s);
+  return glu_launch_s<4>(a, ws, s);
 }
 
 template <int kSave>

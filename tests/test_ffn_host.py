@@ -85,7 +85,7 @@ def test_norm_backward_refusals(L, kw, status, text):
 
 
 BOTH = [(dict(n=5), bl.BL_EUNSUPPORTED, "5:8"), (dict(k=200), bl.BL_ESHAPE, "k must"), (dict(n_out=192), bl.BL_ESHAPE, "multiple of 128"),
-        (dict(n_out=0), bl.BL_ESHAPE, "n_out"), (dict(act=2), bl.BL_EINVAL, "act"), (dict(tokens=-1), bl.BL_ESHAPE, "tokens"),
+        (dict(n_out=0), bl.BL_ESHAPE, "n_out"), (dict(k=1 << 22), bl.BL_ESHAPE, "2^22"), (dict(act=2), bl.BL_EINVAL, "act"), (dict(tokens=-1), bl.BL_ESHAPE, "tokens"),
         (dict(tokens=1 << 24), bl.BL_ESHAPE, "2^"), (dict(save_type=3), bl.BL_EINVAL, "save_type"), (dict(G=B), bl.BL_EINVAL, "G"),
         (dict(U=None), bl.BL_EINVAL, "U"), (dict(G_scales=None), bl.BL_EINVAL, "G_scales"), (dict(save_type=1), bl.BL_EINVAL, "belong"),
         (dict(xq=B), bl.BL_EINVAL, "xq"), (dict(x_scale=None), bl.BL_EINVAL, "x_scale"), (dict(gate=None), bl.BL_EINVAL, "gate"),
