@@ -193,7 +193,9 @@ __global__ __launch_bounds__(1024) void glu_small_kernel(GluArgs a) {
 // Both layers' codes are decoded once into int8 (a pass over the weights, some 6%
 // of the products' time at 4096 tokens), and an int8 product runs on tiles of
 // 128 outputs (256 rows: for each 64 outputs their gate rows, then their up
-// rows) x 64 kWN tokens.  A wavefront computes 64 outputs of both layers
+// rows) x 128 tokens, two workgroups on a CU, so that
+// one's outputs are written under the other's products (256 tokens, one workgroup:
+// 262 us in place of 231 at 6001 tokens, 2048 x 11008).  A wavefront computes 64 outputs of both layers
 // (128 rows) x 64 tokens, so a lane holds g and u of the same outputs and the
 // gating needs no exchange.  Tiles stream through kGluStages LDS stages of 64 k
 // filled by LDS DMA; a step's fragments are read from LDS while the matrix
@@ -261,38 +263,44 @@ __device__ __forceinline__ void glu_wait() {
 // LDS of the stages: separate objects, so that the compiler sees that reads of one
 // stage and DMA into the others touch different memory (namespace scope: a
 // __shared__ array inside a template made the host pass drop the kernel's stub)
-template <int kWN>
-struct GluTile {
-  static constexpr int kTokens = 64 * kWN;
-  static constexpr int kWaves = 2 * kWN;
-  static constexpr int kStageBytes = kGluABytes + kTokens * kGluK;
-  static constexpr int kAInstr = 16 / kWaves;  // DMA instructions of A per wavefront and step
-  static constexpr int kPerStep = kAInstr + 2;
-};
-__shared__ __attribute__((aligned(1024))) char g_glu2_st0[GluTile<2>::kStageBytes];
-__shared__ __attribute__((aligned(1024))) char g_glu2_st1[GluTile<2>::kStageBytes];
-__shared__ __attribute__((aligned(1024))) char g_glu2_st2[GluTile<2>::kStageBytes];
-__shared__ __attribute__((aligned(1024))) char g_glu4_st0[GluTile<4>::kStageBytes];
-__shared__ __attribute__((aligned(1024))) char g_glu4_st1[GluTile<4>::kStageBytes];
-__shared__ __attribute__((aligned(1024))) char g_glu4_st2[GluTile<4>::kStageBytes];
-template <int kWN, int P>
+constexpr int kGluTokens = 128;                              // of a tile
+constexpr int kGluStageBytes = kGluABytes + kGluTokens * kGluK;
+constexpr int kGluPerStep = 6;                               // DMA instructions of a wavefront and step: four of A, two of B
+__shared__ __attribute__((aligned(1024))) char g_glu_st0[kGluStageBytes];
+__shared__ __attribute__((aligned(1024))) char g_glu_st1[kGluStageBytes];
+__shared__ __attribute__((aligned(1024))) char g_glu_st2[kGluStageBytes];
+template <int P>
 __device__ __forceinline__ char* glu_stage() {
-  static_assert(kGluStages == 3 && (kWN == 2 || kWN == 4), "the stages above");
-  if constexpr (kWN == 2) return P == 0 ? g_glu2_st0 : P == 1 ? g_glu2_st1 : g_glu2_st2;
-  else return P == 0 ? g_glu4_st0 : P == 1 ? g_glu4_st1 : g_glu4_st2;
+  return P == 0 ? g_glu_st0 : P == 1 ? g_glu_st1 : g_glu_st2;
 }
 
 struct GluFrags {
   v4i a[8], b[4];
 };
 
-template <int kWN, int kAct>
-__global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs a, const char* __restrict__ codes, int row_tiles,
+// A wavefront's 32 tokens x 64 outputs of one result, kBytes a token, from LDS (rows
+// kBytes + 16 apart) to memory in whole 16-byte pieces: a token's outputs are one
+// or half a 128-byte line
+template <int kBytes>
+__device__ __forceinline__ void glu_flush(const glu_lds_char* rows, void* out, int64_t token, int64_t tokens, int64_t row_bytes,
+                                          int64_t col_bytes, int lane) {
+  constexpr int kPieces = kBytes / 16, kAtOnce = 64 / kPieces;
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int p = 0; p < 32 / kAtOnce; ++p) {
+    const int t = p * kAtOnce + lane / kPieces, c = 16 * (lane % kPieces);
+    const v4i v = *reinterpret_cast<const __attribute__((address_space(3))) v4i*>(rows + t * (kBytes + 16) + c);
+    if (token + t < tokens) st_global(reinterpret_cast<v4i*>(static_cast<char*>(out) + (token + t) * row_bytes + col_bytes + c), v);
+  }
+  asm volatile("" ::: "memory");
+}
+
+template <int kAct>
+__global__ __launch_bounds__(256, 2) void glu_gemm_kernel(GluArgs a, const char* __restrict__ codes, int row_tiles,
                                                        int token_tiles) {
-  typedef GluTile<kWN> T;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / kWN, wn = wave % kWN;
+  const int wm = wave >> 1, wn = wave & 1;
   const int l16 = lane & 15, lg = lane >> 4;
   // Workgroup (XCD x, slot) takes the slot-th tile of XCD x's contiguous eighth of
   // an order in groups of four token tiles, row tiles within a group: an XCD's
@@ -308,15 +316,15 @@ __global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs a, const char* __
     tt = 4 * g + r % gm;
     rt = r / gm;
   }
-  const int64_t t0 = (int64_t)tt * T::kTokens;
+  const int64_t t0 = (int64_t)tt * kGluTokens;
   const int nks = (int)(a.k / kGluK);
   // A: two pairs of 64 outputs, each nks pieces of 8 KiB, in order
   const __amdgpu_buffer_rsrc_t ar = glu_rsrc(codes + (int64_t)rt * 2 * nks * kPairBytes, (int64_t)2 * nks * kPairBytes);
   const __amdgpu_buffer_rsrc_t br = glu_rsrc(a.xq, a.tokens * a.k);
-  uint32_t a_off[T::kAInstr], b_off[2];
+  uint32_t a_off[4], b_off[2];
 #pragma unroll
-  for (int q = 0; q < T::kAInstr; ++q) {
-    const int at = T::kAInstr * wave + q;  // KiB of the stage's 16
+  for (int q = 0; q < 4; ++q) {
+    const int at = 4 * wave + q;  // KiB of the stage's 16
     a_off[q] = (uint32_t)((at >> 3) * nks * kPairBytes + (at & 7) * 1024 + 16 * lane);
   }
 #pragma unroll
@@ -329,11 +337,11 @@ __global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs a, const char* __
   // reads, so the waits can count them
   auto dma = [&](auto stage, int ks) {
     constexpr int P = decltype(stage)::value;
-    glu_lds_char* st = (glu_lds_char*)glu_stage<kWN, P>();
+    glu_lds_char* st = (glu_lds_char*)glu_stage<P>();
     const bool in = ks < nks;
 #pragma unroll
-    for (int q = 0; q < T::kAInstr; ++q)
-      glu_dma16(ar, st + 1024 * (T::kAInstr * wave + q), in ? a_off[q] + (uint32_t)(ks * kPairBytes) : kGluOOB);
+    for (int q = 0; q < 4; ++q)
+      glu_dma16(ar, st + 1024 * (4 * wave + q), in ? a_off[q] + (uint32_t)(ks * kPairBytes) : kGluOOB);
 #pragma unroll
     for (int q = 0; q < 2; ++q)
       glu_dma16(br, st + kGluABytes + 1024 * (2 * wave + q),
@@ -348,7 +356,7 @@ __global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs a, const char* __
   const uint32_t a_base = (uint32_t)(wm * 128 * kGluK) + frag, b_base = (uint32_t)(kGluABytes + wn * 64 * kGluK) + frag;
   auto read = [&](auto stage, GluFrags& f) {
     constexpr int P = decltype(stage)::value;
-    const glu_lds_char* st = (const glu_lds_char*)glu_stage<kWN, P>();
+    const glu_lds_char* st = (const glu_lds_char*)glu_stage<P>();
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       f.b[j] = *reinterpret_cast<const __attribute__((address_space(3))) v4i*>(st + b_base + j * 16 * kGluK);
@@ -361,7 +369,7 @@ __global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs a, const char* __
   // landed for all, is read into `next`.
   auto step = [&](auto stage, int ks, GluFrags& now, GluFrags& next) {
     constexpr int P = decltype(stage)::value;
-    glu_wait<T::kPerStep, true>();
+    glu_wait<kGluPerStep, true>();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -371,6 +379,21 @@ __global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs a, const char* __
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) c[i][j] = mfma_i8(now.a[i], now.b[j], c[i][j]);
+    // order of issue: the reads for the next step first, a product after each (left
+    // alone, the compiler put them last and every step waited for them), then
+    // the DMA, then the rest
+#pragma unroll
+    for (int r = 0; r < 12; ++r) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix instruction
+    }
+#pragma unroll
+    for (int r = 0; r < kGluPerStep; ++r) {
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // load
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 20 - kGluPerStep, 0);
+    __builtin_amdgcn_sched_barrier(0);
   };
   using S0 = std::integral_constant<int, 0>;
   using S1 = std::integral_constant<int, 1>;
@@ -379,7 +402,7 @@ __global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs a, const char* __
   dma(S0{}, 0);
   dma(S1{}, 1);
   dma(S2{}, 2);
-  glu_wait<2 * T::kPerStep>();
+  glu_wait<2 * kGluPerStep>();
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -400,66 +423,81 @@ __global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs a, const char* __
   if (ks + 4 < nks) step(S1{}, ks + 4, f0, f1);
   glu_wait<0, true>();  // no DMA outlives the workgroup, no read its stage
 
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+
   // Lane: outputs n0 + 16 i + 4 lg + q (i < 4: gate, i + 4: up) of token
-  // t0 + 64 wn + 16 j + l16
+  // t0 + 64 wn + 16 j + l16.  Results pass through LDS, 32 tokens at a time, in a part
+  // of the stages that is the wavefront's own, so that they are stored in whole lines.
+  constexpr int kPart = kGluStageBytes / 2;
+  static_assert(32 * (128 + 16) <= kPart, "32 rows of 64 bf16");
+  glu_lds_char* part = (glu_lds_char*)(wave < 2 ? g_glu_st0 : g_glu_st1) + (wave & 1) * kPart;
   const double gg = ld_global(a.gate_gamma), gu = ld_global(a.up_gamma);
   const int64_t n0 = (int64_t)rt * 128 + wm * 64;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t token = t0 + 64 * wn + 16 * j + l16;
-    const bool in = token < a.tokens;
-    const float s = in ? ld_global(a.x_scale + token) : 0.f;
-    const float sg = out_scale(gg, s), su = out_scale(gu, s);
-    float g[16], u[16];
+  for (int half = 0; half < 2; ++half) {
+    const int64_t first = t0 + 64 * wn + 32 * half;
+    float g[2][16], u[2][16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        g[4 * i + q] = out_value(c[i][j][q], sg);
-        u[4 * i + q] = out_value(c[i + 4][j][q], su);
-      }
-    const int64_t e = token * a.n_out + n0 + 4 * lg;
-    if (in) {
+    for (int jj = 0; jj < 2; ++jj) {
+      const int j = 2 * half + jj;
+      const int64_t token = first + 16 * jj + l16;
+      const float s = token < a.tokens ? ld_global(a.x_scale + token) : 0.f;
+      const float sg = out_scale(gg, s), su = out_scale(gu, s);
+      glu_lds_char* row = part + (16 * jj + l16) * (128 + 16) + 8 * lg;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float h[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) h[q] = act_value<kAct>(g[4 * i + q]) * u[4 * i + q];
-        st_global(reinterpret_cast<u32x2*>(a.H + e + 16 * i), u32x2{pair_bf16(h[0], h[1]), pair_bf16(h[2], h[3])});
+        for (int q = 0; q < 4; ++q) {
+          g[jj][4 * i + q] = out_value(c[i][j][q], sg);
+          u[jj][4 * i + q] = out_value(c[i + 4][j][q], su);
+          h[q] = act_value<kAct>(g[jj][4 * i + q]) * u[jj][4 * i + q];
+        }
+        *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(row + 32 * i) =
+            u32x2{pair_bf16(h[0], h[1]), pair_bf16(h[2], h[3])};
       }
     }
+    glu_flush<128>(part, a.H, first, a.tokens, 2 * a.n_out, 2 * n0, lane);
     if (a.save == kSaveNone) continue;
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-      const float* x = z ? u : g;
       void* out = z ? a.U : a.G;
-      if (a.save == kRowQ8) {
-        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = max_u(top, abs_bits(x[i]));
-        top = max_u(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-        top = max_u(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-        const CkptScale cs = ckpt_scale(top);
-        if (!in) continue;
+      for (int jj = 0; jj < 2; ++jj) {
+        const float* x = z ? u[jj] : g[jj];
+        const int64_t token = first + 16 * jj + l16;
+        if (a.save == kRowQ8) {
+          uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t w = 0;
+          for (int i = 0; i < 16; ++i) top = max_u(top, abs_bits(x[i]));
+          top = max_u(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+          top = max_u(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+          const CkptScale cs = ckpt_scale(top);
+          glu_lds_char* row = part + (16 * jj + l16) * (64 + 16) + 4 * lg;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) w |= ckpt_code(x[4 * i + q], cs.inv) << (8 * q);
-          st_global(reinterpret_cast<uint32_t*>(static_cast<int8_t*>(out) + e + 16 * i), w);
-        }
-        if (lg == 0) st_global((z ? a.Us : a.Gs) + (token * a.n_out + n0) / kCkptBlock, cs.scale);
-      } else if (in) {
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (a.save == kRowF32)
-            st_global(reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + e + 16 * i),
-                      f32x4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
-          else
-            st_global(reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + e + 16 * i),
-                      u32x2{pair_bf16(x[4 * i], x[4 * i + 1]), pair_bf16(x[4 * i + 2], x[4 * i + 3])});
+            for (int q = 0; q < 4; ++q) w |= ckpt_code(x[4 * i + q], cs.inv) << (8 * q);
+            *reinterpret_cast<__attribute__((address_space(3))) uint32_t*>(row + 16 * i) = w;
+          }
+          if (lg == 0 && token < a.tokens) st_global((z ? a.Us : a.Gs) + (token * a.n_out + n0) / kCkptBlock, cs.scale);
+        } else if (a.save == kRowBf16) {
+          glu_lds_char* row = part + (16 * jj + l16) * (128 + 16) + 8 * lg;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(row + 32 * i) =
+                u32x2{pair_bf16(x[4 * i], x[4 * i + 1]), pair_bf16(x[4 * i + 2], x[4 * i + 3])};
+        } else if (token < a.tokens) {  // binary32: a lane's four outputs are 16 bytes already
+          float* row = static_cast<float*>(out) + token * a.n_out + n0 + 4 * lg;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            st_global(reinterpret_cast<f32x4_t*>(row + 16 * i), f32x4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
         }
       }
+      if (a.save == kRowQ8) glu_flush<64>(part, out, first, a.tokens, a.n_out, n0, lane);
+      else if (a.save == kRowBf16) glu_flush<128>(part, out, first, a.tokens, 2 * a.n_out, 2 * n0, lane);
     }
   }
 }
@@ -579,14 +617,10 @@ static hipError_t glu_launch(const GluArgs& a, void* ws, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int row_tiles = (int)(a.n_out / 128);
-#ifndef GLU_WN
-#define GLU_WN 2
-#endif
-  typedef GluTile<GLU_WN> T;
-  const int token_tiles = (int)((a.tokens + T::kTokens - 1) / T::kTokens);
+  const int token_tiles = (int)((a.tokens + kGluTokens - 1) / kGluTokens);
   const int64_t tiles = (int64_t)row_tiles * token_tiles;
-  glu_gemm_kernel<GLU_WN, kAct><<<(unsigned)((tiles + 7) / 8 * 8), 64 * T::kWaves, 0, s>>>(a, static_cast<const char*>(ws),
-                                                                                          row_tiles, token_tiles);
+  glu_gemm_kernel<kAct><<<(unsigned)((tiles + 7) / 8 * 8), 256, 0, s>>>(a, static_cast<const char*>(ws), row_tiles,
+                                                                       token_tiles);
   return hipGetLastError();
 }
 template <int S>
