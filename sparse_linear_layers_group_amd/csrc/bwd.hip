@@ -486,11 +486,10 @@ __global__ __launch_bounds__(256, 2) void gemm_nt_bf16_kernel(NtProblem p0, NtPr
 // MFMA.)  The tiles stream through three LDS stages of 32 k filled by LDS
 // DMA (buffer loads that write LDS directly, 16 bytes per lane, 1 KiB per
 // wavefront instruction), issued two stages ahead.  In a stage each
-// operand row's 64 bytes hold four 16-byte pieces, piece c of row r at
-// position c ^ ((r >> 1) & 3): the eight lanes that read one 128-byte bank
-// line at a time (rows r..r+7 of one k piece) then hit distinct banks, and
-// a DMA instruction's 64 lanes still write 1 KiB in order (lane l writes
-// row l / 4, position l % 4, and loads the piece that belongs there).
+// operand row's 64 bytes hold four 16-byte pieces, placed by row64_place
+// so that fragment reads are free of bank conflicts, and a DMA instruction's
+// 64 lanes still write 1 KiB in order (lane l writes row l / 4, position
+// l % 4, and loads the piece that belongs there).
 constexpr int kBigM = 256;
 constexpr int kBigK = 32;                        // k per stage
 constexpr int kBigABytes = kBigM * kBigK * 2;    // 16 KiB
@@ -608,7 +607,7 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   // [32w, 32w + 32), 16 rows per instruction; lane l covers row l / 4 of
   // the instruction's 16 at position l % 4, i.e. logical piece kc / 8
   // below (the same for every instruction)
-  const int kc = 8 * ((lane & 3) ^ ((lane >> 3) & 3));
+  const int kc = 8 * row64_place(lane >> 2, lane & 3);
   uint32_t a_off[T::kAInstr], b_off[2];
 #pragma unroll
   for (int q = 0; q < T::kAInstr; ++q) {
@@ -643,7 +642,7 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
     for (int j = 0; j < 4; ++j) c[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   // fragment of MFMA row tile i / column tile j: row (or column) 16i + l16
   // of the wavefront's range, logical k piece lg
-  const uint32_t frag = (uint32_t)(l16 * 64 + 16 * (lg ^ ((l16 >> 1) & 3)));
+  const uint32_t frag = (uint32_t)(l16 * 64 + 16 * row64_place(l16, lg));
   const uint32_t a_base = (uint32_t)(wm * 128 * 64) + frag;
   const uint32_t b_base = (uint32_t)kBigABytes + (uint32_t)(wn * 64 * 64) + frag;
 
