@@ -528,6 +528,25 @@ __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | ((kLds ? 0 : 15) << 8));
 }
 
+// Order of issue within a step of 12 fragment reads, kLoads DMA instructions and 32
+// products: the reads first, a product after each, then the DMA, then the rest.
+// (Left alone, the compiler put the reads last, where the next step waits.)
+template <int kLoads>
+__device__ __forceinline__ void order_step() {
+#pragma unroll
+  for (int r = 0; r < 12; ++r) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix instruction
+  }
+#pragma unroll
+  for (int r = 0; r < kLoads; ++r) {
+    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // load
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, 20 - kLoads, 0);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // the three stages are separate arrays, each step's stage a compile-time
 // choice: the compiler then sees that a step's fragment reads and the DMA
 // in flight into the other stages touch different objects, and waits only
@@ -584,7 +603,7 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   float* __restrict__ C = pr.C;
   const double* __restrict__ alpha = pr.alpha;
   const int64_t lda = pr.lda, ldb = pr.ldb, ldc = pr.ldc, M = pr.M, N = pr.N, klen = pr.klen;
-  int64_t K = pr.K;
+  int K = (int)pr.K;
   {
     const int64_t tiles_m = (M + kBigM - 1) / kBigM, tiles_n = (N + T::N - 1) / T::N;
     constexpr int64_t kG = 4;  // row tiles per group of the tile order
@@ -594,9 +613,9 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
     n0 = (r / gm) * T::N;
   }
   const int64_t k0 = (int64_t)blockIdx.y * klen;
-  K = K - k0 < klen ? K - k0 : klen;
+  K = (int)(K - k0 < klen ? K - k0 : klen);
   C += (int64_t)blockIdx.y * M * ldc;
-  const int64_t nks = (K + kBigK - 1) / kBigK;
+  const int nks = (K + kBigK - 1) / kBigK;
 
   const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint16_t*>(A), (short)0, (int)(M * lda * 2), 0x00020000);
@@ -622,7 +641,7 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   // every step issues the same instructions per wavefront (past the last
   // step they read zeros into a stage nobody reads), so the waits below
   // can count them
-  auto dma = [&](auto stage, int64_t ks) {
+  auto dma = [&](auto stage, int ks) {
     constexpr int P = decltype(stage)::value;
     const bool kv = ks * kBigK + kc < K;
     const uint32_t ko = (uint32_t)(ks * kBigK * 2);
@@ -649,45 +668,68 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   typedef std::integral_constant<int, 0> S0;
   typedef std::integral_constant<int, 1> S1;
   typedef std::integral_constant<int, 2> S2;
-  // step ks reads stage ks % 3 and refills stage (ks + 2) % 3 (last read in
-  // step ks - 1) with step ks + 2
-  auto step = [&](auto stage, int64_t ks) {
+  // Step ks: its fragments were read in step ks - 1.  Once this wavefront's part of
+  // step ks + 1 has landed, its fragment reads have returned and everyone is
+  // here, stage ks % 3 is free and takes step ks + 3, and step ks + 1 is read from
+  // its stage beside the products.  (Reading a step's fragments in the step itself
+  // left the matrix units waiting for them: the three products of 4096 tokens,
+  // 2560 x 6912 took 497 us, now 476;
+  // the vendor library, 465.)
+  struct Frags {
+    v8bf a[8], b[4];
+  };
+  auto read = [&](auto stage, Frags& f) {
     constexpr int P = decltype(stage)::value;
-    // this wavefront's part of step ks has landed and its reads of step
-    // ks - 1 have returned, then everyone's has.  A plain barrier with
-    // compiler-only fences: __syncthreads()'s workgroup release would wait
-    // for every LDS DMA in flight (they write LDS), draining the steps ahead
+    const lds_char* st = (const lds_char*)big_stage<kWN, P>();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      f.b[j] = *reinterpret_cast<const __attribute__((address_space(3))) v8bf*>(st + b_base + j * 16 * 64);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      f.a[i] = *reinterpret_cast<const __attribute__((address_space(3))) v8bf*>(st + a_base + i * 16 * 64);
+  };
+  auto step = [&](auto stage, int ks, Frags& now, Frags& next) {
+    constexpr int P = decltype(stage)::value;
+    // A plain barrier with compiler-only fences: __syncthreads()'s workgroup
+    // release would wait for every LDS DMA in flight (they write LDS)
     wait_vmcnt<T::kPerStep, true>();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    dma(std::integral_constant<int, (P + 2) % 3>{}, ks + 2);
-    const lds_char* st = (const lds_char*)big_stage<kWN, P>();
-    v8bf a[8], b[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      b[j] = *reinterpret_cast<const __attribute__((address_space(3))) v8bf*>(st + b_base + j * 16 * 64);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      a[i] = *reinterpret_cast<const __attribute__((address_space(3))) v8bf*>(st + a_base + i * 16 * 64);
+    dma(std::integral_constant<int, P>{}, ks + 3);
+    read(std::integral_constant<int, (P + 1) % 3>{}, next);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        c[i][j] = mfma_bf16(a[i], b[j], c[i][j]);
+        c[i][j] = mfma_bf16(now.a[i], now.b[j], c[i][j]);
+    order_step<T::kPerStep>();
   };
 
+  Frags f0, f1;
   dma(S0{}, 0);
   dma(S1{}, 1);
-  int64_t ks = 0;
-  for (; ks + 2 < nks; ks += 3) {
-    step(S0{}, ks);
-    step(S1{}, ks + 1);
-    step(S2{}, ks + 2);
+  dma(S2{}, 2);
+  wait_vmcnt<2 * T::kPerStep>();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  read(S0{}, f0);
+  int ks = 0;
+  for (; ks + 5 < nks; ks += 6) {  // three stages x two fragment sets
+    step(S0{}, ks, f0, f1);
+    step(S1{}, ks + 1, f1, f0);
+    step(S2{}, ks + 2, f0, f1);
+    step(S0{}, ks + 3, f1, f0);
+    step(S1{}, ks + 4, f0, f1);
+    step(S2{}, ks + 5, f1, f0);
   }
-  if (ks < nks) step(S0{}, ks);
-  if (ks + 1 < nks) step(S1{}, ks + 1);
-  wait_vmcnt<0>();  // no LDS DMA outlives the workgroup
+  if (ks < nks) step(S0{}, ks, f0, f1);
+  if (ks + 1 < nks) step(S1{}, ks + 1, f1, f0);
+  if (ks + 2 < nks) step(S2{}, ks + 2, f0, f1);
+  if (ks + 3 < nks) step(S0{}, ks + 3, f1, f0);
+  if (ks + 4 < nks) step(S1{}, ks + 4, f0, f1);
+  wait_vmcnt<0, true>();  // no LDS DMA outlives the workgroup
 
   // lane holds C[m0 + 128wm + 16i + 4lg + q][n0 + 64wn + 16j + l16]
   const double g = alpha ? *alpha : 1.0;
