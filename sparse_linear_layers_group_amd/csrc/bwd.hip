@@ -279,7 +279,7 @@ struct NtProblem {
   float* C;
   const double* alpha;
   int64_t lda, ldb, ldc, M, N, K, klen;
-  // gated epilogue (256-row kernel only): with G set, C is not written;
+  // gated epilogue (256-row kernel only; N a multiple of 4, as for every output of it): with G set, C is not written;
   // the squared-ReLU gating backward of C (as relu2_gate_bwd_kernel
   // computes it from a stored C) goes to dG and dU instead, G, U, dG, dU
   // laid out like C
@@ -702,7 +702,7 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        c[i][j] = mfma_bf16(now.a[i], now.b[j], c[i][j]);
+        c[i][j] = mfma_bf16(now.b[j], now.a[i], c[i][j]);
     order_step<T::kPerStep>();
   };
 
@@ -731,127 +731,74 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   if (ks + 4 < nks) step(S1{}, ks + 4, f0, f1);
   wait_vmcnt<0, true>();  // no LDS DMA outlives the workgroup
 
-  // lane holds C[m0 + 128wm + 16i + 4lg + q][n0 + 64wn + 16j + l16]
+  // B's fragment is the instruction's first operand, so a lane holds four neighbouring
+  // columns: C[m0 + 128wm + 16i + l16][n0 + 64wn + 16j + 4lg + q], in q (N is a multiple
+  // of 4: they are in range together)
   const double g = alpha ? *alpha : 1.0;
   const bool scaled = alpha != nullptr;
+  const int64_t m = m0 + wm * 128 + l16, n = n0 + wn * 64 + 4 * lg;
+  const auto value = [&](const v4f& x) {
+    v4f y = x;
+    if (scaled)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) y[q] = (float)((double)x[q] * g);
+    return y;
+  };
   if (pr.G) {
     const float* __restrict__ G = pr.G;
     const float* __restrict__ U = pr.U;
     uint16_t* __restrict__ dG = pr.dG;
     uint16_t* __restrict__ dU = pr.dU;
-    // software-pipelined over the MFMA row tiles: row tile i + 1's 32
-    // loads issue before row tile i's stores (stores could alias them as
-    // far as the compiler knows, so a load written after a store waits)
-    float gv[2][4][4], uv[2][4][4];
-    auto load = [&](int i, float (&gb)[4][4], float (&ub)[4][4]) {
+    // software-pipelined over the MFMA row tiles: row tile i + 1's loads issue
+    // before row tile i's stores (stores could alias them as far as the compiler
+    // knows, so a load written after a store waits)
+    v4f gv[2][4], uv[2][4];
+    auto load = [&](int i, v4f (&gb)[4], v4f (&ub)[4]) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t m = m0 + wm * 128 + i * 16 + 4 * lg + q;
-          const int64_t n = n0 + wn * 64 + j * 16 + l16;
-          const bool in = m < M && n < N;
-          const int64_t e = in ? m * ldc + n : 0;
-          gb[q][j] = in ? ld_global(G + e) : 0.f;
-          ub[q][j] = in ? ld_global(U + e) : 0.f;
+      for (int j = 0; j < 4; ++j) {
+        const bool in = m + 16 * i < M && n + 16 * j < N;
+        const int64_t e = in ? (m + 16 * i) * ldc + n + 16 * j : 0;
+        gb[j] = ub[j] = v4f{0.f, 0.f, 0.f, 0.f};
+        if (in) {
+          gb[j] = ld_global(reinterpret_cast<const v4f*>(G + e));
+          ub[j] = ld_global(reinterpret_cast<const v4f*>(U + e));
         }
+      }
     };
     load(0, gv[0], uv[0]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i + 1 < 8) load(i + 1, gv[(i + 1) & 1], uv[(i + 1) & 1]);
-      // lanes l16 and l16 ^ 1 hold neighbouring columns of the same four
-      // rows: after one exchange the even lane stores rows 0 and 2 and the
-      // odd lane rows 1 and 3, each as a 4-byte pair of columns (k is a
-      // multiple of 128, so both columns of a pair are in range together)
-      const bool odd = (l16 & 1) != 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t hu[4], hg[4];
+        const v4f dh = value(c[i][j]);
+        v4f hu, hg;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float dh = scaled ? (float)((double)c[i][j][q] * g) : c[i][j][q];
-          const float gq = gv[i & 1][q][j];
+          const float gq = gv[i & 1][j][q];
           const float r = gq > 0.f ? gq : 0.f;
           const float r2 = r * r;
-          const float du = dh * uv[i & 1][q][j];
-          hu[q] = f32_to_bf16_rne(dh * r2);
-          hg[q] = f32_to_bf16_rne(du * (2.f * r));
+          const float du = dh[q] * uv[i & 1][j][q];
+          hu[q] = dh[q] * r2;
+          hg[q] = du * (2.f * r);
         }
-        const uint32_t pu0 = hu[0] | hu[1] << 16, pu1 = hu[2] | hu[3] << 16;
-        const uint32_t pg0 = hg[0] | hg[1] << 16, pg1 = hg[2] | hg[3] << 16;
-        const uint32_t xu0 = lane_xor1(pu0), xu1 = lane_xor1(pu1);
-        const uint32_t xg0 = lane_xor1(pg0), xg1 = lane_xor1(pg1);
-        const int64_t col = n0 + wn * 64 + j * 16 + (l16 & ~1);
-        if (col >= N) continue;
-        const int64_t ra = m0 + wm * 128 + i * 16 + 4 * lg + (odd ? 1 : 0);
-        if (ra < M) {
-          const int64_t e = ra * ldc + col;
-          st_global(reinterpret_cast<uint32_t*>(dU + e),
-                    odd ? (xu0 >> 16) | (pu0 & 0xffff0000u) : (pu0 & 0xffffu) | (xu0 << 16));
-          st_global(reinterpret_cast<uint32_t*>(dG + e),
-                    odd ? (xg0 >> 16) | (pg0 & 0xffff0000u) : (pg0 & 0xffffu) | (xg0 << 16));
-        }
-        if (ra + 2 < M) {
-          const int64_t e = (ra + 2) * ldc + col;
-          st_global(reinterpret_cast<uint32_t*>(dU + e),
-                    odd ? (xu1 >> 16) | (pu1 & 0xffff0000u) : (pu1 & 0xffffu) | (xu1 << 16));
-          st_global(reinterpret_cast<uint32_t*>(dG + e),
-                    odd ? (xg1 >> 16) | (pg1 & 0xffff0000u) : (pg1 & 0xffffu) | (xg1 << 16));
-        }
+        if (m + 16 * i >= M || n + 16 * j >= N) continue;
+        const int64_t e = (m + 16 * i) * ldc + n + 16 * j;
+        st_global(reinterpret_cast<u32x2*>(dU + e), bf16x4(hu));
+        st_global(reinterpret_cast<u32x2*>(dG + e), bf16x4(hg));
       }
     }
-    return;
-  }
-  if (pr.Cb) {
-    uint16_t* __restrict__ Cb = pr.Cb;
-    // lanes l16 and l16 ^ 1 share their columns' pairs as in the gated epilogue
-    const bool odd = (l16 & 1) != 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t h[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) h[q] = f32_to_bf16_rne(scaled ? (float)((double)c[i][j][q] * g) : c[i][j][q]);
-        const uint32_t p0 = h[0] | h[1] << 16, p1 = h[2] | h[3] << 16;
-        const uint32_t x0 = lane_xor1(p0), x1 = lane_xor1(p1);
-        const int64_t col = n0 + wn * 64 + j * 16 + (l16 & ~1);
-        if (col >= N) continue;
-        const int64_t ra = m0 + wm * 128 + i * 16 + 4 * lg + (odd ? 1 : 0);
-        if (ra < M)
-          st_stream(reinterpret_cast<uint32_t*>(Cb + ra * ldc + col),
-                    odd ? (x0 >> 16) | (p0 & 0xffff0000u) : (p0 & 0xffffu) | (x0 << 16));
-        if (ra + 2 < M)
-          st_stream(reinterpret_cast<uint32_t*>(Cb + (ra + 2) * ldc + col),
-                    odd ? (x1 >> 16) | (p1 & 0xffff0000u) : (p1 & 0xffffu) | (x1 << 16));
-      }
-    return;
-  }
-  if (m0 + kBigM <= M && n0 + T::N <= N) {
-    float* cb = C + (m0 + wm * 128 + 4 * lg) * ldc + n0 + wn * 64 + l16;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float* cr = cb + (int64_t)(i * 16 + q) * ldc;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          st_stream(cr + j * 16, scaled ? (float)((double)c[i][j][q] * g) : c[i][j][q]);
-      }
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t m = m0 + wm * 128 + i * 16 + 4 * lg + q;
-      if (m >= M) continue;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t n = n0 + wn * 64 + j * 16 + l16;
-        if (n < N) C[m * ldc + n] = scaled ? (float)((double)c[i][j][q] * g) : c[i][j][q];
-      }
+    for (int j = 0; j < 4; ++j) {
+      if (m + 16 * i >= M || n + 16 * j >= N) continue;
+      const int64_t e = (m + 16 * i) * ldc + n + 16 * j;
+      const v4f y = value(c[i][j]);
+      if (pr.Cb) st_stream(reinterpret_cast<u32x2*>(pr.Cb + e), bf16x4(y));
+      else st_stream(reinterpret_cast<v4f*>(C + e), y);
     }
 }
 

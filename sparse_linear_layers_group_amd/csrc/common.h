@@ -77,8 +77,8 @@ typedef unsigned int u32x3 __attribute__((ext_vector_type(3)));
 // four binary32 outputs as bf16 (nearest, ties to even), packed for one
 // 8-byte store
 __device__ __forceinline__ u32x2 bf16x4(v4f y) {
-  return u32x2{(uint32_t)f32_to_bf16_rne(y[0]) | ((uint32_t)f32_to_bf16_rne(y[1]) << 16),
-               (uint32_t)f32_to_bf16_rne(y[2]) | ((uint32_t)f32_to_bf16_rne(y[3]) << 16)};
+  typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(u32x2, __builtin_convertvector(y, b4));
 }
 
 // Place of 16-byte piece `piece` (0..3) of row `row` in an LDS tile of 64-byte rows
