@@ -200,7 +200,7 @@ __global__ __launch_bounds__(1024) void glu_small_kernel(GluArgs a) {
 // one's outputs are written under the other's products (256 tokens, one workgroup:
 // 262 us in place of 231 at 6001 tokens, 2048 x 11008).  A wavefront computes 64 outputs of both layers
 // (128 rows) x 64 tokens, so a lane holds g and u of the same outputs and the
-// gating needs no exchange.  Tiles stream through kGluStages LDS stages of 64 k
+// gating needs no exchange.  Tiles stream through three LDS stages of 64 k
 // filled by LDS DMA; a step's fragments are read from LDS while the matrix
 // instructions of the step before run, so a stage is refilled as soon as its
 // fragments are in registers.
@@ -213,7 +213,6 @@ constexpr int kGluRows = 256;                 // rows of a tile: 128 outputs
 constexpr int kGluK = 64;                     // k of a stage
 constexpr int kGluABytes = kGluRows * kGluK;  // 16 KiB
 constexpr int kPairBytes = 128 * kGluK;       // decoded codes of 64 outputs, 64 k
-constexpr int kGluStages = 3;
 
 // One packed superblock (64 rows x 128 k) per wavefront: lane c = r + 16 q holds, as
 // the operand (i, h), the codes of row 16 i + r at k = 64 h + 16 q .. + 15, one piece.
