@@ -74,6 +74,7 @@ struct PrepTask {
   uint16_t* out;
   int64_t rows, cols, pitch;
   int32_t kind, jobs;
+  int32_t tiled = 0;  // codes and x_q: out in tiles, pitch its depth
 };
 constexpr int kMaxPrep = 16;
 struct PrepSet {
@@ -124,7 +125,7 @@ __device__ __forceinline__ void prep_dys_tile(const uint16_t* __restrict__ dY,
 // xbT[c][t] = bf16(x_q[t][c]) (exact) for t < tokens, 0 up to tp
 __device__ __forceinline__ void prep_xq_tile(const int8_t* __restrict__ xq, int64_t tokens, int64_t k,
                                              int64_t tp, uint16_t* __restrict__ out, int64_t t0,
-                                             int64_t c0, uint16_t* tile, int tid) {
+                                             int64_t c0, uint16_t* tile, int tid, bool tiled) {
   {
     const int t = tid >> 2, c16 = 16 * (tid & 3);
     const int64_t tt = t0 + t;
@@ -145,7 +146,7 @@ __device__ __forceinline__ void prep_xq_tile(const int8_t* __restrict__ xq, int6
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       o[e] = (uint32_t)tile[(t8 + 2 * e) * kTP + c] | ((uint32_t)tile[(t8 + 2 * e + 1) * kTP + c] << 16);
-    st_global(reinterpret_cast<u32x4*>(out + (c0 + c) * tp + t0 + t8), u32x4{o[0], o[1], o[2], o[3]});
+    st_global(reinterpret_cast<u32x4*>(out + operand_at(c0 + c, t0 + t8, tp, tiled)), u32x4{o[0], o[1], o[2], o[3]});
   }
 }
 
@@ -205,7 +206,7 @@ __device__ __forceinline__ void transpose8_bf16(const uint32_t (&d)[4], uint32_t
 template <int S>
 __device__ __forceinline__ void prep_codes_sb(const uint32_t* __restrict__ packed, int64_t sb,
                                               int64_t nkb, int64_t np, uint16_t* __restrict__ out,
-                                              const u32x2* lut, int lane) {
+                                              const u32x2* lut, int lane, bool tiled) {
   constexpr int kW = block_bytes(S) / 4;
   const int64_t strip = sb / nkb, kb = sb - strip * nkb;
   uint32_t w[kW + 1];
@@ -213,13 +214,13 @@ __device__ __forceinline__ void prep_codes_sb(const uint32_t* __restrict__ packe
 #pragma unroll
   for (int i = 0; i < kW; ++i) w[i] = ld_global(src + i);
   w[kW] = 0;
-  uint16_t* dst = out + (kb * kBlockK + (lane & 7)) * np + strip * kStripRows + (lane & 8);
+  const int64_t row0 = kb * kBlockK + (lane & 7), col0 = strip * kStripRows + (lane & 8);
   auto lk = [&](uint32_t key, int half) { return lut[key * 2 + half]; };
   auto emit = [&](int f, u32x2 lo, u32x2 hi) {
     const uint32_t d[4] = {lo.x, lo.y, hi.x, hi.y};
     uint32_t o[4];
     transpose8_bf16(d, o, lane);
-    st_global(reinterpret_cast<u32x4*>(dst + (int64_t)(8 * field_group(lane, f)) * np + 16 * (f >> 2)),
+    st_global(reinterpret_cast<u32x4*>(out + operand_at(row0 + 8 * field_group(lane, f), col0 + 16 * (f >> 2), np, tiled)),
               u32x4{o[0], o[1], o[2], o[3]});
   };
   decode_groups<S, 0, 16>(w, lk, emit);
@@ -239,7 +240,7 @@ __global__ __launch_bounds__(256) void prep_group_kernel(PrepSet set) {
     const int64_t sb = 4 * (int64_t)job + (tid >> 6);
     if (sb < tk.rows * tk.cols)
       prep_codes_sb<S>(reinterpret_cast<const uint32_t*>(tk.src), sb, tk.rows, tk.pitch, tk.out, lut,
-                       tid & 63);
+                       tid & 63, tk.tiled);
     return;
   }
   const int64_t bx = tk.pitch / 64, t0 = 64 * (job % bx), c0 = 64 * (job / bx);
@@ -248,7 +249,7 @@ __global__ __launch_bounds__(256) void prep_group_kernel(PrepSet set) {
                   t0, c0, tile, tid);
   else
     prep_xq_tile(reinterpret_cast<const int8_t*>(tk.src), tk.rows, tk.cols, tk.pitch, tk.out, t0, c0,
-                 tile, tid);
+                 tile, tid, tk.tiled);
 }
 
 // ------------------------------------------------------------- product
@@ -290,6 +291,8 @@ struct NtProblem {
   // with Cb set, C is not written but rounded to bf16 into Cb, laid out like C
   // (256-row kernel and split sums only; N even)
   uint16_t* Cb = nullptr;
+  // A and B in tiles of depth lda = ldb = K (256-row kernel only)
+  bool tiled = false;
 };
 
 // the products of one launch of the 256-row kernel (its tiles dealt over
@@ -617,10 +620,11 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   C += (int64_t)blockIdx.y * M * ldc;
   const int nks = (K + kBigK - 1) / kBigK;
 
+  const int64_t ra = pr.tiled ? (M + 15) / 16 * 16 : M, rb = pr.tiled ? (N + 15) / 16 * 16 : N;
   const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint16_t*>(A), (short)0, (int)(M * lda * 2), 0x00020000);
+      const_cast<uint16_t*>(A), (short)0, (int)(ra * lda * 2), 0x00020000);
   const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint16_t*>(B), (short)0, (int)(N * ldb * 2), 0x00020000);
+      const_cast<uint16_t*>(B), (short)0, (int)(rb * ldb * 2), 0x00020000);
   constexpr uint32_t kOOB = 0x80000000u;
   // DMA: wavefront w fills A rows [16 kAInstr w, +16 kAInstr) and B rows
   // [32w, 32w + 32), 16 rows per instruction; lane l covers row l / 4 of
@@ -631,20 +635,21 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
 #pragma unroll
   for (int q = 0; q < T::kAInstr; ++q) {
     const int64_t row = 16 * (T::kAInstr * wave + q) + (lane >> 2);
-    a_off[q] = m0 + row < M ? (uint32_t)(((m0 + row) * lda + k0 + kc) * 2) : kOOB;
+    a_off[q] = m0 + row < M ? (uint32_t)((pr.tiled ? (m0 + row - (lane >> 2)) * lda + 8 * lane : (m0 + row) * lda + k0 + kc) * 2) : kOOB;
   }
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int64_t row = 32 * wave + 16 * q + (lane >> 2);
-    b_off[q] = n0 + row < N ? (uint32_t)(((n0 + row) * ldb + k0 + kc) * 2) : kOOB;
+    b_off[q] = n0 + row < N ? (uint32_t)((pr.tiled ? (n0 + row - (lane >> 2)) * ldb + 8 * lane : (n0 + row) * ldb + k0 + kc) * 2) : kOOB;
   }
+  const uint32_t step_bytes = pr.tiled ? 1024 : kBigK * 2;  // from a step's piece of a row (block) to the next
   // every step issues the same instructions per wavefront (past the last
   // step they read zeros into a stage nobody reads), so the waits below
   // can count them
   auto dma = [&](auto stage, int ks) {
     constexpr int P = decltype(stage)::value;
     const bool kv = ks * kBigK + kc < K;
-    const uint32_t ko = (uint32_t)(ks * kBigK * 2);
+    const uint32_t ko = (uint32_t)ks * step_bytes;
     lds_char* st = (lds_char*)big_stage<kWN, P>();
 #pragma unroll
     for (int q = 0; q < T::kAInstr; ++q)
@@ -672,9 +677,8 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   // step ks + 1 has landed, its fragment reads have returned and everyone is
   // here, stage ks % 3 is free and takes step ks + 3, and step ks + 1 is read from
   // its stage beside the products.  (Reading a step's fragments in the step itself
-  // left the matrix units waiting for them: the three products of 4096 tokens,
-  // 2560 x 6912 took 497 us, now 476;
-  // the vendor library, 465.)
+  // left the matrix units waiting for them: the three products of the gated
+  // feed-forward's backward, 4096 tokens, 2560 x 6912, from rows: 493 us, then 476.)
   struct Frags {
     v8bf a[8], b[4];
   };
@@ -1091,24 +1095,27 @@ hipError_t launch_glu_products(const GluBwdArgs& a, int S, hipStream_t s) {
   NtProblem probs[3];
   int np = 0;
   const bool b16 = a.grad_type == BL_TYPE_BF16;
-  const auto add = [&](NtProblem p, void* out) {
+  // split products run on the 128-row kernel, from rows
+  const bool tx = l.dx_tiled, tw = l.dw_tiled;
+  const auto add = [&](NtProblem p, void* out, bool tiled) {
+    p.tiled = tiled;
     p.C = b16 ? nullptr : static_cast<float*>(out);
     p.Cb = b16 ? static_cast<uint16_t*>(out) : nullptr;
     probs[np++] = p;
   };
   if (a.dX) {
     const int32_t jobs = (int32_t)((strips * nkb + 3) / 4);
-    L.t.push_back(PrepTask{a.gate, nullptr, codes_t, nkb, strips, n2, kPrepCodes, jobs});
-    L.t.push_back(PrepTask{a.up, nullptr, codes_t + a.n_out, nkb, strips, n2, kPrepCodes, jobs});
+    L.t.push_back(PrepTask{a.gate, nullptr, codes_t, nkb, strips, n2, kPrepCodes, jobs, tx});
+    L.t.push_back(PrepTask{a.up, nullptr, codes_t + (tx ? 16 : 1) * a.n_out, nkb, strips, n2, kPrepCodes, jobs, tx});
     add(NtProblem{reinterpret_cast<const uint16_t*>(a.ws + l.dgu), codes_t, nullptr, nullptr, n2, n2, a.k, a.tokens,
-                  a.k, n2, n2}, a.dX);
+                  a.k, n2, n2}, a.dX, tx);
   }
   if (a.dWg) {
-    L.t.push_back(PrepTask{a.xq, nullptr, xq_t, a.tokens, a.k, tp, kPrepXq, (int32_t)((tp / 64) * (a.k / 64))});
+    L.t.push_back(PrepTask{a.xq, nullptr, xq_t, a.tokens, a.k, tp, kPrepXq, (int32_t)((tp / 64) * (a.k / 64)), tw});
     add(NtProblem{reinterpret_cast<const uint16_t*>(a.ws + l.dgs_t), xq_t, nullptr, nullptr, tp, tp, a.k, a.n_out,
-                  a.k, tp, tp}, a.dWg);
+                  a.k, tp, tp}, a.dWg, tw);
     add(NtProblem{reinterpret_cast<const uint16_t*>(a.ws + l.dus_t), xq_t, nullptr, nullptr, tp, tp, a.k, a.n_out,
-                  a.k, tp, tp}, a.dWu);
+                  a.k, tp, tp}, a.dWu, tw);
   }
   hipError_t e = L.launch(S, s);
   if (e != hipSuccess) return e;

@@ -94,6 +94,23 @@ __host__ __device__ constexpr int row64_place(int row, int piece) {
   return piece ^ ((((x ^ (x >> 1)) & 1) << 1) | (x >> 1));
 }
 
+// Operands that a call prepares for itself alone may lie in tiles: blocks of 16 rows
+// x 32 contraction indices, 1 KiB each, all blocks of 16 rows one after another and
+// the pieces in the order LDS wants them (row64_place).  A DMA instruction of the
+// 256-row kernel then reads 1 KiB in order; from rows it reads half a 128-byte line
+// of each of 16, and every line crosses from L2 to the CU twice: that bound
+// the products (three of 4096 tokens, 2560 x 6912: 471 us from rows, 397 from tiles,
+// 1.46 PFLOP/s; the vendor library 465).
+// Element (row, c) of a tiled operand of depth `depth` (a multiple of 32); c is the
+// first of a 16-byte piece.
+__device__ __forceinline__ int64_t tiled_at(int64_t row, int64_t c, int64_t depth) {
+  return (row >> 4) * 16 * depth + (c >> 5) * 512 + (row & 15) * 32 + 8 * row64_place((int)row & 15, (int)(c >> 3) & 3);
+}
+// the same for one that lies in rows, `pitch` apart
+__device__ __forceinline__ int64_t operand_at(int64_t row, int64_t c, int64_t pitch, bool tiled) {
+  return tiled ? tiled_at(row, c, pitch) : row * pitch + c;
+}
+
 // explicit global-address-space accesses: pointers that arrive through
 // memory (e.g. from a plan) would otherwise become flat accesses, which also
 // count against the LDS counter and force extra waits

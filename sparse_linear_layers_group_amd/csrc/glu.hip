@@ -562,11 +562,11 @@ __global__ __launch_bounds__(256) void glu_gate_bwd_kernel(GluBwdArgs a, GluBwdL
           y[i] = dg[i] * gg;
           z[i] = du[i] * gu;
         }
-        uint16_t* row = reinterpret_cast<uint16_t*>(a.ws + l.dgu) + token * 2 * a.n_out + col;
+        uint16_t* dgu = reinterpret_cast<uint16_t*>(a.ws + l.dgu);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          store_row8(row, kRowBf16, 8 * h, y + 8 * h);
-          store_row8(row, kRowBf16, a.n_out + 8 * h, z + 8 * h);
+          store_row8(dgu, kRowBf16, operand_at(token, col + 8 * h, 2 * a.n_out, l.dx_tiled), y + 8 * h);
+          store_row8(dgu, kRowBf16, operand_at(token, a.n_out + col + 8 * h, 2 * a.n_out, l.dx_tiled), z + 8 * h);
         }
       }
     }
@@ -587,7 +587,7 @@ __global__ __launch_bounds__(256) void glu_gate_bwd_kernel(GluBwdArgs a, GluBwdL
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       o[e] = (uint32_t)tile[(t8 + 2 * e) * kGatePitch + r] | ((uint32_t)tile[(t8 + 2 * e + 1) * kGatePitch + r] << 16);
-    st_global(reinterpret_cast<u32x4*>(out + (c0 + r) * tp + t0 + t8), u32x4{o[0], o[1], o[2], o[3]});
+    st_global(reinterpret_cast<u32x4*>(out + operand_at(c0 + r, t0 + t8, tp, l.dw_tiled)), u32x4{o[0], o[1], o[2], o[3]});
   }
 }
 
