@@ -216,36 +216,64 @@ constexpr int kPairBytes = 128 * kGluK;       // decoded codes of 64 outputs, 64
 
 // One packed superblock (64 rows x 128 k) per wavefront: lane c = r + 16 q holds, as
 // the operand (i, h), the codes of row 16 i + r at k = 64 h + 16 q .. + 15, one piece.
+// The activations are laid out likewise: 16 tokens x 64 k a KiB, all of 16 tokens one
+// after another (in rows every DMA instruction would read half a line of each of 16
+// tokens, see tiled_at: the product took 137 us in place of 125 at 4096 tokens,
+// 2560 x 6912, 8-bit G and U kept).
+// Bound by memory; a wavefront's first chunk is on its way while the tables are
+// filled, and sixteen wavefronts share one set of them (four, loading after the
+// fill: 15.4 us at 391 tokens, 1536 x 8960 4:8, now 12.8).
+constexpr int kDecodeThreads = 1024;
 template <int S>
-__global__ __launch_bounds__(256) void glu_decode_kernel(const char* __restrict__ gate, const char* __restrict__ up,
-                                                        int64_t superblocks, int nkb, char* __restrict__ out) {
+__global__ __launch_bounds__(kDecodeThreads) void glu_decode_kernel(const char* __restrict__ gate,
+                                                                   const char* __restrict__ up, int64_t superblocks,
+                                                                   int nkb, char* __restrict__ out,
+                                                                   const int8_t* __restrict__ xq, int64_t tokens,
+                                                                   int64_t x_jobs, char* __restrict__ x_out) {
   __shared__ __attribute__((aligned(16))) uint32_t lut[512 * kSmallCopies];
+  constexpr int kBytes = block_bytes(S), kRuns = 512 * kSmallCopies / 4 / kDecodeThreads;
   const int tid = threadIdx.x, lane = tid & 63;
-#pragma unroll
-  for (int r = 0; r < 512 * kSmallCopies / 4 / 256; ++r) {
-    const uint32_t v = ld_global(&kHalfCodeTable.v[(tid + 256 * r) / (kSmallCopies / 4)]);
-    reinterpret_cast<u32x4*>(lut)[tid + 256 * r] = u32x4{v, v, v, v};
-  }
-  const uint32_t* lut_lane = lut + (lane & (kSmallCopies - 1));
-  __syncthreads();
-  // 2 superblocks: gate's of all strips, then up's
-  for (int64_t j = (int64_t)blockIdx.x * 4 + (tid >> 6); j < 2 * superblocks; j += (int64_t)gridDim.x * 4) {
-    const int side = j >= superblocks;
-    const int64_t sb = side ? j - superblocks : j, strip = sb / nkb, kb = sb - strip * nkb;
-    constexpr int kBytes = block_bytes(S);
-    uint32_t w[kBytes / 4];
-    const uint32_t* src = reinterpret_cast<const uint32_t*>((side ? up : gate) + (sb * kStripRows + lane) * kBytes);
+  const int64_t stride = (int64_t)gridDim.x * (kDecodeThreads / 64);
+  // jobs of a wavefront: superblocks, gate's of all strips, then up's; then 16 tokens x 128 k
+  int64_t j = (int64_t)blockIdx.x * (kDecodeThreads / 64) + (tid >> 6);
+  uint32_t w[kBytes / 4], tv[kRuns];
+  const auto load = [&](int64_t job) {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+        (job >= superblocks ? up + (job - superblocks) * kStripRows * kBytes : gate + job * kStripRows * kBytes) + lane * kBytes);
 #pragma unroll
     for (int i = 0; i < kBytes / 4; ++i) w[i] = ld_global(src + i);
+  };
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int r = 0; r < kRuns; ++r) tv[r] = ld_global(&kHalfCodeTable.v[(tid + kDecodeThreads * r) / (kSmallCopies / 4)]);
+  if (j < 2 * superblocks) load(j);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v4i c = chunk_operand<S>(w, 2 * i + h, lut_lane);
-        const int row = 64 * side + 16 * i + (lane & 15);
-        char* dst = out + (strip * (2 * nkb) + 2 * kb + h) * kPairBytes + row * kGluK + 16 * row64_place(row, lane >> 4);
-        st_global(reinterpret_cast<v4i*>(dst), c);
-      }
+  for (int r = 0; r < kRuns; ++r)
+    reinterpret_cast<u32x4*>(lut)[tid + kDecodeThreads * r] = u32x4{tv[r], tv[r], tv[r], tv[r]};
+  const uint32_t* lut_lane = lut + (lane & (kSmallCopies - 1));
+  __syncthreads();
+  for (; j < 2 * superblocks; j += stride) {
+    const int side = j >= superblocks;
+    const int64_t sb = side ? j - superblocks : j, strip = sb / nkb, kb = sb - strip * nkb;
+    v4i c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = chunk_operand<S>(w, i, lut_lane);
+    if (j + stride < 2 * superblocks) load(j + stride);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // operand 2 (row tile) + (k half)
+      const int row = 64 * side + 16 * (i >> 1) + (lane & 15);
+      char* dst = out + (strip * (2 * nkb) + 2 * kb + (i & 1)) * kPairBytes + row * kGluK + 16 * row64_place(row, lane >> 4);
+      st_global(reinterpret_cast<v4i*>(dst), c[i]);
+    }
+  }
+  for (; j < 2 * superblocks + x_jobs; j += stride) {
+    const int64_t x = j - 2 * superblocks, tb = x / nkb, kb = x - tb * nkb;
+    const int row = lane >> 2;
+    const int64_t token = 16 * tb + row < tokens ? 16 * tb + row : tokens - 1;  // rows past the last are not used
+    const v4i* src = reinterpret_cast<const v4i*>(xq + token * nkb * kBlockK + kb * kBlockK) + row64_place(row, lane & 3);
+    v4i* dst = reinterpret_cast<v4i*>(x_out + (tb * nkb + kb) * 2048) + lane;
+    const v4i v0 = ld_global(src), v1 = ld_global(src + 4);
+    st_global(dst, v0);
+    st_global(dst + 64, v1);
   }
 }
 
@@ -296,8 +324,8 @@ __device__ __forceinline__ void glu_flush(const glu_lds_char* rows, void* out, i
 }
 
 template <int kAct>
-__global__ __launch_bounds__(256, 2) void glu_gemm_kernel(GluArgs a, const char* __restrict__ codes, int row_tiles,
-                                                       int token_tiles) {
+__global__ __launch_bounds__(256, 2) void glu_gemm_kernel(GluArgs a, const char* __restrict__ codes,
+                                                          const char* __restrict__ x, int row_tiles, int token_tiles) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -320,7 +348,7 @@ __global__ __launch_bounds__(256, 2) void glu_gemm_kernel(GluArgs a, const char*
   const int nks = (int)(a.k / kGluK);
   // A: two pairs of 64 outputs, each nks pieces of 8 KiB, in order
   const __amdgpu_buffer_rsrc_t ar = glu_rsrc(codes + (int64_t)rt * 2 * nks * kPairBytes, (int64_t)2 * nks * kPairBytes);
-  const __amdgpu_buffer_rsrc_t br = glu_rsrc(a.xq, a.tokens * a.k);
+  const __amdgpu_buffer_rsrc_t br = glu_rsrc(x, (a.tokens + 15) / 16 * 16 * a.k);
   uint32_t a_off[4], b_off[2];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -329,9 +357,8 @@ __global__ __launch_bounds__(256, 2) void glu_gemm_kernel(GluArgs a, const char*
   }
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int row = 32 * wave + 16 * q + (lane >> 2);
-    const int64_t t = t0 + row;
-    b_off[q] = t < a.tokens ? (uint32_t)(t * a.k + 16 * row64_place(row, lane & 3)) : kGluOOB;
+    const int64_t t = t0 + 32 * wave + 16 * q;
+    b_off[q] = t < a.tokens ? (uint32_t)(t * a.k + 16 * lane) : kGluOOB;
   }
   // past the last step the same instructions read zeros into a stage that nobody
   // reads, so the waits can count them
@@ -345,7 +372,7 @@ __global__ __launch_bounds__(256, 2) void glu_gemm_kernel(GluArgs a, const char*
 #pragma unroll
     for (int q = 0; q < 2; ++q)
       glu_dma16(br, st + kGluABytes + 1024 * (2 * wave + q),
-                in && b_off[q] != kGluOOB ? b_off[q] + (uint32_t)(ks * kGluK) : kGluOOB);
+                in && b_off[q] != kGluOOB ? b_off[q] + (uint32_t)(ks * 1024) : kGluOOB);
   };
   v4i c[8][4];
 #pragma unroll
@@ -595,7 +622,7 @@ __global__ __launch_bounds__(256) void glu_gate_bwd_kernel(GluBwdArgs a, GluBwdL
 // From kGluManyTokens tokens on the codes are decoded once for all.
 constexpr int64_t kGluManyTokens = 192;
 size_t glu_ws_bytes(int64_t tokens, int64_t k, int64_t n_out) {
-  return tokens < kGluManyTokens ? 0 : (size_t)(2 * n_out * k);
+  return tokens < kGluManyTokens ? 0 : (size_t)(2 * n_out * k + (tokens + 15) / 16 * 16 * k);
 }
 
 template <int S, int kAct>
@@ -611,16 +638,17 @@ static hipError_t glu_launch(const GluArgs& a, void* ws, hipStream_t s) {
   }
   const int nkb = (int)(a.k / kBlockK);
   const int64_t superblocks = a.n_out / kStripRows * nkb;
-  const int64_t blocks = (2 * superblocks + 3) / 4;
-  glu_decode_kernel<S><<<(unsigned)(blocks < 1024 ? blocks : 1024), 256, 0, s>>>(
-      static_cast<const char*>(a.gate), static_cast<const char*>(a.up), superblocks, nkb, static_cast<char*>(ws));
+  const int64_t x_jobs = (a.tokens + 15) / 16 * nkb, blocks = (2 * superblocks + x_jobs + kDecodeThreads / 64 - 1) / (kDecodeThreads / 64);
+  char* const codes = static_cast<char*>(ws);
+  char* const x = codes + 2 * a.n_out * a.k;
+  glu_decode_kernel<S><<<(unsigned)(blocks < 512 ? blocks : 512), kDecodeThreads, 0, s>>>(
+      static_cast<const char*>(a.gate), static_cast<const char*>(a.up), superblocks, nkb, codes, a.xq, a.tokens, x_jobs, x);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int row_tiles = (int)(a.n_out / 128);
   const int token_tiles = (int)((a.tokens + kGluTokens - 1) / kGluTokens);
   const int64_t tiles = (int64_t)row_tiles * token_tiles;
-  glu_gemm_kernel<kAct><<<(unsigned)((tiles + 7) / 8 * 8), 256, 0, s>>>(a, static_cast<const char*>(ws), row_tiles,
-                                                                       token_tiles);
+  glu_gemm_kernel<kAct><<<(unsigned)((tiles + 7) / 8 * 8), 256, 0, s>>>(a, codes, x, row_tiles, token_tiles);
   return hipGetLastError();
 }
 template <int S>
