@@ -742,9 +742,13 @@ def _blocks(n):
     return -(-n // CKPT_BLOCK)
 
 
+_KINDS = {torch.float32: BL_TYPE_F32, torch.bfloat16: BL_TYPE_BF16}
+
+
 def _kind(t, name):
     """BL_TYPE_* of one float32 or bfloat16 tensor."""
-    return _type_of(name, t)
+    kind = _KINDS.get(getattr(t, "dtype", None))
+    return _type_of(name, t) if kind is None else kind
 
 
 def bitlinear_ckpt_pack(X, rows, n, codes, scales, stream=None):

@@ -456,7 +456,7 @@ hipError_t launch_attn_cache(const AttnCacheArgs& a, int64_t d, hipStream_t s);
 // ---------------------------------------------------------- norm.hip
 constexpr int kCkptBlock = 64;          // values of a row that share a checkpoint's scale
 constexpr int64_t kNormMaxWidth = 16384;
-constexpr int kNormParts = 512;         // workgroups of the norm's backward, at most
+constexpr int kNormParts = 256;         // workgroups of the norm's backward, at most: as many as run at once
 struct NormArgs {
   const void* X;  // rows of n, x_stride elements apart
   int64_t x_stride, rows, n;
@@ -480,7 +480,7 @@ struct NormBwdArgs {
   void* dX;
   int dx_type;
   float *dweight, *dbias;  // either may be NULL
-  float* part;             // rows of 2n partial sums; NULL with both NULL
+  float* part;             // rows of n (2n with dbias) partial sums; NULL with both NULL
 };
 inline size_t norm_bwd_ws_bytes(int64_t n) { return (size_t)kNormParts * 2 * n * 4; }
 hipError_t launch_layernorm(const NormArgs& a, int x_type, hipStream_t s);

@@ -14,17 +14,18 @@ namespace bl {
 template <int kThreads>
 struct RowSums {
   static constexpr int kWaves = kThreads / 64;
-  // sum over the row's threads; `slot`: a different one for each sum between two
-  // barriers that all of the workgroup passes
-  __device__ static __forceinline__ float sum(float v, float (*red)[8], int slot) {
+  // sum over the row's threads (`wave`: this one's in the workgroup); `slot`: a
+  // different one for each sum between two barriers that all of the workgroup passes
+  __device__ static __forceinline__ float sum(float v, float (*red)[8], int slot, int wave) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
     if constexpr (kWaves > 1) {
-      if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = v;
+      if ((threadIdx.x & 63) == 0) red[slot][wave] = v;
       __syncthreads();
-      v = red[slot][0];
+      const int first = wave & ~(kWaves - 1);
+      v = red[slot][first];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) v += red[slot][w];
+      for (int w = 1; w < kWaves; ++w) v += red[slot][first + w];
     }
     return v;
   }
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void layernorm_ker
     for (int i = 0; i < kV; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += raw[i].get(j, 0.f);
-    mean = RowSums<kThreads>::sum(s, red, 0) * inv_n;
+    mean = RowSums<kThreads>::sum(s, red, 0, threadIdx.x >> 6) * inv_n;
   }
   float q = 0.f;
 #pragma unroll
@@ -71,7 +72,7 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void layernorm_ker
       const float d = raw[i].get(j, 0.f) - mean;
       q = in[i] ? fmaf(d, d, q) : q;
     }
-  const float rstd = rstd_of(RowSums<kThreads>::sum(q, red, 1) * inv_n, a.eps);
+  const float rstd = rstd_of(RowSums<kThreads>::sum(q, red, 1, threadIdx.x >> 6) * inv_n, a.eps);
   if (tid == 0) {
     if (a.mean) st_global(a.mean + row, mean);
     if (a.rstd) st_global(a.rstd + row, rstd);
@@ -110,43 +111,68 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void layernorm_ker
 // keeps its share of dw and db in registers; a workgroup's groups are joined in
 // LDS in a fixed order, and each workgroup writes one row of partial sums, which
 // norm_dw_kernel adds in binary64.  No atomics: reruns give the same bits.
-template <int T, int kThreads, int kV>
-__global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void layernorm_bwd_kernel(NormBwdArgs a) {
-  constexpr int kRows = kThreads < 256 ? 256 / kThreads : 1;
+// Bound by memory.  The sums take so many registers that two wavefronts fit a SIMD,
+// so each keeps the next row's x and dy on their way while it sums and writes
+// its row (with 32 values a thread there are no registers left for that).  4096 x
+// 2560, 8-bit x, bf16 dy, binary32 dR and dX: 27.4 us for 115 MB, 4.2 TB/s (one
+// wavefront a row, 40 values a lane, nothing ahead: 42.0); 2049 x 8960 bf16 with
+// binary32 dy and bias: 38.5 us, 3.8 TB/s (45.4).
+template <int T, int D, int kThreads, int kV, bool kBias>
+__global__ __launch_bounds__(512) void layernorm_bwd_kernel(NormBwdArgs a) {
+  constexpr int kRows = 512 / kThreads;  // rows of a workgroup at a time
   __shared__ float red[4][8];
+  constexpr bool kAhead = kV < 4;
   const int tid = kRows > 1 ? threadIdx.x % kThreads : threadIdx.x;
-  const int group = kRows > 1 ? threadIdx.x / kThreads : 0;
+  const int group = kRows > 1 ? threadIdx.x / kThreads : 0, wave = threadIdx.x >> 6;
   const float inv_n = 1.f / (float)a.n;
-  const int64_t blocks = (a.n + kCkptBlock - 1) / kCkptBlock;
-  float gw[kV][8], gb[kV][8];
+  const int64_t blocks = (a.n + kCkptBlock - 1) / kCkptBlock, stride = (int64_t)gridDim.x * kRows;
+  float gw[kV][8], gb[kBias ? kV : 1][8];
 #pragma unroll
   for (int i = 0; i < kV; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) gw[i][j] = gb[i][j] = 0.f;
-  int slot = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kRows + group; row < a.rows; row += (int64_t)gridDim.x * kRows) {
-    Raw8<T> rx[kV];
-    float xs[kV];
-    Raw8<kRowF32> rd[kV];  // binary32 dy, or bf16 in the first half
+    for (int j = 0; j < 8; ++j) gw[i][j] = gb[kBias ? i : 0][j] = 0.f;
+  Raw8<T> rx[kV];
+  Raw8<D> rd[kV];
+  float xs[kV], mean = 0.f, rstd = 0.f;
+  // (a group without a row takes part in the barriers, with zeros)
+  const auto load = [&](int64_t row) {
+    const bool live = row < a.rows;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       const int64_t e = 8 * ((int64_t)i * kThreads + tid);
       rx[i].zero();
       rd[i].zero();
       xs[i] = 0.f;
-      if (e < a.n) {
+      if (live && e < a.n) {
         rx[i].load(a.X, row * a.x_stride + e);
+        rd[i].load(a.dY, row * a.n + e);
         if (T == kRowQ8) xs[i] = ld_global(a.x_scales + row * blocks + e / kCkptBlock);
-        if (a.dy_type == kRowF32) {
-          rd[i].load(a.dY, row * a.n + e);
+      }
+    }
+    mean = live && a.mean ? ld_global(a.mean + row) : 0.f;
+    rstd = live ? ld_global(a.rstd + row) : 0.f;
+  };
+  int slot = 0;
+  if (kAhead) load((int64_t)blockIdx.x * kRows + group);
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.rows; base += stride) {
+    const int64_t row = base + group;
+    const bool live = row < a.rows;
+    if (!kAhead) load(row);
+    Raw8<kRowF32> rr[kV];  // binary32 dR, or bf16 in the first half
+    if (a.dR) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const int64_t e = 8 * ((int64_t)i * kThreads + tid);
+        if (!live || e >= a.n) continue;
+        if (a.dx_type == kRowF32) {
+          rr[i].load(a.dR, row * a.n + e);
         } else {
-          Raw8<kRowBf16> b;
-          b.load(a.dY, row * a.n + e);
-          rd[i].a = __builtin_bit_cast(f32x4_t, b.a);
+          Raw8<kRowBf16> h;
+          h.load(a.dR, row * a.n + e);
+          rr[i].a = __builtin_bit_cast(f32x4_t, h.a);
         }
       }
     }
-    const float mean = a.mean ? ld_global(a.mean + row) : 0.f, rstd = ld_global(a.rstd + row);
     float sa = 0.f, sn = 0.f;
     float x[kV][8], d[kV][8];
 #pragma unroll
@@ -155,97 +181,112 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void layernorm_bwd
       Raw8<kRowF32> w;
       if (a.weight && e < a.n) w.load(a.weight, e);
       else w.a = w.b = f32x4_t{1.f, 1.f, 1.f, 1.f};
-      const u32x4 half = __builtin_bit_cast(u32x4, rd[i].a);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        // threads past the row hold dy = 0, so whatever n they form counts nothing
+        // threads past the row hold dy = 0, and n = 0
         const float n = e < a.n ? (rx[i].get(j, xs[i]) - mean) * rstd : 0.f;
-        const float dy = a.dy_type == kRowF32 ? rd[i].get(j, 0.f) : (j & 1) ? bf16_hi(half[j >> 1]) : bf16_lo(half[j >> 1]);
+        const float dy = rd[i].get(j, 0.f);
         gw[i][j] = fmaf(dy, n, gw[i][j]);
-        gb[i][j] += dy;
+        if (kBias) gb[kBias ? i : 0][j] += dy;
         x[i][j] = n;
         d[i][j] = dy * w.get(j, 0.f);
         sa += d[i][j];
         sn = fmaf(d[i][j], n, sn);
       }
     }
-    sn = RowSums<kThreads>::sum(sn, red, slot) * inv_n;
-    sa = a.mean ? RowSums<kThreads>::sum(sa, red, slot + 1) * inv_n : 0.f;
+    const float r = rstd;
+    const bool centred = a.mean != nullptr;
+    if (kAhead) load(row + stride);
+    sn = RowSums<kThreads>::sum(sn, red, slot, wave) * inv_n;
+    sa = centred ? RowSums<kThreads>::sum(sa, red, slot + 1, wave) * inv_n : 0.f;
     slot ^= 2;  // a row's sums are read before the barriers of the next row's, which use the other slots
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       const int64_t e = 8 * ((int64_t)i * kThreads + tid);
-      if (e >= a.n) continue;
+      if (!live || e >= a.n) continue;
       float y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = rstd * fmaf(-x[i][j], sn, d[i][j] - sa);
+      for (int j = 0; j < 8; ++j) y[j] = r * fmaf(-x[i][j], sn, d[i][j] - sa);
       if (a.dR) {
-        if (a.dx_type == kRowF32) {
-          Raw8<kRowF32> r;
-          r.load(a.dR, row * a.n + e);
+        const u32x4 h = __builtin_bit_cast(u32x4, rr[i].a);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] += r.get(j, 0.f);
-        } else {
-          Raw8<kRowBf16> r;
-          r.load(a.dR, row * a.n + e);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] += r.get(j, 0.f);
-        }
+        for (int j = 0; j < 8; ++j)
+          y[j] += a.dx_type == kRowF32 ? rr[i].get(j, 0.f) : (j & 1) ? bf16_hi(h[j >> 1]) : bf16_lo(h[j >> 1]);
       }
       store_row8(a.dX, a.dx_type, row * a.n + e, y);
     }
   }
   if (!a.part) return;
+  // one row of partial sums for each workgroup: dw's n, and with kBias db's behind them
+  float* out = a.part + (int64_t)blockIdx.x * (kBias ? 2 : 1) * a.n;
   if constexpr (kRows == 1) {
-    float* out = a.part + (int64_t)blockIdx.x * 2 * a.n;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       const int64_t e = 8 * ((int64_t)i * kThreads + tid);
       if (e >= a.n) continue;
       store_row8(out, kRowF32, e, gw[i]);
-      store_row8(out, kRowF32, a.n + e, gb[i]);
+      if (kBias) store_row8(out, kRowF32, a.n + e, gb[kBias ? i : 0]);
     }
   } else {
+    // one run at a time: the groups' values beside each other, then summed in order
     __shared__ __attribute__((aligned(16))) float join[kRows][kThreads * 8];
-    // one run at a time: group g's values beside each other, then summed in order
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < (kBias ? 2 : 1); ++s)
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) join[group][j * kThreads + tid] = s ? gb[i][j] : gw[i][j];
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<f32x4_t*>(&join[group][tid * 8 + 4 * h]) =
+              s ? f32x4_t{gb[kBias ? i : 0][4 * h], gb[kBias ? i : 0][4 * h + 1], gb[kBias ? i : 0][4 * h + 2],
+                          gb[kBias ? i : 0][4 * h + 3]}
+                : f32x4_t{gw[i][4 * h], gw[i][4 * h + 1], gw[i][4 * h + 2], gw[i][4 * h + 3]};
         __syncthreads();
-        for (int c = threadIdx.x; c < kThreads * 8; c += 256) {
-          const int64_t e = 8 * ((int64_t)i * kThreads + c % kThreads) + c / kThreads;
+        for (int c = threadIdx.x; c < kThreads * 8; c += 512) {
+          const int64_t e = 8 * (int64_t)i * kThreads + c;
           if (e >= a.n) continue;
           float v = join[0][c];
 #pragma unroll
           for (int g = 1; g < kRows; ++g) v += join[g][c];
-          st_global(a.part + (int64_t)blockIdx.x * 2 * a.n + s * a.n + e, v);
+          st_global(out + s * a.n + e, v);
         }
       }
   }
 }
 
-// dw and db: sums of the workgroups' rows of partials, 64 columns of [dw | db] a
-// workgroup, its 16 wavefronts a share of the rows each, joined in LDS; binary64,
-// fixed order
-__global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__ part, int rows, int64_t n,
-                                                       float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ double red[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  double s = 0.0;
-  if (c < 2 * n)
-    for (int r = wave; r < rows; r += 16) s += (double)ld_global(part + (int64_t)r * 2 * n + c);
-  red[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && c < 2 * n) {
+// dw and db: sums of the workgroups' rows of partials.  A workgroup takes 32 columns,
+// its 32 groups of 8 threads (4 columns each) every 32nd row, all of them asked
+// for at once; joined in LDS, all in binary64 and in a fixed order (256 rows of
+// 2560: 4.7 us, latency).
+constexpr int kPartsEach = kNormParts / 32;
+__global__ __launch_bounds__(256) void norm_dw_kernel(const float* __restrict__ part, int rows, int64_t n, int64_t cols,
+                                                     float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ double red[32][33];
+  const int c4 = 4 * (threadIdx.x & 7), g = threadIdx.x >> 3;
+  const int64_t c = (int64_t)blockIdx.x * 32 + c4;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  if (c < cols) {
+    f32x4_t v[kPartsEach];
 #pragma unroll
-    for (int w = 1; w < 16; ++w) s += red[w][lane];
-    float* out = c < n ? dw : db;
-    if (out) st_global(out + (c < n ? c : c - n), (float)s);
+    for (int u = 0; u < kPartsEach; ++u) {
+      v[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (g + 32 * u < rows) v[u] = ld_global(reinterpret_cast<const f32x4_t*>(part + (int64_t)(g + 32 * u) * cols + c));
+    }
+#pragma unroll
+    for (int u = 0; u < kPartsEach; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s[q] += (double)v[u][q];
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) red[g][c4 + q] = s[q];
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int64_t e = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    double t = red[0][threadIdx.x];
+#pragma unroll
+    for (int h = 1; h < 32; ++h) t += red[h][threadIdx.x];
+    float* out = e < n ? dw : db;
+    if (e < cols && out) st_global(out + (e < n ? e : e - n), (float)t);
   }
 }
 
@@ -293,8 +334,9 @@ __global__ __launch_bounds__(256) void ckpt_unpack_kernel(const int8_t* __restri
 }
 
 // ------------------------------------------------------------------ host
-// Threads of a row: one wavefront up to 2560 values (five runs of eight a lane:
-// no barriers, and the backward's sums fit its registers), then four, then eight.
+// Threads of a row, forward: one wavefront up to 2560 values (five runs of eight a
+// lane, no barriers), then four.  Backward: as many as leave a thread 24 values,
+// whose sums and whose next row's inputs fit its registers.
 template <int T, int kThreads, int kV>
 static hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
   constexpr int kRows = kThreads < 256 ? 256 / kThreads : 1;
@@ -313,45 +355,49 @@ static hipError_t norm_pick(const NormArgs& a, hipStream_t s) {
   if (runs <= 512) return norm_launch<T, 256, 2>(a, s);
   if (runs <= 768) return norm_launch<T, 256, 3>(a, s);
   if (runs <= 1024) return norm_launch<T, 256, 4>(a, s);
-  if (runs <= 1536) return norm_launch<T, 512, 3>(a, s);
-  return norm_launch<T, 512, 4>(a, s);
+  if (runs <= 1280) return norm_launch<T, 256, 5>(a, s);
+  if (runs <= 1536) return norm_launch<T, 256, 6>(a, s);
+  return norm_launch<T, 256, 8>(a, s);
 }
 hipError_t launch_layernorm(const NormArgs& a, int x_type, hipStream_t s) {
   return x_type == kRowF32 ? norm_pick<kRowF32>(a, s) : norm_pick<kRowBf16>(a, s);
 }
 
-template <int T, int kThreads, int kV>
+template <int T, int D, int kThreads, int kV>
 static hipError_t norm_bwd_launch(const NormBwdArgs& a, hipStream_t s) {
-  constexpr int kRows = kThreads < 256 ? 256 / kThreads : 1;
+  constexpr int kRows = 512 / kThreads;
   int64_t blocks = (a.rows + kRows - 1) / kRows;
   if (blocks > kNormParts) blocks = kNormParts;
-  layernorm_bwd_kernel<T, kThreads, kV><<<(unsigned)blocks, kThreads < 256 ? 256 : kThreads, 0, s>>>(a);
+  if (a.dbias) layernorm_bwd_kernel<T, D, kThreads, kV, true><<<(unsigned)blocks, 512, 0, s>>>(a);
+  else layernorm_bwd_kernel<T, D, kThreads, kV, false><<<(unsigned)blocks, 512, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.part) return e;
-  norm_dw_kernel<<<(unsigned)((2 * a.n + 63) / 64), 1024, 0, s>>>(a.part, (int)blocks, a.n, a.dweight, a.dbias);
+  const int64_t cols = a.dbias ? 2 * a.n : a.n;
+  norm_dw_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(a.part, (int)blocks, a.n, cols, a.dweight, a.dbias);
   return hipGetLastError();
 }
-template <int T>
+template <int T, int D>
 static hipError_t norm_bwd_pick(const NormBwdArgs& a, hipStream_t s) {
   const int64_t runs = (a.n + 7) / 8;
-  if (runs <= 64) return norm_bwd_launch<T, 64, 1>(a, s);
-  if (runs <= 128) return norm_bwd_launch<T, 64, 2>(a, s);
-  if (runs <= 192) return norm_bwd_launch<T, 64, 3>(a, s);
-  if (runs <= 256) return norm_bwd_launch<T, 64, 4>(a, s);
-  if (runs <= 320) return norm_bwd_launch<T, 64, 5>(a, s);
-  if (runs <= 512) return norm_bwd_launch<T, 256, 2>(a, s);
-  if (runs <= 768) return norm_bwd_launch<T, 256, 3>(a, s);
-  if (runs <= 1024) return norm_bwd_launch<T, 256, 4>(a, s);
-  if (runs <= 1536) return norm_bwd_launch<T, 512, 3>(a, s);
-  return norm_bwd_launch<T, 512, 4>(a, s);
+  if (runs <= 64) return norm_bwd_launch<T, D, 64, 1>(a, s);
+  if (runs <= 128) return norm_bwd_launch<T, D, 64, 2>(a, s);
+  if (runs <= 192) return norm_bwd_launch<T, D, 64, 3>(a, s);
+  if (runs <= 384) return norm_bwd_launch<T, D, 128, 3>(a, s);
+  if (runs <= 768) return norm_bwd_launch<T, D, 256, 3>(a, s);
+  if (runs <= 1536) return norm_bwd_launch<T, D, 512, 3>(a, s);
+  return norm_bwd_launch<T, D, 512, 4>(a, s);
+}
+template <int T>
+static hipError_t norm_bwd_pick_dy(const NormBwdArgs& a, hipStream_t s) {
+  return a.dy_type == kRowF32 ? norm_bwd_pick<T, kRowF32>(a, s) : norm_bwd_pick<T, kRowBf16>(a, s);
 }
 hipError_t launch_layernorm_bwd(const NormBwdArgs& a, int x_type, hipStream_t s) {
   if (a.rows == 0) {
     norm_zero_kernel<<<(unsigned)((a.n + 255) / 256), 256, 0, s>>>(a.dweight, a.dbias, a.n);
     return hipGetLastError();
   }
-  if (x_type == kRowF32) return norm_bwd_pick<kRowF32>(a, s);
-  return x_type == kRowBf16 ? norm_bwd_pick<kRowBf16>(a, s) : norm_bwd_pick<kRowQ8>(a, s);
+  if (x_type == kRowF32) return norm_bwd_pick_dy<kRowF32>(a, s);
+  return x_type == kRowBf16 ? norm_bwd_pick_dy<kRowBf16>(a, s) : norm_bwd_pick_dy<kRowQ8>(a, s);
 }
 
 hipError_t launch_ckpt_pack(const void* X, int x_type, int64_t x_stride, int64_t rows, int64_t n, int8_t* codes,
