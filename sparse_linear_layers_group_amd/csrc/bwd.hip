@@ -60,6 +60,11 @@ __device__ constexpr HalfBf16Table kHalfBf16Table = make_half_bf16_table();
 static_assert(make_half_bf16_table().v[2 * (2 * 0x1f + 0)] == 0x3f80bf80u,
               "low half, bitmap 1111, sign of nonzero 0: -1.0 then +1.0");
 
+// the place of (row, c) in an operand that lies in tiles, or in rows `pitch` apart
+__device__ __forceinline__ int64_t operand_at(int64_t row, int64_t c, int64_t pitch, bool tiled) {
+  return tiled ? tiled_at(row, c, pitch) : row * pitch + c;
+}
+
 enum PrepKind : int32_t { kPrepCodes = 0, kPrepDys = 1, kPrepXq = 2 };
 
 // One matrix of a prep launch.
@@ -289,10 +294,14 @@ struct NtProblem {
   uint16_t* dG = nullptr;
   uint16_t* dU = nullptr;
   // with Cb set, C is not written but rounded to bf16 into Cb, laid out like C
-  // (256-row kernel and split sums only; N even)
+  // (256-row kernel only)
   uint16_t* Cb = nullptr;
-  // A and B in tiles of depth lda = ldb = K (256-row kernel only)
+  // A and B in tiles of depth K (256-row kernel only)
   bool tiled = false;
+  // cut along the depth into this many ranges of whole blocks of 32, range i to plane
+  // i of C (256-row kernel, tiled).  The tiles of a range are neighbours in the
+  // tile order, so an XCD runs most of a range and its L2 serves their common operands
+  int32_t parts = 1;
 };
 
 // the products of one launch of the 256-row kernel (its tiles dealt over
@@ -508,7 +517,7 @@ struct BigTile {
 
 template <int kWN>
 __host__ __device__ inline int64_t nt_tiles_big(const NtProblem& p) {
-  return ((p.M + kBigM - 1) / kBigM) * ((p.N + BigTile<kWN>::N - 1) / BigTile<kWN>::N);
+  return ((p.M + kBigM - 1) / kBigM) * ((p.N + BigTile<kWN>::N - 1) / BigTile<kWN>::N) * p.parts;
 }
 
 // gfx950-only builtins sit in plain (non-template) functions: used directly
@@ -587,11 +596,15 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   {
     // workgroup (XCD x, slot) takes the slot-th tile of XCD x's run: the XCD
     // shares of the problems one after the other
+    // (each problem's shares start where the ones before it left off, or the XCDs
+    // that get a tile more would always be the same)
     const int64_t xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-    int64_t before = 0;
+    int64_t before = 0, dealt = 0;
     for (int i = 0; i < set.n; ++i) {
       int64_t s0, c0;
-      xcd_share(nt_tiles_big<kWN>(set.p[i]), xcd, s0, c0);
+      const int64_t tiles = nt_tiles_big<kWN>(set.p[i]);
+      xcd_share(tiles, (xcd - dealt) & 7, s0, c0);
+      dealt += tiles;
       if (which < 0 && slot < before + c0) {
         which = i;
         t = s0 + slot - before;
@@ -607,15 +620,22 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   const double* __restrict__ alpha = pr.alpha;
   const int64_t lda = pr.lda, ldb = pr.ldb, ldc = pr.ldc, M = pr.M, N = pr.N, klen = pr.klen;
   int K = (int)pr.K;
+  int64_t k0 = (int64_t)blockIdx.y * klen;
   {
     const int64_t tiles_m = (M + kBigM - 1) / kBigM, tiles_n = (N + T::N - 1) / T::N;
+    if (pr.parts > 1) {
+      const int part = (int)(t / (tiles_m * tiles_n)), n32 = K / kBigK;
+      t -= part * tiles_m * tiles_n;
+      k0 = (int64_t)(n32 * part / pr.parts) * kBigK;
+      K = (n32 * (part + 1) / pr.parts) * kBigK;
+      C += part * M * ldc;
+    }
     constexpr int64_t kG = 4;  // row tiles per group of the tile order
     const int64_t g = t / (kG * tiles_n), r = t - g * kG * tiles_n;
     const int64_t gm = tiles_m - g * kG < kG ? tiles_m - g * kG : kG;
     m0 = (g * kG + r % gm) * kBigM;
     n0 = (r / gm) * T::N;
   }
-  const int64_t k0 = (int64_t)blockIdx.y * klen;
   K = (int)(K - k0 < klen ? K - k0 : klen);
   C += (int64_t)blockIdx.y * M * ldc;
   const int nks = (K + kBigK - 1) / kBigK;
@@ -635,12 +655,12 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
 #pragma unroll
   for (int q = 0; q < T::kAInstr; ++q) {
     const int64_t row = 16 * (T::kAInstr * wave + q) + (lane >> 2);
-    a_off[q] = m0 + row < M ? (uint32_t)((pr.tiled ? (m0 + row - (lane >> 2)) * lda + 8 * lane : (m0 + row) * lda + k0 + kc) * 2) : kOOB;
+    a_off[q] = m0 + row < M ? (uint32_t)((pr.tiled ? (m0 + row - (lane >> 2)) * lda + 16 * k0 + 8 * lane : (m0 + row) * lda + k0 + kc) * 2) : kOOB;
   }
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int64_t row = 32 * wave + 16 * q + (lane >> 2);
-    b_off[q] = n0 + row < N ? (uint32_t)((pr.tiled ? (n0 + row - (lane >> 2)) * ldb + 8 * lane : (n0 + row) * ldb + k0 + kc) * 2) : kOOB;
+    b_off[q] = n0 + row < N ? (uint32_t)((pr.tiled ? (n0 + row - (lane >> 2)) * ldb + 16 * k0 + 8 * lane : (n0 + row) * ldb + k0 + kc) * 2) : kOOB;
   }
   const uint32_t step_bytes = pr.tiled ? 1024 : kBigK * 2;  // from a step's piece of a row (block) to the next
   // every step issues the same instructions per wavefront (past the last
@@ -844,10 +864,8 @@ static hipError_t gemm_nt_split(NtProblem p, float* partials, hipStream_t s) {
   const int64_t klen = bwd_split_len(p.K, splits);
   const int used = (int)((p.K + klen - 1) / klen);
   float* C = p.C;
-  uint16_t* Cb = p.Cb;
   const double* alpha = p.alpha;
   p.C = partials;
-  p.Cb = nullptr;
   p.ldc = p.N;
   p.alpha = nullptr;
   p.klen = klen;
@@ -857,7 +875,7 @@ static hipError_t gemm_nt_split(NtProblem p, float* partials, hipStream_t s) {
   gemm_nt_bf16_kernel<<<dim3(gx, (unsigned)used), 256, 0, s>>>(p, none);
   const int64_t n4 = p.M * p.N / 4;
   const int64_t blocks = (n4 + 255) / 256;
-  split_sum_kernel<<<(unsigned)(blocks < 2048 ? blocks : 2048), 256, 0, s>>>(partials, used, n4, alpha, C, Cb);
+  split_sum_kernel<<<(unsigned)(blocks < 2048 ? blocks : 2048), 256, 0, s>>>(partials, used, n4, alpha, C, nullptr);
   return hipGetLastError();
 }
 
@@ -1083,56 +1101,60 @@ hipError_t launch_zero(float* p, int64_t n, hipStream_t s) {
 
 // The products of the gated feed-forward's backward.  dX is one product of
 // depth 2 n_out: dG gate_gamma and dU up_gamma stand side by side in dgu and so do the two
-// layers' codes in codes_t, so it is written once, and its tiles (twice as
-// deep as the weights') start first.
+// layers' codes in codes_t, so it is written once.  The deepest products' tiles start
+// first.
 hipError_t launch_glu_products(const GluBwdArgs& a, int S, hipStream_t s) {
   const GluBwdLayout l = glu_bwd_layout(a.tokens, a.k, a.n_out);
   const int64_t tp = bwd_tokens_padded(a.tokens), nkb = a.k / kBlockK, strips = a.n_out / kStripRows, n2 = 2 * a.n_out;
-  uint16_t* const xq_t = reinterpret_cast<uint16_t*>(a.ws + l.xq_t);
-  uint16_t* const codes_t = reinterpret_cast<uint16_t*>(a.ws + l.codes_t);
-  float* const partials = reinterpret_cast<float*>(a.ws + l.partials);
+  const auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(a.ws + o); };
   PrepList L;
-  NtProblem probs[3];
-  int np = 0;
-  const bool b16 = a.grad_type == BL_TYPE_BF16;
-  // split products run on the 128-row kernel, from rows
-  const bool tx = l.dx_tiled, tw = l.dw_tiled;
-  const auto add = [&](NtProblem p, void* out, bool tiled) {
-    p.tiled = tiled;
-    p.C = b16 ? nullptr : static_cast<float*>(out);
-    p.Cb = b16 ? static_cast<uint16_t*>(out) : nullptr;
-    probs[np++] = p;
-  };
   if (a.dX) {
     const int32_t jobs = (int32_t)((strips * nkb + 3) / 4);
-    L.t.push_back(PrepTask{a.gate, nullptr, codes_t, nkb, strips, n2, kPrepCodes, jobs, tx});
-    L.t.push_back(PrepTask{a.up, nullptr, codes_t + (tx ? 16 : 1) * a.n_out, nkb, strips, n2, kPrepCodes, jobs, tx});
-    add(NtProblem{reinterpret_cast<const uint16_t*>(a.ws + l.dgu), codes_t, nullptr, nullptr, n2, n2, a.k, a.tokens,
-                  a.k, n2, n2}, a.dX, tx);
+    L.t.push_back(PrepTask{a.gate, nullptr, at(l.codes_t), nkb, strips, n2, kPrepCodes, jobs, 1});
+    // (column n_out of a tiled operand: n_out / 32 blocks of 512 on)
+    L.t.push_back(PrepTask{a.up, nullptr, at(l.codes_t) + 16 * a.n_out, nkb, strips, n2, kPrepCodes, jobs, 1});
   }
-  if (a.dWg) {
-    L.t.push_back(PrepTask{a.xq, nullptr, xq_t, a.tokens, a.k, tp, kPrepXq, (int32_t)((tp / 64) * (a.k / 64)), tw});
-    add(NtProblem{reinterpret_cast<const uint16_t*>(a.ws + l.dgs_t), xq_t, nullptr, nullptr, tp, tp, a.k, a.n_out,
-                  a.k, tp, tp}, a.dWg, tw);
-    add(NtProblem{reinterpret_cast<const uint16_t*>(a.ws + l.dus_t), xq_t, nullptr, nullptr, tp, tp, a.k, a.n_out,
-                  a.k, tp, tp}, a.dWu, tw);
-  }
+  if (a.dWg)
+    L.t.push_back(PrepTask{a.xq, nullptr, at(l.xq_t), a.tokens, a.k, tp, kPrepXq, (int32_t)((tp / 64) * (a.k / 64)), 1});
   hipError_t e = L.launch(S, s);
   if (e != hipSuccess) return e;
-  std::stable_sort(probs, probs + np, [](const NtProblem& x, const NtProblem& y) { return x.K > y.K; });
+
+  const bool b16 = a.grad_type == BL_TYPE_BF16;
   NtSet set{};
-  for (int i = 0; i < np; ++i)
-    if (bwd_splits(probs[i].M, probs[i].N, probs[i].K) == 1) set.p[set.n++] = probs[i];
-  if (set.n) {
-    e = launch_big(set, big_kind(set), s);
-    if (e != hipSuccess) return e;
+  // out [rows][k] = A [rows][depth] B [k][depth]^T
+  const auto add = [&](size_t A, size_t B, void* out, size_t planes, int64_t rows, int64_t depth, int parts) {
+    NtProblem p{at(A), at(B), nullptr, nullptr, depth, depth, a.k, rows, a.k, depth, depth};
+    p.tiled = true;
+    p.parts = parts;
+    if (parts > 1) p.C = reinterpret_cast<float*>(a.ws + planes);
+    else if (b16) p.Cb = static_cast<uint16_t*>(out);
+    else p.C = static_cast<float*>(out);
+    set.p[set.n++] = p;
+  };
+  if (a.dX) add(l.dgu, l.codes_t, a.dX, l.planes_x, a.tokens, n2, l.split_x);
+  if (a.dWg) {
+    add(l.dgs_t, l.xq_t, a.dWg, l.planes_g, a.n_out, tp, l.split_w);
+    add(l.dus_t, l.xq_t, a.dWu, l.planes_u, a.n_out, tp, l.split_w);
   }
-  for (int i = 0; i < np; ++i)
-    if (bwd_splits(probs[i].M, probs[i].N, probs[i].K) > 1) {
-      e = gemm_nt_split(probs[i], partials, s);
-      if (e != hipSuccess) return e;
-    }
-  return hipSuccess;
+  std::stable_sort(set.p, set.p + set.n, [](const NtProblem& x, const NtProblem& y) { return x.K / x.parts > y.K / y.parts; });
+  // Where one round of 256 x 256 tiles does not fill the CUs, twice as many of 256 x
+  // 128, two on a CU (547 tokens, 896 x 4864: 33.4 us in place of 37.4; 4096
+  // tokens, 2560 x 6912, several rounds: 487 in place of 391)
+  int64_t tiles = 0;
+  for (int i = 0; i < set.n; ++i) tiles += nt_tiles_big<4>(set.p[i]);
+  e = launch_big(set, tiles <= 256 ? 2 : 3, s);
+  const auto sum = [&](void* out, size_t planes, int64_t rows, int parts) {
+    if (e != hipSuccess || !out || parts == 1) return;
+    const int64_t n4 = rows * a.k / 4, blocks = (n4 + 255) / 256;
+    split_sum_kernel<<<(unsigned)(blocks < 2048 ? blocks : 2048), 256, 0, s>>>(
+        reinterpret_cast<const float*>(a.ws + planes), parts, n4, nullptr, b16 ? nullptr : static_cast<float*>(out),
+        b16 ? static_cast<uint16_t*>(out) : nullptr);
+    e = hipGetLastError();
+  };
+  sum(a.dX, l.planes_x, a.tokens, l.split_x);
+  sum(a.dWg, l.planes_g, a.n_out, l.split_w);
+  sum(a.dWu, l.planes_u, a.n_out, l.split_w);
+  return e;
 }
 
 hipError_t launch_bwd_group(const BwdItem* items, int count, int64_t tokens, int S, void* ws, int phase,

@@ -106,11 +106,6 @@ __host__ __device__ constexpr int row64_place(int row, int piece) {
 __device__ __forceinline__ int64_t tiled_at(int64_t row, int64_t c, int64_t depth) {
   return (row >> 4) * 16 * depth + (c >> 5) * 512 + (row & 15) * 32 + 8 * row64_place((int)row & 15, (int)(c >> 3) & 3);
 }
-// the same for one that lies in rows, `pitch` apart
-__device__ __forceinline__ int64_t operand_at(int64_t row, int64_t c, int64_t pitch, bool tiled) {
-  return tiled ? tiled_at(row, c, pitch) : row * pitch + c;
-}
-
 // explicit global-address-space accesses: pointers that arrive through
 // memory (e.g. from a plan) would otherwise become flat accesses, which also
 // count against the LDS counter and force extra waits

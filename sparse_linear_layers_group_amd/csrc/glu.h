@@ -39,30 +39,42 @@ struct GluBwdArgs {
   char* ws;
 };
 
-// Workspace of the backward: bf16 operands of its three products (each region
-// 256-byte aligned) and the planes of products that are split along k.
-//   dgu    [tokens][2 n_out]: dG gate_gamma beside dU up_gamma
-//   dgs_t, dus_t  [n_out][tp]: (dG s_t)^T, (dU s_t)^T, tp = tokens rounded up to 64
+// Workspace of the backward: bf16 operands of its three products, in tiles
+// (tiled_at; each region 256-byte aligned), and the planes of products that are
+// split along their depth.
+//   dgu    [tp][2 n_out]: dG gate_gamma, then dU up_gamma; tp = tokens rounded up to 64
+//   dgs_t, dus_t  [n_out][tp]: (dG s_t)^T, (dU s_t)^T
 //   xq_t   [k][tp];  codes_t  [k][2 n_out]: both layers' codes, transposed
-// The operands of a product that is not split lie in tiles (rows rounded up to 16).
 struct GluBwdLayout {
-  size_t dgu, dgs_t, dus_t, xq_t, codes_t, partials, bytes;
-  bool dx_tiled, dw_tiled;
+  size_t dgu, dgs_t, dus_t, xq_t, codes_t, planes_x, planes_g, planes_u, bytes;
+  int split_x, split_w;  // parts of dX's depth, of each weight gradient's
 };
+// All products run in one launch of 256 x 256 tiles, one on a CU.  A product is cut
+// along its depth where it is deeper than a CU's share of all the work, but no
+// part shallower than kGluPart: a part costs a binary32 plane of the output to
+// write and to read.
+constexpr int64_t kGluPart = 1024;
+inline int glu_parts(int64_t depth, int64_t share, int most) {
+  const int64_t per = share > kGluPart ? share : kGluPart, parts = (depth + per - 1) / per;
+  return parts > most ? most : (int)parts;
+}
 inline GluBwdLayout glu_bwd_layout(int64_t tokens, int64_t k, int64_t n_out) {
   const int64_t tp = bwd_tokens_padded(tokens);
+  const int64_t cols = (k + 255) / 256, tiles_x = (tokens + 255) / 256 * cols, tiles_w = (n_out + 255) / 256 * cols;
+  const int64_t share = (tiles_x * 2 * n_out + 2 * tiles_w * tp) / 256;
   GluBwdLayout l;
+  l.split_x = glu_parts(2 * n_out, share, 8);
+  l.split_w = glu_parts(tp, share, 4);
   l.dgu = 0;
   l.dgs_t = l.dgu + bwd_align((size_t)tp * 2 * n_out * 2);
   l.dus_t = l.dgs_t + bwd_align((size_t)n_out * tp * 2);
   l.xq_t = l.dus_t + bwd_align((size_t)n_out * tp * 2);
   l.codes_t = l.xq_t + bwd_align((size_t)k * tp * 2);
-  l.partials = l.codes_t + bwd_align((size_t)k * 2 * n_out * 2);
-  const int sx = bwd_splits(tokens, k, 2 * n_out), sw = bwd_splits(n_out, k, tp);
-  l.dx_tiled = sx == 1;
-  l.dw_tiled = sw == 1;
-  const size_t px = sx > 1 ? (size_t)sx * tokens * k * 4 : 0, pw = sw > 1 ? (size_t)sw * n_out * k * 4 : 0;
-  l.bytes = l.partials + bwd_align(px > pw ? px : pw);
+  l.planes_x = l.codes_t + bwd_align((size_t)k * 2 * n_out * 2);
+  l.planes_g = l.planes_x + (l.split_x > 1 ? bwd_align((size_t)l.split_x * tokens * k * 4) : 0);
+  const size_t w = l.split_w > 1 ? bwd_align((size_t)l.split_w * n_out * k * 4) : 0;
+  l.planes_u = l.planes_g + w;
+  l.bytes = l.planes_u + w;
   return l;
 }
 hipError_t launch_glu_bwd(const GluBwdArgs& a, int S, hipStream_t s);

@@ -592,8 +592,8 @@ __global__ __launch_bounds__(256) void glu_gate_bwd_kernel(GluBwdArgs a, GluBwdL
         uint16_t* dgu = reinterpret_cast<uint16_t*>(a.ws + l.dgu);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          store_row8(dgu, kRowBf16, operand_at(token, col + 8 * h, 2 * a.n_out, l.dx_tiled), y + 8 * h);
-          store_row8(dgu, kRowBf16, operand_at(token, a.n_out + col + 8 * h, 2 * a.n_out, l.dx_tiled), z + 8 * h);
+          store_row8(dgu, kRowBf16, tiled_at(token, col + 8 * h, 2 * a.n_out), y + 8 * h);
+          store_row8(dgu, kRowBf16, tiled_at(token, a.n_out + col + 8 * h, 2 * a.n_out), z + 8 * h);
         }
       }
     }
@@ -614,7 +614,7 @@ __global__ __launch_bounds__(256) void glu_gate_bwd_kernel(GluBwdArgs a, GluBwdL
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       o[e] = (uint32_t)tile[(t8 + 2 * e) * kGatePitch + r] | ((uint32_t)tile[(t8 + 2 * e + 1) * kGatePitch + r] << 16);
-    st_global(reinterpret_cast<u32x4*>(out + operand_at(c0 + r, t0 + t8, tp, l.dw_tiled)), u32x4{o[0], o[1], o[2], o[3]});
+    st_global(reinterpret_cast<u32x4*>(out + tiled_at(c0 + r, t0 + t8, tp)), u32x4{o[0], o[1], o[2], o[3]});
   }
 }
 
