@@ -38,7 +38,7 @@ __device__ __forceinline__ void act_both(float g, float& value, float& slope) {
 }
 
 // ------------------------------------------------------- forward, few tokens
-// A workgroup computes 64 outputs (one packed strip of each layer) of 16 kTT
+// A workgroup computes 64 outputs (one packed strip of each layer) of 16
 // tokens: eight wavefronts take the gate strip's k blocks and eight the up
 // strip's, each every eighth.  A lane's chunk of a superblock holds the A
 // operands it needs (rows along the matrix instruction's rows), the activations
@@ -123,7 +123,7 @@ __device__ __forceinline__ void glu_output(const GluArgs& a, float g, float u, i
   }
 }
 
-template <int S, int kAct, int kTT>
+template <int S, int kAct>
 __global__ __launch_bounds__(1024) void glu_small_kernel(GluArgs a) {
   __shared__ __attribute__((aligned(16))) int lds[16 * 16 * kSmallPitch];
   static_assert(16 * 16 * kSmallPitch >= 512 * kSmallCopies, "the tables fit where the sums meet");
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(1024) void glu_small_kernel(GluArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int side = wave >> 3, first = wave & 7;  // gate or up; first k block
-  const int64_t strip = blockIdx.x, t0 = (int64_t)blockIdx.y * (16 * kTT);
+  const int64_t strip = blockIdx.x, t0 = 16 * (int64_t)blockIdx.y;
   const int nkb = (int)(a.k / kBlockK);
 #pragma unroll
   for (int r = 0; r < 512 * kSmallCopies / 4 / 1024; ++r) {
@@ -142,52 +142,284 @@ __global__ __launch_bounds__(1024) void glu_small_kernel(GluArgs a) {
   constexpr int kSb = kStripRows * block_bytes(S);  // bytes of a superblock
   const char* base = static_cast<const char*>(side ? a.up : a.gate) + strip * nkb * (int64_t)kSb;
   const __amdgpu_buffer_rsrc_t pr = glu_rsrc(base, (int64_t)nkb * kSb), xr = glu_rsrc(a.xq, a.tokens * a.k);
-  uint32_t xo[kTT];
+  const int64_t t = t0 + (lane & 15);
+  const uint32_t xo = t < a.tokens ? (uint32_t)(t * a.k + 16 * (lane >> 4)) : kGluOOB;
+  v4i c[4];
 #pragma unroll
-  for (int j = 0; j < kTT; ++j) {
-    const int64_t t = t0 + 16 * j + (lane & 15);
-    xo[j] = t < a.tokens ? (uint32_t)(t * a.k + 16 * (lane >> 4)) : kGluOOB;
-  }
-  v4i c[kTT][4];
-#pragma unroll
-  for (int j = 0; j < kTT; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[j][i] = v4i{0, 0, 0, 0};
+  for (int i = 0; i < 4; ++i) c[i] = v4i{0, 0, 0, 0};
   __syncthreads();
   for (int kb = first; kb < nkb; kb += 8) {
     uint32_t w[block_bytes(S) / 4];
     load_chunk_at<S>(pr, (uint32_t)(kb * kSb + lane * block_bytes(S)), w);
-    v4i b[kTT][2];
+    v4i b[2];
 #pragma unroll
-    for (int j = 0; j < kTT; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        b[j][h] = load_b128(xr, xo[j] == kGluOOB ? kGluOOB : xo[j] + (uint32_t)(kb * kBlockK + 64 * h));
+    for (int h = 0; h < 2; ++h) b[h] = load_b128(xr, xo == kGluOOB ? kGluOOB : xo + (uint32_t)(kb * kBlockK + 64 * h));
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v4i op = chunk_operand<S>(w, 2 * i + h, lut_lane);
-#pragma unroll
-        for (int j = 0; j < kTT; ++j) c[j][i] = mfma_i8(op, b[j][h], c[j][i]);
-      }
+      for (int h = 0; h < 2; ++h) c[i] = mfma_i8(chunk_operand<S>(w, 2 * i + h, lut_lane), b[h], c[i]);
   }
   const double gg = ld_global(a.gate_gamma), gu = ld_global(a.up_gamma);
+  __syncthreads();  // the tables are read
 #pragma unroll
-  for (int j = 0; j < kTT; ++j) {
-    __syncthreads();  // tables, or the sums of the tile before, are read
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<v4i*>(&lds[(wave * 16 + (lane & 15)) * kSmallPitch + 16 * i + 4 * (lane >> 4)]) = c[i];
+  __syncthreads();
+  const int64_t token = t0 + wave;
+  int sums[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<v4i*>(&lds[(wave * 16 + (lane & 15)) * kSmallPitch + 16 * i + 4 * (lane >> 4)]) = c[j][i];
-    __syncthreads();
-    const int64_t token = t0 + 16 * j + wave;
-    int sums[2] = {0, 0};
+  for (int z = 0; z < 16; ++z) sums[z >> 3] += lds[(z * 16 + wave) * kSmallPitch + lane];
+  if (token < a.tokens) {
+    const float s = ld_global(a.x_scale + token);
+    glu_output<kAct>(a, out_value(sums[0], out_scale(gg, s)), out_value(sums[1], out_scale(gu, s)), token,
+                     strip * kStripRows + lane, lane);
+  }
+}
+
+typedef __attribute__((address_space(3))) char glu_lds_char;
+typedef __attribute__((address_space(3))) void glu_lds_void;
+__device__ __forceinline__ void glu_dma16(__amdgpu_buffer_rsrc_t r, glu_lds_char* dst, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (glu_lds_void*)dst, 16, off, 0, 0, 0);
+}
+template <int N, bool kLds = false>
+__device__ __forceinline__ void glu_wait() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | ((kLds ? 0 : 15) << 8));
+}
+
+// Workgroup barrier behind which LDS writes are seen; loads into registers stay in
+// flight
+__device__ __forceinline__ void glu_barrier() {
+  __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8));  // lgkmcnt(0) only
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// ------------------------------------------------------ forward, some tokens
+// A workgroup computes 16 kRT outputs (of both layers) of up to 128 kTG
+// tokens.  Each wavefront decodes an equal share of a k block's A operands, once for
+// all tokens, into LDS, where all read them.  The activations come to LDS by DMA in
+// whole 128-byte lines, eight rows an instruction (as operands, 16 rows of 64 bytes,
+// straight from memory they bound the kernel: 24.4 us in place of 19.4 at 256 tokens,
+// 2560 x 6912).  One k block (128 k) per barrier: while its products run, the next
+// block's operands are decoded, and the activations two and the codes three blocks
+// on are on their way.  Bound by LDS (operands read by every wavefront, look-ups, the
+// DMA: 700 of the 1100 clocks of a block at 128 tokens) and the way through it
+// between two barriers; fragments read a block ahead, or codes by DMA, gave nothing.  Half a strip (kRT = 2) makes enough workgroups for the CUs; a checkpoint's block
+// of 64 outputs needs a whole one (kRT = 4).
+constexpr int kMidThreads = 512;
+// place of 16-byte piece `piece` (0..7) of activation row `row` in its 128 bytes: reads
+// of 16 rows' pieces as operands are free of bank conflicts (see row64_place)
+__device__ __forceinline__ int row128_place(int row, int piece) { return piece ^ ((row >> 1) & 7); }
+// the stages of the activations, kTokens rows of 128 bytes
+__shared__ __attribute__((aligned(1024))) char g_mid128_st0[128 * 128], g_mid128_st1[128 * 128], g_mid128_st2[128 * 128];
+__shared__ __attribute__((aligned(1024))) char g_mid256_st0[256 * 128], g_mid256_st1[256 * 128], g_mid256_st2[256 * 128];
+template <int kTokens, int P>
+__device__ __forceinline__ char* mid_stage() {
+  static_assert(kTokens == 128 || kTokens == 256, "the stages above");
+  if constexpr (kTokens == 128) return P == 0 ? g_mid128_st0 : P == 1 ? g_mid128_st1 : g_mid128_st2;
+  else return P == 0 ? g_mid256_st0 : P == 1 ? g_mid256_st1 : g_mid256_st2;
+}
+
+template <int S, int kAct, int kRT, int kTG>
+__global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
+  constexpr int kOps = 4 * kRT;       // A operands of a k block: (layer, row tile, k half)
+  constexpr int kShare = kOps / 8;    // of one wavefront
+  constexpr int kTokens = 128 * kTG;
+  // code table copies (8: two workgroups of 128 tokens fit a CU, 14.2 us in place of 17.1
+  // at 128 tokens, 1536 x 8960, where there are more workgroups than CUs; 4% slower
+  // where there are not)
+  constexpr int kMidCopies = kTG == 1 && kRT == 2 ? 8 : 16;
+  constexpr int kX = kTokens / 64;    // DMA instructions of a wavefront and block
+  __shared__ __attribute__((aligned(16))) uint32_t lut[512 * kMidCopies];
+  __shared__ __attribute__((aligned(16))) v4i A[2][kOps * 64];
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int kPer = 4 / kRT;  // workgroups of a strip
+  const int64_t strip = blockIdx.x / kPer;
+  const int part = blockIdx.x % kPer;  // which kRT row tiles of it
+  const int64_t t0 = (int64_t)blockIdx.y * kTokens;
+  const int nkb = (int)(a.k / kBlockK);
+  constexpr int kSb = kStripRows * block_bytes(S);
+  const int64_t at = strip * nkb * (int64_t)kSb;
+  const __amdgpu_buffer_rsrc_t xr = glu_rsrc(a.xq, a.tokens * a.k);
+  // A operand `op`: layer op / (2 kRT), row tile part kRT + op / 2 % kRT, k half op % 2.
+  // Its two fields of a lane's chunk start at bit 2 m (8 + S), m = 2 (row tile) + half: at
+  // most 32 bits, in two words (a word behind the chunk is never used)
+  constexpr int kField = 8 + S;
+  auto field_bit = [&](int op) { return 2 * (2 * (part * kRT + (op >> 1) % kRT) + (op & 1)) * kField; };
+  const __amdgpu_buffer_rsrc_t pr[2] = {glu_rsrc(static_cast<const char*>(a.gate) + at, (int64_t)nkb * kSb),
+                                        glu_rsrc(static_cast<const char*>(a.up) + at, (int64_t)nkb * kSb)};
+  uint32_t w[3][kShare][2];  // codes: block kb's in w[kb % 3], until they are decoded
+  auto load_codes = [&](int kb, uint32_t (&dst)[kShare][2]) {
 #pragma unroll
-    for (int z = 0; z < 16; ++z) sums[z >> 3] += lds[(z * 16 + wave) * kSmallPitch + lane];
-    if (token < a.tokens) {
-      const float s = ld_global(a.x_scale + token);
-      glu_output<kAct>(a, out_value(sums[0], out_scale(gg, s)), out_value(sums[1], out_scale(gu, s)), token,
-                       strip * kStripRows + lane, lane);
+    for (int s = 0; s < kShare; ++s) {
+      const int op = wave * kShare + s;
+      const uint32_t o = (uint32_t)(kb * kSb + lane * block_bytes(S) + (field_bit(op) >> 5) * 4);
+      const __amdgpu_buffer_rsrc_t r = op >= 2 * kRT ? pr[1] : pr[0];
+      dst[s][0] = __builtin_amdgcn_raw_buffer_load_b32(r, kb < nkb ? o : kGluOOB, 0, 0);
+      dst[s][1] = __builtin_amdgcn_raw_buffer_load_b32(r, kb < nkb ? o + 4 : kGluOOB, 0, 0);
+    }
+  };
+  const uint32_t* lut_lane = lut + (lane & (kMidCopies - 1));
+  auto look_up = [&](const uint32_t (&src)[kShare][2], v4i (&v)[kShare]) {
+#pragma unroll
+    for (int s = 0; s < kShare; ++s) {
+      const uint32_t f = funnel(src[s][1], src[s][0], field_bit(wave * kShare + s) & 31);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t x = f >> (e * kField);
+        v[s][2 * e] = (int)lut_lane[((x & 0xffu) * 2 + 0) * kMidCopies];
+        v[s][2 * e + 1] = (int)lut_lane[((x >> S & 0xffu) * 2 + 1) * kMidCopies];
+      }
+    }
+  };
+  auto put = [&](const v4i (&v)[kShare], v4i* to) {
+#pragma unroll
+    for (int s = 0; s < kShare; ++s) to[(wave * kShare + s) * 64 + lane] = v[s];
+  };
+  uint32_t xo[kX];
+#pragma unroll
+  for (int q = 0; q < kX; ++q) {
+    const int row = 8 * (wave * kX + q) + (lane >> 3);
+    const int64_t t = t0 + row;
+    xo[q] = t < a.tokens ? (uint32_t)(t * a.k + 16 * row128_place(row, lane & 7)) : kGluOOB;
+  }
+  auto load_x = [&](auto stage, int kb) {
+    glu_lds_char* st = (glu_lds_char*)mid_stage<kTokens, decltype(stage)::value>();
+#pragma unroll
+    for (int q = 0; q < kX; ++q)
+      glu_dma16(xr, st + 1024 * (wave * kX + q), xo[q] == kGluOOB || kb >= nkb ? kGluOOB : xo[q] + (uint32_t)(kb * kBlockK));
+  };
+  uint32_t tv[512 * kMidCopies / 4 / kMidThreads];
+#pragma unroll
+  for (int r = 0; r < 512 * kMidCopies / 4 / kMidThreads; ++r)
+    tv[r] = ld_global(&kHalfCodeTable.v[(tid + kMidThreads * r) / (kMidCopies / 4)]);
+  load_codes(0, w[0]);
+  load_codes(1, w[1]);
+  load_codes(2, w[2]);
+  load_x(std::integral_constant<int, 0>{}, 0);
+  load_x(std::integral_constant<int, 1>{}, 1);
+#pragma unroll
+  for (int r = 0; r < 512 * kMidCopies / 4 / kMidThreads; ++r)
+    reinterpret_cast<u32x4*>(lut)[tid + kMidThreads * r] = u32x4{tv[r], tv[r], tv[r], tv[r]};
+  v4i c[2 * kRT][kTG];
+#pragma unroll
+  for (int i = 0; i < 2 * kRT; ++i)
+#pragma unroll
+    for (int j = 0; j < kTG; ++j) c[i][j] = v4i{0, 0, 0, 0};
+  __syncthreads();
+  v4i next[kShare];
+  look_up(w[0], next);
+  put(next, A[0]);
+  glu_wait<kX, true>();  // block 0's activations
+  glu_barrier();
+  // block kb: its operands are in A[kb % 2], its activations in stage kb % 3; blocks past
+  // the last read zeros and are not used
+  const uint32_t x_at = (uint32_t)((16 * wave * kTG + l16) * 128);
+  auto block = [&](auto number, int kb) {
+    constexpr int U = decltype(number)::value, P = U & 1;
+    load_codes(kb + 3, w[U % 3]);
+    load_x(std::integral_constant<int, (U + 2) % 3>{}, kb + 2);
+    // (fences: left alone the compiler moved the loads to where they are used and
+    // read each operand after the products of the one before)
+    __builtin_amdgcn_sched_barrier(0);
+    const glu_lds_char* st = (const glu_lds_char*)mid_stage<kTokens, U % 3>() + x_at;
+    v4i op[2 * kRT][2], b[kTG][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < kTG; ++j)
+        b[j][h] = *reinterpret_cast<const __attribute__((address_space(3))) v4i*>(
+            st + 2048 * j + 16 * row128_place(l16, 4 * h + lg));
+#pragma unroll
+      for (int i = 0; i < 2 * kRT; ++i) op[i][h] = A[P][(2 * i + h) * 64 + lane];
+    }
+    look_up(w[(U + 1) % 3], next);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 2 * kRT; ++i)
+#pragma unroll
+        for (int j = 0; j < kTG; ++j) c[i][j] = mfma_i8(op[i][h], b[j][h], c[i][j]);
+    put(next, A[P ^ 1]);
+    __builtin_amdgcn_sched_barrier(0);
+    glu_wait<2 * kShare + kX, true>();  // the next block's activations
+    glu_barrier();
+  };
+  int kb = 0;
+  for (; kb + 5 < nkb; kb += 6) {
+    block(std::integral_constant<int, 0>{}, kb);
+    block(std::integral_constant<int, 1>{}, kb + 1);
+    block(std::integral_constant<int, 2>{}, kb + 2);
+    block(std::integral_constant<int, 3>{}, kb + 3);
+    block(std::integral_constant<int, 4>{}, kb + 4);
+    block(std::integral_constant<int, 5>{}, kb + 5);
+  }
+  if (kb < nkb) block(std::integral_constant<int, 0>{}, kb);
+  if (kb + 1 < nkb) block(std::integral_constant<int, 1>{}, kb + 1);
+  if (kb + 2 < nkb) block(std::integral_constant<int, 2>{}, kb + 2);
+  if (kb + 3 < nkb) block(std::integral_constant<int, 3>{}, kb + 3);
+  if (kb + 4 < nkb) block(std::integral_constant<int, 4>{}, kb + 4);
+  glu_wait<0>();  // no DMA outlives the workgroup
+  // lane: outputs n0 + 16 i + 4 lg + q (i < kRT: gate, i + kRT: up) of token 16 j + l16 of the
+  // wavefront's
+  const double gg = ld_global(a.gate_gamma), gu = ld_global(a.up_gamma);
+  const int64_t n0 = strip * kStripRows + 16 * kRT * part;
+#pragma unroll
+  for (int j = 0; j < kTG; ++j) {
+    const int64_t token = t0 + 16 * (wave * kTG + j) + l16;
+    const bool in = token < a.tokens;
+    const float s = in ? ld_global(a.x_scale + token) : 0.f;
+    const float sg = out_scale(gg, s), su = out_scale(gu, s);
+    const int64_t e = token * a.n_out + n0 + 4 * lg;
+    float g[4 * kRT], u[4 * kRT];
+#pragma unroll
+    for (int i = 0; i < kRT; ++i) {
+      float h[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        g[4 * i + q] = out_value(c[i][j][q], sg);
+        u[4 * i + q] = out_value(c[i + kRT][j][q], su);
+        h[q] = act_value<kAct>(g[4 * i + q]) * u[4 * i + q];
+      }
+      if (in) st_global(reinterpret_cast<u32x2*>(a.H + e + 16 * i), u32x2{pair_bf16(h[0], h[1]), pair_bf16(h[2], h[3])});
+    }
+    if (a.save != kSaveNone) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const float* x = z ? u : g;
+        void* out = z ? a.U : a.G;
+        if (kRT == 4 && a.save == kRowQ8) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 4 * kRT; ++i) top = max_u(top, abs_bits(x[i]));
+          top = max_u(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+          top = max_u(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+          const CkptScale cs = ckpt_scale(top);
+          if (!in) continue;
+#pragma unroll
+          for (int i = 0; i < kRT; ++i) {
+            uint32_t word = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) word |= ckpt_code(x[4 * i + q], cs.inv) << (8 * q);
+            st_global(reinterpret_cast<uint32_t*>(static_cast<int8_t*>(out) + e + 16 * i), word);
+          }
+          if (lg == 0) st_global((z ? a.Us : a.Gs) + (token * a.n_out + n0) / kCkptBlock, cs.scale);
+        } else if (in) {
+#pragma unroll
+          for (int i = 0; i < kRT; ++i) {
+            if (a.save == kRowF32)
+              st_global(reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + e + 16 * i),
+                        f32x4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
+            else
+              st_global(reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + e + 16 * i),
+                        u32x2{pair_bf16(x[4 * i], x[4 * i + 1]), pair_bf16(x[4 * i + 2], x[4 * i + 3])});
+          }
+        }
+      }
     }
   }
 }
@@ -275,17 +507,6 @@ __global__ __launch_bounds__(kDecodeThreads) void glu_decode_kernel(const char* 
     st_global(dst, v0);
     st_global(dst + 64, v1);
   }
-}
-
-typedef __attribute__((address_space(3))) char glu_lds_char;
-typedef __attribute__((address_space(3))) void glu_lds_void;
-__device__ __forceinline__ void glu_dma16(__amdgpu_buffer_rsrc_t r, glu_lds_char* dst, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (glu_lds_void*)dst, 16, off, 0, 0, 0);
-}
-template <int N, bool kLds = false>
-__device__ __forceinline__ void glu_wait() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | ((kLds ? 0 : 15) << 8));
 }
 
 // LDS of the stages: separate objects, so that the compiler sees that reads of one
@@ -619,21 +840,28 @@ __global__ __launch_bounds__(256) void glu_gate_bwd_kernel(GluBwdArgs a, GluBwdL
 }
 
 // ------------------------------------------------------------------ host
-// From kGluManyTokens tokens on the codes are decoded once for all.
-constexpr int64_t kGluManyTokens = 192;
+// Up to kGluFewTokens tokens every 16 have workgroups of their own (96 tokens of
+// 896 x 4864, 1536 x 8960, 2560 x 6912: 6.1, 12.3, 13.3 us, by the kernel for some
+// tokens 6.9, 14.1, 13.9; 128 tokens: 8.3, 15.1, 16.6 and 7.1, 14.4, 14.4).  From
+// kGluManyTokens on the codes are decoded once for all (256 tokens: 9.7, 24.6, 19.7 us for
+// some, 16.9, 27.3, 32.1 for many; 320: 16.7, 34.5, 35.6 and 17.1, 28.0, 32.5).
+constexpr int64_t kGluFewTokens = 96, kGluManyTokens = 257;
 size_t glu_ws_bytes(int64_t tokens, int64_t k, int64_t n_out) {
   return tokens < kGluManyTokens ? 0 : (size_t)(2 * n_out * k + (tokens + 15) / 16 * 16 * k);
 }
 
 template <int S, int kAct>
 static hipError_t glu_launch(const GluArgs& a, void* ws, hipStream_t s) {
+  const unsigned strips = (unsigned)(a.n_out / kStripRows);
+  const auto blocks_of = [&](int tokens) { return (unsigned)((a.tokens + tokens - 1) / tokens); };
+  if (a.tokens <= kGluFewTokens) {
+    glu_small_kernel<S, kAct><<<dim3(strips, blocks_of(16)), 1024, 0, s>>>(a);
+    return hipGetLastError();
+  }
   if (a.tokens < kGluManyTokens) {
-    const unsigned strips = (unsigned)(a.n_out / kStripRows);
-    const int tiles = a.tokens <= 16 ? 1 : a.tokens <= 32 ? 2 : 4;
-    const dim3 grid(strips, (unsigned)((a.tokens + 16 * tiles - 1) / (16 * tiles)));
-    if (tiles == 1) glu_small_kernel<S, kAct, 1><<<grid, 1024, 0, s>>>(a);
-    else if (tiles == 2) glu_small_kernel<S, kAct, 2><<<grid, 1024, 0, s>>>(a);
-    else glu_small_kernel<S, kAct, 4><<<grid, 1024, 0, s>>>(a);
+    if (a.save == kRowQ8) glu_mid_kernel<S, kAct, 4, 1><<<dim3(strips, blocks_of(128)), kMidThreads, 0, s>>>(a);
+    else if (a.tokens <= 128) glu_mid_kernel<S, kAct, 2, 1><<<dim3(2 * strips, 1), kMidThreads, 0, s>>>(a);
+    else glu_mid_kernel<S, kAct, 2, 2><<<dim3(2 * strips, 1), kMidThreads, 0, s>>>(a);
     return hipGetLastError();
   }
   const int nkb = (int)(a.k / kBlockK);

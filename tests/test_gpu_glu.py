@@ -53,6 +53,7 @@ def check_h(H, g, u, act):
 @pytest.mark.parametrize("t,k,n_out,nm", [
     (1, 128, 128, (6, 8)), (2, 256, 384, (8, 8)), (7, 896, 128, (2, 4)), (16, 1152, 256, (3, 8)), (17, 384, 640, (2, 8)),
     (31, 1024, 128, (4, 8)), (33, 640, 256, (6, 8)), (64, 2560, 128, (6, 8)), (65, 128, 512, (8, 8)), (130, 1536, 384, (4, 8)),
+    (96, 384, 256, (2, 8)), (97, 768, 128, (3, 8)), (200, 1152, 128, (2, 4)), (256, 640, 256, (4, 8)),
     (257, 512, 1152, (6, 8)), (300, 896, 640, (2, 4)), (520, 640, 256, (2, 8)), (1025, 256, 384, (3, 8))])
 def test_forward(t, k, n_out, nm, act):
     pair = layers(k, n_out, *nm, seed=t)
@@ -74,7 +75,7 @@ def test_forward(t, k, n_out, nm, act):
                 assert np.array_equal(host(v), want if keep == "f32" else R.bf16(want))
 
 
-@pytest.mark.parametrize("t", [1, 16, 40, 200, 700])
+@pytest.mark.parametrize("t", [1, 16, 40, 128, 200, 700])
 def test_forward_equals_the_layers_one_by_one(t):
     """The existing path: two contractions, then the gating with its own pass."""
     k, n_out = 1280, 640
