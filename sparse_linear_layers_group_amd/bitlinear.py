@@ -8,6 +8,7 @@ computation runs in the HIP library; if the library is not built, loading
 fails with an error -- there is no fallback path.
 """
 import ctypes
+import functools
 import os
 import re
 
@@ -745,6 +746,16 @@ def _blocks(n):
 _KINDS = {torch.float32: BL_TYPE_F32, torch.bfloat16: BL_TYPE_BF16}
 
 
+def _stream_on(stream, dev):
+    """_stream, for a caller that knows the current device."""
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+
+
+# Sizes that short calls ask for every time: what the C functions answered for the same
+# integers (0 for an unsupported layer).
+_packed_bytes = functools.lru_cache(maxsize=1024)(bitlinear_packed_bytes)
+
+
 def _kind(t, name):
     """BL_TYPE_* of one float32 or bfloat16 tensor."""
     kind = _KINDS.get(getattr(t, "dtype", None))
@@ -758,7 +769,7 @@ def bitlinear_ckpt_pack(X, rows, n, codes, scales, stream=None):
     x, xs, _ = _rows(X, _FLOATS, n, "X", dev, rows)
     st = lib().bitlinear_ckpt_pack(
         x, _kind(X, "X"), xs, rows, n, _arg(codes, _I8T, rows * n, "codes", dev),
-        _arg(scales, _F32T, rows * _blocks(n), "scales", dev), _stream(stream))
+        _arg(scales, _F32T, rows * _blocks(n), "scales", dev), _stream_on(stream, dev))
     _check(st, "bitlinear_ckpt_pack")
 
 
@@ -767,7 +778,7 @@ def bitlinear_ckpt_unpack(codes, scales, rows, n, Y, stream=None):
     dev = torch.cuda.current_device()
     st = lib().bitlinear_ckpt_unpack(
         _arg(codes, _I8T, rows * n, "codes", dev), _arg(scales, _F32T, rows * _blocks(n), "scales", dev), rows, n,
-        _arg(Y, _FLOATS, rows * n, "Y", dev), _kind(Y, "Y"), _stream(stream))
+        _arg(Y, _FLOATS, rows * n, "Y", dev), _kind(Y, "Y"), _stream_on(stream, dev))
     _check(st, "bitlinear_ckpt_unpack")
 
 
@@ -782,7 +793,7 @@ def bitlinear_layernorm(X, rows, n, weight, bias, eps, center, Y, mean=None, rst
         x, _kind(X, "X"), xs, rows, n, _opt(weight, _F32T, n, "weight", dev), _opt(bias, _F32T, n, "bias", dev), eps,
         int(bool(center)), _arg(Y, _FLOATS, rows * n, "Y", dev), _kind(Y, "Y"), _opt(mean, _F32T, rows, "mean", dev),
         _opt(rstd, _F32T, rows, "rstd", dev), _opt(codes, _I8T, rows * n, "codes", dev),
-        _opt(scales, _F32T, rows * _blocks(n), "scales", dev), _stream(stream))
+        _opt(scales, _F32T, rows * _blocks(n), "scales", dev), _stream_on(stream, dev))
     _check(st, "bitlinear_layernorm")
 
 
@@ -808,7 +819,7 @@ def bitlinear_layernorm_bwd(X, x_scales, rows, n, weight, mean, rstd, dY, dX, dw
         _opt(weight, _F32T, n, "weight", dev), _opt(mean, _F32T, rows, "mean", dev), _arg(rstd, _F32T, rows, "rstd", dev),
         _arg(dY, _FLOATS, rows * n, "dY", dev), _kind(dY, "dY"), _opt(dR, _FLOATS, rows * n, "dR", dev),
         _arg(dX, _FLOATS, rows * n, "dX", dev), dx_type, _opt(dweight, _F32T, n, "dweight", dev),
-        _opt(dbias, _F32T, n, "dbias", dev), w, wn, _stream(stream))
+        _opt(dbias, _F32T, n, "dbias", dev), w, wn, _stream_on(stream, dev))
     _check(st, "bitlinear_layernorm_bwd")
 
 
@@ -824,8 +835,13 @@ def _saved(G, G_scales, U, U_scales, tokens, n_out, dev):
             _arg(U, (kind,), n, "U", dev), _opt(U_scales, _F32T, ns, "U_scales", dev))
 
 
+@functools.lru_cache(maxsize=1024)
+def _glu_ws_bytes(tokens, k, n_out):
+    return int(lib().bitlinear_glu_workspace_bytes(tokens, k, n_out))
+
+
 def bitlinear_glu_workspace_bytes(tokens, k, n_out):
-    return int(lib().bitlinear_glu_workspace_bytes(int(tokens), int(k), int(n_out)))
+    return _glu_ws_bytes(int(tokens), int(k), int(n_out))
 
 
 def bitlinear_glu(xq, x_scale, tokens, k, gate, gate_gamma, up, up_gamma, n_out, n, m, act, H, G=None, G_scales=None,
@@ -842,14 +858,14 @@ def bitlinear_glu(xq, x_scale, tokens, k, gate, gate_gamma, up, up_gamma, n_out,
         _arg(xq, _I8T, tokens * k, "xq", dev), _arg(x_scale, _F32T, tokens, "x_scale", dev), tokens, k,
         _packed(gate, n_out, k, n, m, "gate", dev), _arg(gate_gamma, _F64T, 1, "gate_gamma", dev),
         _packed(up, n_out, k, n, m, "up", dev), _arg(up_gamma, _F64T, 1, "up_gamma", dev), n_out, n, m, act,
-        _arg(H, _BF16, tokens * n_out, "H", dev), *saved, w, wn, _stream(stream))
+        _arg(H, _BF16, tokens * n_out, "H", dev), *saved, w, wn, _stream_on(stream, dev))
     _check(st, "bitlinear_glu")
 
 
 def _packed(t, n_out, k, n, m, name, dev):
     """Packed codes of an [n_out, k] layer (an unsupported layer is refused by
     the call itself)."""
-    return _arg(t, _U8T, bitlinear_packed_bytes(n_out, k, n, m) or None, name, dev)
+    return _arg(t, _U8T, _packed_bytes(n_out, k, n, m) or None, name, dev)
 
 
 def bitlinear_glu_bwd_workspace_bytes(tokens, k, n_out):
@@ -872,5 +888,5 @@ def bitlinear_glu_bwd(dH, G, G_scales, U, U_scales, xq, x_scale, gate, gate_gamm
         _packed(gate, n_out, k, n, m, "gate", dev), _arg(gate_gamma, _F64T, 1, "gate_gamma", dev),
         _packed(up, n_out, k, n, m, "up", dev), _arg(up_gamma, _F64T, 1, "up_gamma", dev), tokens, k, n_out, n, m, act,
         grad_type, _opt(dX, _FLOATS, tokens * k, "dX", dev), _opt(dW_gate, _FLOATS, n_out * k, "dW_gate", dev),
-        _opt(dW_up, _FLOATS, n_out * k, "dW_up", dev), w, wn, _stream(stream))
+        _opt(dW_up, _FLOATS, n_out * k, "dW_up", dev), w, wn, _stream_on(stream, dev))
     _check(st, "bitlinear_glu_bwd")
