@@ -38,71 +38,100 @@ __device__ __forceinline__ float rstd_of(float var, float eps) {
   return v < __builtin_inff() ? __builtin_amdgcn_rsqf(v) : __builtin_nanf("");
 }
 
+// Forward.  Up to 2560 values a row is a wavefront's, four rows a workgroup, and the
+// weights come from L2 behind the sums (kept in registers from the start they
+// cost wavefronts: 4096 x 2560 binary32 with a checkpoint 18.6 us, so 16.4 us for 95
+// MB).  Longer rows are 256 threads'; from 4097 to 12288 values a workgroup walks over
+// rows with the weights and bias in registers, as many workgroups as the CUs hold: 2049 x
+// 8960 bf16 17.4 us for 73 MB, 4.2 TB/s (a workgroup for each row, which reads 72 KB of
+// parameters for its 18 KB: 20.3).  8192 x 6144 binary32 47.5 us (56.0).  Shorter rows
+// gain nothing by it (8192 x 4096 bf16 22.9 us either way), and longer ones leave too
+// few wavefronts (2048 x 16384 bf16 29.2 us without, 35.3 with).
+constexpr int norm_walkers(int threads, int values) {  // workgroups, or 0 for one a row
+  return threads < 256 || values < 3 || values > 6 ? 0 : values < 5 ? 768 : 512;
+}
 template <int T, int kThreads, int kV>
-__global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void layernorm_kernel(NormArgs a) {
-  constexpr int kRows = kThreads < 256 ? 256 / kThreads : 1;  // rows of a workgroup
-  __shared__ float red[2][8];
+__global__ __launch_bounds__(256) void layernorm_kernel(NormArgs a) {
+  constexpr int kRows = 256 / kThreads;  // rows of a workgroup
+  constexpr bool kWalk = norm_walkers(kThreads, kV) > 0;
+  __shared__ float red[4][8];
   const int tid = kRows > 1 ? threadIdx.x % kThreads : threadIdx.x, lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * kRows + (kRows > 1 ? threadIdx.x / kThreads : 0);
+  int64_t row = (int64_t)blockIdx.x * kRows + (kRows > 1 ? threadIdx.x / kThreads : 0);
   if (row >= a.rows) return;  // whole wavefronts, and no barrier follows where a workgroup has several rows
   Raw8<T> raw[kV];
   bool in[kV];
+  const auto load = [&](int64_t r) {
 #pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    const int64_t e = 8 * ((int64_t)i * kThreads + tid);
-    in[i] = e < a.n;
-    raw[i].zero();
-    if (in[i]) raw[i].load(a.X, row * a.x_stride + e);
+    for (int i = 0; i < kV; ++i) {
+      const int64_t e = 8 * ((int64_t)i * kThreads + tid);
+      in[i] = e < a.n;
+      raw[i].zero();
+      if (in[i] && r < a.rows) raw[i].load(a.X, r * a.x_stride + e);
+    }
+  };
+  load(row);
+  Raw8<kRowF32> w[kWalk ? kV : 1], b[kWalk ? kV : 1];
+  if (kWalk) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      if (in[i] && a.weight) w[kWalk ? i : 0].load(a.weight, 8 * ((int64_t)i * kThreads + tid));
+      if (in[i] && a.bias) b[kWalk ? i : 0].load(a.bias, 8 * ((int64_t)i * kThreads + tid));
+    }
   }
-  float mean = 0.f;
   const float inv_n = 1.f / (float)a.n;
-  if (a.center) {
-    float s = 0.f;
+  int slot = 0;
+  do {
+    float mean = 0.f;
+    if (a.center) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < kV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += raw[i].get(j, 0.f);
+      mean = RowSums<kThreads>::sum(s, red, slot, threadIdx.x >> 6) * inv_n;
+    }
+    float q = 0.f;
 #pragma unroll
     for (int i = 0; i < kV; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += raw[i].get(j, 0.f);
-    mean = RowSums<kThreads>::sum(s, red, 0, threadIdx.x >> 6) * inv_n;
-  }
-  float q = 0.f;
-#pragma unroll
-  for (int i = 0; i < kV; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float d = raw[i].get(j, 0.f) - mean;
-      q = in[i] ? fmaf(d, d, q) : q;
+      for (int j = 0; j < 8; ++j) {
+        const float d = raw[i].get(j, 0.f) - mean;
+        q = in[i] ? fmaf(d, d, q) : q;
+      }
+    const float rstd = rstd_of(RowSums<kThreads>::sum(q, red, slot + 1, threadIdx.x >> 6) * inv_n, a.eps);
+    slot ^= 2;  // a row's sums are read before the barriers of the next row's, which use the other slots
+    if (tid == 0) {
+      if (a.mean) st_global(a.mean + row, mean);
+      if (a.rstd) st_global(a.rstd + row, rstd);
     }
-  const float rstd = rstd_of(RowSums<kThreads>::sum(q, red, 1, threadIdx.x >> 6) * inv_n, a.eps);
-  if (tid == 0) {
-    if (a.mean) st_global(a.mean + row, mean);
-    if (a.rstd) st_global(a.rstd + row, rstd);
-  }
 #pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    const int64_t e = 8 * ((int64_t)i * kThreads + tid);
-    float x[8], y[8];
+    for (int i = 0; i < kV; ++i) {
+      const int64_t e = 8 * ((int64_t)i * kThreads + tid);
+      float x[8], y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = raw[i].get(j, 0.f);
-    if (a.codes)
-      ckpt_store8(x, in[i], lane, a.codes + row * a.n + e,
-                  a.scales + row * ((a.n + kCkptBlock - 1) / kCkptBlock) + e / kCkptBlock);
-    if (!in[i]) continue;
+      for (int j = 0; j < 8; ++j) x[j] = raw[i].get(j, 0.f);
+      if (a.codes)
+        ckpt_store8(x, in[i], lane, a.codes + row * a.n + e,
+                    a.scales + row * ((a.n + kCkptBlock - 1) / kCkptBlock) + e / kCkptBlock);
+      if (!in[i]) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = (x[j] - mean) * rstd;
-    if (a.weight) {
-      Raw8<kRowF32> w;
-      w.load(a.weight, e);
+      for (int j = 0; j < 8; ++j) y[j] = (x[j] - mean) * rstd;
+      if (a.weight) {
+        if (!kWalk) w[0].load(a.weight, e);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] *= w.get(j, 0.f);
+        for (int j = 0; j < 8; ++j) y[j] *= w[kWalk ? i : 0].get(j, 0.f);
+      }
+      if (a.bias) {
+        if (!kWalk) b[0].load(a.bias, e);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] += b[kWalk ? i : 0].get(j, 0.f);
+      }
+      store_row8(a.Y, a.y_type, row * a.n + e, y);
     }
-    if (a.bias) {
-      Raw8<kRowF32> b;
-      b.load(a.bias, e);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] += b.get(j, 0.f);
-    }
-    store_row8(a.Y, a.y_type, row * a.n + e, y);
-  }
+    if (!kWalk) return;
+    row += gridDim.x;
+    load(row);
+  } while (row < a.rows);
 }
 
 // Backward of rows: with n = (x - mean) rstd and a = w dy,
@@ -113,15 +142,23 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void layernorm_ker
 // norm_dw_kernel adds in binary64.  No atomics: reruns give the same bits.
 // Bound by memory.  The sums take so many registers that two wavefronts fit a SIMD,
 // so each keeps the next row's x and dy on their way while it sums and writes
-// its row (with 32 values a thread there are no registers left for that).  4096 x
-// 2560, 8-bit x, bf16 dy, binary32 dR and dX: 27.4 us for 115 MB, 4.2 TB/s (one
-// wavefront a row, 40 values a lane, nothing ahead: 42.0); 2049 x 8960 bf16 with
-// binary32 dy and bias: 38.5 us, 3.8 TB/s (45.4).
+// its row (with 32 values a thread there are no registers left for that).  The weights
+// lie in LDS (from L2 for each row: 27.4 and 38.0 us below).  4096 x 2560, 8-bit x,
+// bf16 dy, binary32 dR and dX: 25.7 us for 115 MB, 4.5 TB/s (one wavefront a row, 40
+// values a lane, nothing ahead: 42.0); 2049 x 8960 bf16 with binary32 dy and bias: 36.4
+// us, 4.0 TB/s (45.4).
 template <int T, int D, int kThreads, int kV, bool kBias>
 __global__ __launch_bounds__(512) void layernorm_bwd_kernel(NormBwdArgs a) {
   constexpr int kRows = 512 / kThreads;  // rows of a workgroup at a time
   __shared__ float red[4][8];
   constexpr bool kAhead = kV < 4;
+  __shared__ __attribute__((aligned(16))) f32x4_t weight[kThreads * kV * 2];
+  for (int c = threadIdx.x; c < kThreads * kV * 2; c += 512) {
+    f32x4_t v{1.f, 1.f, 1.f, 1.f};
+    if (a.weight && 4 * c < a.n) v = ld_global(reinterpret_cast<const f32x4_t*>(a.weight) + c);
+    weight[c] = v;
+  }
+  __syncthreads();
   const int tid = kRows > 1 ? threadIdx.x % kThreads : threadIdx.x;
   const int group = kRows > 1 ? threadIdx.x / kThreads : 0, wave = threadIdx.x >> 6;
   const float inv_n = 1.f / (float)a.n;
@@ -178,9 +215,7 @@ __global__ __launch_bounds__(512) void layernorm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       const int64_t e = 8 * ((int64_t)i * kThreads + tid);
-      Raw8<kRowF32> w;
-      if (a.weight && e < a.n) w.load(a.weight, e);
-      else w.a = w.b = f32x4_t{1.f, 1.f, 1.f, 1.f};
+      const Raw8<kRowF32> w{weight[e / 4], weight[e / 4 + 1]};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // threads past the row hold dy = 0, and n = 0
@@ -339,9 +374,11 @@ __global__ __launch_bounds__(256) void ckpt_unpack_kernel(const int8_t* __restri
 // whose sums and whose next row's inputs fit its registers.
 template <int T, int kThreads, int kV>
 static hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
-  constexpr int kRows = kThreads < 256 ? 256 / kThreads : 1;
-  layernorm_kernel<T, kThreads, kV>
-      <<<(unsigned)((a.rows + kRows - 1) / kRows), kThreads < 256 ? 256 : kThreads, 0, s>>>(a);
+  constexpr int kRows = 256 / kThreads;
+  int64_t blocks = (a.rows + kRows - 1) / kRows;
+  constexpr int kWalkers = norm_walkers(kThreads, kV);
+  if (kWalkers && blocks > kWalkers) blocks = kWalkers;
+  layernorm_kernel<T, kThreads, kV><<<(unsigned)blocks, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 template <int T>
