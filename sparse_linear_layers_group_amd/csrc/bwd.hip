@@ -20,6 +20,7 @@
 #include "bitlinear.h"
 #include "common.h"
 #include "glu.h"
+#include "glu_gate.h"
 #include "launch.h"
 
 #include <algorithm>
@@ -79,7 +80,6 @@ struct PrepTask {
   uint16_t* out;
   int64_t rows, cols, pitch;
   int32_t kind, jobs;
-  int32_t tiled = 0;  // codes and x_q: out in tiles, pitch its depth
 };
 constexpr int kMaxPrep = 16;
 struct PrepSet {
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(256) void prep_group_kernel(PrepSet set) {
     const int64_t sb = 4 * (int64_t)job + (tid >> 6);
     if (sb < tk.rows * tk.cols)
       prep_codes_sb<S>(reinterpret_cast<const uint32_t*>(tk.src), sb, tk.rows, tk.pitch, tk.out, lut,
-                       tid & 63, tk.tiled);
+                       tid & 63, false);
     return;
   }
   const int64_t bx = tk.pitch / 64, t0 = 64 * (job % bx), c0 = 64 * (job / bx);
@@ -254,7 +254,44 @@ __global__ __launch_bounds__(256) void prep_group_kernel(PrepSet set) {
                   t0, c0, tile, tid);
   else
     prep_xq_tile(reinterpret_cast<const int8_t*>(tk.src), tk.rows, tk.cols, tk.pitch, tk.out, t0, c0,
-                 tile, tid, tk.tiled);
+                 tile, tid, false);
+}
+
+// Everything the products of the gated feed-forward's backward read, in one launch:
+// the gating's 64 x 64 tiles, then the codes of both layers, then x_q^T.  Bound by
+// memory: 4096 tokens, 2560 x 6912 6:8, 8-bit G and U, 89 us for 450 MB, 5.0 TB/s
+// (the gating in a launch of its own: 71 + 28); 547 tokens, 896 x 4864: 13.4 (10.4 + 8.0).
+struct GluPrepJobs {
+  int32_t gate, codes, xq;  // codes: of one layer
+};
+template <int S, int kSave, int kAct>
+__global__ __launch_bounds__(256) void glu_prep_kernel(GluBwdArgs a, GluBwdLayout l, GluPrepJobs jobs) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 64 * kGatePitch];
+  static_assert(sizeof(lds) >= sizeof(kHalfBf16Table) && kGatePitch >= kTP, "the table, or a tile of x_q");
+  const int tid = threadIdx.x;
+  int job = (int)blockIdx.x;
+  if (job < jobs.gate) {
+    glu_gate_tile<kSave, kAct>(a, l, job, tid, lds, lds + 64 * kGatePitch);
+    return;
+  }
+  job -= jobs.gate;
+  const int64_t nkb = a.k / kBlockK, n2 = 2 * a.n_out;
+  if (job < 2 * jobs.codes) {
+    const bool up = job >= jobs.codes;
+    u32x2* lut = reinterpret_cast<u32x2*>(lds);
+    reinterpret_cast<u32x4*>(lds)[tid] = ld_global(reinterpret_cast<const u32x4*>(kHalfBf16Table.v) + tid);
+    __syncthreads();
+    const int64_t sb = 4 * (int64_t)(up ? job - jobs.codes : job) + (tid >> 6);
+    // (column n_out of a tiled operand: n_out / 32 blocks of 512 on)
+    uint16_t* out = reinterpret_cast<uint16_t*>(a.ws + l.codes_t) + (up ? 16 * a.n_out : 0);
+    if (sb < a.n_out / kStripRows * nkb)
+      prep_codes_sb<S>(static_cast<const uint32_t*>(up ? a.up : a.gate), sb, nkb, n2, out, lut, tid & 63, true);
+    return;
+  }
+  job -= 2 * jobs.codes;
+  const int64_t tp = bwd_tokens_padded(a.tokens), bx = tp / 64;
+  prep_xq_tile(a.xq, a.tokens, a.k, tp, reinterpret_cast<uint16_t*>(a.ws + l.xq_t), 64 * (job % bx), 64 * (job / bx), lds, tid,
+               true);
 }
 
 // ------------------------------------------------------------- product
@@ -1099,24 +1136,33 @@ hipError_t launch_zero(float* p, int64_t n, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int S>
+static hipError_t glu_prep(const GluBwdArgs& a, const GluBwdLayout& l, hipStream_t s) {
+  const int64_t tb = bwd_tokens_padded(a.tokens) / 64, superblocks = a.n_out / kStripRows * (a.k / kBlockK);
+  GluPrepJobs jobs{};
+  jobs.gate = (int32_t)(tb * (a.n_out / 64));
+  if (a.dX) jobs.codes = (int32_t)((superblocks + 3) / 4);
+  if (a.dWg) jobs.xq = (int32_t)(tb * (a.k / 64));
+  const unsigned grid = (unsigned)(jobs.gate + 2 * jobs.codes + jobs.xq);
+  const auto run = [&](auto save) {
+    constexpr int kSave = decltype(save)::value;
+    if (a.act == kActRelu2) glu_prep_kernel<S, kSave, kActRelu2><<<grid, 256, 0, s>>>(a, l, jobs);
+    else glu_prep_kernel<S, kSave, kActSilu><<<grid, 256, 0, s>>>(a, l, jobs);
+    return hipGetLastError();
+  };
+  if (a.save == kRowF32) return run(std::integral_constant<int, kRowF32>{});
+  return a.save == kRowBf16 ? run(std::integral_constant<int, kRowBf16>{}) : run(std::integral_constant<int, kRowQ8>{});
+}
+
 // The products of the gated feed-forward's backward.  dX is one product of
 // depth 2 n_out: dG gate_gamma and dU up_gamma stand side by side in dgu and so do the two
 // layers' codes in codes_t, so it is written once.  The deepest products' tiles start
 // first.
-hipError_t launch_glu_products(const GluBwdArgs& a, int S, hipStream_t s) {
+hipError_t launch_glu_bwd(const GluBwdArgs& a, int S, hipStream_t s) {
   const GluBwdLayout l = glu_bwd_layout(a.tokens, a.k, a.n_out);
-  const int64_t tp = bwd_tokens_padded(a.tokens), nkb = a.k / kBlockK, strips = a.n_out / kStripRows, n2 = 2 * a.n_out;
+  const int64_t tp = bwd_tokens_padded(a.tokens), n2 = 2 * a.n_out;
   const auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(a.ws + o); };
-  PrepList L;
-  if (a.dX) {
-    const int32_t jobs = (int32_t)((strips * nkb + 3) / 4);
-    L.t.push_back(PrepTask{a.gate, nullptr, at(l.codes_t), nkb, strips, n2, kPrepCodes, jobs, 1});
-    // (column n_out of a tiled operand: n_out / 32 blocks of 512 on)
-    L.t.push_back(PrepTask{a.up, nullptr, at(l.codes_t) + 16 * a.n_out, nkb, strips, n2, kPrepCodes, jobs, 1});
-  }
-  if (a.dWg)
-    L.t.push_back(PrepTask{a.xq, nullptr, at(l.xq_t), a.tokens, a.k, tp, kPrepXq, (int32_t)((tp / 64) * (a.k / 64)), 1});
-  hipError_t e = L.launch(S, s);
+  hipError_t e = S == 8 ? glu_prep<8>(a, l, s) : S == 6 ? glu_prep<6>(a, l, s) : S == 2 ? glu_prep<2>(a, l, s) : glu_prep<4>(a, l, s);
   if (e != hipSuccess) return e;
 
   const bool b16 = a.grad_type == BL_TYPE_BF16;

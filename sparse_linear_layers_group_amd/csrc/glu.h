@@ -78,9 +78,6 @@ inline GluBwdLayout glu_bwd_layout(int64_t tokens, int64_t k, int64_t n_out) {
   return l;
 }
 hipError_t launch_glu_bwd(const GluBwdArgs& a, int S, hipStream_t s);
-// the rest of the backward once dgu, dgs_t and dus_t are written: the other
-// operands, then the products
-hipError_t launch_glu_products(const GluBwdArgs& a, int S, hipStream_t s);
 hipError_t launch_zero(float* p, int64_t n, hipStream_t s);
 
 }  // namespace bl
