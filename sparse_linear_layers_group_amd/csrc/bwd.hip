@@ -858,7 +858,12 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
       if (m + 16 * i >= M || n + 16 * j >= N) continue;
       const int64_t e = (m + 16 * i) * ldc + n + 16 * j;
       const v4f y = value(c[i][j]);
-      if (pr.Cb) st_stream(reinterpret_cast<u32x2*>(pr.Cb + e), bf16x4(y));
+      // (A row's 128 bytes are four stores here.  Streaming ones reach memory one by one:
+      // 64 tokens of the gated feed-forward's backward, 2560 x 6912, bf16 gradients, took
+      // 18 us more, with binary32 ones 8 more.  The layers' own backward keeps them: -1 to
+      // 6 us either way.)
+      if (pr.Cb) st_global(reinterpret_cast<u32x2*>(pr.Cb + e), bf16x4(y));
+      else if (pr.tiled) st_global(reinterpret_cast<v4f*>(C + e), y);
       else st_stream(reinterpret_cast<v4f*>(C + e), y);
     }
 }
@@ -871,10 +876,16 @@ __global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict_
   const double g = alpha ? *alpha : 1.0;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
     v4f acc = ld_global(reinterpret_cast<const v4f*>(P) + i);
-    for (int s = 1; s < splits; ++s) {
-      const v4f v = ld_global(reinterpret_cast<const v4f*>(P) + (int64_t)s * n4 + i);
+    for (int s = 1; s < splits; s += 8) {  // eight planes' loads at a time
+      v4f v[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] += v[e];
+      for (int u = 0; u < 8; ++u)
+        if (s + u < splits) v[u] = ld_global(reinterpret_cast<const v4f*>(P) + (int64_t)(s + u) * n4 + i);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (s + u < splits)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] += v[u][e];
     }
     if (alpha) {
 #pragma unroll
@@ -1183,12 +1194,7 @@ hipError_t launch_glu_bwd(const GluBwdArgs& a, int S, hipStream_t s) {
     add(l.dus_t, l.xq_t, a.dWu, l.planes_u, a.n_out, tp, l.split_w);
   }
   std::stable_sort(set.p, set.p + set.n, [](const NtProblem& x, const NtProblem& y) { return x.K / x.parts > y.K / y.parts; });
-  // Where one round of 256 x 256 tiles does not fill the CUs, twice as many of 256 x
-  // 128, two on a CU (547 tokens, 896 x 4864: 33.4 us in place of 37.4; 4096
-  // tokens, 2560 x 6912, several rounds: 487 in place of 391)
-  int64_t tiles = 0;
-  for (int i = 0; i < set.n; ++i) tiles += nt_tiles_big<4>(set.p[i]);
-  e = launch_big(set, tiles <= 256 ? 2 : 3, s);
+  e = launch_big(set, l.narrow ? 2 : 3, s);
   const auto sum = [&](void* out, size_t planes, int64_t rows, int parts) {
     if (e != hipSuccess || !out || parts == 1) return;
     const int64_t n4 = rows * a.k / 4, blocks = (n4 + 255) / 256;

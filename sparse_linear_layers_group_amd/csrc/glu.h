@@ -48,11 +48,19 @@ struct GluBwdArgs {
 struct GluBwdLayout {
   size_t dgu, dgs_t, dus_t, xq_t, codes_t, planes_x, planes_g, planes_u, bytes;
   int split_x, split_w;  // parts of dX's depth, of each weight gradient's
+  bool narrow;           // tiles of 256 x 128, else 256 x 256
 };
 // All products run in one launch of 256 x 256 tiles, one on a CU.  A product is cut
 // along its depth where it is deeper than a CU's share of all the work, but no
 // part shallower than kGluPart: a part costs a binary32 plane of the output to
-// write and to read.
+// write and to read.  Where one round of such tiles does not fill the CUs, dX, the
+// deepest, is cut into as many parts as do, and the launch takes twice as many tiles of
+// 256 x 128, two on a CU (forward and backward of 32 tokens, 896 x 4864: 35.5 us in
+// place of 39.0; 547 tokens, 8 parts either way, the products alone 33.4 in place of 37.4).
+// Up to 256 tokens, where the weight gradients' tiles are little more than their
+// stores, it takes those too (32 tokens, 1536 x 8960: 58.8 us in place of 65.6, 256
+// tokens: 95.3 and 102.4; 300: 103.3 and 102.9; 4096 tokens, 2560 x 6912, the products
+// alone: 487 in place of 391).
 constexpr int64_t kGluPart = 1024;
 inline int glu_parts(int64_t depth, int64_t share, int most) {
   const int64_t per = share > kGluPart ? share : kGluPart, parts = (depth + per - 1) / per;
@@ -65,6 +73,13 @@ inline GluBwdLayout glu_bwd_layout(int64_t tokens, int64_t k, int64_t n_out) {
   GluBwdLayout l;
   l.split_x = glu_parts(2 * n_out, share, 8);
   l.split_w = glu_parts(tp, share, 4);
+  const int64_t all_w = 2 * tiles_w * l.split_w;
+  const bool one_round = tiles_x * l.split_x + all_w <= 256;
+  if (one_round && tiles_x > 0) {
+    const int64_t room = (256 - all_w) / tiles_x, most = 2 * n_out / 512, parts = room < most ? room : most;
+    l.split_x = (int)(parts > 32 ? 32 : parts > l.split_x ? parts : l.split_x);
+  }
+  l.narrow = one_round || tp <= 256;
   l.dgu = 0;
   l.dgs_t = l.dgu + bwd_align((size_t)tp * 2 * n_out * 2);
   l.dus_t = l.dgs_t + bwd_align((size_t)n_out * tp * 2);

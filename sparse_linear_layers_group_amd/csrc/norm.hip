@@ -40,7 +40,7 @@ __device__ __forceinline__ float rstd_of(float var, float eps) {
 
 // Forward.  Up to 2560 values a row is a wavefront's, four rows a workgroup, and the
 // weights come from L2 behind the sums (kept in registers from the start they
-// cost wavefronts: 4096 x 2560 binary32 with a checkpoint 18.6 us, so 16.4 us for 95
+// cost wavefronts: 4096 x 2560 binary32 with a checkpoint 18.6 us, so 16.4 us for 74
 // MB).  Longer rows are 256 threads'; from 4097 to 12288 values a workgroup walks over
 // rows with the weights and bias in registers, as many workgroups as the CUs hold: 2049 x
 // 8960 bf16 17.4 us for 73 MB, 4.2 TB/s (a workgroup for each row, which reads 72 KB of
