@@ -140,7 +140,11 @@ def values(kept_pair):
     (63, 384, 256, (2, 4), "relu2", "bf16", "bf16", "f32"), (64, 640, 128, (4, 8), "silu", "q8", "f32", "bf16"),
     (65, 128, 1152, (3, 8), "relu2", "f32", "f32", "bf16"), (200, 1024, 2048, (2, 8), "silu", "bf16", "bf16", "f32"),
     (300, 896, 1280, (6, 8), "relu2", "q8", "bf16", "bf16"), (515, 1280, 640, (6, 8), "silu", "q8", "f32", "f32"),
-    (2100, 256, 384, (6, 8), "relu2", "q8", "bf16", "f32"), (1030, 2304, 2560, (4, 8), "relu2", "f32", "f32", "bf16")])
+    (2100, 256, 384, (6, 8), "relu2", "q8", "bf16", "f32"), (1030, 2304, 2560, (4, 8), "relu2", "f32", "f32", "bf16"),
+    # dX in 32 and in 19 parts, few tokens with wide layers, 256 tokens and one more
+    (9, 128, 8704, (6, 8), "relu2", "q8", "bf16", "bf16"), (40, 256, 4992, (8, 8), "silu", "bf16", "f32", "f32"),
+    (33, 1536, 7680, (4, 8), "relu2", "q8", "bf16", "bf16"), (256, 1408, 6400, (6, 8), "relu2", "bf16", "f32", "f32"),
+    (257, 1408, 6400, (6, 8), "silu", "q8", "bf16", "bf16")])
 def test_backward(t, k, n_out, nm, act, keep, dh, grad):
     pair, xq, xs, G, U, dH, out = backward_case(t, k, n_out, nm, act, keep, dh, grad, seed=t)
     backward(pair, xq, xs, G, U, dH, out, k, n_out, act)
@@ -196,6 +200,37 @@ def test_neighbours_stay():
         backward(pair, xq, xs, G, U, dH, [big[0][:t], big[1][:n_out], big[2][:n_out]], k, n_out, "relu2", ws=ws[:need])
         assert (big[0][t:] == 5).all() and (big[1][n_out:] == 5).all() and (big[2][n_out:] == 5).all()
         assert (ws[need:] == 171).all()
+
+
+@pytest.mark.parametrize("t", [5, 70, 300])
+def test_what_the_workspace_held_does_not_matter(t):
+    k, n_out = 384, 640
+    pair, xq, xs, G, U, dH, out = backward_case(t, k, n_out, (6, 8), "relu2", "bf16", "f32", "f32")
+    (gate, _), (up, _) = pair
+    need = bl.bitlinear_glu_workspace_bytes(t, k, n_out), bl.bitlinear_glu_bwd_workspace_bytes(t, k, n_out)
+    got = []
+    for fill in (0, 255):  # 255: NaN in every type
+        ws = [torch.full((n,), fill, dtype=torch.uint8, device="cuda") if n else None for n in need]
+        H, g = empty(t, n_out, dtype=torch.bfloat16), [torch.empty_like(v) for v in out]
+        bl.bitlinear_glu(xq, xs, t, k, gate.packed, gate.gamma, up.packed, up.gamma, n_out, 6, 8, ACT["relu2"], H, ws=ws[0])
+        backward(pair, xq, xs, G, U, dH, g, k, n_out, "relu2", ws=ws[1])
+        got.append([H, *g])
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and all(torch.isfinite(a).all() for a in got[1])
+
+
+def test_a_token_that_is_nan_stays_by_itself():
+    """In dX; the weights' gradients sum over tokens and show it in the outputs' rows it has."""
+    t, k, n_out = 70, 256, 384
+    pair, xq, xs, G, U, dH, out = backward_case(t, k, n_out, (6, 8), "silu", "q8", "f32", "f32")
+    want = [torch.empty_like(v) for v in out]
+    backward(pair, xq, xs, G, U, dH, want, k, n_out, "silu")
+    dH[17, 5] = float("nan")
+    backward(pair, xq, xs, G, U, dH, out, k, n_out, "silu")
+    others = torch.arange(t, device="cuda") != 17
+    rows = torch.arange(n_out, device="cuda") != 5
+    assert torch.equal(out[0][others], want[0][others]) and out[0][17].isnan().any()
+    for a, b in zip(out[1:], want[1:]):
+        assert torch.equal(a[rows], b[rows]) and a[5].isnan().all()
 
 
 def test_refusals_of_tensors():
