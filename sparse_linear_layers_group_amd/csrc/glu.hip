@@ -19,6 +19,8 @@ namespace bl {
 // are the B operands; the sixteen partial sums meet in LDS over the code tables,
 // where each thread then owns one output: a wavefront holds one token's 64
 // outputs, which is one checkpoint block.
+// Bound by latency (launch, tables, one chunk's loads after another, the join): one
+// token, 896 x 4864 6:8, 4.1 us; 16 tokens, 2560 x 6912, 6.0 us for 8 MB.
 constexpr int kSmallCopies = 32;  // code table copies: lane l reads copy l % 32
 constexpr int kSmallPitch = 68;   // int32 of a token's 64 sums, padded
 constexpr uint32_t kGluOOB = 0x80000000u;
@@ -402,9 +404,12 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
 // Both layers' codes are decoded once into int8 (a pass over the weights, some 6%
 // of the products' time at 4096 tokens), and an int8 product runs on tiles of
 // 128 outputs (256 rows: for each 64 outputs their gate rows, then their up
-// rows) x 128 tokens, two workgroups on a CU, so that
-// one's outputs are written under the other's products (256 tokens, one workgroup:
-// 262 us in place of 231 at 6001 tokens, 2048 x 11008).  A wavefront computes 64 outputs of both layers
+// rows) x 128 tokens, two workgroups on a CU, so that one's outputs are written under
+// the other's products (6001 tokens, 2048 x 11008: 214 us, then 234 as the clock
+// falls, 2.3 POPS; one workgroup of 256 tokens took 13 % more; 64 tokens, twice the
+// workgroups, 10 % less at 391 tokens, 1536 x 8960, and up to 28 % more elsewhere).
+// Bound by the way through LDS beside the products: 4096 tokens, 2560 x 6912, 127 us,
+// matrix units busy 54 % of the time.  A wavefront computes 64 outputs of both layers
 // (128 rows) x 64 tokens, so a lane holds g and u of the same outputs and the
 // gating needs no exchange.  Tiles stream through three LDS stages of 64 k
 // filled by LDS DMA; a step's fragments are read from LDS while the matrix
