@@ -173,17 +173,18 @@ __device__ __forceinline__ void glu_barrier() {
 }
 
 // ------------------------------------------------------ forward, some tokens
-// A workgroup computes 16 kRT outputs (of both layers) of up to 128 kTG
-// tokens.  Each wavefront decodes an equal share of a k block's A operands, once for
-// all tokens, into LDS, where all read them.  The activations come to LDS by DMA in
-// whole 128-byte lines, eight rows an instruction (as operands, 16 rows of 64 bytes,
-// straight from memory they bound the kernel: 24.4 us in place of 19.4 at 256 tokens,
-// 2560 x 6912).  One k block (128 k) per barrier: while its products run, the next
-// block's operands are decoded, and the activations two and the codes three blocks
-// on are on their way.  Bound by LDS (operands read by every wavefront, look-ups, the
-// DMA: 700 of the 1100 clocks of a block at 128 tokens) and the way through it
-// between two barriers; fragments read a block ahead, or codes by DMA, gave nothing.  Half a strip (kRT = 2) makes enough workgroups for the CUs; a checkpoint's block
-// of 64 outputs needs a whole one (kRT = 4).
+// A workgroup computes 16 kRT outputs (of both layers) of 128 kTG tokens.  Each
+// wavefront decodes an equal share of a k block's A operands, once for all tokens,
+// into LDS, where all read them.  The activations come to LDS by DMA in whole 128-byte
+// lines, eight rows an instruction (as operands, 16 rows of 64 bytes, straight from
+// memory they bound the kernel: 24.4 us in place of 19.4 at 256 tokens, 2560 x 6912;
+// 17.2 now).  One k block (128 k) per barrier: while its products run, the next
+// block's operands are decoded, and the activations and the codes two blocks on are on
+// their way.  Bound by LDS (operands read by every wavefront, look-ups, the DMA) and
+// the way through it between two barriers; fragments read a block ahead, or codes by
+// DMA, gave nothing, codes three blocks ahead cost 10 %.  Half a strip (kRT = 2) makes
+// enough workgroups for the CUs; a checkpoint's block of 64 outputs needs a whole one
+// (kRT = 4).
 constexpr int kMidThreads = 512;
 // place of 16-byte piece `piece` (0..7) of activation row `row` in its 128 bytes: reads
 // of 16 rows' pieces as operands are free of bank conflicts (see row64_place)
@@ -227,7 +228,7 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
   auto field_bit = [&](int op) { return 2 * (2 * (part * kRT + (op >> 1) % kRT) + (op & 1)) * kField; };
   const __amdgpu_buffer_rsrc_t pr[2] = {glu_rsrc(static_cast<const char*>(a.gate) + at, (int64_t)nkb * kSb),
                                         glu_rsrc(static_cast<const char*>(a.up) + at, (int64_t)nkb * kSb)};
-  uint32_t w[3][kShare][2];  // codes: block kb's in w[kb % 3], until they are decoded
+  uint32_t w[2][kShare][2];  // codes: block kb's in w[kb % 2], until they are decoded
   auto load_codes = [&](int kb, uint32_t (&dst)[kShare][2]) {
 #pragma unroll
     for (int s = 0; s < kShare; ++s) {
@@ -272,11 +273,10 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
 #pragma unroll
   for (int r = 0; r < 512 * kMidCopies / 4 / kMidThreads; ++r)
     tv[r] = ld_global(&kHalfCodeTable.v[(tid + kMidThreads * r) / (kMidCopies / 4)]);
-  load_codes(0, w[0]);
-  load_codes(1, w[1]);
-  load_codes(2, w[2]);
   load_x(std::integral_constant<int, 0>{}, 0);
+  load_codes(0, w[0]);
   load_x(std::integral_constant<int, 1>{}, 1);
+  load_codes(1, w[1]);
 #pragma unroll
   for (int r = 0; r < 512 * kMidCopies / 4 / kMidThreads; ++r)
     reinterpret_cast<u32x4*>(lut)[tid + kMidThreads * r] = u32x4{tv[r], tv[r], tv[r], tv[r]};
@@ -289,15 +289,16 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
   v4i next[kShare];
   look_up(w[0], next);
   put(next, A[0]);
-  glu_wait<kX, true>();  // block 0's activations
+  glu_wait<0>();  // the first two blocks' activations
   glu_barrier();
   // block kb: its operands are in A[kb % 2], its activations in stage kb % 3; blocks past
   // the last read zeros and are not used
   const uint32_t x_at = (uint32_t)((16 * wave * kTG + l16) * 128);
   auto block = [&](auto number, int kb) {
     constexpr int U = decltype(number)::value, P = U & 1;
-    load_codes(kb + 3, w[U % 3]);
     load_x(std::integral_constant<int, (U + 2) % 3>{}, kb + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    load_codes(kb + 2, w[U % 2]);
     // (fences: left alone the compiler moved the loads to where they are used and
     // read each operand after the products of the one before)
     __builtin_amdgcn_sched_barrier(0);
@@ -312,7 +313,7 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
 #pragma unroll
       for (int i = 0; i < 2 * kRT; ++i) op[i][h] = A[P][(2 * i + h) * 64 + lane];
     }
-    look_up(w[(U + 1) % 3], next);
+    look_up(w[(U + 1) % 2], next);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -322,7 +323,9 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
         for (int j = 0; j < kTG; ++j) c[i][j] = mfma_i8(op[i][h], b[j][h], c[i][j]);
     put(next, A[P ^ 1]);
     __builtin_amdgcn_sched_barrier(0);
-    glu_wait<2 * kShare + kX, true>();  // the next block's activations
+    // The next block's activations are there: loads return in order, and its codes, which
+    // were just decoded, were asked for behind them.  (No count of loads in flight: how
+    // many load_codes leaves is the compiler's, which joins some and drops others.)
     glu_barrier();
   };
   int kb = 0;
@@ -731,13 +734,19 @@ __global__ __launch_bounds__(256, 2) void glu_gemm_kernel(GluArgs a, const char*
 
 // ------------------------------------------------------------------ host
 // Up to kGluFewTokens tokens every 16 have workgroups of their own (96 tokens of
-// 896 x 4864, 1536 x 8960, 2560 x 6912: 6.1, 12.3, 13.3 us, by the kernel for some
-// tokens 6.9, 14.1, 13.9; 128 tokens: 8.3, 15.1, 16.6 and 7.1, 14.4, 14.4).  From
-// kGluManyTokens on the codes are decoded once for all (256 tokens: 9.7, 24.6, 19.7 us for
-// some, 16.9, 27.3, 32.1 for many; 320: 16.7, 34.5, 35.6 and 17.1, 28.0, 32.5).
-constexpr int64_t kGluFewTokens = 96, kGluManyTokens = 257;
+// 896 x 4864, 1536 x 8960, 2560 x 6912: 6.0, 12.1, 13.2 us, by the kernel for some
+// tokens 6.4, 13.0, 12.3; 64 tokens: 5.7, 9.5, 9.5 and 6.3, 12.7, 12.0; 128 tokens: 8.3,
+// 15.1, 16.6 and 6.6, 13.4, 12.5).  Beyond, tiles that decode for themselves as long as two
+// on each CU hold them, 256 tokens and 32 outputs each (512 tokens, 2048 x 8192, 512
+// tiles: 28.8 us, decoded once for all 33.6; 1024 x 2816, 176 tiles: 9.5 and 17.4; 2048
+// x 8320, 520 tiles: 41.8 and 39.4, at 300 tokens 40.2 and 30.3; 768 tokens, 896 x 4864,
+// 456 tiles: 16.7 and 22.6, with 8-bit G and U 23.9 and 27.9).
+constexpr int64_t kGluFewTokens = 96, kGluMidTiles = 512;
+static bool glu_decodes_once(int64_t tokens, int64_t n_out) {
+  return tokens > kGluFewTokens && n_out / 32 * ((tokens + 255) / 256) > kGluMidTiles;
+}
 size_t glu_ws_bytes(int64_t tokens, int64_t k, int64_t n_out) {
-  return tokens < kGluManyTokens ? 0 : (size_t)(2 * n_out * k + (tokens + 15) / 16 * 16 * k);
+  return glu_decodes_once(tokens, n_out) ? (size_t)(2 * n_out * k + (tokens + 15) / 16 * 16 * k) : 0;
 }
 
 template <int S, int kAct>
@@ -748,10 +757,10 @@ static hipError_t glu_launch(const GluArgs& a, void* ws, hipStream_t s) {
     glu_small_kernel<S, kAct><<<dim3(strips, blocks_of(16)), 1024, 0, s>>>(a);
     return hipGetLastError();
   }
-  if (a.tokens < kGluManyTokens) {
+  if (!glu_decodes_once(a.tokens, a.n_out)) {
     if (a.save == kRowQ8) glu_mid_kernel<S, kAct, 4, 1><<<dim3(strips, blocks_of(128)), kMidThreads, 0, s>>>(a);
     else if (a.tokens <= 128) glu_mid_kernel<S, kAct, 2, 1><<<dim3(2 * strips, 1), kMidThreads, 0, s>>>(a);
-    else glu_mid_kernel<S, kAct, 2, 2><<<dim3(2 * strips, 1), kMidThreads, 0, s>>>(a);
+    else glu_mid_kernel<S, kAct, 2, 2><<<dim3(2 * strips, blocks_of(256)), kMidThreads, 0, s>>>(a);
     return hipGetLastError();
   }
   const int nkb = (int)(a.k / kBlockK);

@@ -53,8 +53,12 @@ def check_h(H, g, u, act):
 @pytest.mark.parametrize("t,k,n_out,nm", [
     (1, 128, 128, (6, 8)), (2, 256, 384, (8, 8)), (7, 896, 128, (2, 4)), (16, 1152, 256, (3, 8)), (17, 384, 640, (2, 8)),
     (31, 1024, 128, (4, 8)), (33, 640, 256, (6, 8)), (64, 2560, 128, (6, 8)), (65, 128, 512, (8, 8)), (130, 1536, 384, (4, 8)),
-    (96, 384, 256, (2, 8)), (97, 768, 128, (3, 8)), (200, 1152, 128, (2, 4)), (256, 640, 256, (4, 8)),
-    (257, 512, 1152, (6, 8)), (300, 896, 640, (2, 4)), (520, 640, 256, (2, 8)), (1025, 256, 384, (3, 8))])
+    (96, 384, 256, (2, 8)), (97, 768, 128, (3, 8)), (111, 2304, 256, (8, 8)), (128, 1408, 384, (8, 8)), (250, 2688, 128, (8, 8)),
+    (129, 1408, 256, (6, 8)), (128, 1408, 256, (4, 8)), (256, 2176, 128, (2, 8)), (100, 1408, 128, (2, 8)), (200, 1152, 128, (2, 4)), (256, 640, 256, (4, 8)),
+    (257, 512, 1152, (6, 8)), (300, 896, 640, (2, 4)), (520, 640, 256, (2, 8)), (1025, 256, 384, (3, 8)),
+    # codes decoded once for all
+    (257, 128, 8320, (6, 8)), (300, 384, 8448, (2, 4)), (520, 640, 5632, (2, 8)), (1025, 256, 3584, (3, 8)),
+    (2100, 640, 1920, (4, 8)), (130, 128, 16512, (8, 8))])
 def test_forward(t, k, n_out, nm, act):
     pair = layers(k, n_out, *nm, seed=t)
     xq, xs = activations(t, k, t)
@@ -75,7 +79,7 @@ def test_forward(t, k, n_out, nm, act):
                 assert np.array_equal(host(v), want if keep == "f32" else R.bf16(want))
 
 
-@pytest.mark.parametrize("t", [1, 16, 40, 128, 200, 700])
+@pytest.mark.parametrize("t", [1, 16, 40, 128, 200, 700, 6700])
 def test_forward_equals_the_layers_one_by_one(t):
     """The existing path: two contractions, then the gating with its own pass."""
     k, n_out = 1280, 640
@@ -202,9 +206,9 @@ def test_neighbours_stay():
         assert (ws[need:] == 171).all()
 
 
-@pytest.mark.parametrize("t", [5, 70, 300])
-def test_what_the_workspace_held_does_not_matter(t):
-    k, n_out = 384, 640
+@pytest.mark.parametrize("t,n_out", [(5, 640), (70, 640), (300, 640), (300, 8320)])
+def test_what_the_workspace_held_does_not_matter(t, n_out):
+    k = 384
     pair, xq, xs, G, U, dH, out = backward_case(t, k, n_out, (6, 8), "relu2", "bf16", "f32", "f32")
     (gate, _), (up, _) = pair
     need = bl.bitlinear_glu_workspace_bytes(t, k, n_out), bl.bitlinear_glu_bwd_workspace_bytes(t, k, n_out)
