@@ -46,6 +46,8 @@ __device__ __forceinline__ uint32_t pair_bf16(float a, float b) {
   typedef float f2 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
 }
+// one of them (a NaN stays one, whatever its bits)
+__device__ __forceinline__ uint16_t one_bf16(float a) { return (uint16_t)pair_bf16(a, a); }
 
 // Eight consecutive values of a row as they lie in memory
 enum RowType { kRowF32 = 0, kRowBf16 = 1, kRowQ8 = 2 };

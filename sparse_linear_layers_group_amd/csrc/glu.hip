@@ -78,7 +78,7 @@ __device__ __forceinline__ v4i load_b128(__amdgpu_buffer_rsrc_t r, uint32_t o) {
 template <int kAct>
 __device__ __forceinline__ void glu_output(const GluArgs& a, float g, float u, int64_t token, int64_t col, int lane) {
   const int64_t e = token * a.n_out + col;
-  st_global(a.H + e, f32_to_bf16_rne(act_value<kAct>(g) * u));
+  st_global(a.H + e, one_bf16(act_value<kAct>(g) * u));
   if (a.save == kSaveNone) return;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -87,7 +87,7 @@ __device__ __forceinline__ void glu_output(const GluArgs& a, float g, float u, i
     if (a.save == kRowF32) {
       st_global(static_cast<float*>(out) + e, x);
     } else if (a.save == kRowBf16) {
-      st_global(static_cast<uint16_t*>(out) + e, f32_to_bf16_rne(x));
+      st_global(static_cast<uint16_t*>(out) + e, one_bf16(x));
     } else {
       uint32_t top = abs_bits(x);
 #pragma unroll

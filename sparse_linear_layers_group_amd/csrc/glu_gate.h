@@ -107,8 +107,8 @@ __device__ __forceinline__ void glu_gate_tile(const GluBwdArgs& a, const GluBwdL
     if (!a.dWg) return;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      tg[t * kGatePitch + c16 + i] = f32_to_bf16_rne(dg[i] * s);
-      tu[t * kGatePitch + c16 + i] = f32_to_bf16_rne(du[i] * s);
+      tg[t * kGatePitch + c16 + i] = one_bf16(dg[i] * s);
+      tu[t * kGatePitch + c16 + i] = one_bf16(du[i] * s);
     }
   }
   __syncthreads();

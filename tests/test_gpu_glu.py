@@ -222,19 +222,36 @@ def test_what_the_workspace_held_does_not_matter(t, n_out):
     assert all(torch.equal(a, b) for a, b in zip(*got)) and all(torch.isfinite(a).all() for a in got[1])
 
 
-def test_a_token_that_is_nan_stays_by_itself():
+@pytest.mark.parametrize("bits", [0x7FC00000, 0x7FFFFFFF, -1])
+def test_a_token_that_is_nan_stays_by_itself(bits):
     """In dX; the weights' gradients sum over tokens and show it in the outputs' rows it has."""
     t, k, n_out = 70, 256, 384
     pair, xq, xs, G, U, dH, out = backward_case(t, k, n_out, (6, 8), "silu", "q8", "f32", "f32")
     want = [torch.empty_like(v) for v in out]
     backward(pair, xq, xs, G, U, dH, want, k, n_out, "silu")
-    dH[17, 5] = float("nan")
+    dH.view(torch.int32)[17, 5] = bits
     backward(pair, xq, xs, G, U, dH, out, k, n_out, "silu")
     others = torch.arange(t, device="cuda") != 17
     rows = torch.arange(n_out, device="cuda") != 5
     assert torch.equal(out[0][others], want[0][others]) and out[0][17].isnan().any()
     for a, b in zip(out[1:], want[1:]):
         assert torch.equal(a[rows], b[rows]) and a[5].isnan().all()
+
+
+@pytest.mark.parametrize("t", [20, 200, 2100])
+@pytest.mark.parametrize("bits", [0x7FC00000, 0x7FFFFFFF, -1])
+def test_a_scale_that_is_nan_shows(t, bits):
+    k, n_out = 256, 2048
+    pair = layers(k, n_out, 6, 8)
+    xq, xs = activations(t, k, 1)
+    xs.view(torch.int32)[3] = bits
+    for keep in ("f32", "bf16", "q8"):
+        H, G, U = empty(t, n_out, dtype=torch.bfloat16), kept(t, n_out, keep), kept(t, n_out, keep)
+        forward(xq, xs, pair, k, n_out, "silu", H, G, U)
+        others = torch.arange(t, device="cuda") != 3
+        assert H[3].isnan().all() and H[others].isfinite().all()
+        for v in ((G[1], U[1]) if keep == "q8" else (G[0], U[0])):
+            assert v[3].isnan().all() and v[others].isfinite().all()
 
 
 def test_refusals_of_tensors():
