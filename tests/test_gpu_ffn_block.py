@@ -85,6 +85,17 @@ def test_rows_may_be_overwritten_after_a_forward_that_keeps_8_bits():
     assert all(torch.equal(got[n], want[n]) for n in want)
 
 
+@pytest.mark.parametrize("keep", [torch.int8, torch.float32])
+def test_no_tokens(keep):
+    ffn, _ = block(keep=keep)
+    y, kept = ffn.fwd(torch.empty(0, K, device="cuda"))
+    assert y.shape == (0, K)
+    grads = ffn.bwd(torch.empty(0, K, device="cuda", dtype=torch.bfloat16), kept)
+    assert grads["X"].shape == (0, K)
+    for name in ("gate", "up", "down", "norm_weight", "norm_bias"):
+        assert not grads[name].any(), name
+
+
 def test_refused_blocks():
     a, b, c = BitLinearWeight(N, K), BitLinearWeight(N, K, 4, 8), BitLinearWeight(K, N)
     with pytest.raises(ValueError):
