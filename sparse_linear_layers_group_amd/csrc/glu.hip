@@ -736,17 +736,28 @@ __global__ __launch_bounds__(256, 2) void glu_gemm_kernel(GluArgs a, const char*
 // Up to kGluFewTokens tokens every 16 have workgroups of their own (96 tokens of
 // 896 x 4864, 1536 x 8960, 2560 x 6912: 6.0, 12.1, 13.2 us, by the kernel for some
 // tokens 6.4, 13.0, 12.3; 64 tokens: 5.7, 9.5, 9.5 and 6.3, 12.7, 12.0; 128 tokens: 8.3,
-// 15.1, 16.6 and 6.6, 13.4, 12.5).  Beyond, tiles that decode for themselves as long as two
-// on each CU hold them, 256 tokens and 32 outputs each (512 tokens, 2048 x 8192, 512
-// tiles: 28.8 us, decoded once for all 33.6; 1024 x 2816, 176 tiles: 9.5 and 17.4; 2048
-// x 8320, 520 tiles: 41.8 and 39.4, at 300 tokens 40.2 and 30.3; 768 tokens, 896 x 4864,
-// 456 tiles: 16.7 and 22.6, with 8-bit G and U 23.9 and 27.9).
-constexpr int64_t kGluFewTokens = 96, kGluMidTiles = 512;
-static bool glu_decodes_once(int64_t tokens, int64_t n_out) {
-  return tokens > kGluFewTokens && n_out / 32 * ((tokens + 255) / 256) > kGluMidTiles;
+// 15.1, 16.6 and 6.6, 13.4, 12.5).
+// Beyond, tiles of 32 outputs that decode for themselves, for 256 tokens at a time, one
+// on a CU, or for 128, of which a CU holds two and runs one in some half of the
+// time: whichever gives a CU less to do (256 tokens of 2560 x 6912, 1 or 2 of them on a
+// CU: 17.1 us, of 128 tokens 20.4; of 1536 x 8960, 2 or 3: 22.0 and 19.6).  With more
+// than kGluMidRounds of the smaller on a CU the codes are decoded once for all (300
+// tokens of 2048 x 11008, 5: 37.5 us, decoded once 42.1; 512 tokens of 1536 x 8960, 5:
+// 30.7 and 35.5; 768 tokens of 2560 x 6912, 6: 50.0 and 45.7).  8-bit G and U need tiles
+// of 64 outputs and 128 tokens, one on a CU, which win up to two (768 tokens, 896 x
+// 4864, 2: 23.9 and 27.9; 1280 tokens, 2048 x 4096, 3: 53.0 and 44.3).
+constexpr int64_t kGluFewTokens = 96, kGluMidRounds = 5, kGluMidRoundsQ8 = 2;
+// tokens of a tile that decodes for itself; 0: the codes are decoded once
+static int glu_mid_tokens(int64_t tokens, int64_t n_out, bool q8) {
+  const auto on_a_cu = [&](int64_t outputs, int64_t t) { return (n_out / outputs * ((tokens + t - 1) / t) + 255) / 256; };
+  if (q8) return on_a_cu(64, 128) <= kGluMidRoundsQ8 ? 128 : 0;
+  const int64_t small = on_a_cu(32, 128), large = 2 * on_a_cu(32, 256);
+  return (small < large ? small : large) > kGluMidRounds ? 0 : small < large ? 128 : 256;
 }
+// (of a call that keeps G and U in whatever type)
 size_t glu_ws_bytes(int64_t tokens, int64_t k, int64_t n_out) {
-  return glu_decodes_once(tokens, n_out) ? (size_t)(2 * n_out * k + (tokens + 15) / 16 * 16 * k) : 0;
+  if (tokens <= kGluFewTokens || (glu_mid_tokens(tokens, n_out, false) && glu_mid_tokens(tokens, n_out, true))) return 0;
+  return (size_t)(2 * n_out * k + (tokens + 15) / 16 * 16 * k);
 }
 
 template <int S, int kAct>
@@ -757,9 +768,9 @@ static hipError_t glu_launch(const GluArgs& a, void* ws, hipStream_t s) {
     glu_small_kernel<S, kAct><<<dim3(strips, blocks_of(16)), 1024, 0, s>>>(a);
     return hipGetLastError();
   }
-  if (!glu_decodes_once(a.tokens, a.n_out)) {
+  if (const int tile = glu_mid_tokens(a.tokens, a.n_out, a.save == kRowQ8)) {
     if (a.save == kRowQ8) glu_mid_kernel<S, kAct, 4, 1><<<dim3(strips, blocks_of(128)), kMidThreads, 0, s>>>(a);
-    else if (a.tokens <= 128) glu_mid_kernel<S, kAct, 2, 1><<<dim3(2 * strips, 1), kMidThreads, 0, s>>>(a);
+    else if (tile == 128) glu_mid_kernel<S, kAct, 2, 1><<<dim3(2 * strips, blocks_of(128)), kMidThreads, 0, s>>>(a);
     else glu_mid_kernel<S, kAct, 2, 2><<<dim3(2 * strips, blocks_of(256)), kMidThreads, 0, s>>>(a);
     return hipGetLastError();
   }
