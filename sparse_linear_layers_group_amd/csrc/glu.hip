@@ -173,7 +173,7 @@ __device__ __forceinline__ void glu_barrier() {
 }
 
 // ------------------------------------------------------ forward, some tokens
-// A workgroup computes 16 kRT outputs (of both layers) of 128 kTG tokens.  Each
+// A workgroup computes 16 kRT outputs (of both layers) of kTokens tokens.  Each
 // wavefront decodes an equal share of a k block's A operands, once for all tokens,
 // into LDS, where all read them.  The activations come to LDS by DMA in whole 128-byte
 // lines, eight rows an instruction (as operands, 16 rows of 64 bytes, straight from
@@ -184,30 +184,34 @@ __device__ __forceinline__ void glu_barrier() {
 // the way through it between two barriers; fragments read a block ahead, or codes by
 // DMA, gave nothing, codes three blocks ahead cost 10 %.  Half a strip (kRT = 2) makes
 // enough workgroups for the CUs; a checkpoint's block of 64 outputs needs a whole one
-// (kRT = 4).
+// (kRT = 4), whose row tiles two wavefronts share.
 constexpr int kMidThreads = 512;
 // place of 16-byte piece `piece` (0..7) of activation row `row` in its 128 bytes: reads
 // of 16 rows' pieces as operands are free of bank conflicts (see row64_place)
 __device__ __forceinline__ int row128_place(int row, int piece) { return piece ^ ((row >> 1) & 7); }
 // the stages of the activations, kTokens rows of 128 bytes
+__shared__ __attribute__((aligned(1024))) char g_mid64_st0[64 * 128], g_mid64_st1[64 * 128], g_mid64_st2[64 * 128];
 __shared__ __attribute__((aligned(1024))) char g_mid128_st0[128 * 128], g_mid128_st1[128 * 128], g_mid128_st2[128 * 128];
 __shared__ __attribute__((aligned(1024))) char g_mid256_st0[256 * 128], g_mid256_st1[256 * 128], g_mid256_st2[256 * 128];
 template <int kTokens, int P>
 __device__ __forceinline__ char* mid_stage() {
-  static_assert(kTokens == 128 || kTokens == 256, "the stages above");
-  if constexpr (kTokens == 128) return P == 0 ? g_mid128_st0 : P == 1 ? g_mid128_st1 : g_mid128_st2;
+  static_assert(kTokens == 64 || kTokens == 128 || kTokens == 256, "the stages above");
+  if constexpr (kTokens == 64) return P == 0 ? g_mid64_st0 : P == 1 ? g_mid64_st1 : g_mid64_st2;
+  else if constexpr (kTokens == 128) return P == 0 ? g_mid128_st0 : P == 1 ? g_mid128_st1 : g_mid128_st2;
   else return P == 0 ? g_mid256_st0 : P == 1 ? g_mid256_st1 : g_mid256_st2;
 }
 
-template <int S, int kAct, int kRT, int kTG>
+template <int S, int kAct, int kRT, int kTokens>
 __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
   constexpr int kOps = 4 * kRT;       // A operands of a k block: (layer, row tile, k half)
   constexpr int kShare = kOps / 8;    // of one wavefront
-  constexpr int kTokens = 128 * kTG;
+  constexpr int kRW = 2;              // row tiles of a wavefront's products
+  constexpr int kGroups = 8 * kRW / kRT;       // wavefronts side by side along the tokens
+  constexpr int kTG = kTokens / 16 / kGroups;  // token tiles of a wavefront
   // code table copies (8: two workgroups of 128 tokens fit a CU, 14.2 us in place of 17.1
   // at 128 tokens, 1536 x 8960, where there are more workgroups than CUs; 4% slower
   // where there are not)
-  constexpr int kMidCopies = kTG == 1 && kRT == 2 ? 8 : 16;
+  constexpr int kMidCopies = kTG == 1 ? 8 : 16;
   constexpr int kX = kTokens / 64;    // DMA instructions of a wavefront and block
   __shared__ __attribute__((aligned(16))) uint32_t lut[512 * kMidCopies];
   __shared__ __attribute__((aligned(16))) v4i A[2][kOps * 64];
@@ -217,6 +221,7 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
   const int64_t strip = blockIdx.x / kPer;
   const int part = blockIdx.x % kPer;  // which kRT row tiles of it
   const int64_t t0 = (int64_t)blockIdx.y * kTokens;
+  const int group = wave % kGroups, row0 = wave / kGroups * kRW;  // of the wavefront: its tokens, its first row tile
   const int nkb = (int)(a.k / kBlockK);
   constexpr int kSb = kStripRows * block_bytes(S);
   const int64_t at = strip * nkb * (int64_t)kSb;
@@ -280,9 +285,9 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
 #pragma unroll
   for (int r = 0; r < 512 * kMidCopies / 4 / kMidThreads; ++r)
     reinterpret_cast<u32x4*>(lut)[tid + kMidThreads * r] = u32x4{tv[r], tv[r], tv[r], tv[r]};
-  v4i c[2 * kRT][kTG];
+  v4i c[2 * kRW][kTG];  // gate's row tiles, then up's
 #pragma unroll
-  for (int i = 0; i < 2 * kRT; ++i)
+  for (int i = 0; i < 2 * kRW; ++i)
 #pragma unroll
     for (int j = 0; j < kTG; ++j) c[i][j] = v4i{0, 0, 0, 0};
   __syncthreads();
@@ -293,7 +298,7 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
   glu_barrier();
   // block kb: its operands are in A[kb % 2], its activations in stage kb % 3; blocks past
   // the last read zeros and are not used
-  const uint32_t x_at = (uint32_t)((16 * wave * kTG + l16) * 128);
+  const uint32_t x_at = (uint32_t)((16 * group * kTG + l16) * 128);
   auto block = [&](auto number, int kb) {
     constexpr int U = decltype(number)::value, P = U & 1;
     load_x(std::integral_constant<int, (U + 2) % 3>{}, kb + 2);
@@ -303,7 +308,7 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
     // read each operand after the products of the one before)
     __builtin_amdgcn_sched_barrier(0);
     const glu_lds_char* st = (const glu_lds_char*)mid_stage<kTokens, U % 3>() + x_at;
-    v4i op[2 * kRT][2], b[kTG][2];
+    v4i op[2 * kRW][2], b[kTG][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -311,14 +316,14 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
         b[j][h] = *reinterpret_cast<const __attribute__((address_space(3))) v4i*>(
             st + 2048 * j + 16 * row128_place(l16, 4 * h + lg));
 #pragma unroll
-      for (int i = 0; i < 2 * kRT; ++i) op[i][h] = A[P][(2 * i + h) * 64 + lane];
+      for (int i = 0; i < 2 * kRW; ++i) op[i][h] = A[P][(2 * (i / kRW * kRT + row0 + i % kRW) + h) * 64 + lane];
     }
     look_up(w[(U + 1) % 2], next);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < 2 * kRT; ++i)
+      for (int i = 0; i < 2 * kRW; ++i)
 #pragma unroll
         for (int j = 0; j < kTG; ++j) c[i][j] = mfma_i8(op[i][h], b[j][h], c[i][j]);
     put(next, A[P ^ 1]);
@@ -343,60 +348,68 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
   if (kb + 3 < nkb) block(std::integral_constant<int, 3>{}, kb + 3);
   if (kb + 4 < nkb) block(std::integral_constant<int, 4>{}, kb + 4);
   glu_wait<0>();  // no DMA outlives the workgroup
-  // lane: outputs n0 + 16 i + 4 lg + q (i < kRT: gate, i + kRT: up) of token 16 j + l16 of the
+  // lane: outputs n0 + 16 i + 4 lg + q (i < kRW: gate, i + kRW: up) of token 16 j + l16 of the
   // wavefront's
   const double gg = ld_global(a.gate_gamma), gu = ld_global(a.up_gamma);
-  const int64_t n0 = strip * kStripRows + 16 * kRT * part;
+  const int64_t n0 = strip * kStripRows + 16 * (kRT * part + row0);
 #pragma unroll
   for (int j = 0; j < kTG; ++j) {
-    const int64_t token = t0 + 16 * (wave * kTG + j) + l16;
+    const int64_t token = t0 + 16 * (group * kTG + j) + l16;
     const bool in = token < a.tokens;
     const float s = in ? ld_global(a.x_scale + token) : 0.f;
     const float sg = out_scale(gg, s), su = out_scale(gu, s);
     const int64_t e = token * a.n_out + n0 + 4 * lg;
-    float g[4 * kRT], u[4 * kRT];
+    float g[4 * kRW], u[4 * kRW];
 #pragma unroll
-    for (int i = 0; i < kRT; ++i) {
+    for (int i = 0; i < kRW; ++i) {
       float h[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         g[4 * i + q] = out_value(c[i][j][q], sg);
-        u[4 * i + q] = out_value(c[i + kRT][j][q], su);
+        u[4 * i + q] = out_value(c[i + kRW][j][q], su);
         h[q] = act_value<kAct>(g[4 * i + q]) * u[4 * i + q];
       }
       if (in) st_global(reinterpret_cast<u32x2*>(a.H + e + 16 * i), u32x2{pair_bf16(h[0], h[1]), pair_bf16(h[2], h[3])});
     }
-    if (a.save != kSaveNone) {
+    if constexpr (kRT == 4) {
+      // 8-bit G and U (the only use of whole strips): a block's largest lies in two wavefronts
+      __shared__ uint32_t tops[2][2][kTokens];  // [row half][layer][token]
+      uint32_t top[2] = {0u, 0u};
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+#pragma unroll
+        for (int i = 0; i < 4 * kRW; ++i) top[z] = max_u(top[z], abs_bits(z ? u[i] : g[i]));
+        top[z] = max_u(top[z], (uint32_t)__shfl_xor((int)top[z], 16, 64));
+        top[z] = max_u(top[z], (uint32_t)__shfl_xor((int)top[z], 32, 64));
+        if (lg == 0) tops[row0 / kRW][z][16 * (group * kTG + j) + l16] = top[z];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        if (!in) break;
+        const CkptScale cs = ckpt_scale(max_u(top[z], tops[1 - row0 / kRW][z][16 * (group * kTG + j) + l16]));
+#pragma unroll
+        for (int i = 0; i < kRW; ++i) {
+          uint32_t word = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) word |= ckpt_code(z ? u[4 * i + q] : g[4 * i + q], cs.inv) << (8 * q);
+          st_global(reinterpret_cast<uint32_t*>(static_cast<int8_t*>(z ? a.U : a.G) + e + 16 * i), word);
+        }
+        if (lg == 0 && row0 == 0) st_global((z ? a.Us : a.Gs) + (token * a.n_out + n0) / kCkptBlock, cs.scale);
+      }
+    } else if (in && a.save != kSaveNone) {
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
         const float* x = z ? u : g;
         void* out = z ? a.U : a.G;
-        if (kRT == 4 && a.save == kRowQ8) {
-          uint32_t top = 0;
 #pragma unroll
-          for (int i = 0; i < 4 * kRT; ++i) top = max_u(top, abs_bits(x[i]));
-          top = max_u(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-          top = max_u(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-          const CkptScale cs = ckpt_scale(top);
-          if (!in) continue;
-#pragma unroll
-          for (int i = 0; i < kRT; ++i) {
-            uint32_t word = 0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) word |= ckpt_code(x[4 * i + q], cs.inv) << (8 * q);
-            st_global(reinterpret_cast<uint32_t*>(static_cast<int8_t*>(out) + e + 16 * i), word);
-          }
-          if (lg == 0) st_global((z ? a.Us : a.Gs) + (token * a.n_out + n0) / kCkptBlock, cs.scale);
-        } else if (in) {
-#pragma unroll
-          for (int i = 0; i < kRT; ++i) {
-            if (a.save == kRowF32)
-              st_global(reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + e + 16 * i),
-                        f32x4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
-            else
-              st_global(reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + e + 16 * i),
-                        u32x2{pair_bf16(x[4 * i], x[4 * i + 1]), pair_bf16(x[4 * i + 2], x[4 * i + 3])});
-          }
+        for (int i = 0; i < kRW; ++i) {
+          if (a.save == kRowF32)
+            st_global(reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + e + 16 * i),
+                      f32x4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
+          else
+            st_global(reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + e + 16 * i),
+                      u32x2{pair_bf16(x[4 * i], x[4 * i + 1]), pair_bf16(x[4 * i + 2], x[4 * i + 3])});
         }
       }
     }
@@ -744,15 +757,19 @@ __global__ __launch_bounds__(256, 2) void glu_gemm_kernel(GluArgs a, const char*
 // than kGluMidRounds of the smaller on a CU the codes are decoded once for all (300
 // tokens of 2048 x 11008, 5: 37.5 us, decoded once 42.1; 512 tokens of 1536 x 8960, 5:
 // 30.7 and 35.5; 768 tokens of 2560 x 6912, 6: 50.0 and 45.7).  8-bit G and U need tiles
-// of 64 outputs and 128 tokens, one on a CU, which win up to two (768 tokens, 896 x
-// 4864, 2: 23.9 and 27.9; 1280 tokens, 2048 x 4096, 3: 53.0 and 44.3).
-constexpr int64_t kGluFewTokens = 96, kGluMidRounds = 5, kGluMidRoundsQ8 = 2;
+// of 64 outputs, of 64 or 128 tokens (192 tokens of 1536 x 8960, 2 or 2 on a CU: 19.9 us,
+// of 128 tokens 27.0; 300 tokens of 2048 x 4096, 2 or 1: 22.8 and 17.8), which win up to
+// kGluMidRoundsQ8 (768 tokens, 896 x 4864, 4: 23.4 us, decoded once 28.2; 391 tokens,
+// 1536 x 8960, 4: 34.6 and 39.3; 512 tokens, 2560 x 6912, 4: 41.2 and 39.2; 1280 tokens,
+// 896 x 4864, 5: 36.5 and 34.4).
+constexpr int64_t kGluFewTokens = 96, kGluMidRounds = 5, kGluMidRoundsQ8 = 4;
 // tokens of a tile that decodes for itself; 0: the codes are decoded once
 static int glu_mid_tokens(int64_t tokens, int64_t n_out, bool q8) {
-  const auto on_a_cu = [&](int64_t outputs, int64_t t) { return (n_out / outputs * ((tokens + t - 1) / t) + 255) / 256; };
-  if (q8) return on_a_cu(64, 128) <= kGluMidRoundsQ8 ? 128 : 0;
-  const int64_t small = on_a_cu(32, 128), large = 2 * on_a_cu(32, 256);
-  return (small < large ? small : large) > kGluMidRounds ? 0 : small < large ? 128 : 256;
+  const int64_t outputs = q8 ? 64 : 32, t = q8 ? 64 : 128;
+  const auto on_a_cu = [&](int64_t t) { return (n_out / outputs * ((tokens + t - 1) / t) + 255) / 256; };
+  const int64_t small = on_a_cu(t), large = 2 * on_a_cu(2 * t);
+  if ((small < large ? small : large) > (q8 ? kGluMidRoundsQ8 : kGluMidRounds)) return 0;
+  return (int)(small < large ? t : 2 * t);
 }
 // (of a call that keeps G and U in whatever type)
 size_t glu_ws_bytes(int64_t tokens, int64_t k, int64_t n_out) {
@@ -769,9 +786,10 @@ static hipError_t glu_launch(const GluArgs& a, void* ws, hipStream_t s) {
     return hipGetLastError();
   }
   if (const int tile = glu_mid_tokens(a.tokens, a.n_out, a.save == kRowQ8)) {
-    if (a.save == kRowQ8) glu_mid_kernel<S, kAct, 4, 1><<<dim3(strips, blocks_of(128)), kMidThreads, 0, s>>>(a);
-    else if (tile == 128) glu_mid_kernel<S, kAct, 2, 1><<<dim3(2 * strips, blocks_of(128)), kMidThreads, 0, s>>>(a);
-    else glu_mid_kernel<S, kAct, 2, 2><<<dim3(2 * strips, blocks_of(256)), kMidThreads, 0, s>>>(a);
+    if (tile == 64) glu_mid_kernel<S, kAct, 4, 64><<<dim3(strips, blocks_of(64)), kMidThreads, 0, s>>>(a);
+    else if (a.save == kRowQ8) glu_mid_kernel<S, kAct, 4, 128><<<dim3(strips, blocks_of(128)), kMidThreads, 0, s>>>(a);
+    else if (tile == 128) glu_mid_kernel<S, kAct, 2, 128><<<dim3(2 * strips, blocks_of(128)), kMidThreads, 0, s>>>(a);
+    else glu_mid_kernel<S, kAct, 2, 256><<<dim3(2 * strips, blocks_of(256)), kMidThreads, 0, s>>>(a);
     return hipGetLastError();
   }
   const int nkb = (int)(a.k / kBlockK);

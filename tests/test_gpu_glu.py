@@ -56,9 +56,11 @@ def check_h(H, g, u, act):
     (96, 384, 256, (2, 8)), (97, 768, 128, (3, 8)), (111, 2304, 256, (8, 8)), (128, 1408, 384, (8, 8)), (250, 2688, 128, (8, 8)),
     (129, 1408, 256, (6, 8)), (128, 1408, 256, (4, 8)), (256, 2176, 128, (2, 8)), (100, 1408, 128, (2, 8)), (200, 1152, 128, (2, 4)), (256, 640, 256, (4, 8)),
     (257, 512, 1152, (6, 8)), (300, 896, 640, (2, 4)), (520, 640, 256, (2, 8)), (1025, 256, 384, (3, 8)),
+    # tiles of 256 tokens (128 with 8-bit G and U): layers wide enough to fill the CUs
+    (256, 384, 4352, (8, 8)), (250, 1408, 4352, (6, 8)), (130, 640, 6400, (2, 8)), (129, 128, 4608, (4, 8)), (300, 128, 6400, (2, 4)),
     # codes decoded once for all
-    (257, 128, 8320, (6, 8)), (300, 384, 8448, (2, 4)), (520, 640, 5632, (2, 8)), (1025, 256, 3584, (3, 8)),
-    (2100, 640, 1920, (4, 8)), (130, 128, 16512, (8, 8))])
+    (257, 128, 16384, (6, 8)), (300, 384, 14464, (2, 4)), (520, 640, 8576, (2, 8)), (1025, 256, 4608, (3, 8)),
+    (2100, 640, 2688, (4, 8)), (130, 128, 20608, (8, 8))])
 def test_forward(t, k, n_out, nm, act):
     pair = layers(k, n_out, *nm, seed=t)
     xq, xs = activations(t, k, t)
@@ -79,7 +81,7 @@ def test_forward(t, k, n_out, nm, act):
                 assert np.array_equal(host(v), want if keep == "f32" else R.bf16(want))
 
 
-@pytest.mark.parametrize("t", [1, 16, 40, 128, 200, 700, 6700])
+@pytest.mark.parametrize("t", [1, 16, 40, 128, 200, 700, 8300])
 def test_forward_equals_the_layers_one_by_one(t):
     """The existing path: two contractions, then the gating with its own pass."""
     k, n_out = 1280, 640
@@ -206,7 +208,7 @@ def test_neighbours_stay():
         assert (ws[need:] == 171).all()
 
 
-@pytest.mark.parametrize("t,n_out", [(5, 640), (70, 640), (300, 640), (300, 8320)])
+@pytest.mark.parametrize("t,n_out", [(5, 640), (70, 640), (300, 640), (300, 14464)])
 def test_what_the_workspace_held_does_not_matter(t, n_out):
     k = 384
     pair, xq, xs, G, U, dH, out = backward_case(t, k, n_out, (6, 8), "relu2", "bf16", "f32", "f32")
@@ -238,7 +240,7 @@ def test_a_token_that_is_nan_stays_by_itself(bits):
         assert torch.equal(a[rows], b[rows]) and a[5].isnan().all()
 
 
-@pytest.mark.parametrize("t", [20, 200, 2100])
+@pytest.mark.parametrize("t", [20, 200, 2900])
 @pytest.mark.parametrize("bits", [0x7FC00000, 0x7FFFFFFF, -1])
 def test_a_scale_that_is_nan_shows(t, bits):
     k, n_out = 256, 2048
