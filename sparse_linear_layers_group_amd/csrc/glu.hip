@@ -180,9 +180,10 @@ __device__ __forceinline__ void glu_barrier() {
 // memory they bound the kernel: 24.4 us in place of 19.4 at 256 tokens, 2560 x 6912;
 // 17.2 now).  One k block (128 k) per barrier: while its products run, the next
 // block's operands are decoded, and the activations and the codes two blocks on are on
-// their way.  Bound by LDS (operands read by every wavefront, look-ups, the DMA) and
-// the way through it between two barriers; fragments read a block ahead, or codes by
-// DMA, gave nothing, codes three blocks ahead cost 10 %.  Half a strip (kRT = 2) makes
+// their way.  Bound by the way from the codes through LDS to the products between two
+// barriers; fragments read a block ahead, codes by DMA, or a fifth fewer operand reads
+// (one row tile and two token tiles a wavefront) gave nothing, codes three blocks
+// ahead cost 10 %.  Half a strip (kRT = 2) makes
 // enough workgroups for the CUs; a checkpoint's block of 64 outputs needs a whole one
 // (kRT = 4), whose row tiles two wavefronts share.
 constexpr int kMidThreads = 512;
