@@ -619,6 +619,21 @@ __device__ __forceinline__ char* big_stage() {
 // (512 threads at most: two wavefronts per SIMD either way, so the
 // register budget is the same; bounds that depend on kWN broke the host
 // side's template deduction)
+// Lanes l and l ^ 1 hold four-column pieces 0..3 of rows r and r + 1 (l even: r) in p;
+// in d the even lane gets pieces 0 and 2, the odd one 1 and 3, of both rows: d[e] is row
+// r + e % 2
+__device__ __forceinline__ void exchange_rows(const v4f (&p)[4], v4f (&d)[4], bool odd) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float own = odd ? p[2 * h + 1][q] : p[2 * h][q], other = odd ? p[2 * h][q] : p[2 * h + 1][q];
+      const float got = __uint_as_float(lane_xor1(__float_as_uint(other)));
+      d[2 * h][q] = odd ? got : own;
+      d[2 * h + 1][q] = odd ? own : got;
+    }
+}
+
 template <int kWN>
 __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   typedef BigTile<kWN> T;
@@ -794,79 +809,93 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   wait_vmcnt<0, true>();  // no LDS DMA outlives the workgroup
 
   // B's fragment is the instruction's first operand, so a lane holds four neighbouring
-  // columns: C[m0 + 128wm + 16i + l16][n0 + 64wn + 16j + 4lg + q], in q (N is a multiple
-  // of 4: they are in range together)
+  // columns of a row: C[m0 + 128wm + 16i + l16][n0 + 64wn + 16j + 4lg + q], in q.  Lanes
+  // l16 and l16 ^ 1 then exchange half of theirs (exchange_rows), and eight lanes hold 128
+  // bytes of one row: entry e of d is row `row` + 16i + e % 2, columns `col` + 32 (e / 2) + q
+  // (N is a multiple of 4: a lane's four are in range together).  Whole tiles take no
+  // branch inside.  (With a branch to a store and four stores to a row's 128 bytes,
+  // dX and dW of 64 tokens of 2560 x 2560 took 36.5 us, now 33.9; 2048 of 2560 x 640 50.0
+  // and 44.3; 4096 of 6912 x 2560 284 and 263, with the gating 355 and 323; 8192 of
+  // 11008 x 2048 786 and 705.  Streaming stores of quarter lines reached memory one by
+  // one; of whole lines they are as fast as others at few tokens and up to 8 % faster
+  // at many.)
   const double g = alpha ? *alpha : 1.0;
-  const bool scaled = alpha != nullptr;
-  const int64_t m = m0 + wm * 128 + l16, n = n0 + wn * 64 + 4 * lg;
-  const auto value = [&](const v4f& x) {
-    v4f y = x;
-    if (scaled)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) y[q] = (float)((double)x[q] * g);
-    return y;
-  };
+  const bool odd = (l16 & 1) != 0, whole_tile = m0 + kBigM <= M && n0 + T::N <= N;
+  const int64_t row = m0 + wm * 128 + (l16 & ~1), col = n0 + wn * 64 + 4 * lg + (odd ? 16 : 0);
+  const int64_t first = row * ldc + col;
+  const auto at = [&](int i, int e) { return first + (16 * i + (e & 1)) * ldc + 32 * (e >> 1); };
+  const auto out_of_range = [&](int i, int e) { return row + 16 * i + (e & 1) >= M || col + 32 * (e >> 1) >= N; };
+  using Yes = std::true_type;
+  using No = std::false_type;
   if (pr.G) {
     const float* __restrict__ G = pr.G;
     const float* __restrict__ U = pr.U;
     uint16_t* __restrict__ dG = pr.dG;
     uint16_t* __restrict__ dU = pr.dU;
-    // software-pipelined over the MFMA row tiles: row tile i + 1's loads issue
-    // before row tile i's stores (stores could alias them as far as the compiler
-    // knows, so a load written after a store waits)
-    v4f gv[2][4], uv[2][4];
-    auto load = [&](int i, v4f (&gb)[4], v4f (&ub)[4]) {
+    const auto gate = [&](auto whole) {
+      // software-pipelined over the MFMA row tiles: row tile i + 1's loads issue
+      // before row tile i's stores (stores could alias them as far as the compiler
+      // knows, so a load written after a store waits)
+      v4f gv[2][4], uv[2][4];
+      const auto load = [&](int i, v4f (&gb)[4], v4f (&ub)[4]) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = m + 16 * i < M && n + 16 * j < N;
-        const int64_t e = in ? (m + 16 * i) * ldc + n + 16 * j : 0;
-        gb[j] = ub[j] = v4f{0.f, 0.f, 0.f, 0.f};
-        if (in) {
-          gb[j] = ld_global(reinterpret_cast<const v4f*>(G + e));
-          ub[j] = ld_global(reinterpret_cast<const v4f*>(U + e));
+        for (int e = 0; e < 4; ++e) {
+          gb[e] = ub[e] = v4f{0.f, 0.f, 0.f, 0.f};
+          if (!decltype(whole)::value && out_of_range(i, e)) continue;
+          gb[e] = ld_global(reinterpret_cast<const v4f*>(G + at(i, e)));
+          ub[e] = ld_global(reinterpret_cast<const v4f*>(U + at(i, e)));
+        }
+      };
+      load(0, gv[0], uv[0]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i + 1 < 8) load(i + 1, gv[(i + 1) & 1], uv[(i + 1) & 1]);
+        v4f d[4];
+        exchange_rows(c[i], d, odd);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v4f hu, hg;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float dh = (float)((double)d[e][q] * g);
+            const float gq = gv[i & 1][e][q];
+            const float r = gq > 0.f ? gq : 0.f;
+            const float r2 = r * r;
+            const float du = dh * uv[i & 1][e][q];
+            hu[q] = dh * r2;
+            hg[q] = du * (2.f * r);
+          }
+          if (!decltype(whole)::value && out_of_range(i, e)) continue;
+          st_global(reinterpret_cast<u32x2*>(dU + at(i, e)), bf16x4(hu));
+          st_global(reinterpret_cast<u32x2*>(dG + at(i, e)), bf16x4(hg));
         }
       }
     };
-    load(0, gv[0], uv[0]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i + 1 < 8) load(i + 1, gv[(i + 1) & 1], uv[(i + 1) & 1]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const v4f dh = value(c[i][j]);
-        v4f hu, hg;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float gq = gv[i & 1][j][q];
-          const float r = gq > 0.f ? gq : 0.f;
-          const float r2 = r * r;
-          const float du = dh[q] * uv[i & 1][j][q];
-          hu[q] = dh[q] * r2;
-          hg[q] = du * (2.f * r);
-        }
-        if (m + 16 * i >= M || n + 16 * j >= N) continue;
-        const int64_t e = (m + 16 * i) * ldc + n + 16 * j;
-        st_global(reinterpret_cast<u32x2*>(dU + e), bf16x4(hu));
-        st_global(reinterpret_cast<u32x2*>(dG + e), bf16x4(hg));
-      }
-    }
+    if (whole_tile) gate(Yes{});
+    else gate(No{});
     return;
   }
+  const auto store = [&](auto whole, auto scaled, auto narrow) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) {
+      v4f d[4];
+      exchange_rows(c[i], d, odd);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (m + 16 * i >= M || n + 16 * j >= N) continue;
-      const int64_t e = (m + 16 * i) * ldc + n + 16 * j;
-      const v4f y = value(c[i][j]);
-      // (A row's 128 bytes are four stores here.  Streaming ones reach memory one by one:
-      // 64 tokens of the gated feed-forward's backward, 2560 x 6912, bf16 gradients, took
-      // 18 us more, with binary32 ones 8 more.  The layers' own backward keeps them: -1 to
-      // 6 us either way.)
-      if (pr.Cb) st_global(reinterpret_cast<u32x2*>(pr.Cb + e), bf16x4(y));
-      else if (pr.tiled) st_global(reinterpret_cast<v4f*>(C + e), y);
-      else st_stream(reinterpret_cast<v4f*>(C + e), y);
+      for (int e = 0; e < 4; ++e) {
+        if (!decltype(whole)::value && out_of_range(i, e)) continue;
+        v4f y = d[e];
+        if (decltype(scaled)::value)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) y[q] = (float)((double)d[e][q] * g);
+        if (decltype(narrow)::value) st_global(reinterpret_cast<u32x2*>(pr.Cb + at(i, e)), bf16x4(y));
+        else st_stream(reinterpret_cast<v4f*>(C + at(i, e)), y);
+      }
     }
+  };
+  // (bf16 results carry no factor)
+  if (pr.Cb) whole_tile ? store(Yes{}, No{}, Yes{}) : store(No{}, No{}, Yes{});
+  else if (alpha) whole_tile ? store(Yes{}, Yes{}, No{}) : store(No{}, Yes{}, No{});
+  else whole_tile ? store(Yes{}, No{}, No{}) : store(No{}, No{}, No{});
 }
 
 // C = alpha * (sum of the split planes, in order), binary32 sums; to Cb in bf16
