@@ -966,26 +966,58 @@ int bwd_set_tiles(int tiles) {
   g_bwd_tiles.store(tiles, std::memory_order_relaxed);
   return 0;
 }
-// The tile size with the shorter estimated time, in rounds of one XCD's
-// 32 CUs (each XCD runs an eighth of every product).  256 x 256 tiles run
-// one per CU and a round costs 1, a partly filled last round too; 256 x 128
-// tiles run two per CU at ~1.18 per round (the same flops per CU at the
-// lower rate the narrower tiles reach), except a last round that leaves
-// every CU at most one tile, which costs ~0.6.  Ties (within 5%) go to
-// 256 x 256.  E.g. a 4096 x 2560 dX with its 2560 x 2560 dW (260 large
-// tiles: two rounds, the second nearly empty) takes 256 x 128; gate and up
-// of the BitNet-2B4T block together (860 large tiles) take 256 x 256.
-static int big_kind(const NtSet& set) {
-  int64_t n3 = 0, n2 = 0;
+// The tile size with the shorter estimated time.  Each of an XCD's 32 CUs is given the
+// next tile (the deepest products first, as they are launched) when it has least to do.
+// A 256 x 256 tile, one on a CU, costs its depth; 256 x 128 tiles run two on a CU, both
+// in 1.18 times a large one's time (they reach a lower rate), one alone in 0.6.  The
+// choice is the faster one, or within 5% of it, for layers of 640 to 8960 at 512 to
+// 8192 tokens.  (Counting rounds of tiles as if all were equally deep it was not: 1024
+// tokens of 6912 x 2560, where 14 deep tiles and 34 shallow ones on an XCD are no
+// longer than one deep tile and a half: 88 us with large tiles, 111 with small ones; 512
+// tokens of 2560 x 6912 twice, the other way round: 174 and 143.)
+static double big_time(const NtSet& set, bool wide) {
+  struct Cu {
+    double load;
+    bool odd;
+    int64_t last;  // depth of its last tile
+  };
+  Cu cu[32] = {};
+  const auto later = [](const Cu& a, const Cu& b) { return a.load > b.load; };
+  const double cost = wide ? 1.0 : 1.18 / 2;
   for (int i = 0; i < set.n; ++i) {
-    n3 += (nt_tiles_big<4>(set.p[i]) + 7) / 8;
-    n2 += (nt_tiles_big<2>(set.p[i]) + 7) / 8;
+    int64_t tiles = ((wide ? nt_tiles_big<4>(set.p[i]) : nt_tiles_big<2>(set.p[i])) + 7) / 8;
+    const int64_t depth = set.p[i].K;
+    const double step = cost * (double)depth;
+    // in one go, while there are enough tiles: those that bring every CU to within a tile
+    // of the busiest, then rounds of one each
+    double most = 0.0;
+    for (const Cu& c : cu) most = c.load > most ? c.load : most;
+    const auto lacks = [&](const Cu& c) { return (int64_t)((most - c.load) / step); };
+    int64_t level = 0;
+    for (const Cu& c : cu) level += lacks(c);
+    if (level + 32 <= tiles) {
+      const int64_t rounds = (tiles - level) / 32;
+      for (Cu& c : cu) {
+        const int64_t n = lacks(c) + rounds;
+        if (n > 0) c = Cu{c.load + (double)n * step, c.odd != ((n & 1) != 0), depth};
+      }
+      tiles -= level + 32 * rounds;
+      std::make_heap(cu, cu + 32, later);
+    }
+    for (; tiles > 0; --tiles) {
+      std::pop_heap(cu, cu + 32, later);
+      cu[31] = Cu{cu[31].load + step, !cu[31].odd, depth};
+      std::push_heap(cu, cu + 32, later);
+    }
   }
-  const double t3 = (double)((n3 + 31) / 32);
-  const int64_t rem2 = n2 % 64;
-  const double t2 = 1.18 * (double)(n2 / 64) + (rem2 == 0 ? 0.0 : rem2 <= 32 ? 0.6 : 1.18);
-  return t2 < 0.95 * t3 ? 2 : 3;
+  double most = 0.0;
+  for (const Cu& c : cu) {
+    const double time = c.load + (!wide && c.odd ? (0.6 - cost) * (double)c.last : 0.0);
+    most = time > most ? time : most;
+  }
+  return most;
 }
+static int big_kind(const NtSet& set) { return big_time(set, false) < big_time(set, true) ? 2 : 3; }
 static int bwd_tile_kind(const NtSet& set) {
   const int f = g_bwd_tiles.load(std::memory_order_relaxed);
   return f ? f : big_kind(set);
