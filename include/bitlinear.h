@@ -798,7 +798,8 @@ int bitlinear_layernorm_bwd(const void *X, int x_type, const float *x_scales, in
  *       (binary32, exactly bitlinear_contract's Y of the two layers),
  *   h = act(G) * U in binary32, rounded once to bf16: the down BitLinear's X.
  * BL_ACT_RELU2: act(g) = max(g, 0)^2, products rounded as bitlinear_relu2_gate
- * rounds them; BL_ACT_SILU: act(g) = g / (1 + exp(-g)).
+ * rounds them; BL_ACT_SILU: act(g) = g / (1 + exp(-g)).  A NaN g is a NaN act(g)
+ * and act'(g) with either (bitlinear_relu2_gate takes it for 0).
  *   xq, x_scale  device int8 [tokens x k] and float [tokens], as
  *           bitlinear_act_quant writes them.
  *   gate, up     device packed codes of two [n_out x k] layers under n:m;

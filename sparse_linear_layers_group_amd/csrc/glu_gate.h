@@ -13,10 +13,12 @@ namespace bl {
 // (v_exp_f32 and v_rcp_f32, 1 ulp each; an infinite exp gives 0, the limit.  With a
 // correctly rounded division 6001 tokens, 2048 x 11008 took 226 us, now 216.)
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.f + __expf(-g)); }
+// max(g, 0) that keeps a NaN: where a scale or a checkpoint's block is NaN, the outputs show it
+__device__ __forceinline__ float relu(float g) { return g <= 0.f ? 0.f : g; }
 template <int kAct>
 __device__ __forceinline__ float act_value(float g) {
   if constexpr (kAct == kActRelu2) {
-    const float r = g > 0.f ? g : 0.f;
+    const float r = relu(g);
     return r * r;
   } else {
     return g * sigmoid(g);
@@ -26,7 +28,7 @@ __device__ __forceinline__ float act_value(float g) {
 template <int kAct>
 __device__ __forceinline__ void act_both(float g, float& value, float& slope) {
   if constexpr (kAct == kActRelu2) {
-    const float r = g > 0.f ? g : 0.f;
+    const float r = relu(g);
     value = r * r;
     slope = 2.f * r;
   } else {
