@@ -303,8 +303,6 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
   auto block = [&](auto number, int kb) {
     constexpr int U = decltype(number)::value, P = U & 1;
     load_x(std::integral_constant<int, (U + 2) % 3>{}, kb + 2);
-    __builtin_amdgcn_sched_barrier(0);
-    load_codes(kb + 2, w[U % 2]);
     // (fences: left alone the compiler moved the loads to where they are used and
     // read each operand after the products of the one before)
     __builtin_amdgcn_sched_barrier(0);
@@ -319,7 +317,13 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
 #pragma unroll
       for (int i = 0; i < 2 * kRW; ++i) op[i][h] = A[P][(2 * (i / kRW * kRT + row0 + i % kRW) + h) * 64 + lane];
     }
+    // The next block's activations and codes are there once no more than the kX loads
+    // above, the last that were asked for, are in flight (loads return in order; those of
+    // codes are not counted, as the compiler joins some of them).  Behind the barrier
+    // below that holds for all wavefronts.
+    glu_wait<kX>();
     look_up(w[(U + 1) % 2], next);
+    load_codes(kb + 2, w[U % 2]);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -329,9 +333,6 @@ __global__ __launch_bounds__(kMidThreads, 2) void glu_mid_kernel(GluArgs a) {
         for (int j = 0; j < kTG; ++j) c[i][j] = mfma_i8(op[i][h], b[j][h], c[i][j]);
     put(next, A[P ^ 1]);
     __builtin_amdgcn_sched_barrier(0);
-    // The next block's activations are there: loads return in order, and its codes, which
-    // were just decoded, were asked for behind them.  (No count of loads in flight: how
-    // many load_codes leaves is the compiler's, which joins some and drops others.)
     glu_barrier();
   };
   int kb = 0;
