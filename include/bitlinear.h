@@ -751,7 +751,10 @@ int bitlinear_ckpt_unpack(const int8_t *codes, const float *scales, int64_t rows
  *   y = (x - mu) rstd weight + bias
  * in binary32, rounded once.  With center = 0 it is the root-mean-square norm.
  * The row stays in registers: the variance is formed from the differences.
- * A row whose variance leaves binary32 (from some 1e19 on) gives NaN.
+ * A row whose variance leaves binary32 (from some 1e19 on) gives NaN.  Small
+ * rows, whose squares would, are squared at a scale of their own: with any eps a
+ * row comes out as others do while its rstd stays in binary32 (up to 3e38).  With
+ * eps = 0 a constant row (0 without centring) has an infinite rstd and gives NaN.
  *   X       device rows, binary32 or bf16 (x_type), x_stride elements apart.
  *   weight, bias  device float [n]; each may be NULL (1 and 0).
  *   Y       device [rows][n], bf16 (a BitLinear's X) or binary32 (y_type).

@@ -31,12 +31,16 @@ struct RowSums {
   }
 };
 
-// mean and 1 / sqrt(variance + eps); a variance outside binary32 gives NaN, not
-// rows of zeros
-__device__ __forceinline__ float rstd_of(float var, float eps) {
-  const float v = var + eps;
+// 1 / sqrt(v), v the variance + eps; one that leaves binary32 gives NaN, not rows of
+// zeros
+__device__ __forceinline__ float rstd_of(float v) {
   return v < __builtin_inff() ? __builtin_amdgcn_rsqf(v) : __builtin_nanf("");
 }
+// Below kTinyVar squares lose bits or vanish, and v_rsq_f32 takes what is below 2^-126 for
+// 0: such rows (values of 1e-12 and less, eps no larger than their squares) are squared
+// once more, scaled by kTinyScale.  The smallest value's square is then 2^-106, and rows
+// of 16384 below the limit stay below 2^127.
+constexpr float kTinyVar = 0x1p-80f, kTinyScale = 0x1p96f;
 
 // Forward.  Up to 2560 values a row is a wavefront's, four rows a workgroup, and the
 // weights come from L2 behind the sums (kept in registers from the start they
@@ -98,7 +102,21 @@ __global__ __launch_bounds__(256) void layernorm_kernel(NormArgs a) {
         const float d = raw[i].get(j, 0.f) - mean;
         q = in[i] ? fmaf(d, d, q) : q;
       }
-    const float rstd = rstd_of(RowSums<kThreads>::sum(q, red, slot + 1, threadIdx.x >> 6) * inv_n, a.eps);
+    const float v = RowSums<kThreads>::sum(q, red, slot + 1, threadIdx.x >> 6) * inv_n + a.eps;
+    float rstd = rstd_of(v);
+    if (v < kTinyVar) {  // the same for all of the row's threads
+      q = 0.f;
+#pragma unroll
+      for (int i = 0; i < kV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float d = (raw[i].get(j, 0.f) - mean) * kTinyScale;
+          q = in[i] ? fmaf(d, d, q) : q;
+        }
+      // (the mean's slot: everyone has read it before the barrier of the sum above)
+      q = RowSums<kThreads>::sum(q, red, slot, threadIdx.x >> 6) * inv_n;
+      rstd = rstd_of(q + a.eps * kTinyScale * kTinyScale) * kTinyScale;
+    }
     slot ^= 2;  // a row's sums are read before the barriers of the next row's, which use the other slots
     if (tid == 0) {
       if (a.mean) st_global(a.mean + row, mean);
