@@ -813,7 +813,8 @@ int bitlinear_layernorm_bwd(const void *X, int x_type, const float *x_scales, in
  *           bitlinear_ckpt_pack writes them, scales to G_scales and U_scales,
  *           float [tokens x n_out / 64]; otherwise those are NULL).
  *   ws      bitlinear_glu_workspace_bytes() bytes, 256-byte aligned,
- *           clobbered; NULL where that is 0.
+ *           clobbered; NULL where that is 0.  (That is enough with G and U kept
+ *           in any type; a call whose type needs none takes NULL as well.)
  * n_out a positive multiple of 128 (the next BitLinear's k), k below 2^22;
  * other sizes as for bitlinear_contract.  tokens == 0 is a no-op. */
 #define BL_ACT_RELU2  0

@@ -1498,7 +1498,7 @@ bool glu_bwd_fits(int64_t tokens, int64_t k, int64_t n_out) {
 
 size_t bitlinear_glu_workspace_bytes(int64_t tokens, int64_t k, int64_t n_out) {
   if (check_glu(tokens, k, n_out, 8, 8, BL_ACT_RELU2) != BL_OK || tokens == 0) return 0;
-  return bl::glu_ws_bytes(tokens, k, n_out);
+  return std::max(bl::glu_ws_bytes(tokens, k, n_out, false), bl::glu_ws_bytes(tokens, k, n_out, true));
 }
 
 int bitlinear_glu(const int8_t* xq, const float* x_scale, int64_t tokens, int64_t k, const void* gate,
@@ -1516,7 +1516,7 @@ int bitlinear_glu(const int8_t* xq, const float* x_scale, int64_t tokens, int64_
   TRY(check_ptr(H, 16, "H"));
   if (!G && !U && (G_scales || U_scales)) return fail(BL_EINVAL, "G_scales and U_scales belong to G and U");
   if (G || U) TRY(check_saved(save_type, G, G_scales, U, U_scales));
-  const size_t need = bl::glu_ws_bytes(tokens, k, n_out);
+  const size_t need = bl::glu_ws_bytes(tokens, k, n_out, G && save_type == BL_TYPE_Q8);
   if (need) {
     if (!ws || ws_bytes < need)
       return fail(BL_EWORKSPACE, "gated feed-forward workspace needs %zu bytes (got %zu)", need, ws ? ws_bytes : (size_t)0);

@@ -22,7 +22,7 @@ struct GluArgs {
   float *Gs, *Us;
 };
 hipError_t launch_glu(const GluArgs& a, int S, void* ws, hipStream_t s);
-size_t glu_ws_bytes(int64_t tokens, int64_t k, int64_t n_out);
+size_t glu_ws_bytes(int64_t tokens, int64_t k, int64_t n_out, bool q8);  // q8: G and U are kept in 8 bits
 
 struct GluBwdArgs {
   const void* dH;

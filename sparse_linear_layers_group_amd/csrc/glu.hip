@@ -773,9 +773,8 @@ static int glu_mid_tokens(int64_t tokens, int64_t n_out, bool q8) {
   if ((small < large ? small : large) > (q8 ? kGluMidRoundsQ8 : kGluMidRounds)) return 0;
   return (int)(small < large ? t : 2 * t);
 }
-// (of a call that keeps G and U in whatever type)
-size_t glu_ws_bytes(int64_t tokens, int64_t k, int64_t n_out) {
-  if (tokens <= kGluFewTokens || (glu_mid_tokens(tokens, n_out, false) && glu_mid_tokens(tokens, n_out, true))) return 0;
+size_t glu_ws_bytes(int64_t tokens, int64_t k, int64_t n_out, bool q8) {
+  if (tokens <= kGluFewTokens || glu_mid_tokens(tokens, n_out, q8)) return 0;
   return (size_t)(2 * n_out * k + (tokens + 15) / 16 * 16 * k);
 }
 
