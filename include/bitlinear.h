@@ -777,7 +777,9 @@ int bitlinear_layernorm(const void *X, int x_type, int64_t x_stride, int64_t row
  * order: reruns give the same bits.
  *   X, x_type, x_stride  as in the forward, or its codes with BL_TYPE_Q8
  *           (x_stride then n, x_scales their scales; otherwise x_scales NULL).
- *   mean    what the forward wrote, or NULL for a norm that is not centred.
+ *   mean    what a centred forward wrote; NULL says that the norm is not centred
+ *           (the zeros that a forward with center = 0 writes do not say so: with
+ *           them mean(a) is taken off).
  *   dY      device [rows][n], binary32 or bf16 (dy_type).
  *   dR      NULL, or device [rows][n] of dX's type: the gradient that reaches X
  *           past the norm (a residual's), added before the one rounding.
@@ -794,8 +796,9 @@ int bitlinear_layernorm_bwd(const void *X, int x_type, const float *x_scales, in
                             void *dX, int dx_type, float *dweight, float *dbias, void *ws,
                             size_t ws_bytes, void *stream);
 
-/* The gated feed-forward's first half in one kernel: both projections, the
- * activation and the product.  BitNet b1.58 2B4T article §一 (squared ReLU,
+/* The gated feed-forward's first half in one call: both projections, with the
+ * activation and the product in their epilogue (for many tokens behind a launch
+ * that decodes both layers' codes into ws).  BitNet b1.58 2B4T article §一 (squared ReLU,
  * gated, in place of SwiGLU; both are here).
  *   G = acc_gate * gate_gamma * s_t,  U = acc_up * up_gamma * s_t
  *       (binary32, exactly bitlinear_contract's Y of the two layers),

@@ -804,7 +804,8 @@ def bitlinear_layernorm_bwd_workspace_bytes(n):
 def bitlinear_layernorm_bwd(X, x_scales, rows, n, weight, mean, rstd, dY, dX, dweight=None, dbias=None, dR=None, ws=None,
                             ws_bytes=None, stream=None):
     """Backward of bitlinear_layernorm from X (x_scales None) or from the
-    checkpoint (X its int8 codes); mean None for a norm that is not centred.
+    checkpoint (X its int8 codes); mean None for a norm that is not centred
+    (a tensor, the zeros of an uncentred forward too, makes it a centred one).
     dX: float32 or bfloat16, dR (a residual's gradient, added) of its type."""
     dev = torch.cuda.current_device()
     if getattr(X, "dtype", None) == torch.int8:

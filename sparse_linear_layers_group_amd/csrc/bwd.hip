@@ -534,7 +534,7 @@ __global__ __launch_bounds__(256, 2) void gemm_nt_bf16_kernel(NtProblem p0, NtPr
 // the register allocator shuttle them between register files around every
 // MFMA.)  The tiles stream through three LDS stages of 32 k filled by LDS
 // DMA (buffer loads that write LDS directly, 16 bytes per lane, 1 KiB per
-// wavefront instruction), issued two stages ahead.  In a stage each
+// wavefront instruction), issued three steps ahead.  In a stage each
 // operand row's 64 bytes hold four 16-byte pieces, placed by row64_place
 // so that fragment reads are free of bank conflicts, and a DMA instruction's
 // 64 lanes still write 1 KiB in order (lane l writes row l / 4, position
@@ -751,7 +751,8 @@ __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   // its stage beside the products.  (Reading a step's fragments in the step itself
   // left the matrix units waiting for them: the three products of the gated
   // feed-forward's backward, 4096 tokens, 2560 x 6912, from rows: 493 us, then 476;
-  // from tiles 391, 1.48 PFLOP/s, matrix units busy 71 % of the time at 2.0 GHz.)
+  // from tiles 391, and 380 with results in whole lines, 1.53 PFLOP/s, matrix units busy
+  // 71 % of the time at 2.0 GHz.)
   struct Frags {
     v8bf a[8], b[4];
   };

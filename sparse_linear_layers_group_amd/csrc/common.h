@@ -86,9 +86,9 @@ __device__ __forceinline__ u32x2 bf16x4(v4f y) {
 // next 16).  LDS serves such a read 16 lanes at a time: 0-3, 12-15 and 20-27,
 // then 4-11, 16-19 and 28-31, and the same of the upper half.  For that four rows 4
 // apart need, with f the permutation of row / 4 % 4, distinct f0, f3, 1^f1, 1^f2
-// (and f1, f2, 1^f0, 1^f3) within a 256-byte line: f = 0, 2, 3, 1.  (Permutations by
-// row / 2 or row / 4 as they are left every read two ways in conflict, by
-// SQ_LDS_BANK_CONFLICT 4 of its 8 clocks.)
+// (and f1, f2, 1^f0, 1^f3) within a 256-byte line: f = 0, 2, 3, 1.  (SQ_LDS_BANK_CONFLICT
+// 0, 4 clocks a read.  So it is with the permutation by row / 2; by row / 4 as it is, f =
+// 0, 1, 2, 3, every read is two ways in conflict: 8 clocks, 4 of them counted.)
 __host__ __device__ constexpr int row64_place(int row, int piece) {
   const int x = (row >> 2) & 3;
   return piece ^ ((((x ^ (x >> 1)) & 1) << 1) | (x >> 1));

@@ -55,12 +55,10 @@ struct GluBwdLayout {
 // part shallower than kGluPart: a part costs a binary32 plane of the output to
 // write and to read.  Where one round of such tiles does not fill the CUs, dX, the
 // deepest, is cut into as many parts as do, and the launch takes twice as many tiles of
-// 256 x 128, two on a CU (forward and backward of 32 tokens, 896 x 4864: 35.5 us in
-// place of 39.0; 547 tokens, 8 parts either way, the products alone 33.4 in place of 37.4).
-// Up to 256 tokens, where the weight gradients' tiles are little more than their
-// stores, it takes those too (32 tokens, 1536 x 8960: 58.8 us in place of 65.6, 256
-// tokens: 95.3 and 102.4; 300: 103.3 and 102.9; 4096 tokens, 2560 x 6912, the products
-// alone: 487 in place of 391).
+// 256 x 128, two on a CU (547 tokens, 896 x 4864, binary32 gradients: 42.7 us in place of
+// 46.9; 32 tokens: 30.9 and 32.7).  Up to 256 tokens, where the weight gradients' tiles are
+// little more than their stores, it takes those too (32 tokens, 1536 x 8960: 58 us in place of
+// 66, 256 tokens: 64 and 75; 300: 73 and 74; 4096 tokens, 2560 x 6912: 560 in place of 477).
 constexpr int64_t kGluPart = 1024;
 inline int glu_parts(int64_t depth, int64_t share, int most) {
   const int64_t per = share > kGluPart ? share : kGluPart, parts = (depth + per - 1) / per;

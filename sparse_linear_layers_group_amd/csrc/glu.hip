@@ -1,6 +1,6 @@
-// glu.hip -- the gated feed-forward's first half in one kernel (two ternary x
-// int8 projections, the activation and the product) and the gating part of its
-// backward.
+// glu.hip -- the gated feed-forward's first half: two ternary x int8 projections
+// with the activation and the product in their epilogue, in one kernel up to some
+// hundred tokens, behind a launch that decodes the codes once for many.
 #include "ckpt.h"
 #include "common.h"
 #include "glu.h"
@@ -178,7 +178,7 @@ __device__ __forceinline__ void glu_barrier() {
 // into LDS, where all read them.  The activations come to LDS by DMA in whole 128-byte
 // lines, eight rows an instruction (as operands, 16 rows of 64 bytes, straight from
 // memory they bound the kernel: 24.4 us in place of 19.4 at 256 tokens, 2560 x 6912;
-// 17.2 now).  One k block (128 k) per barrier: while its products run, the next
+// 16.4 now).  One k block (128 k) per barrier: while its products run, the next
 // block's operands are decoded, and the activations and the codes two blocks on are on
 // their way.  Bound by the way from the codes through LDS to the products between two
 // barriers; fragments read a block ahead, codes by DMA, or a fifth fewer operand reads
@@ -748,22 +748,22 @@ __global__ __launch_bounds__(256, 2) void glu_gemm_kernel(GluArgs a, const char*
 }
 
 // ------------------------------------------------------------------ host
-// Up to kGluFewTokens tokens every 16 have workgroups of their own (96 tokens of
-// 896 x 4864, 1536 x 8960, 2560 x 6912: 6.0, 12.1, 13.2 us, by the kernel for some
-// tokens 6.4, 13.0, 12.3; 64 tokens: 5.7, 9.5, 9.5 and 6.3, 12.7, 12.0; 128 tokens: 8.3,
-// 15.1, 16.6 and 6.6, 13.4, 12.5).
+// Up to kGluFewTokens tokens every 16 have workgroups of their own (calls, 6:8; 96 tokens
+// of 896 x 4864, 1536 x 8960, 2560 x 6912: 7.6, 12.0, 12.7 us, by the kernel for some
+// tokens 7.8, 12.6, 11.5; 64 tokens: 7.7, 9.8, 9.5 and 7.7, 12.7, 11.6; 128 tokens: 8.3,
+// 14.9, 15.8 and 7.8, 13.0, 11.8).
 // Beyond, tiles of 32 outputs that decode for themselves, for 256 tokens at a time, one
 // on a CU, or for 128, of which a CU holds two and runs one in some half of the
 // time: whichever gives a CU less to do (256 tokens of 2560 x 6912, 1 or 2 of them on a
-// CU: 17.1 us, of 128 tokens 20.4; of 1536 x 8960, 2 or 3: 22.0 and 19.6).  With more
+// CU: 16.8 us, of 128 tokens 18.7; of 1536 x 8960, 2 or 3: 21.5 and 18.2).  With more
 // than kGluMidRounds of the smaller on a CU the codes are decoded once for all (300
-// tokens of 2048 x 11008, 5: 37.5 us, decoded once 42.1; 512 tokens of 1536 x 8960, 5:
-// 30.7 and 35.5; 768 tokens of 2560 x 6912, 6: 50.0 and 45.7).  8-bit G and U need tiles
-// of 64 outputs, of 64 or 128 tokens (192 tokens of 1536 x 8960, 2 or 2 on a CU: 19.9 us,
-// of 128 tokens 27.0; 300 tokens of 2048 x 4096, 2 or 1: 22.8 and 17.8), which win up to
-// kGluMidRoundsQ8 (768 tokens, 896 x 4864, 4: 23.4 us, decoded once 28.2; 391 tokens,
-// 1536 x 8960, 4: 34.6 and 39.3; 512 tokens, 2560 x 6912, 4: 41.2 and 39.2; 1280 tokens,
-// 896 x 4864, 5: 36.5 and 34.4).
+// tokens of 2048 x 11008, 5: 34.2 us, decoded once 41.7; 512 tokens of 1536 x 8960, 5:
+// 27.9 and 33.6; 768 tokens of 2560 x 6912, 6: 46.2 and 42.7).  8-bit G and U need tiles
+// of 64 outputs, of 64 or 128 tokens (192 tokens of 1536 x 8960, 2 or 2 on a CU: 18.6 us,
+// of 128 tokens 25.2; 300 tokens of 2048 x 4096, 2 or 1: 22.0 and 17.3), which win up to
+// kGluMidRoundsQ8 (768 tokens, 896 x 4864, 4: 22.5 us, decoded once 27.9; 391 tokens,
+// 1536 x 8960, 4: 32.3 and 38.5; 512 tokens, 2560 x 6912, 4: 37.7 and 36.9; 1280 tokens,
+// 896 x 4864, 5: 32.9 and 34.0).
 constexpr int64_t kGluFewTokens = 96, kGluMidRounds = 5, kGluMidRoundsQ8 = 4;
 // tokens of a tile that decodes for itself; 0: the codes are decoded once
 static int glu_mid_tokens(int64_t tokens, int64_t n_out, bool q8) {

@@ -10,8 +10,11 @@
 namespace bl {
 
 // ---------------------------------------------------------------- the gating
-// (v_exp_f32 and v_rcp_f32, 1 ulp each; an infinite exp gives 0, the limit.  With a
-// correctly rounded division 6001 tokens, 2048 x 11008 took 226 us, now 216.)
+// exp(-g) is v_exp_f32 (1 ulp) of RN(-g log2 e), whose rounding and constant cost it
+// 1.5 |g| 2^-24 of its value; v_rcp_f32 adds 1 ulp, so for g > 0 the sigmoid is good to
+// some 2 ulp and for g < 0 to (1.5 |g| + 7) 2^-24.  Where 1 + exp(-g) passes 2^126 it is 0 in
+// place of less than 2^-126.  (With a correctly rounded division 6001 tokens, 2048 x
+// 11008 took 226 us, now 216.)
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.f + __expf(-g)); }
 // max(g, 0) that keeps a NaN: where a scale or a checkpoint's block is NaN, the outputs show it
 __device__ __forceinline__ float relu(float g) { return g <= 0.f ? 0.f : g; }

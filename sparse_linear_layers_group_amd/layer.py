@@ -200,7 +200,7 @@ class BlockAttention:
 
 class BlockFeedForward:
     """The feed-forward side of a block: the norm, the gate and up BitLinears
-    with the gating in one kernel, and the down BitLinear, over rows of a
+    with the gating in their epilogue, and the down BitLinear, over rows of a
     residual stream (float32 or bfloat16).  The three BitLinearWeights are the
     caller's (quantised before a forward, once per training step).
 
