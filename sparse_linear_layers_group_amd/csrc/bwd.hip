@@ -616,9 +616,6 @@ __device__ __forceinline__ char* big_stage() {
   else return P == 0 ? g_big4_st0 : P == 1 ? g_big4_st1 : g_big4_st2;
 }
 
-// (512 threads at most: two wavefronts per SIMD either way, so the
-// register budget is the same; bounds that depend on kWN broke the host
-// side's template deduction)
 // Lanes l and l ^ 1 hold four-column pieces 0..3 of rows r and r + 1 (l even: r) in p;
 // in d the even lane gets pieces 0 and 2, the odd one 1 and 3, of both rows: d[e] is row
 // r + e % 2
@@ -634,6 +631,9 @@ __device__ __forceinline__ void exchange_rows(const v4f (&p)[4], v4f (&d)[4], bo
     }
 }
 
+// (512 threads at most: two wavefronts per SIMD either way, so the
+// register budget is the same; bounds that depend on kWN broke the host
+// side's template deduction)
 template <int kWN>
 __global__ __launch_bounds__(512) void gemm_nt_bf16_big_kernel(NtSet set) {
   typedef BigTile<kWN> T;
