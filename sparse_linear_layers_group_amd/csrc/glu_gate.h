@@ -48,8 +48,8 @@ __device__ __forceinline__ void act_both(float g, float& value, float& slope) {
 // transposed through LDS (for the weights' gradients, whose contraction runs over
 // tokens; tokens past the last give zeros).  bf16 is what the matrix instructions
 // take, whatever the types of dH and the gradients: 2.3e-3 of the exact gradients where
-// results rounded once to bf16 have 1.7e-3; two parts for each operand would take three
-// times the products.
+// results rounded once to bf16 have 1.7e-3.  A second part for each (codes and x_q are
+// exact) would take twice the products.
 constexpr int kGatePitch = 66;  // LDS pitch (bf16) of a transposed tile
 
 // 16 consecutive values of a row
